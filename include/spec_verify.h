@@ -47,14 +47,14 @@
 extern "C" {
 #endif
 
-typedef enum { SPEC_F32 = 0, SPEC_BF16 = 1 } spec_dtype_t;
+typedef enum { SPEC_F32 = 0, SPEC_BF16 = 1, SPEC_F16 = 2 } spec_dtype_t;   /* F16: KV cache only */
 
 /* host-side return codes */
 #define SPEC_OK 0
 #define SPEC_ERR_NULL (-1)      /* a required pointer is NULL                                */
 #define SPEC_ERR_SHAPE (-2)     /* B, gamma, N, V or rows out of range (see limits below)     */
 #define SPEC_ERR_TEMP (-3)      /* temperature not 0 and not in [FLT_MIN, FLT_MAX]             */
-#define SPEC_ERR_DTYPE (-4)     /* dtype not SPEC_F32 / SPEC_BF16                             */
+#define SPEC_ERR_DTYPE (-4)     /* dtype not one the call takes                               */
 #define SPEC_ERR_WORKSPACE (-5) /* workspace smaller than spec_workspace_bytes(...)            */
 #define SPEC_ERR_ALIGN (-6)     /* a pointer is not aligned to its element size (16 for the
                                    workspace)                                                */
@@ -65,6 +65,12 @@ typedef enum { SPEC_F32 = 0, SPEC_BF16 = 1 } spec_dtype_t;
 #define SPEC_ERR_PARENT (-22)    /* parents[b,0] != -1 or parents[b,i] not in [0, i)          */
 #define SPEC_ERR_TIMEOUT (-23)   /* a bounded wait inside a kernel gave up (an on-chip copy or
                                     tensor-core result did not arrive within 2 s)             */
+#define SPEC_ERR_LENGTH (-25)    /* KV cache: a sequence length is negative or runs past its page
+                                    table, or a count of new tokens is outside [0, N]         */
+#define SPEC_ERR_PAGE (-26)      /* KV cache: a page number is outside [0, num_pages)          */
+#define SPEC_ERR_POSITION (-27)  /* KV cache: a token's position is outside the rotation table */
+#define SPEC_ERR_PATH (-28)      /* KV cache: accept_len outside [-1, N), or path nodes that do
+                                    not increase from node 0 within [0, N)                    */
 #define SPEC_ERR_CHECK (-24)     /* checked build only (libspec_verify_checked.so): an index the
                                     kernels computed fell outside its buffer; the access was
                                     skipped. Never seen from a correct library.               */
@@ -281,6 +287,113 @@ int spec_topk(const void *logits, int dtype, int rows, int V, int k, int32_t *ou
  */
 int spec_tree_mask(const int32_t *parents, int B, int N, uint32_t *mask_words, int32_t *status,
                    void *stream);
+
+/*
+ * The paged 8-bit KV cache of the model that verification runs on, and the three operations a
+ * verification step makes on it: the drafted tokens' keys and values are appended (spec_kv_append),
+ * every drafted position attends to the cache (spec_kv_attention), and once the drafts are verified
+ * the accepted path is kept (spec_kv_commit; a verified chain needs none: its accepted tokens are
+ * the first ones, so the sequence only gets longer). The target scores every drafted position in
+ * one parallel pass ("Fast Inference from Transformers via Speculative Decoding", pith.science
+ * review, "The pith"), a tree with every node attending to itself and its ancestors (Falcon review,
+ * Figure 3, "SAR decoding tree attention"); the pages have no cache layout of their own.
+ *
+ *   k, v      [num_pages, kv_heads, page_size, head_dim] e4m3 (one byte an element)
+ *   k_scale, v_scale  [num_pages, kv_heads] fp32: what a page's bytes of one head are multiplied by
+ *   page_table [B, pages_per_seq] int32: token slot t of sequence b is row t % page_size of page
+ *             page_table[b, t / page_size]; entries past a sequence's last token are not read
+ *   seq_lens  [B] int32: the tokens a sequence holds before the N new ones (which get the slots
+ *             seq_lens[b] .. seq_lens[b] + N - 1, node i of a tree slot seq_lens[b] + i)
+ *   new_lens  [B] int32 or NULL: how many of the N new tokens sequence b has (NULL: all N); the
+ *             others are padding, neither read nor stored
+ *   mask_words [B, N, ceil(N / 32)] from spec_tree_mask, or NULL for a chain
+ * Limits: head_dim 64 or 128; page_size 16, 32, 64 or 128; kv_heads 1 .. 1024;
+ * num_pages * kv_heads * page_size < 2^31; pages_per_seq * page_size < 2^30; 1 <= N <= 2^20 (with
+ * mask_words: SPEC_MAX_NODES); B >= 0. k and v are 16-byte aligned.
+ * A page that is written belongs to one sequence; full pages may be shared by any number.
+ */
+typedef struct {
+  void *k, *v;
+  float *k_scale, *v_scale;
+  int32_t num_pages, page_size, kv_heads, head_dim;
+} spec_kv_cache_t;
+
+/*
+ * Appends N new tokens to each of B sequences: rotates the keys by their positions, stores keys and
+ * values as e4m3 with one power-of-two scale for each page and head, and rotates the queries.
+ *
+ *   rotation  of dims j < rope_dim by row `position` of rope [rope_rows, rope_dim] fp32, whose first
+ *             rope_dim / 2 columns are the cosines and the others the sines (c_j, s_j):
+ *               (x_j, x_{j+R/2}) -> (x_j c_j - x_{j+R/2} s_j, x_{j+R/2} c_j + x_j s_j), R = rope_dim
+ *             or, with interleaved != 0, the same of the pairs (x_{2j}, x_{2j+1}). Position of token
+ *             i: positions[b, i] if given, else seq_lens[b] + depth of node i if mask_words is
+ *             given, else seq_lens[b] + i. rope NULL (rope_dim 0): no rotation.
+ *   storage   a page's scale becomes s = max(its scale if it held tokens already, the smallest power
+ *             of two with max |x| <= 448 s over the tokens it receives, 2^-64); each value is stored
+ *             as x / s rounded to the nearest e4m3 (ties to even), in fp32 until then. When s grows,
+ *             the tokens the page held are stored again at the new scale (between powers of two this
+ *             loses nothing but the last bits of subnormal values).
+ *   q_out     [B, N, q_heads, head_dim] dtype, rounded once; may be q itself when q is contiguous
+ *
+ * q [B, N, q_heads, head_dim], k, v [B, N, kv_heads, head_dim]: dtype SPEC_BF16 or SPEC_F16; heads
+ * and dims contiguous, consecutive tokens *_stride elements apart (slices of one projection's
+ * output need no copy). q may be NULL with q_heads = 0. Base addresses 16-byte aligned, strides
+ * multiples of 8.
+ * rope_dim a multiple of 16, at most head_dim.
+ * In the data: a bad length (SPEC_ERR_LENGTH) skips the sequence, a bad page number
+ * (SPEC_ERR_PAGE) the tokens in that page; a token whose position is outside the table
+ * (SPEC_ERR_POSITION) is stored as if its position were 0; NaN is stored as NaN and infinities as
+ * the largest value of the page's scale, which ignores them (SPEC_ERR_NONFINITE).
+ */
+int spec_kv_append(const spec_kv_cache_t *cache, const int32_t *page_table, int pages_per_seq,
+                   const int32_t *seq_lens, const int32_t *new_lens, int B, int N, const void *k,
+                   int64_t k_stride, const void *v, int64_t v_stride, const void *q,
+                   int64_t q_stride, int q_heads, void *q_out, int dtype, const float *rope,
+                   int rope_rows, int rope_dim, int interleaved, const int32_t *positions,
+                   const uint32_t *mask_words, int32_t *status, void *stream);
+
+/*
+ * Attention of the N new tokens of each sequence over its cache, which already holds them
+ * (spec_kv_append): with q_heads = G * kv_heads, query head h reading key head h / G,
+ *   out[b, i, h] = sum_t softmax_t(scale * q[b, i, h] . k[t]) v[t]
+ * over the slots t < seq_lens[b] and, of the new ones, those node i may see: its ancestors and
+ * itself by mask_words (bit j of row i: node j), or without a mask the new tokens 0 .. i.
+ * N = 1 is ordinary decoding, a large N a piece of a prompt.
+ *   q    [B, N, q_heads, head_dim] SPEC_BF16 or SPEC_F16, tokens q_stride elements apart
+ *   out  [B, N, q_heads, head_dim] the same type, contiguous
+ *   lse  [B, N, q_heads] fp32 or NULL: the natural logarithm of the softmax's denominator
+ * Scores, statistics and sums are held in fp32 and the softmax weights are rounded to fp16 before
+ * their product with the values. A query that sees no token (an empty mask row of an empty
+ * sequence, or padding) gets zeros and lse = -inf. What lies in slots that no query of the
+ * sequence sees is not used, NaN included. A NaN in a query, key or value reaches every element
+ * of the queries that see it.
+ *   workspace  at least spec_kv_attention_workspace_bytes(B, N, q_heads, kv_heads, head_dim) bytes
+ * In the data: a bad length or page number makes every output of the sequence NaN and sets
+ * *status.
+ */
+size_t spec_kv_attention_workspace_bytes(int B, int N, int q_heads, int kv_heads, int head_dim);
+int spec_kv_attention(const spec_kv_cache_t *cache, const int32_t *page_table, int pages_per_seq,
+                      const int32_t *seq_lens, const int32_t *new_lens, int B, int N, const void *q,
+                      int64_t q_stride, int q_heads, int dtype, float scale,
+                      const uint32_t *mask_words, void *out, float *lse, int32_t *status,
+                      void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Keeps the accepted path of B verified trees, in `layers` caches that lie one after another in
+ * memory ([layers, num_pages, ...], scales too) and share page numbers: row
+ * seq_lens[b] + path_nodes[b, k] moves to row seq_lens[b] + k for k = 0 .. accept_len[b], and
+ * out_lens[b] = seq_lens[b] + accept_len[b] + 1. accept_len and path_nodes are what
+ * spec_verify_tree and spec_verify_tree_sample return. A page that receives rows has its scale
+ * raised to hold them as spec_kv_append does (never lowered).
+ *   accept_len [B], path_nodes [B, N], out_lens [B] int32 (out_lens apart from seq_lens)
+ * accept_len -1 (a batch row that verification refused) leaves the sequence as it is, as do a bad
+ * path (SPEC_ERR_PATH) and a bad length (SPEC_ERR_LENGTH); a bad page number (SPEC_ERR_PAGE)
+ * leaves out the rows it concerns. N <= SPEC_MAX_NODES.
+ */
+int spec_kv_commit(const spec_kv_cache_t *cache, int layers, const int32_t *page_table,
+                   int pages_per_seq, const int32_t *seq_lens, int B, int N,
+                   const int32_t *path_nodes, const int32_t *accept_len, int32_t *out_lens,
+                   int32_t *status, void *stream);
 
 /* Static text for any SPEC_* code ("unknown status" otherwise). */
 const char *spec_status_string(int code);

@@ -2,8 +2,9 @@
 
 The C library libspec_verify.so (csrc/, declared in include/spec_verify.h) holds the kernels:
 batched chain verification by rejection sampling, greedy and stochastic tree verification, the
-temperature softmax, the drafter-side sampler and top-k, the tree-attention mask, and chain
-verification fused with its LM-head GEMMs on the tensor cores. This package is its thin Python
+temperature softmax, the drafter-side sampler and top-k, the tree-attention mask, chain
+verification fused with its LM-head GEMMs on the tensor cores, and the paged 8-bit KV cache that a
+verification step appends to, attends over and keeps the accepted path of. This package is its thin Python
 binding (argument marshalling only); see _binding.py.
 """
 
@@ -18,4 +19,7 @@ from ._binding import (  # noqa: F401
     spec_workspace_bytes,
     spec_workspace_init, topk, tree_mask, verify_chain, verify_chain_lmhead, verify_tree,
     verify_tree_sample, spec_verify_chain_lmhead, spec_lmhead_workspace_bytes, SPEC_ERR_TIMEOUT,
-    spec_last_cuda_error, spec_cuda_error_string, spec_selftest_bounded_wait)
+    spec_last_cuda_error, spec_cuda_error_string, spec_selftest_bounded_wait,
+    SPEC_F16, SPEC_ERR_LENGTH, SPEC_ERR_PAGE, SPEC_ERR_POSITION, SPEC_ERR_PATH, KVCache,
+    SpecKVCache, kv_append, kv_attention, kv_commit, new_attention_workspace, new_kv_cache,
+    spec_kv_append, spec_kv_attention, spec_kv_attention_workspace_bytes, spec_kv_commit)

@@ -18,12 +18,13 @@ LIB_PATH = os.path.join(PKG, "libspec_verify.so")
 # the same kernels compiled with SPEC_CHECKED: computed indices range-checked (SPEC_ERR_CHECK)
 CHECKED_LIB_PATH = os.path.join(PKG, "libspec_verify_checked.so")
 
-SPEC_F32, SPEC_BF16 = 0, 1
+SPEC_F32, SPEC_BF16, SPEC_F16 = 0, 1, 2
 SPEC_OK = 0
 SPEC_ERR_NULL, SPEC_ERR_SHAPE, SPEC_ERR_TEMP, SPEC_ERR_DTYPE = -1, -2, -3, -4
 SPEC_ERR_WORKSPACE, SPEC_ERR_ALIGN, SPEC_ERR_LAUNCH = -5, -6, -7
 SPEC_ERR_NONFINITE, SPEC_ERR_TOKEN, SPEC_ERR_PARENT, SPEC_ERR_CHECK = -20, -21, -22, -24
 SPEC_ERR_TIMEOUT = -23
+SPEC_ERR_LENGTH, SPEC_ERR_PAGE, SPEC_ERR_POSITION, SPEC_ERR_PATH = -25, -26, -27, -28
 SPEC_MAX_V, SPEC_MAX_GAMMA, SPEC_MAX_NODES = 1 << 20, 255, 1024
 SPEC_LMHEAD_MAX_V = 1 << 19
 
@@ -33,7 +34,8 @@ EXPORTS = ("spec_workspace_bytes", "spec_workspace_init", "spec_verify_chain",
            "spec_verify_chain_lmhead", "spec_probs", "spec_status_string",
            "spec_last_cuda_error", "spec_cuda_error_string",
            "spec_launch_shape", "spec_verify_chain_static", "spec_sample", "spec_topk",
-           "spec_tree_mask", "spec_selftest_bounded_wait")
+           "spec_tree_mask", "spec_selftest_bounded_wait", "spec_kv_append",
+           "spec_kv_attention_workspace_bytes", "spec_kv_attention", "spec_kv_commit")
 SPEC_MAX_TOPK = 16
 SPEC_STATIC_SCRATCH_BYTES = 4 << 20
 SPEC_CALL_CHAIN, SPEC_CALL_TREE, SPEC_CALL_PROBS = 0, 1, 2
@@ -41,6 +43,14 @@ SPEC_CALL_CHAIN, SPEC_CALL_TREE, SPEC_CALL_PROBS = 0, 1, 2
 _lock = threading.Lock()
 _lib = None
 _checked_lib = None
+
+
+class SpecKVCache(ctypes.Structure):
+    """spec_kv_cache_t: one layer's paged 8-bit cache as the library sees it."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("num_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32)]
 
 
 class SpecError(RuntimeError):
@@ -106,6 +116,17 @@ def load_library(checked: bool = False):
         lib.spec_tree_mask.restype = i32
         lib.spec_selftest_bounded_wait.argtypes = [vp, ctypes.c_double, vp]
         lib.spec_selftest_bounded_wait.restype = i32
+        i64, cache = ctypes.c_int64, ctypes.POINTER(SpecKVCache)
+        lib.spec_kv_append.argtypes = [cache, vp, i32, vp, vp, i32, i32, vp, i64, vp, i64, vp, i64,
+                                       i32, vp, i32, vp, i32, i32, i32, vp, vp, vp, vp]
+        lib.spec_kv_append.restype = i32
+        lib.spec_kv_attention_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
+        lib.spec_kv_attention_workspace_bytes.restype = sz
+        lib.spec_kv_attention.argtypes = [cache, vp, i32, vp, vp, i32, i32, vp, i64, i32, i32, f32,
+                                          vp, vp, vp, vp, vp, sz, vp]
+        lib.spec_kv_attention.restype = i32
+        lib.spec_kv_commit.argtypes = [cache, i32, vp, i32, vp, i32, i32, vp, vp, vp, vp, vp]
+        lib.spec_kv_commit.restype = i32
         if checked:
             _checked_lib = lib
         else:
@@ -352,6 +373,155 @@ def spec_selftest_bounded_wait(status, limit_seconds: float, stream=None) -> int
                                                          _stream(stream)))
 
 
+# ------------------------------------------------------------------ the paged 8-bit KV cache
+
+_E4M3 = torch.float8_e4m3fn
+_KV_DTYPES = {torch.bfloat16: SPEC_BF16, torch.float16: SPEC_F16}
+
+
+class KVCache:
+    """The paged 8-bit KV cache of one or several layers: k, v [layers, num_pages, kv_heads,
+    page_size, head_dim] float8_e4m3fn (or uint8) and k_scale, v_scale [layers, num_pages,
+    kv_heads] fp32, all contiguous CUDA tensors that the caller owns; without the layers axis they
+    are one layer. Layers share page numbers (one page table serves them all)."""
+
+    def __init__(self, k, v, k_scale, v_scale):
+        if not isinstance(k, torch.Tensor) or k.dim() not in (4, 5):
+            raise ValueError("k must be a [layers, num_pages, kv_heads, page_size, head_dim] "
+                             "tensor (or one layer of it)")
+        if k.dim() == 4:
+            k, v, k_scale, v_scale = (t[None] for t in (k, v, k_scale, v_scale))
+        self.layers, self.num_pages, self.kv_heads, self.page_size, self.head_dim = k.shape
+        for t, name in ((k, "k"), (v, "v")):
+            _expect(t, name, k.numel(), (_E4M3, torch.uint8))
+        for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            _expect(t, name, self.layers * self.num_pages * self.kv_heads, (torch.float32,))
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        ptrs = [_ptr(t).value if t.numel() else 0 for t in (k, v, k_scale, v_scale)]
+        page = self.num_pages * self.kv_heads
+        steps = [page * self.page_size * self.head_dim] * 2 + [page * 4] * 2
+        self._structs = [SpecKVCache(*(p + i * s for p, s in zip(ptrs, steps)), self.num_pages,
+                                     self.page_size, self.kv_heads, self.head_dim)
+                         for i in range(self.layers)]
+
+    def struct(self, layer=0):
+        """The spec_kv_cache_t of one layer."""
+        if not 0 <= layer < self.layers:
+            raise ValueError(f"layer {layer} of a cache of {self.layers}")
+        return self._structs[layer]
+
+
+def _kv_dtype(t, name):
+    if not isinstance(t, torch.Tensor) or t.dim() != 4:
+        raise ValueError(f"{name} must be a [B, N, heads, head_dim] tensor")
+    flag = _KV_DTYPES.get(t.dtype)
+    if flag is None:
+        raise TypeError(f"{name} must be bfloat16 or float16 (got {t.dtype})")
+    return flag
+
+
+def _tokens(t, name, B, N, heads, D, dtype):
+    """(pointer, token stride) of a [B, N, heads, D] operand whose heads and dims are contiguous
+    and whose tokens lie evenly apart."""
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype:
+        raise TypeError(f"{name}: expected a {dtype} tensor")
+    if tuple(t.shape) != (B, N, heads, D):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(B, N, heads, D)}")
+    if not t.numel():
+        return None, heads * D
+    if not t.is_cuda:
+        raise ValueError("device tensor expected (the library takes device pointers)")
+    sb, sn, sh, sd = t.stride()
+    step = sn if N > 1 else sb if B > 1 else heads * D
+    if sd != 1 or (heads > 1 and sh != D) or (B > 1 and N > 1 and sb != N * sn):
+        raise ValueError(f"{name}: heads and dims must be contiguous and tokens evenly apart "
+                         f"(strides {t.stride()})")
+    return t.data_ptr(), step
+
+
+def _kv_shared(page_table, seq_lens, new_lens, mask, status, B, N):
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2 or \
+            page_table.shape[0] != B:
+        raise ValueError(f"page_table must be a [{B}, pages] tensor")
+    i32 = (torch.int32,)
+    _expect(page_table, "page_table", page_table.numel(), i32)
+    _expect(seq_lens, "seq_lens", B, i32)
+    _expect(new_lens, "new_lens", B, i32)
+    _expect(mask, "mask", B * N * ((N + 31) // 32), i32)
+    _expect(status, "status", 1, i32)
+    return page_table.shape[1]
+
+
+def spec_kv_append(cache, layer, page_table, seq_lens, new_lens, k, v, q, q_out, rope, interleaved,
+                   positions, mask_words, status, stream=None) -> int:
+    """k, v [B, N, kv_heads, D] and q, q_out [B, N, q_heads, D] (bf16 or fp16; q None: no queries);
+    page_table [B, pages], seq_lens [B], new_lens [B] or None, positions [B, N] or None int32;
+    rope [rows, rope_dim] fp32 or None; mask_words [B, N, ceil(N/32)] int32 or None."""
+    flag = _kv_dtype(k, "k")
+    B, N = k.shape[:2]
+    D = cache.head_dim
+    pps = _kv_shared(page_table, seq_lens, new_lens, mask_words, status, B, N)
+    kp, ks = _tokens(k, "k", B, N, cache.kv_heads, D, k.dtype)
+    vp, vs = _tokens(v, "v", B, N, cache.kv_heads, D, k.dtype)
+    heads, qp, qs = 0, None, D
+    if q is not None:
+        heads = q.shape[2] if q.dim() == 4 else -1
+        qp, qs = _tokens(q, "q", B, N, heads, D, k.dtype)
+        _expect(q_out, "q_out", q.numel(), (k.dtype,))
+    rows = width = 0
+    if rope is not None:
+        if not isinstance(rope, torch.Tensor) or rope.dim() != 2:
+            raise ValueError("rope must be a [rows, rope_dim] tensor")
+        rows, width = rope.shape
+        _expect(rope, "rope", rows * width, (torch.float32,))
+    _expect(positions, "positions", B * N, (torch.int32,))
+    return load_library().spec_kv_append(
+        ctypes.byref(cache.struct(layer)), _ptr(page_table), pps, _ptr(seq_lens), _ptr(new_lens), B,
+        N, kp, ks, vp, vs, qp, qs, heads, _ptr(q_out) if q is not None else None, flag, _ptr(rope),
+        rows, width, int(bool(interleaved)), _ptr(positions), _ptr(mask_words), _ptr(status),
+        _stream(stream))
+
+
+def spec_kv_attention_workspace_bytes(B: int, N: int, q_heads: int, kv_heads: int,
+                                      head_dim: int) -> int:
+    return int(load_library().spec_kv_attention_workspace_bytes(B, N, q_heads, kv_heads, head_dim))
+
+
+def spec_kv_attention(cache, layer, page_table, seq_lens, new_lens, q, scale, mask_words, out, lse,
+                      status, workspace, stream=None) -> int:
+    """q, out [B, N, q_heads, D] (bf16 or fp16); lse [B, N, q_heads] fp32 or None; workspace uint8
+    (scratch); the others as for spec_kv_append."""
+    flag = _kv_dtype(q, "q")
+    B, N, heads, D = q.shape
+    if D != cache.head_dim:
+        raise ValueError(f"q: head_dim {D}, the cache's is {cache.head_dim}")
+    pps = _kv_shared(page_table, seq_lens, new_lens, mask_words, status, B, N)
+    qp, qs = _tokens(q, "q", B, N, heads, D, q.dtype)
+    _expect(out, "out", q.numel(), (q.dtype,))
+    _expect(lse, "lse", B * N * heads, (torch.float32,))
+    return load_library().spec_kv_attention(
+        ctypes.byref(cache.struct(layer)), _ptr(page_table), pps, _ptr(seq_lens), _ptr(new_lens), B,
+        N, qp, qs, heads, flag, float(scale), _ptr(mask_words), _ptr(out), _ptr(lse), _ptr(status),
+        _ptr(workspace), _nbytes(workspace), _stream(stream))
+
+
+def spec_kv_commit(cache, page_table, seq_lens, path_nodes, accept_len, out_lens, status,
+                   stream=None) -> int:
+    """path_nodes [B, N], accept_len [B] (as spec_verify_tree returns them), out_lens [B] int32:
+    every layer of the cache."""
+    if not isinstance(path_nodes, torch.Tensor) or path_nodes.dim() != 2:
+        raise ValueError("path_nodes must be a [B, N] tensor")
+    B, N = path_nodes.shape
+    i32 = (torch.int32,)
+    pps = _kv_shared(page_table, seq_lens, None, None, status, B, N)
+    _expect(path_nodes, "path_nodes", B * N, i32)
+    _expect(accept_len, "accept_len", B, i32)
+    _expect(out_lens, "out_lens", B, i32)
+    return load_library().spec_kv_commit(
+        ctypes.byref(cache.struct(0)), cache.layers, _ptr(page_table), pps, _ptr(seq_lens), B, N,
+        _ptr(path_nodes), _ptr(accept_len), _ptr(out_lens), _ptr(status), _stream(stream))
+
+
 # ------------------------------------------------------------------ conveniences (allocation)
 
 def new_workspace(B: int, rows_per_b: int, V: int, dtype: int, device=None) -> torch.Tensor:
@@ -488,3 +658,66 @@ def tree_mask(parents, stream=None):
     st = torch.zeros(1, dtype=torch.int32, device=parents.device)
     check(spec_tree_mask(parents, out, st, stream), "spec_tree_mask")
     return out, st
+
+
+def new_kv_cache(num_pages, kv_heads, head_dim, page_size=64, layers=1, device=None) -> KVCache:
+    """An empty paged 8-bit KV cache (its pages need no initial contents)."""
+    shape = (layers, num_pages, kv_heads, page_size, head_dim)
+    k, v = (torch.empty(shape, dtype=torch.uint8, device=device or "cuda").view(_E4M3)
+            for _ in range(2))
+    ks, vs = (torch.ones(shape[:3], dtype=torch.float32, device=k.device) for _ in range(2))
+    return KVCache(k, v, ks, vs)
+
+
+def new_attention_workspace(B, N, q_heads, kv_heads, head_dim, device=None) -> torch.Tensor:
+    """A workspace for kv_attention calls of this shape (scratch; never needs zeroing)."""
+    n = spec_kv_attention_workspace_bytes(B, N, q_heads, kv_heads, head_dim)
+    if n == 0:
+        raise SpecError(SPEC_ERR_SHAPE, "spec_kv_attention_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def kv_append(cache, page_table, seq_lens, k, v, q=None, rope=None, layer=0, interleaved=False,
+              positions=None, mask=None, new_lens=None, q_out=None, status=None, stream=None):
+    """Appends the new tokens' keys (rotated) and values to one layer of the cache and rotates the
+    queries (spec_kv_append). Returns (q_out, status); q_out is None without q."""
+    if q is not None and q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if status is None:
+        status = torch.zeros(1, dtype=torch.int32, device=seq_lens.device)
+    check(spec_kv_append(cache, layer, page_table, seq_lens, new_lens, k, v, q, q_out, rope,
+                         interleaved, positions, mask, status, stream), "spec_kv_append")
+    return q_out, status
+
+
+def kv_attention(cache, page_table, seq_lens, q, scale=None, mask=None, layer=0, new_lens=None,
+                 out=None, workspace=None, status=None, return_lse=False, stream=None):
+    """Attention of the new tokens over one layer of the cache, which already holds them
+    (spec_kv_attention). scale: 1 / sqrt(head_dim) by default. Returns (out, lse, status); lse is
+    None unless return_lse."""
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    B, N, heads, D = q.shape
+    lse = torch.empty((B, N, heads), dtype=torch.float32, device=q.device) if return_lse else None
+    if status is None:
+        status = torch.zeros(1, dtype=torch.int32, device=q.device)
+    if workspace is None:
+        workspace = new_attention_workspace(B, N, heads, cache.kv_heads, D, q.device)
+    if scale is None:
+        scale = D ** -0.5
+    check(spec_kv_attention(cache, layer, page_table, seq_lens, new_lens, q, scale, mask, out, lse,
+                            status, workspace, stream), "spec_kv_attention")
+    return out, lse, status
+
+
+def kv_commit(cache, page_table, seq_lens, path_nodes, accept_len, out_lens=None, status=None,
+              stream=None):
+    """Keeps the accepted paths of verified trees in every layer of the cache (spec_kv_commit).
+    Returns (the sequences' new lengths, status)."""
+    if out_lens is None:
+        out_lens = torch.empty_like(seq_lens)
+    if status is None:
+        status = torch.zeros(1, dtype=torch.int32, device=seq_lens.device)
+    check(spec_kv_commit(cache, page_table, seq_lens, path_nodes, accept_len, out_lens, status,
+                         stream), "spec_kv_commit")
+    return out_lens, status

@@ -593,6 +593,10 @@ const char *spec_status_string(int code) {
     case SPEC_ERR_TOKEN: return "a draft or node token is outside [0, V)";
     case SPEC_ERR_PARENT: return "a tree parent index is invalid";
     case SPEC_ERR_CHECK: return "checked build: a computed index fell outside its buffer";
+    case SPEC_ERR_LENGTH: return "a sequence length is out of its page table's range";
+    case SPEC_ERR_PAGE: return "a page number is outside [0, num_pages)";
+    case SPEC_ERR_POSITION: return "a position is outside the rotation table";
+    case SPEC_ERR_PATH: return "an accepted path is invalid";
     case SPEC_ERR_TIMEOUT: return "a bounded wait inside a kernel gave up";
     default: return "unknown status";
   }
