@@ -368,8 +368,9 @@ int spec_kv_append(const spec_kv_cache_t *cache, const int32_t *page_table, int 
  * sequence sees is not used, NaN included. A NaN in a query, key or value reaches every element
  * of the queries that see it.
  *   workspace  at least spec_kv_attention_workspace_bytes(B, N, q_heads, kv_heads, head_dim) bytes
- * In the data: a bad length or page number makes every output of the sequence NaN and sets
- * *status.
+ * In the data: a bad length makes every output of the sequence NaN, a bad page number those of the
+ * queries that see a token of the page; both set *status. A wait inside the kernel that gives up
+ * (after 2 s) sets *status to SPEC_ERR_TIMEOUT.
  */
 size_t spec_kv_attention_workspace_bytes(int B, int N, int q_heads, int kv_heads, int head_dim);
 int spec_kv_attention(const spec_kv_cache_t *cache, const int32_t *page_table, int pages_per_seq,
