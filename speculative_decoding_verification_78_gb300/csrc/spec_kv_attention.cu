@@ -38,10 +38,11 @@ namespace specv {
 namespace {
 
 constexpr int kTile = 128;          // tokens
-constexpr int kSoftWarps = 8;
-constexpr int kSoftThreads = 32 * kSoftWarps;
-constexpr int kProducer = kSoftWarps, kMma = kSoftWarps + 1;   // warps
-constexpr int kAttnThreads = 32 * (kSoftWarps + 2);
+constexpr int kGroupWarps = 8;      // softmax warps of a tile
+constexpr int kGroupThreads = 32 * kGroupWarps;
+constexpr int kSoftThreads = 2 * kGroupThreads;
+constexpr int kProducer = 2 * kGroupWarps, kMma = kProducer + 1;   // warps
+constexpr int kAttnThreads = 32 * (kMma + 1);
 constexpr int kMaxCtas = 304;       // workspace parts are sized for this many CTAs
 constexpr float kBias = 8.f;        // a new reference puts the largest weight at 2^8 ...
 constexpr float kTrigger = 15.f;    // ... and is taken when one exceeds 2^15 (fp16 ends at 2^16)
@@ -117,17 +118,34 @@ __device__ __forceinline__ void mma_commit(uint64_t *bar) {
           tc::saddr(bar))
       : "memory");
 }
-// 8 / 16 consecutive fp32 columns of this thread's lane, complete on return
+// 4 / 8 / 16 consecutive fp32 columns of this thread's lane; valid after tmem_wait of the same array
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&v)[4]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+               : "r"(taddr));
+}
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&v)[8]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
       : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
         "=r"(v[7])
       : "r"(taddr));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&v)[16]) {
-  tc::tmem_load16(taddr, v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15}, [%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+        "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
+        "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr));
+}
+// the registers pass through, so nothing that uses them is scheduled ahead of the wait
+template <int K>
+__device__ __forceinline__ void tmem_wait(uint32_t (&v)[K]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < K; ++i) asm volatile("" : "+r"(v[i]));
 }
 __device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&v)[8]) {
   asm volatile(
@@ -149,19 +167,34 @@ __device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
-// barrier 1 over the softmax threads; true in all of them if `p` was in any
-__device__ __forceinline__ bool soft_any(bool p) {
+// barrier 1 + group over a group's threads; true in all of them if `p` was in any
+__device__ __forceinline__ bool group_any(int group, bool p) {
   uint32_t r;
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, 1, %2, p;\n\t"
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, %3, %2, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"(static_cast<uint32_t>(p)), "n"(kSoftThreads)
+      : "r"(static_cast<uint32_t>(p)), "n"(kGroupThreads), "r"(1 + group)
       : "memory");
   return r != 0;
 }
-__device__ __forceinline__ void soft_sync() {
-  asm volatile("bar.sync 1, %0;" ::"n"(kSoftThreads) : "memory");
+__device__ __forceinline__ void group_sync(int group) {
+  asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(kGroupThreads) : "memory");
+}
+__device__ __forceinline__ void soft_sync() {   // both groups
+  asm volatile("bar.sync 3, %0;" ::"n"(kSoftThreads) : "memory");
+}
+// true in one lane of a converged warp
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+// tc::mbar_wait whose usual case, a phase that has completed, costs no call
+__device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity) {
+  return tc::mbar_try(bar, parity) || tc::mbar_wait(bar, parity);
 }
 __device__ __forceinline__ void fence_async() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -193,15 +226,16 @@ __host__ __device__ constexpr uint32_t attn_idesc(int M, int N, bool mn_major) {
 
 // ------------------------------------------------------------------ configuration
 
-// T: query type; D: head dim; NT: columns (query rows of a tile); S: stages of K and V; NB: buffers
-// of P and of the widened V.
-template <typename T_, int D_, int NT_, int S_, int NB_, int CTAS_>
+// T: query type; D: head dim; NT: columns (query rows of a tile); S: stages of K and V
+template <typename T_, int D_, int NT_, int S_>
 struct Cfg {
   using T = T_;
-  static constexpr int D = D_, NT = NT_, S = S_, NB = NB_, CTAS = CTAS_;
-  static constexpr int kTerms = sizeof(T) == 2 && __is_same(T, __half) ? 3 : 2;
+  static constexpr int D = D_, NT = NT_, S = S_;
+  static constexpr int kTerms = __is_same(T, __half) ? 3 : 2;
   static constexpr int C = NT / 2;                       // columns of a softmax thread
-  static constexpr int CH = C < 16 ? C : 16;             // columns read at a time
+  static constexpr int CH = 8;                           // columns read at a time
+  static constexpr int EC = NT / 4;                      // columns of a thread in the epilogue
+  static constexpr int ECH = EC < 16 ? EC : 16;
   static constexpr int kSideBytes = kTile * D;           // K or V of a stage
   static constexpr int kPSpan = NT >= 64 ? 128 : 2 * NT; // bytes of a row of P
   static constexpr int kPBlocks = NT > 64 ? NT / 64 : 1;
@@ -209,21 +243,21 @@ struct Cfg {
   static constexpr int kVfBytes = kTile * D * 2;
   static constexpr int kQBytes = NT * D;                 // one term
   static constexpr int kOffV16 = S * 2 * kSideBytes;
-  static constexpr int kOffP = kOffV16 + NB * kVfBytes;
-  static constexpr int kOffQ = kOffP + NB * kPBytes;
+  static constexpr int kOffP = kOffV16 + 2 * kVfBytes;
+  static constexpr int kOffQ = kOffP + 2 * kPBytes;
   static constexpr int kOffSmall = kOffQ + kTerms * kQBytes;
-  static constexpr uint32_t kTmem = 4 * NT;              // S0, S1, O and a power of two
+  static constexpr uint32_t kTmem = 4 * NT;              // each group's S and O
 };
 
 struct __align__(16) Small {   // the small parts of shared memory; arrays of NT follow
   uint64_t full[4], empty[4], sfull[2], pfull[2], pfree[2], qfull, done;
   float ks[4][8], vs[4][8];
-  uint8_t vnan[kTile];         // token's values hold NaN (see convert)
+  uint8_t vnan[2][kTile];      // by group: the token's values hold NaN (see widen)
   uint32_t tmem;
   int b0, skip0;
   int warp_sum[kAttnThreads / 32];
 };
-template <class F> constexpr int smem_bytes() {
+template <class F> constexpr int smem_bytes() {   // + qs, nm of each group, tok
   return F::kOffSmall + static_cast<int>(sizeof(Small)) + 4 * F::NT * 4;
 }
 
@@ -333,7 +367,7 @@ __device__ void locate(const AttnArgs &p, Small &sm, int &t0, int &t1, Item &x, 
 // ------------------------------------------------------------------ softmax threads
 
 // Rows of the item's tile as e4m3 terms in shared memory (16 or 8 lanes a row), each in units of a
-// power of two that puts its largest element in [2^7, 2^8); qs[n] undoes it.
+// power of two that puts its largest element in [2^7, 2^8); qs[n] undoes it. All softmax threads.
 template <class F>
 __device__ __forceinline__ void load_queries(const AttnArgs &p, const Item &x, uint8_t *sq,
                                              float *qs, float *nm, int *tok) {
@@ -343,7 +377,7 @@ __device__ __forceinline__ void load_queries(const AttnArgs &p, const Item &x, u
 #pragma unroll
   for (int n0 = 0; n0 < F::NT; n0 += kRows) {
     const int n = n0 + row0;
-    if (F::NT % kRows != 0 && n >= F::NT) break;   // whole warps: kRows is a multiple of 16
+    if (n >= F::NT) break;   // whole warps: a warp's rows are 2 or 4
     const long long r = static_cast<long long>(x.rt) * F::NT + n;
     const int i = static_cast<int>(r / p.G), g = static_cast<int>(r - static_cast<long long>(i) * p.G);
     float f[8];
@@ -365,7 +399,7 @@ __device__ __forceinline__ void load_queries(const AttnArgs &p, const Item &x, u
     const float mul = __uint_as_float(static_cast<uint32_t>(127 + 127 + 7 - e) << 23);
     if (sub == 0) {
       qs[n] = m < INFINITY ? __uint_as_float(static_cast<uint32_t>(e - 7) << 23) : NAN;
-      nm[n] = kNoRef;
+      nm[n] = nm[F::NT + n] = kNoRef;
       tok[n] = min(i, p.a.N - 1);
     }
 #pragma unroll
@@ -384,51 +418,64 @@ __device__ __forceinline__ void load_queries(const AttnArgs &p, const Item &x, u
   }
 }
 
-// V's bytes of the tile to fp16 rows of 64 dims (128 bytes, swizzled); tokens from `valid` on are
-// zero. NaN codes become zero and mark their token: the weights of the rows that see it then turn
-// NaN instead (a NaN operand would reach the rows that do not). Returns whether there was one.
+// V's bytes of a tile, on their way to fp16: 16 bytes a lane and step, whole rows side by side.
+template <class F> struct Widen {
+  static constexpr int kLanes = F::D / 16;               // lanes of a token
+  static constexpr int kRows = kGroupThreads / kLanes;   // tokens a step
+  static constexpr int kSteps = kTile / kRows;
+};
 template <class F>
-__device__ __forceinline__ bool convert(const uint8_t *sv, uint8_t *out, int valid, uint8_t *vnan) {
-  constexpr int kLanes = F::D / 16;                      // 16 bytes a thread and step
-  constexpr int kRows = kSoftThreads / kLanes;           // tokens a step
-  const int c = threadIdx.x % kLanes, row0 = threadIdx.x / kLanes;
-  bool nan = false;
+__device__ __forceinline__ void fetch_values(const uint8_t *sv, int gtid, int valid,
+                                             uint4 (&w)[Widen<F>::kSteps]) {
 #pragma unroll
-  for (int t0 = 0; t0 < kTile; t0 += kRows) {
-    const int t = t0 + row0;
-    uint4 w = *reinterpret_cast<const uint4 *>(sv + t * F::D + c * 16);
-    if (t >= valid) w = make_uint4(0, 0, 0, 0);
-    uint32_t b[4] = {w.x, w.y, w.z, w.w};
-    uint32_t any = 0;
+  for (int u = 0; u < Widen<F>::kSteps; ++u) {
+    const int t = u * Widen<F>::kRows + gtid / Widen<F>::kLanes;
+    w[u] = *reinterpret_cast<const uint4 *>(sv + t * F::D + gtid % Widen<F>::kLanes * 16);
+    if (t >= valid) w[u] = make_uint4(0, 0, 0, 0);
+  }
+}
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) {   // bit 7 of each NaN byte
+  return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+}
+// The values as fp16 rows of 64 dims (128 bytes, swizzled). NaN codes become zero and mark their
+// token: the weights of the rows that see it then turn NaN instead (a NaN operand would reach the
+// rows that do not). Returns whether there was one.
+template <class F>
+__device__ __forceinline__ bool widen(uint4 (&w)[Widen<F>::kSteps], uint8_t *out, int gtid,
+                                      uint8_t *vnan) {
+  const int c = gtid % Widen<F>::kLanes, row0 = gtid / Widen<F>::kLanes;
+  uint32_t any = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) any |= (b[i] & 0x7f7f7f7fu) + 0x01010101u;
-    if (any & 0x80808080u) {
+  for (int u = 0; u < Widen<F>::kSteps; ++u)
+    any |= nan_codes(w[u].x) | nan_codes(w[u].y) | nan_codes(w[u].z) | nan_codes(w[u].w);
+  if (any) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t hit = ((b[i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-        b[i] &= ~((hit >> 7) * 255u);
-      }
-      vnan[t] = 1;
-      nan = true;
+    for (int u = 0; u < Widen<F>::kSteps; ++u) {
+      const uint32_t hx = nan_codes(w[u].x), hy = nan_codes(w[u].y), hz = nan_codes(w[u].z),
+                     hw = nan_codes(w[u].w);
+      w[u].x &= ~((hx >> 7) * 255u);
+      w[u].y &= ~((hy >> 7) * 255u);
+      w[u].z &= ~((hz >> 7) * 255u);
+      w[u].w &= ~((hw >> 7) * 255u);
+      if (hx | hy | hz | hw) vnan[u * Widen<F>::kRows + row0] = 1;
     }
-    uint4 lo, hi;
-    lo.x = e4m3_to_half2(b[0] & 0xffffu);
-    lo.y = e4m3_to_half2(b[0] >> 16);
-    lo.z = e4m3_to_half2(b[1] & 0xffffu);
-    lo.w = e4m3_to_half2(b[1] >> 16);
-    hi.x = e4m3_to_half2(b[2] & 0xffffu);
-    hi.y = e4m3_to_half2(b[2] >> 16);
-    hi.z = e4m3_to_half2(b[3] & 0xffffu);
-    hi.w = e4m3_to_half2(b[3] >> 16);
-    // 64 dims (4 threads) a block of kTile rows; the second block's threads store their halves the
-    // other way round, so that eight neighbours never meet in a bank
-    uint8_t *blk = out + (c >> 2) * (kTile * 128);
+  }
+  // 64 dims (4 lanes) a block of kTile rows; the second block's lanes store their halves the other
+  // way round, so that eight neighbours never meet in a bank
+  uint8_t *blk = out + (c >> 2) * (kTile * 128);
+  const bool flip = (c >> 2) & 1;
+#pragma unroll
+  for (int u = 0; u < Widen<F>::kSteps; ++u) {
+    const int t = u * Widen<F>::kRows + row0;
+    const uint4 lo = make_uint4(e4m3_to_half2(w[u].x & 0xffffu), e4m3_to_half2(w[u].x >> 16),
+                                e4m3_to_half2(w[u].y & 0xffffu), e4m3_to_half2(w[u].y >> 16));
+    const uint4 hi = make_uint4(e4m3_to_half2(w[u].z & 0xffffu), e4m3_to_half2(w[u].z >> 16),
+                                e4m3_to_half2(w[u].w & 0xffffu), e4m3_to_half2(w[u].w >> 16));
     const uint32_t a0 = swz<128>(t * 128 + (c & 3) * 32), a1 = swz<128>(t * 128 + (c & 3) * 32 + 16);
-    const bool flip = (c >> 2) & 1;
     *reinterpret_cast<uint4 *>(blk + (flip ? a1 : a0)) = flip ? hi : lo;
     *reinterpret_cast<uint4 *>(blk + (flip ? a0 : a1)) = flip ? lo : hi;
   }
-  return nan;
+  return any != 0;
 }
 
 // Sums (or maxima) over a warp's 32 lanes of C per-lane values, C a power of two up to 32: on
@@ -472,18 +519,22 @@ __device__ __forceinline__ bool sees(const AttnArgs &p, const Item &x, const Tok
 }
 
 // The weights of the tile against the reference as it stands: fp16 to P, their sums (over the value
-// scale) to lt; true if one exceeds what fp16 holds comfortably.
+// scale) added to l; true if one exceeds what fp16 holds comfortably. The scores of the next
+// columns are on their way from tensor memory while these are worked on.
 template <class F, bool kMasked>
 __device__ __forceinline__ bool weigh(const AttnArgs &p, const Item &x, const Token &t, bool poison,
                                       uint32_t ts, int col0, uint8_t *sp, const float *qs,
                                       const float *nm, const int *tok, int row,
-                                      f32x2 (&lt)[F::C / 2]) {
+                                      f32x2 (&l)[F::C / 2]) {
   const f32x2 ks2 = pk2(t.ks2, t.ks2), lvs2 = pk2(t.lvs, t.lvs), ivs2 = pk2(t.ivs, t.ivs);
   float big = -INFINITY;
+  uint32_t s[2][F::CH];
+  tmem_ld(ts, s[0]);
 #pragma unroll
   for (int c0 = 0; c0 < F::C; c0 += F::CH) {
-    uint32_t s[F::CH];
-    tmem_ld(ts + c0, s);
+    uint32_t(&v)[F::CH] = s[(c0 / F::CH) & 1];
+    tmem_wait(v);
+    if (c0 + F::CH < F::C) tmem_ld(ts + c0 + F::CH, s[(c0 / F::CH + 1) & 1]);
     uint32_t h[F::CH / 2];
 #pragma unroll
     for (int c = 0; c < F::CH; c += 4) {
@@ -494,7 +545,7 @@ __device__ __forceinline__ bool weigh(const AttnArgs &p, const Item &x, const To
         const int k = c + 2 * u;
         const f32x2 q2 = u ? pk2(q4.z, q4.w) : pk2(q4.x, q4.y);
         const f32x2 m2 = u ? pk2(m4.z, m4.w) : pk2(m4.x, m4.y);
-        const f32x2 sv = pk2(__uint_as_float(s[k]), __uint_as_float(s[k + 1]));
+        const f32x2 sv = pk2(__uint_as_float(v[k]), __uint_as_float(v[k + 1]));
         float y0, y1;
         up2(fma2(mul2(sv, ks2), q2, add2(m2, lvs2)), y0, y1);
         if (kMasked) {
@@ -506,36 +557,48 @@ __device__ __forceinline__ bool weigh(const AttnArgs &p, const Item &x, const To
         big = fmaxf(big, fmaxf(y0, y1));
         const float p0 = ex2(y0), p1 = ex2(y1);
         const int li = (c0 + k) / 2;
-        lt[li] = fma2(pk2(p0, p1), ivs2, lt[li]);
+        l[li] = fma2(pk2(p0, p1), ivs2, l[li]);
         h[k / 2] = pack_pair(p0, p1, __half());
       }
     }
-#pragma unroll
-    for (int c = 0; c < F::CH; c += 8) {
-      const int n = col0 + c0 + c;
-      const uint32_t at = swz<F::kPSpan>(row * F::kPSpan + (n % (F::kPSpan / 2)) * 2);
-      *reinterpret_cast<uint4 *>(sp + (n / (F::kPSpan / 2)) * (kTile * F::kPSpan) + at) =
-          make_uint4(h[c / 2], h[c / 2 + 1], h[c / 2 + 2], h[c / 2 + 3]);
-    }
+    const int n = col0 + c0;
+    const uint32_t at = swz<F::kPSpan>(row * F::kPSpan + (n % (F::kPSpan / 2)) * 2);
+    *reinterpret_cast<uint4 *>(sp + (n / (F::kPSpan / 2)) * (kTile * F::kPSpan) + at) =
+        make_uint4(h[0], h[1], h[2], h[3]);
   }
   return big > kTrigger;
 }
 
-// The largest y of each of this thread's columns over the warp's 32 tokens, to wmax[column].
+// Before a tile is taken again: the largest y of each of this thread's columns over the warp's 32
+// tokens, to wmax[column], and what the first attempt added to l taken off again. (That leaves at
+// most 2^-24 of the weight taken off, which stays in the new sum anyway; where it was infinite, the
+// old sum is less than 2^-100 of the new one. A NaN stays.)
 template <class F>
-__device__ __forceinline__ void column_maxima(const AttnArgs &p, const Item &x, const Token &t,
-                                              uint32_t ts, int col0, const float *qs,
-                                              const int *tok, int lane, float *wmax) {
-#pragma unroll 1
+__device__ __forceinline__ void retract(const AttnArgs &p, const Item &x, const Token &t, uint32_t ts,
+                                        int col0, const float *qs, const float *nm, const int *tok,
+                                        int lane, float *wmax, f32x2 (&l)[F::C / 2]) {
+#pragma unroll
   for (int c0 = 0; c0 < F::C; c0 += F::CH) {
     uint32_t s[F::CH];
     tmem_ld(ts + c0, s);
+    tmem_wait(s);
     float y[F::CH];
 #pragma unroll
     for (int c = 0; c < F::CH; ++c) {
       const int n = col0 + c0 + c;
       y[c] = __fmaf_rn(__uint_as_float(s[c]) * t.ks2, qs[n], t.lvs);
-      if (!sees<F>(p, x, t, n, tok) || y[c] != y[c]) y[c] = -INFINITY;
+      if (!sees<F>(p, x, t, n, tok)) y[c] = -INFINITY;
+    }
+#pragma unroll
+    for (int c = 0; c < F::CH; c += 2) {
+      const int n = col0 + c0 + c;
+      float l0, l1;
+      up2(l[(c0 + c) / 2], l0, l1);
+      l0 = l0 == INFINITY ? 0.f : l0 - ex2(y[c] + nm[n]) * t.ivs;
+      l1 = l1 == INFINITY ? 0.f : l1 - ex2(y[c + 1] + nm[n + 1]) * t.ivs;
+      l[(c0 + c) / 2] = pk2(l0, l1);
+      if (y[c] != y[c]) y[c] = -INFINITY;
+      if (y[c + 1] != y[c + 1]) y[c + 1] = -INFINITY;
     }
     const float m = reduce_columns<F::CH, true>(y, lane);
     if (lane < F::CH) wmax[col0 + c0 + lane] = m;
@@ -543,21 +606,21 @@ __device__ __forceinline__ void column_maxima(const AttnArgs &p, const Item &x, 
 }
 
 template <class F>
-__global__ void __launch_bounds__(kAttnThreads, F::CTAS)
+__global__ void __launch_bounds__(kAttnThreads, 1)
     kv_attention_kernel(const __grid_constant__ CUtensorMap map_k,
                         const __grid_constant__ CUtensorMap map_v,
                         const __grid_constant__ AttnArgs p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   Small &sm = *reinterpret_cast<Small *>(smem + F::kOffSmall);
   float *qs = reinterpret_cast<float *>(smem + F::kOffSmall + sizeof(Small));
-  float *nm = qs + F::NT, *fac = nm + F::NT;
-  int *tok = reinterpret_cast<int *>(fac + F::NT);
+  float *nm = qs + F::NT;   // -m of each group
+  int *tok = reinterpret_cast<int *>(nm + 2 * F::NT);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int s = 0; s < F::S; ++s) {
       tc::mbar_init(&sm.full[s], 33);               // 32 lanes' scales and the byte count
-      tc::mbar_init(&sm.empty[s], 1 + kSoftWarps);  // the score MMAs; each softmax warp
+      tc::mbar_init(&sm.empty[s], 1 + kGroupWarps); // the score MMAs; each warp of a group
     }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&sm.sfull[i], 1);
@@ -568,7 +631,7 @@ __global__ void __launch_bounds__(kAttnThreads, F::CTAS)
     tc::mbar_init(&sm.done, 1);
     tc::mbar_fence_init();
   }
-  if (tid < kTile) sm.vnan[tid] = 0;
+  if (tid < 2 * kTile) sm.vnan[tid / kTile][tid % kTile] = 0;
   if (warp == kMma) tmem_alloc(&sm.tmem, F::kTmem);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   int t0 = 0, t1 = 0, skip = 0;
@@ -589,15 +652,23 @@ __global__ void __launch_bounds__(kAttnThreads, F::CTAS)
     const int per_tile = kTile >> p.a.page_shift;
     for (int t = t0; t < t1 && ok;) {
       const int cnt = min(x.tiles - skip, t1 - t);
+      // the page number of this lane's page in tile k of the segment (0 past the end)
+      const int32_t *table = p.a.page_table + static_cast<long long>(x.b) * p.a.pps;
+      auto page_of = [&](int k) {
+        const int slot = (skip + k) * kTile + (lane << p.a.page_shift);
+        return lane < per_tile && slot < x.end ? __ldg(table + (slot >> p.a.page_shift)) : 0;
+      };
+      int next = page_of(0);
       for (int k = 0; k < cnt && ok; ++k, ++it) {
         const int s = it % F::S;
         const int slot = (skip + k) * kTile + (lane << p.a.page_shift);
         const bool want = lane < per_tile && slot < x.end;
-        int page = 0;
-        const bool good = want && kv_page(p.a, x.b, slot >> p.a.page_shift, page);
+        const int page = next;
+        if (k + 1 < cnt) next = page_of(k + 1);   // on its way while this tile waits for room
+        const bool good = want && page >= 0 && page < p.a.num_pages;
         if (want && !good) set_status(p.a.status, SPEC_ERR_PAGE);
         const uint32_t goods = __ballot_sync(0xffffffffu, good);
-        ok = tc::mbar_wait(&sm.empty[s], ((it / F::S) & 1) ^ 1);
+        ok = wait_for(&sm.empty[s], ((it / F::S) & 1) ^ 1);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         if (lane == 0)
@@ -626,78 +697,93 @@ __global__ void __launch_bounds__(kAttnThreads, F::CTAS)
     for (int k = max(0, it - F::S); k < it; ++k)
       if (!tc::mbar_wait(&sm.full[k % F::S], (k / F::S) & 1)) ok = false;
   } else if (warp == kMma) {
-    if (lane == 0) {
-      constexpr uint32_t id_s = attn_idesc(kTile, F::NT, false), id_o = attn_idesc(128, F::NT, true);
-      auto scores = [&](int it) {
-        const uint32_t k = tc::saddr(smem + (it % F::S) * 2 * F::kSideBytes);
-        const uint32_t q = tc::saddr(smem + F::kOffQ);
-        const uint32_t d = tmem + (it & 1) * F::NT;
+    // The whole warp walks the tiles and one elected lane issues: inside a branch of one lane the
+    // descriptors are not known to be uniform, and issuing a tile's 16 MMAs took 1400 clocks.
+    constexpr uint32_t id_s = attn_idesc(kTile, F::NT, false), id_o = attn_idesc(128, F::NT, true);
+    const uint32_t base = tc::saddr(smem);
+    auto scores = [&](int it) {
+      const uint64_t da = smem_desc<F::D>(base + (it % F::S) * 2 * F::kSideBytes, 16, 8 * F::D);
+      const uint64_t db = smem_desc<F::D>(base + F::kOffQ, 16, 8 * F::D);
+      const uint32_t d = tmem + (it & 1) * F::NT;   // the group's scores
+      if (elect_one()) {
 #pragma unroll
-        for (int term = 0; term < F::kTerms; ++term) {
-          const uint64_t da = smem_desc<F::D>(k, 16, 8 * F::D);
-          const uint64_t db = smem_desc<F::D>(q + term * F::kQBytes, 16, 8 * F::D);
+        for (int term = 0; term < F::kTerms; ++term)
 #pragma unroll
           for (int kk = 0; kk < F::D / 32; ++kk)   // 32 dims of e4m3: 32 bytes on
-            mma_f8(d, da + 2 * kk, db + 2 * kk, id_s, (term | kk) != 0);
-        }
+            mma_f8(d, da + 2 * kk, db + term * (F::kQBytes / 16) + 2 * kk, id_s,
+                   (term | kk) != 0);
         mma_commit(&sm.empty[it % F::S]);
         mma_commit(&sm.sfull[it & 1]);
-      };
-      auto values = [&](int it, bool first) {
-        const int nb = it % F::NB;
-        const uint32_t v = tc::saddr(smem + F::kOffV16 + nb * F::kVfBytes);
-        const uint32_t w = tc::saddr(smem + F::kOffP + nb * F::kPBytes);
-        // one block of 64 dims (D = 64) stands for both halves of the MMA's rows
-        const uint64_t da = smem_desc<128>(v, F::D > 64 ? kTile * 128 : 0, 1024);
-        const uint64_t db = smem_desc<F::kPSpan>(w, kTile * F::kPSpan, 8 * F::kPSpan);
+      }
+      __syncwarp();
+    };
+    auto values = [&](int it, bool first) {
+      const int grp = it & 1;
+      // one block of 64 dims (D = 64) stands for both halves of the MMA's rows
+      const uint64_t da = smem_desc<128>(base + F::kOffV16 + grp * F::kVfBytes,
+                                         F::D > 64 ? kTile * 128 : 0, 1024);
+      const uint64_t db = smem_desc<F::kPSpan>(base + F::kOffP + grp * F::kPBytes,
+                                               kTile * F::kPSpan, 8 * F::kPSpan);
+      const uint32_t d = tmem + (2 + grp) * F::NT;
+      if (elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < kTile / 16; ++kk)   // 16 tokens
-          mma_f16(tmem + 2 * F::NT, da + kk * (16 * 128 / 16), db + kk * F::kPSpan, id_o,
-                  !(first && kk == 0));
-        mma_commit(&sm.pfree[nb]);
-      };
-      int it = 0, seg = 0;
-      bool pending = false, pending_first = false;
-      auto drain = [&]() {   // the value MMAs of the tile before
-        if (!pending) return;
-        ok = ok && tc::mbar_wait(&sm.pfull[(it - 1) & 1], ((it - 1) >> 1) & 1);
-        if (!ok) return;
-        tc::fence_after_sync();
-        values(it - 1, pending_first);
-        pending = false;
-      };
-      for (int t = t0; t < t1 && ok; ++seg) {
-        const int cnt = min(x.tiles - skip, t1 - t);
-        drain();
-        ok = ok && tc::mbar_wait(&sm.qfull, seg & 1);
-        for (int k = 0; k < cnt && ok; ++k) {
-          ok = tc::mbar_wait(&sm.full[it % F::S], (it / F::S) & 1);
-          if (!ok) break;
-          tc::fence_after_sync();
-          scores(it);
-          drain();
-          if (!ok) break;
-          pending = true;
-          pending_first = k == 0;
-          ++it;
-        }
-        t += cnt;
-        skip = 0;
-        if (t < t1) item_next<F::NT>(p, x);
+          mma_f16(d, da + kk * (16 * 128 / 16), db + kk * F::kPSpan, id_o, !(first && kk == 0));
+        mma_commit(&sm.pfree[grp]);
       }
-      if (ok) drain();
-      mma_commit(&sm.done);   // every MMA issued has completed before the CTA may end
-      if (!tc::mbar_wait(&sm.done, 0)) ok = false;
+      __syncwarp();
+    };
+    int it = 0, seg = 0;
+    bool pending = false, pending_first = false;
+    auto wait = [&](uint64_t *bar, int parity) {
+      ok = ok && wait_for(bar, parity);
+      ok = __all_sync(0xffffffffu, ok);
+      tc::fence_after_sync();
+    };
+    auto drain = [&]() {   // the value MMAs of the tile before
+      if (!pending) return;
+      wait(&sm.pfull[(it - 1) & 1], ((it - 1) >> 1) & 1);
+      if (!ok) return;
+      values(it - 1, pending_first);
+      pending = false;
+    };
+    for (int t = t0; t < t1 && ok; ++seg) {
+      const int cnt = min(x.tiles - skip, t1 - t);
+      drain();
+      wait(&sm.qfull, seg & 1);
+      for (int k = 0; k < cnt && ok; ++k) {
+        wait(&sm.full[it % F::S], (it / F::S) & 1);
+        if (!ok) break;
+        scores(it);
+        drain();
+        if (!ok) break;
+        pending = true;
+        pending_first = k < 2;   // each group's first tile of the segment
+        ++it;
+      }
+      t += cnt;
+      skip = 0;
+      if (t < t1) item_next<F::NT>(p, x);
     }
+    if (ok) drain();
+    if (elect_one()) mma_commit(&sm.done);   // every MMA issued has completed before the CTA may end
+    if (!wait_for(&sm.done, 0)) ok = false;
     __syncwarp();
   } else {
-    const int wg = warp >> 2, quad = warp & 3;
-    const int col0 = wg * F::C;
-    const int row = quad * 32 + lane;   // token of the tile; also the dim of an output lane
-    const uint32_t tlane = static_cast<uint32_t>(quad * 32) << 16;
-    int it = 0;
+    const int grp = warp / kGroupWarps, gtid = tid % kGroupThreads;
+    const int quad = warp & 3;
+    const int col0 = (warp >> 2 & 1) * F::C;
+    const int row = quad * 32 + lane;   // token of the tile; in the epilogue the dim
+    const uint32_t tlane = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    const uint32_t ts = tlane + grp * F::NT + col0;         // this thread's scores
+    const uint32_t to = tlane + (2 + grp) * F::NT + col0;   // its group's accumulators
+    uint8_t *sv16 = smem + F::kOffV16 + grp * F::kVfBytes;
+    uint8_t *sp = smem + F::kOffP + grp * F::kPBytes;
+    float *gnm = nm + grp * F::NT;
+    uint8_t *vnan = sm.vnan[grp];
+    int it = 0;   // tiles of the range so far; the groups take them in turn
     auto wait = [&](uint64_t *bar, int parity) {
-      if (ok) ok = tc::mbar_wait(bar, parity);
+      ok = ok && wait_for(bar, parity);
       __syncwarp();
     };
     for (int t = t0; t < t1;) {
@@ -709,14 +795,15 @@ __global__ void __launch_bounds__(kAttnThreads, F::CTAS)
       f32x2 l[F::C / 2];
 #pragma unroll
       for (int c = 0; c < F::C / 2; ++c) l[c] = pk2(0.f, 0.f);
-      for (int k = 0; k < cnt; ++k, ++it) {
-        const int s = it % F::S, nb = it % F::NB, use = it / F::NB;
+      for (int k = (it ^ grp) & 1; k < cnt; k += 2) {
+        const int n = it + k, s = n % F::S, use = n >> 1;
         const int slot0 = (skip + k) * kTile;
-        wait(&sm.full[s], (it / F::S) & 1);
+        wait(&sm.full[s], (n / F::S) & 1);
+        uint4 w[Widen<F>::kSteps];
+        fetch_values<F>(smem + s * 2 * F::kSideBytes + F::kSideBytes, gtid, x.end - slot0, w);
         const float ks = sm.ks[s][row >> p.a.page_shift], vs = sm.vs[s][row >> p.a.page_shift];
-        wait(&sm.pfree[nb], (use & 1) ^ 1);
-        bool nan = convert<F>(smem + s * 2 * F::kSideBytes + F::kSideBytes,
-                              smem + F::kOffV16 + nb * F::kVfBytes, x.end - slot0, sm.vnan);
+        wait(&sm.pfree[grp], (use & 1) ^ 1);
+        const bool nan = widen<F>(w, sv16, gtid, vnan);
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.empty[s]);
         // a NaN scale (a bad page) makes the scores of its tokens NaN through lvs, and only those:
@@ -725,7 +812,7 @@ __global__ void __launch_bounds__(kAttnThreads, F::CTAS)
         const float vse = vs < kMinValueScale ? kMinValueScale : vs;
         tk.ks2 = ks * p.scale2;
         tk.lvs = __log2f(vse);
-        tk.ivs = vs == vs ? 1.f / vse : 1.f;
+        tk.ivs = vs == vs ? __frcp_rn(vse) : 1.f;
         const int j = slot0 + row - x.len;
         tk.j = -1;
         tk.from = 0;
@@ -739,97 +826,105 @@ __global__ void __launch_bounds__(kAttnThreads, F::CTAS)
               min(static_cast<long long>(F::NT),
                   static_cast<long long>(j) * p.G - static_cast<long long>(x.rt) * F::NT));
         const bool masked = slot0 + kTile > min(x.len, x.end);
-        const uint32_t ts = tmem + tlane + (it & 1) * F::NT + col0;
-        uint8_t *sp = smem + F::kOffP + nb * F::kPBytes;
-        wait(&sm.sfull[it & 1], (it >> 1) & 1);
+        wait(&sm.sfull[grp], use & 1);
         tc::fence_after_sync();
-        f32x2 lt[F::C / 2];
         bool again = false;
 #pragma unroll 1
         for (;;) {
-#pragma unroll
-          for (int c = 0; c < F::C / 2; ++c) lt[c] = pk2(0.f, 0.f);
           bool over;
           if (masked || again)
-            over = weigh<F, true>(p, x, tk, again && sm.vnan[row], ts, col0, sp, qs, nm, tok, row,
-                                  lt);
+            over = weigh<F, true>(p, x, tk, again && vnan[row], ts, col0, sp, qs, gnm, tok, row, l);
           else
-            over = weigh<F, false>(p, x, tk, false, ts, col0, sp, qs, nm, tok, row, lt);
+            over = weigh<F, false>(p, x, tk, false, ts, col0, sp, qs, gnm, tok, row, l);
           fence_async();
           tc::fence_before_sync();
-          if (!soft_any(!again && (over || nan))) break;
+          if (!group_any(grp, !again && (over || nan))) break;
           tc::fence_after_sync();
           // new references: maxima over the tile's tokens (P's buffer holds them meanwhile)
-          float *wmax = reinterpret_cast<float *>(sp);
-          column_maxima<F>(p, x, tk, ts, col0, qs, tok, lane, wmax + quad * F::NT);
-          soft_sync();
-          if (tid < F::NT) {
-            float m = fmaxf(fmaxf(wmax[tid], wmax[F::NT + tid]),
-                            fmaxf(wmax[2 * F::NT + tid], wmax[3 * F::NT + tid]));
-            const float old = nm[tid];
+          float *wmax = reinterpret_cast<float *>(sp), *fac = wmax + 4 * F::NT;
+          retract<F>(p, x, tk, ts, col0, qs, gnm, tok, lane, wmax + quad * F::NT, l);
+          group_sync(grp);
+          if (gtid < F::NT) {
+            const float m = fmaxf(fmaxf(wmax[gtid], wmax[F::NT + gtid]),
+                                  fmaxf(wmax[2 * F::NT + gtid], wmax[3 * F::NT + gtid]));
+            const float old = gnm[gtid];
             const bool grow = m + old > kTrigger;
             const float now = grow ? kBias - m : old;
-            fac[tid] = grow ? ex2(now - old) : 1.f;   // 2^(m_old - m_new)
-            nm[tid] = now;
+            fac[gtid] = grow ? ex2(now - old) : 1.f;   // 2^(m_old - m_new)
+            gnm[gtid] = now;
           }
-          soft_sync();
-          const uint32_t to = tmem + tlane + 2 * F::NT + col0;
-          if (k > 0) wait(&sm.pfree[(it - 1) % F::NB], ((it - 1) / F::NB) & 1);
-          tc::fence_after_sync();
+          group_sync(grp);
+          // (the group's last value MMAs completed before its buffers were written)
 #pragma unroll
           for (int c0 = 0; c0 < F::C; c0 += F::CH) {
-            if (k > 0) {
+            float f[F::CH];
+#pragma unroll
+            for (int c = 0; c < F::CH; ++c) f[c] = fac[col0 + c0 + c];
+            if (k > 1) {
               uint32_t o[F::CH];
               tmem_ld(to + c0, o);
+              tmem_wait(o);
 #pragma unroll
               for (int c = 0; c < F::CH; ++c)
-                o[c] = __float_as_uint(__uint_as_float(o[c]) * fac[col0 + c0 + c]);
+                o[c] = __float_as_uint(__uint_as_float(o[c]) * f[c]);
               tmem_st(to + c0, o);
             }
 #pragma unroll
             for (int c = 0; c < F::CH; c += 2)
-              l[(c0 + c) / 2] = mul2(l[(c0 + c) / 2],
-                                     pk2(fac[col0 + c0 + c], fac[col0 + c0 + c + 1]));
+              l[(c0 + c) / 2] = mul2(l[(c0 + c) / 2], pk2(f[c], f[c + 1]));
           }
           asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+          group_sync(grp);   // fac is read before P overwrites it
           again = true;
         }
         if (again) {
-          soft_sync();
-          if (wg == 0) sm.vnan[row] = 0;
-          soft_sync();   // the next tile's marks come after
+          group_sync(grp);
+          if (gtid < kTile) vnan[gtid] = 0;
+          group_sync(grp);   // the next tile's marks come after
         }
-        if (tid == 0) mbar_arrive(&sm.pfull[it & 1]);
-#pragma unroll
-        for (int c = 0; c < F::C / 2; ++c) l[c] = add2(l[c], lt[c]);
+        if (gtid == 0) mbar_arrive(&sm.pfull[grp]);
       }
-      // the item's (or its part's) result: denominators over the tile's 128 lanes, then each lane's
-      // dim of every column
-      wait(&sm.pfree[(it - 1) % F::NB], ((it - 1) / F::NB) & 1);
+      it += cnt;
+      // The item's (or its part's) result. All value MMAs have completed: each group's denominators
+      // over the tile's 128 lanes, then the groups joined, each lane's dim of every column.
+      for (int last = it - 1; last >= 0 && last >= it - 2; --last)
+        wait(&sm.pfree[last & 1], (last >> 1) & 1);
       tc::fence_after_sync();
-      float *lsum = reinterpret_cast<float *>(smem + F::kOffP);
+      float *lsum = reinterpret_cast<float *>(smem + F::kOffP), *fac = lsum + 8 * F::NT;
+      soft_sync();
 #pragma unroll
       for (int c0 = 0; c0 < F::C; c0 += F::CH) {
         float v[F::CH];
 #pragma unroll
         for (int c = 0; c < F::CH; c += 2) up2(l[(c0 + c) / 2], v[c], v[c + 1]);
         const float sum = reduce_columns<F::CH, false>(v, lane);
-        if (lane < F::CH) lsum[quad * F::NT + col0 + c0 + lane] = sum;
+        if (lane < F::CH) lsum[(grp * 4 + quad) * F::NT + col0 + c0 + lane] = sum;
       }
       soft_sync();
       const bool whole = skip == 0 && cnt == x.tiles;
       const long long part = 2LL * blockIdx.x + (skip == 0 ? 1 : 0);
       if (tid < F::NT) {
-        const float sum = (lsum[tid] + lsum[F::NT + tid]) + (lsum[2 * F::NT + tid] + lsum[3 * F::NT + tid]);
+        float sum[2], wt[2];
+        const float m = fminf(nm[tid], nm[F::NT + tid]);   // -m of the larger reference
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          const float *v = lsum + 4 * g * F::NT + tid;
+          sum[g] = (v[0] + v[F::NT]) + (v[2 * F::NT] + v[3 * F::NT]);
+          wt[g] = ex2(m - nm[g * F::NT + tid]);   // 0 for a group that saw nothing, beside one that did
+        }
+        const float total = sum[0] * wt[0] + sum[1] * wt[1];
         const long long r = static_cast<long long>(x.rt) * F::NT + tid;
         const int i = static_cast<int>(r / p.G), g = static_cast<int>(r - static_cast<long long>(i) * p.G);
-        float lse2 = sum == 0.f ? -INFINITY : log2f(sum) - nm[tid];
-        if (!x.ok) lse2 = NAN;
-        fac[tid] = !x.ok ? NAN : sum == 0.f ? 0.f : 1.f / sum;
-        if (whole && i >= x.n && x.ok) {   // padding
-          fac[tid] = 0.f;
+        float lse2 = total == 0.f ? -INFINITY : log2f(total) - m;
+        float f = total == 0.f ? 0.f : 1.f / total;
+        if (!x.ok) {
+          lse2 = f = NAN;
+        } else if (whole && i >= x.n) {   // padding
+          f = 0.f;
           lse2 = -INFINITY;
         }
+        fac[tid] = sum[0] == 0.f ? 0.f * f : wt[0] * f;   // (0 NaN is NaN)
+        fac[F::NT + tid] = sum[1] == 0.f ? 0.f * f : wt[1] * f;
         if (!whole)
           p.part_lse[part * F::NT + tid] = lse2;
         else if (p.lse && i < p.a.N)
@@ -838,17 +933,22 @@ __global__ void __launch_bounds__(kAttnThreads, F::CTAS)
       }
       soft_sync();
       using T = typename F::T;
-      const uint32_t to = tmem + tlane + 2 * F::NT + col0;
+      const int e0 = (warp >> 2) * F::EC;
 #pragma unroll 1
-      for (int c0 = 0; c0 < F::C; c0 += F::CH) {
-        uint32_t o[F::CH];
-        tmem_ld(to + c0, o);
+      for (int c0 = e0; c0 < e0 + F::EC; c0 += F::ECH) {
+        uint32_t o[F::ECH], o1[F::ECH];
+        tmem_ld(tlane + 2 * F::NT + c0, o);
+        tmem_ld(tlane + 3 * F::NT + c0, o1);
+        tmem_wait(o);
+        tmem_wait(o1);
         if (row < F::D) {
 #pragma unroll
-          for (int c = 0; c < F::CH; ++c) {
-            const int n = col0 + c0 + c;
-            // 0 columns (nothing seen) stay 0 whatever the accumulator holds
-            const float f = fac[n], v = f == 0.f ? 0.f : __uint_as_float(o[c]) * f;
+          for (int c = 0; c < F::ECH; ++c) {
+            const int n = c0 + c;
+            // a group that saw nothing counts 0 whatever its accumulator holds
+            const float f0 = fac[n], f1 = fac[F::NT + n];
+            const float v = (f0 == 0.f ? 0.f : __uint_as_float(o[c]) * f0) +
+                            (f1 == 0.f ? 0.f : __uint_as_float(o1[c]) * f1);
             if (!whole) {
               p.part_o[(part * F::NT + n) * F::D + row] = v;
             } else {
@@ -1003,7 +1103,7 @@ cudaError_t launch_cfg(AttnArgs &p, const CUtensorMap &mk, const CUtensorMap &mv
     if (e != cudaSuccess) return e;
     if (dev < 64) ready[dev].store(true, std::memory_order_release);
   }
-  const int ctas = sms * F::CTAS < kMaxCtas ? sms * F::CTAS : kMaxCtas;
+  const int ctas = sms < kMaxCtas ? sms : kMaxCtas;
   p.start = reinterpret_cast<int4 *>(ws);
   p.part_lse = reinterpret_cast<float *>(ws + 2 * kMaxCtas * sizeof(int4));
   p.part_o = p.part_lse + 2 * kMaxCtas * F::NT;
@@ -1020,11 +1120,11 @@ cudaError_t launch_cfg(AttnArgs &p, const CUtensorMap &mk, const CUtensorMap &mv
 template <typename T, int D>
 cudaError_t launch_columns(int nt, AttnArgs &p, const CUtensorMap &mk, const CUtensorMap &mv,
                            int sms, char *ws, cudaStream_t stream) {
-  if (nt == 16) return launch_cfg<Cfg<T, D, 16, 4, 2, 1>>(p, mk, mv, sms, ws, stream);
-  if (nt == 32) return launch_cfg<Cfg<T, D, 32, 4, 2, 1>>(p, mk, mv, sms, ws, stream);
+  if (nt == 16) return launch_cfg<Cfg<T, D, 16, 4>>(p, mk, mv, sms, ws, stream);
+  if (nt == 32) return launch_cfg<Cfg<T, D, 32, 4>>(p, mk, mv, sms, ws, stream);
   if constexpr (!__is_same(T, __half))
-    if (nt == 128) return launch_cfg<Cfg<T, D, 128, 2, 2, 1>>(p, mk, mv, sms, ws, stream);
-  return launch_cfg<Cfg<T, D, 64, 3, 2, 1>>(p, mk, mv, sms, ws, stream);
+    if (nt == 128) return launch_cfg<Cfg<T, D, 128, 2>>(p, mk, mv, sms, ws, stream);
+  return launch_cfg<Cfg<T, D, 64, 3>>(p, mk, mv, sms, ws, stream);
 }
 
 }  // namespace
