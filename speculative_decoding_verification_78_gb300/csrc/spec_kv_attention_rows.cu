@@ -1,0 +1,577 @@
+// spec_kv_attention_rows.cu -- attention of many query rows (more than 32 for a key head: candidate
+// trees, pieces of prompts, chains with many query heads) over the paged e4m3 cache, on the
+// 5th-generation tensor cores.
+//
+// The same mathematics as the kernel for few rows: with y = scale log2(e) ks (q . kb) + log2 vs and a
+// reference m, weights p = 2^(y - m) multiply the e4m3 bytes vb and p / vs adds to the denominator.
+//
+// Here the query rows lie along the MMA's 128 rows and the tokens along its columns: S = Q K^T (Q as
+// 2 or 3 e4m3 terms, K's bytes as TMA lands them), O = P V. A softmax thread owns a query row, so
+// its reference, its sum and its query's unit are registers; what differs by token, the page scales,
+// is constant over 16 columns (pages hold at least 16 tokens). P is written back to tensor memory,
+// over the scores it came from, as the fp16 operand of the second MMA: nothing of the softmax passes
+// through shared memory, which the operands of the MMAs already load. V is widened to fp16 by four
+// warps of their own, once for all rows of the CTA.
+//
+// Two groups of four softmax warps work half a step apart, so that the tensor cores have one group's
+// MMAs while the other group exponentiates: with more than 128 rows each group has 128 rows of its
+// own and both take every tile; with fewer, the groups take the tiles in turn and are joined at the
+// end of the item. Unit u of a segment belongs to group u & 1; the MMA warp issues scores(u), then
+// values(u - 1).
+//
+// What bounds it: a 256-row tile of 128 tokens (D = 128) is 2048 clocks of MMA (two e4m3 terms cost
+// what one 16-bit operand would) and 1024 of ex2.
+#include "spec_kv_attn.cuh"
+
+namespace specv {
+
+using namespace attn;
+
+namespace {
+
+constexpr int kSoftWarps = 8;            // two groups of four
+constexpr int kSoftThreads = 32 * kSoftWarps;
+constexpr int kWidenWarp = kSoftWarps;   // four warps widen V
+constexpr int kWidenThreads = 128;
+constexpr int kProducer = kSoftWarps + 4, kMma = kProducer + 1;
+constexpr int kRowsThreads = 32 * (kMma + 1);
+constexpr float kBias = 8.f;        // a new reference puts the row's largest weight at 2^8 ...
+constexpr float kTrigger = 15.f;    // ... and is taken when one exceeds 2^15 (fp16 ends at 2^16)
+
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                           uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc));
+}
+__device__ __forceinline__ void rows_sync() {   // the softmax threads
+  asm volatile("bar.sync 1, %0;" ::"n"(kSoftThreads) : "memory");
+}
+__device__ __forceinline__ void widen_sync() {
+  asm volatile("bar.sync 2, %0;" ::"n"(kWidenThreads) : "memory");
+}
+
+// RTC: row tiles of 128 a CTA works on at once; S: stages of K and V
+template <typename T_, int D_, int RTC_, int S_>
+struct RowsCfg {
+  using T = T_;
+  static constexpr int D = D_, RTC = RTC_, S = S_, NT = 128 * RTC;
+  static constexpr int kTerms = __is_same(T, __half) ? 3 : 2;
+  static constexpr int kSideBytes = kTile * D;
+  static constexpr int kVfBytes = kTile * D * 2;
+  static constexpr int kQBytes = 128 * D;                // one term of a row tile
+  static constexpr int kOffV16 = S * 2 * kSideBytes;
+  static constexpr int kOffQ = kOffV16 + 2 * kVfBytes;
+  static constexpr int kOffSmall = kOffQ + RTC * kTerms * kQBytes;
+  static constexpr uint32_t kColS = 0, kColO = 256;      // tensor memory: S of each group, O of each
+};
+
+struct __align__(16) RowsSmall {
+  uint64_t full[4], empty[4];    // stages
+  uint64_t vfull[2], vfree[2];   // widened V
+  uint64_t sfull[2], pfull[2], ofull[2];   // by group
+  uint64_t qfull, done;
+  float ks[4][8], vs[4][8];
+  float4 page[2][8];             // by 16 tokens: scale log2(e) ks, log2 vs, 1 / vs
+  uint32_t vnan[2][4];           // tokens whose values hold NaN
+  uint32_t tmem;
+  LocateScratch loc;
+};
+template <class F> constexpr int rows_smem() {   // + qs; groups that share rows: references, sums
+  return F::kOffSmall + static_cast<int>(sizeof(RowsSmall)) + F::NT * 4 +
+         (F::RTC == 1 ? 4 * 128 * 4 : 0);
+}
+
+// Bits of the 32 slots from number `j0` among the new tokens on (negative: the cached ones, which
+// every row sees) that row (b, i) sees; `n` new tokens.
+__device__ __forceinline__ uint32_t seen_bits(const AttnArgs &p, int b, int i, int j0, int n) {
+  const int lim = p.a.mask ? n : min(n, i + 1);
+  if (j0 >= lim) return 0;
+  uint32_t r = 0xffffffffu;
+  if (p.a.mask && j0 > -32) {
+    const uint32_t *m = p.a.mask + (static_cast<long long>(b) * p.a.N + i) * p.a.W;
+    if (j0 < 0) {
+      r = (__ldg(m) << -j0) | ((1u << -j0) - 1u);
+    } else {
+      const int w = j0 >> 5;
+      const uint32_t lo = __ldg(m + w), hi = w + 1 < p.a.W ? __ldg(m + w + 1) : 0u;
+      r = __funnelshift_r(lo, hi, j0 & 31);
+    }
+  }
+  if (lim - j0 < 32) r &= (1u << (lim - j0)) - 1u;
+  return r;
+}
+
+// One row of the tile: weights against -nm, as fp16 pairs in h, and their sum over the value scales;
+// returns the largest exponent. The next 16 scores are on their way while these are worked on.
+template <bool kMasked>
+__device__ __forceinline__ float row_weights(uint32_t ts, const float4 *page, float qs, float nm,
+                                             const uint32_t (&see)[4], const uint32_t (&nan)[4],
+                                             uint32_t (&h)[64], float &sum) {
+  float big = -INFINITY;
+  sum = 0.f;
+  uint32_t s[2][16];
+  tmem_ld(ts, s[0]);
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    uint32_t(&v)[16] = s[c & 1];
+    tmem_wait(v);
+    if (c < 7) tmem_ld(ts + 16 * (c + 1), s[(c + 1) & 1]);
+    const float4 pg = page[c];
+    const float k = pg.x * qs, d = pg.y + nm;
+    const f32x2 k2 = pk2(k, k), d2 = pk2(d, d);
+    f32x2 acc = pk2(0.f, 0.f);
+#pragma unroll
+    for (int e = 0; e < 16; e += 2) {
+      float y0, y1;
+      up2(fma2(pk2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), k2, d2), y0, y1);
+      if (kMasked) {
+        const int at = 16 * c + e;
+        if (nan[at >> 5] >> (at & 31) & 1u) y0 = NAN;
+        if (nan[at >> 5] >> (at & 31) & 2u) y1 = NAN;
+        if (!(see[at >> 5] >> (at & 31) & 1u)) y0 = -INFINITY;
+        if (!(see[at >> 5] >> (at & 31) & 2u)) y1 = -INFINITY;
+      }
+      big = fmaxf(big, fmaxf(y0, y1));
+      const float p0 = ex2(y0), p1 = ex2(y1);
+      acc = add2(acc, pk2(p0, p1));
+      h[8 * c + e / 2] = pack_pair(p0, p1, __half());
+    }
+    float a0, a1;
+    up2(acc, a0, a1);
+    sum = __fmaf_rn(a0 + a1, pg.z, sum);
+  }
+  return big;
+}
+// The largest y of the row's tile, without the reference.
+template <bool kMasked>
+__device__ __forceinline__ float row_maximum(uint32_t ts, const float4 *page, float qs,
+                                             const uint32_t (&see)[4]) {
+  float big = -INFINITY;
+#pragma unroll 2
+  for (int c = 0; c < 8; ++c) {
+    uint32_t v[16];
+    tmem_ld(ts + 16 * c, v);
+    tmem_wait(v);
+    const float4 pg = page[c];
+    const float k = pg.x * qs;
+    const uint32_t bits = kMasked ? (c < 4 ? c < 2 ? see[0] : see[1] : c < 6 ? see[2] : see[3]) >> (16 * (c & 1))
+                                  : 0xffffu;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const float y = __fmaf_rn(__uint_as_float(v[e]), k, pg.y);
+      if (!kMasked || (bits >> e & 1u)) big = fmaxf(big, y);
+    }
+  }
+  return big;
+}
+
+template <class F>
+__global__ void __launch_bounds__(kRowsThreads, 1)
+    kv_attention_rows_kernel(const __grid_constant__ CUtensorMap map_k,
+                             const __grid_constant__ CUtensorMap map_v,
+                             const __grid_constant__ AttnArgs p) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  RowsSmall &sm = *reinterpret_cast<RowsSmall *>(smem + F::kOffSmall);
+  float *qs = reinterpret_cast<float *>(smem + F::kOffSmall + sizeof(RowsSmall));
+  constexpr int NT = F::NT, D = F::D;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int s = 0; s < F::S; ++s) {
+      tc::mbar_init(&sm.full[s], 33);     // 32 lanes' scales and the byte count
+      tc::mbar_init(&sm.empty[s], 1 + 4); // the score MMAs; the widening warps
+    }
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&sm.vfull[i], 4);
+      tc::mbar_init(&sm.vfree[i], 1);
+      tc::mbar_init(&sm.sfull[i], 1);
+      tc::mbar_init(&sm.pfull[i], 4);
+      tc::mbar_init(&sm.ofull[i], 1);
+    }
+    tc::mbar_init(&sm.qfull, 1);
+    tc::mbar_init(&sm.done, 1);
+    tc::mbar_fence_init();
+  }
+  if (warp == kMma) tmem_alloc(&sm.tmem, 512);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  int t0 = 0, t1 = 0, skip = 0;
+  Item x{};
+  tc::fence_before_sync();
+  locate<NT, kRowsThreads>(p, sm.loc, t0, t1, x, skip);
+  tc::fence_after_sync();
+  const uint32_t tmem = sm.tmem;
+  if (tid == 0) publish_range(p, x, skip, t0, t1);
+  bool ok = true;   // false after a wait gave up: no further waits, and no further work is issued
+  auto wait = [&](uint64_t *bar, int parity) {   // whole warps
+    ok = ok && wait_for(bar, parity);
+    ok = __all_sync(0xffffffffu, ok);
+  };
+  if (warp == kProducer) {
+    int it = 0;
+    const int per_tile = kTile >> p.a.page_shift;
+    for (int t = t0; t < t1 && ok;) {
+      const int cnt = min(x.tiles - skip, t1 - t);
+      // the page number of this lane's page in tile k of the segment (0 past the end)
+      const int32_t *table = p.a.page_table + static_cast<long long>(x.b) * p.a.pps;
+      auto page_of = [&](int k) {
+        const int slot = (skip + k) * kTile + (lane << p.a.page_shift);
+        return lane < per_tile && slot < x.end ? __ldg(table + (slot >> p.a.page_shift)) : 0;
+      };
+      int next = page_of(0);
+      for (int k = 0; k < cnt && ok; ++k, ++it) {
+        const int s = it % F::S;
+        const int slot = (skip + k) * kTile + (lane << p.a.page_shift);
+        const bool want = lane < per_tile && slot < x.end;
+        const int page = next;
+        if (k + 1 < cnt) next = page_of(k + 1);   // on its way while this tile waits for room
+        const bool good = want && page >= 0 && page < p.a.num_pages;
+        if (want && !good) set_status(p.a.status, SPEC_ERR_PAGE);
+        const uint32_t goods = __ballot_sync(0xffffffffu, good);
+        wait(&sm.empty[s], ((it / F::S) & 1) ^ 1);
+        if (!ok) break;
+        if (lane == 0)
+          tc::mbar_expect_tx(&sm.full[s], __popc(goods) * 2 * (D << p.a.page_shift));
+        __syncwarp();
+        if (good) {
+          const int head = page * p.a.Hkv + x.h;
+          const int row = head << p.a.page_shift;
+          const uint32_t dst = tc::saddr(smem + s * 2 * F::kSideBytes) +
+                               (lane << p.a.page_shift) * D;
+          tma_load_2d(dst, &map_k, 0, row, &sm.full[s]);
+          tma_load_2d(dst + F::kSideBytes, &map_v, 0, row, &sm.full[s]);
+          copy4(&sm.ks[s][lane], p.a.k_scale + head);
+          copy4(&sm.vs[s][lane], p.a.v_scale + head);
+          mbar_arrive_copies(&sm.full[s]);
+        } else {
+          if (want) sm.ks[s][lane] = sm.vs[s][lane] = NAN;   // what reads the page is NaN
+          mbar_arrive(&sm.full[s]);
+        }
+      }
+      t += cnt;
+      skip = 0;
+      if (t < t1) item_next<NT>(p, x);
+    }
+    // the last copies of each stage land before the CTA may end
+    for (int k = max(0, it - F::S); k < it; ++k)
+      if (!tc::mbar_wait(&sm.full[k % F::S], (k / F::S) & 1)) ok = false;
+  } else if (warp == kMma) {
+    // the whole warp walks the units, one elected lane issues
+    constexpr uint32_t id_s = attn_idesc(128, kTile, false);
+    constexpr uint32_t id_o = (1u << 4) | (1u << 16) | (static_cast<uint32_t>(D >> 3) << 17) |
+                              (static_cast<uint32_t>(128 >> 4) << 24);   // B MN-major
+    const uint32_t base = tc::saddr(smem);
+    // unit u of a segment whose first tile is number `it` of the range
+    auto scores = [&](int u, int it, bool last) {
+      const int g = u & 1, tile = it + (F::RTC == 2 ? u >> 1 : u);
+      const uint64_t da = smem_desc<D>(
+          base + F::kOffQ + (F::RTC == 2 ? g * F::kTerms * F::kQBytes : 0), 16, 8 * D);
+      const uint64_t db = smem_desc<D>(base + tile % F::S * 2 * F::kSideBytes, 16, 8 * D);
+      const uint32_t d = tmem + F::kColS + g * 128;
+      if (elect_one()) {
+#pragma unroll
+        for (int term = 0; term < F::kTerms; ++term)
+#pragma unroll
+          for (int kk = 0; kk < D / 32; ++kk)   // 32 dims of e4m3: 32 bytes on
+            mma_f8(d, da + term * (F::kQBytes / 16) + 2 * kk, db + 2 * kk, id_s, (term | kk) != 0);
+        if (last) mma_commit(&sm.empty[tile % F::S]);
+        mma_commit(&sm.sfull[g]);
+      }
+      __syncwarp();
+    };
+    auto values = [&](int u, int it, bool first, bool last) {
+      const int g = u & 1, tile = it + (F::RTC == 2 ? u >> 1 : u);
+      const uint64_t db = smem_desc<128>(base + F::kOffV16 + (tile & 1) * F::kVfBytes,
+                                         D > 64 ? kTile * 128 : 0, 1024);
+      const uint32_t d = tmem + F::kColO + g * D, a = tmem + F::kColS + g * 128;
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < kTile / 16; ++kk)   // 16 tokens: 8 columns of pairs
+          mma_f16_ts(d, a + 8 * kk, db + kk * (16 * 128 / 16), id_o, !(first && kk == 0));
+        if (last) mma_commit(&sm.vfree[tile & 1]);
+        mma_commit(&sm.ofull[g]);
+      }
+      __syncwarp();
+    };
+    int it = 0, seg = 0;
+    int uses[2] = {0, 0};   // units of each group so far
+    for (int t = t0; t < t1 && ok; ++seg) {
+      const int cnt = min(x.tiles - skip, t1 - t);
+      wait(&sm.qfull, seg & 1);
+      tc::fence_after_sync();
+      const int units = F::RTC * cnt;
+      for (int u = 0; u <= units && ok; ++u) {
+        if (u < units) {
+          const int tile = it + (F::RTC == 2 ? u >> 1 : u);
+          if (F::RTC == 1 || !(u & 1)) wait(&sm.full[tile % F::S], (tile / F::S) & 1);
+          if (!ok) break;
+          tc::fence_after_sync();
+          scores(u, it, F::RTC == 1 || (u & 1));
+        }
+        if (u > 0) {
+          const int w = u - 1, g = w & 1, tile = it + (F::RTC == 2 ? w >> 1 : w);
+          if (F::RTC == 1 || !g) wait(&sm.vfull[tile & 1], (tile >> 1) & 1);
+          wait(&sm.pfull[g], uses[g] & 1);
+          if (!ok) break;
+          ++uses[g];
+          tc::fence_after_sync();
+          values(w, it, w < 2, F::RTC == 1 || g);
+        }
+      }
+      it += cnt;
+      t += cnt;
+      skip = 0;
+      if (t < t1) item_next<NT>(p, x);
+    }
+    if (elect_one()) mma_commit(&sm.done);   // every MMA issued has completed before the CTA may end
+    if (!wait_for(&sm.done, 0)) ok = false;
+    __syncwarp();
+  } else if (warp >= kWidenWarp) {
+    const int wtid = tid - 32 * kWidenWarp;
+    int it = 0;
+    for (int t = t0; t < t1;) {
+      const int cnt = min(x.tiles - skip, t1 - t);
+      for (int k = 0; k < cnt; ++k, ++it) {
+        const int s = it % F::S, buf = it & 1;
+        const int slot0 = (skip + k) * kTile;
+        wait(&sm.full[s], (it / F::S) & 1);
+        uint4 w[Widen<D, kWidenThreads>::kSteps];
+        fetch_values<D, kWidenThreads>(smem + s * 2 * F::kSideBytes + F::kSideBytes, wtid,
+                                       x.end - slot0, w);
+        float ks = 0.f, vs = 0.f;
+        const bool used = wtid < 8 && slot0 + 16 * wtid < x.end;   // else no scale was copied
+        if (used) {
+          ks = sm.ks[s][16 * wtid >> p.a.page_shift];
+          vs = sm.vs[s][16 * wtid >> p.a.page_shift];
+        }
+        wait(&sm.vfree[buf], ((it >> 1) & 1) ^ 1);
+        if (wtid < 4) sm.vnan[buf][wtid] = 0;
+        if (wtid < 8) {
+          // a NaN scale (a bad page) makes its tokens' scores NaN through log2 vs; 1 / vs multiplies
+          // the zero weights of the rows that do not see them too, so it stays finite
+          const float vse = vs < kMinValueScale ? kMinValueScale : vs;
+          sm.page[buf][wtid] = used ? make_float4(ks * p.scale2, __log2f(vse),
+                                                  vs == vs ? __frcp_rn(vse) : 1.f, 0.f)
+                                    : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        widen_sync();
+        widen<D, kWidenThreads>(w, smem + F::kOffV16 + buf * F::kVfBytes, wtid, [&](int at) {
+          atomicOr(&sm.vnan[buf][at >> 5], 1u << (at & 31));
+        });
+        fence_async();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&sm.empty[s]);
+          mbar_arrive(&sm.vfull[buf]);
+        }
+      }
+      t += cnt;
+      skip = 0;
+      if (t < t1) item_next<NT>(p, x);
+    }
+  } else {
+    const int grp = warp >> 2, quad = warp & 3;
+    const int lrow = quad * 32 + lane;                        // row of the MMA tile
+    const int n = F::RTC == 2 ? grp * 128 + lrow : lrow;      // row of the item's tile
+    const uint32_t tlane = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    const uint32_t ts = tlane + F::kColS + grp * 128;
+    int it = 0, use = 0;   // tiles so far; this group's units so far
+    for (int t = t0; t < t1;) {
+      const int cnt = min(x.tiles - skip, t1 - t);
+      load_queries<typename F::T, D, NT, 128, F::kTerms, kSoftThreads>(p, x, tid, smem + F::kOffQ,
+                                                                       qs);
+      fence_async();
+      rows_sync();
+      if (tid == 0) mbar_arrive(&sm.qfull);
+      const long long r = static_cast<long long>(x.rt) * NT + n;
+      const int i = static_cast<int>(r / p.G), gq = static_cast<int>(r - static_cast<long long>(i) * p.G);
+      const bool live = i < x.n && x.ok;
+      const bool idle = !__any_sync(0xffffffffu, live);   // no row of this warp: nothing to weigh
+      const float q = qs[n];
+      float nm = kNoRef, l = 0.f;
+      const int step = F::RTC == 2 ? 1 : 2;
+      const int k0 = F::RTC == 2 ? 0 : grp;
+      for (int k = k0; k < cnt; k += step, ++use) {
+        const int tile = it + k, buf = tile & 1;
+        const int slot0 = (skip + k) * kTile;
+        const bool edge = slot0 + kTile > min(x.len, x.end);
+        uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};
+        if (edge)
+#pragma unroll
+          for (int w = 0; w < 4; ++w)
+            see[w] = live ? seen_bits(p, x.b, i, slot0 + 32 * w - x.len, x.n) : 0u;
+        wait(&sm.vfull[buf], (tile >> 1) & 1);   // its page scales and NaN marks
+        uint32_t nan[4];
+        *reinterpret_cast<uint4 *>(nan) = *reinterpret_cast<const uint4 *>(sm.vnan[buf]);
+        const bool masked = edge || (nan[0] | nan[1] | nan[2] | nan[3]) != 0;
+        const float4 *page = sm.page[buf];
+        wait(&sm.sfull[grp], use & 1);
+        tc::fence_after_sync();
+        if (!idle) {
+          uint32_t h[64];
+          float sum = 0.f;
+          bool fresh = __any_sync(0xffffffffu, nm == kNoRef);   // a row's first tile, mostly
+#pragma unroll 1
+          for (;;) {
+            if (fresh) {   // new references
+              const float m = masked ? row_maximum<true>(ts, page, q, see)
+                                     : row_maximum<false>(ts, page, q, see);
+              const bool grow = m + nm > kTrigger;
+              const float now = grow ? kBias - m : nm;
+              const float f = grow ? ex2(now - nm) : 1.f;   // 2^(m_old - m_new)
+              nm = now;
+              l *= f;
+              if (k > k0)   // the group's earlier value MMAs completed before these scores
+#pragma unroll 1
+                for (int c = 0; c < D; c += 16) {
+                  uint32_t o[16];
+                  tmem_ld(tlane + F::kColO + grp * D + c, o);
+                  tmem_wait(o);
+#pragma unroll
+                  for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                  tmem_st(tlane + F::kColO + grp * D + c, o);
+                }
+            }
+            const float big = masked ? row_weights<true>(ts, page, q, nm, see, nan, h, sum)
+                                     : row_weights<false>(ts, page, q, nm, see, nan, h, sum);
+            if (fresh || !__any_sync(0xffffffffu, big > kTrigger)) break;
+            fresh = true;
+          }
+          l += sum;
+#pragma unroll
+          for (int c = 0; c < 64; c += 16) {
+            uint32_t v[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[e] = h[c + e];
+            tmem_st(ts + c, v);
+          }
+          asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        }
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.pfull[grp]);
+      }
+      it += cnt;
+      // The item's (or its part's) result.
+      const bool whole = skip == 0 && cnt == x.tiles;
+      const long long part = 2LL * blockIdx.x + (skip == 0 ? 1 : 0);
+      if (use > 0) wait(&sm.ofull[grp], (use - 1) & 1);
+      tc::fence_after_sync();
+      float f0 = 0.f, f1 = 0.f;   // what the accumulator(s) are multiplied by
+      float lse2;
+      if constexpr (F::RTC == 2) {
+        lse2 = l == 0.f ? -INFINITY : log2f(l) - nm;
+        f0 = l == 0.f ? 0.f : 1.f / l;
+      } else {
+        float *merge = qs + NT;   // [group][reference, sum][row]
+        merge[grp * 256 + lrow] = nm;
+        merge[grp * 256 + 128 + lrow] = l;
+        rows_sync();   // and both groups' value MMAs have completed
+        tc::fence_after_sync();
+        const float nmo = merge[(grp ^ 1) * 256 + lrow], lo = merge[(grp ^ 1) * 256 + 128 + lrow];
+        const float m = fminf(nm, nmo);   // -m of the larger reference
+        const float w = ex2(m - nm), wo = ex2(m - nmo);
+        const float total = grp ? lo * wo + l * w : l * w + lo * wo;
+        const float inv = total == 0.f ? 0.f : 1.f / total;
+        lse2 = total == 0.f ? -INFINITY : log2f(total) - m;
+        const float fm = l == 0.f ? 0.f * inv : w * inv, fo = lo == 0.f ? 0.f * inv : wo * inv;
+        f0 = grp ? fo : fm;
+        f1 = grp ? fm : fo;
+      }
+      if (!x.ok) lse2 = f0 = NAN;
+      if (i < p.a.N && (F::RTC == 2 || grp == 0)) {
+        if (!whole)
+          p.part_lse[part * NT + n] = lse2;
+        else if (p.lse)
+          p.lse[(static_cast<long long>(x.b) * p.a.N + i) * p.a.Hq +
+                static_cast<long long>(x.h) * p.G + gq] = live || !x.ok ? lse2 * kLn2 : -INFINITY;
+      }
+      const bool zero = x.ok && !live;   // padding
+      // both groups' halves of the dims when they share rows, else all of the group's own
+      const int d0 = F::RTC == 2 ? 0 : grp * (D / 2), d1 = F::RTC == 2 ? D : d0 + D / 2;
+      using T = typename F::T;
+      T *out = static_cast<T *>(p.out) + ((static_cast<long long>(x.b) * p.a.N + i) * p.a.Hq +
+                                          static_cast<long long>(x.h) * p.G + gq) * D;
+      float *po = p.part_o + (part * NT + n) * D;
+#pragma unroll 1
+      for (int c = d0; c < d1; c += 16) {
+        uint32_t o[16], o1[16];
+        tmem_ld(tlane + F::kColO + (F::RTC == 2 ? grp * D : 0) + c, o);
+        if (F::RTC == 1) tmem_ld(tlane + F::kColO + D + c, o1);
+        tmem_wait(o);
+        if (F::RTC == 1) tmem_wait(o1);
+        if (i < p.a.N) {
+          float v[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            // an accumulator that nothing was added to counts 0 whatever it holds
+            v[e] = f0 == 0.f ? 0.f : __uint_as_float(o[e]) * f0;
+            if (F::RTC == 1) v[e] += f1 == 0.f ? 0.f : __uint_as_float(o1[e]) * f1;
+            if (zero) v[e] = 0.f;
+          }
+          if (!whole) {
+#pragma unroll
+            for (int e = 0; e < 16; e += 4)
+              *reinterpret_cast<float4 *>(po + c + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; e += 8)
+              *reinterpret_cast<uint4 *>(out + c + e) =
+                  make_uint4(pack_pair(v[e], v[e + 1], T()), pack_pair(v[e + 2], v[e + 3], T()),
+                             pack_pair(v[e + 4], v[e + 5], T()), pack_pair(v[e + 6], v[e + 7], T()));
+          }
+        }
+      }
+      if (!x.ok && tid == 0) set_status(p.a.status, SPEC_ERR_LENGTH);
+      tc::fence_before_sync();
+      rows_sync();   // every accumulator is read and every score MMA done before the next item
+      t += cnt;
+      skip = 0;
+      if (t < t1) item_next<NT>(p, x);
+    }
+  }
+  if (!ok) set_status(p.a.status, SPEC_ERR_TIMEOUT);
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == kMma) {
+    tc::fence_after_sync();
+    tmem_free(tmem, 512);
+  }
+}
+
+template <class F>
+cudaError_t launch_cfg(AttnArgs &p, const CUtensorMap &mk, const CUtensorMap &mv, int ctas, char *ws,
+                       cudaStream_t stream) {
+  static std::atomic<bool> ready[64];
+  constexpr int smem = rows_smem<F>();
+  static_assert(smem <= 227 * 1024, "shared memory of a CTA");
+  cudaError_t e = allow_smem(kv_attention_rows_kernel<F>, smem, ready);
+  if (e != cudaSuccess) return e;
+  plan_parts(p, ws, F::NT);
+  // a plain stream-ordered launch: nearly all of an SM's shared memory is one CTA's
+  kv_attention_rows_kernel<F><<<ctas, kRowsThreads, smem, stream>>>(mk, mv, p);
+  e = cudaGetLastError();
+  return e != cudaSuccess ? e : launch_join<typename F::T, F::D, F::NT>(p, ctas, stream);
+}
+
+template <typename T, int D>
+cudaError_t launch_rows(AttnArgs &p, const CUtensorMap &mk, const CUtensorMap &mv, int ctas,
+                        char *ws, cudaStream_t stream) {
+  if (static_cast<long long>(p.a.N) * p.G > 128)
+    return launch_cfg<RowsCfg<T, D, 2, 2>>(p, mk, mv, ctas, ws, stream);
+  return launch_cfg<RowsCfg<T, D, 1, 3>>(p, mk, mv, ctas, ws, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_attention_rows(AttnArgs &p, int dtype, const CUtensorMap &mk,
+                                  const CUtensorMap &mv, int ctas, char *ws, cudaStream_t stream) {
+  if (dtype == SPEC_BF16)
+    return p.a.D == 64 ? launch_rows<__nv_bfloat16, 64>(p, mk, mv, ctas, ws, stream)
+                       : launch_rows<__nv_bfloat16, 128>(p, mk, mv, ctas, ws, stream);
+  return p.a.D == 64 ? launch_rows<__half, 64>(p, mk, mv, ctas, ws, stream)
+                     : launch_rows<__half, 128>(p, mk, mv, ctas, ws, stream);
+}
+
+}  // namespace specv

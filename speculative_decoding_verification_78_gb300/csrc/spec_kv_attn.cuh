@@ -1,0 +1,541 @@
+// spec_kv_attn.cuh -- what the two attention kernels share: tensor-core and barrier helpers, the line
+// of 128-token tiles and its even cut over the SMs, queries as e4m3 terms, values widened to fp16, and
+// the join of the parts of an item that several CTAs worked on.
+#pragma once
+
+#include <cudaTypedefs.h>
+
+#include <atomic>
+
+#include "spec_kv.cuh"
+#include "spec_tc.cuh"
+
+namespace specv {
+namespace attn {
+
+constexpr int kTile = 128;          // tokens
+constexpr int kMaxCtas = 152;       // workspace parts are sized for this many CTAs
+constexpr float kNoRef = 1e30f;     // -m of a row that has seen nothing
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kMinValueScale = 8.271806125530277e-25f;   // 2^-80: a zero scale's logarithm
+
+struct AttnArgs {
+  KvArgs a;
+  const void *q;
+  long long q_stride;
+  float scale2;        // scale * log2(e)
+  void *out;
+  float *lse;
+  float *part_o;       // [2 G][NT][D]
+  float *part_lse;     // [2 G][NT], base 2
+  int4 *start;         // [G]: (item's b, h, row tile, first tile) of each CTA's range; then [G]
+                       // its tiles
+  int G;               // query heads per key head
+  int RT;              // row tiles
+};
+
+// ------------------------------------------------------------------ tensor-core helpers
+
+__device__ __forceinline__ void mbar_arrive(uint64_t *b) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(tc::saddr(b)) : "memory");
+}
+// an arrival once this thread's cp.async copies so far have landed (counted at initialisation)
+__device__ __forceinline__ void mbar_arrive_copies(uint64_t *b) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(tc::saddr(b))
+               : "memory");
+}
+__device__ __forceinline__ void copy4(void *dst, const void *src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(tc::saddr(dst)), "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map, int c0, int c1,
+                                            uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cta.global.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(tc::saddr(bar))
+      : "memory");
+}
+__device__ __forceinline__ void tmem_alloc(uint32_t *slot, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                   tc::saddr(slot)),
+               "r"(ncols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_free(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols)
+               : "memory");
+}
+__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc));
+}
+__device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                        uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc));
+}
+__device__ __forceinline__ void mma_commit(uint64_t *bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+          tc::saddr(bar))
+      : "memory");
+}
+// 4 / 8 / 16 consecutive fp32 columns of this thread's lane; valid after tmem_wait of the same array
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&v)[4]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+               : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&v)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+        "=r"(v[7])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15}, [%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+        "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
+        "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr));
+}
+// the registers pass through, so nothing that uses them is scheduled ahead of the wait
+template <int K>
+__device__ __forceinline__ void tmem_wait(uint32_t (&v)[K]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < K; ++i) asm volatile("" : "+r"(v[i]));
+}
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&v)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(v[0]),
+      "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, "
+      "%10, %11, %12, %13, %14, %15};" ::"r"(v[0]),
+      "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+      "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]),
+      "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+// true in one lane of a converged warp
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+// tc::mbar_wait whose usual case, a phase that has completed, costs no call
+__device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity) {
+  return tc::mbar_try(bar, parity) || tc::mbar_wait(bar, parity);
+}
+__device__ __forceinline__ void fence_async() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// Byte offset `at` of a tile whose rows are `kSpan` bytes (32, 64 or 128), swizzled as TMA and the
+// MMA do: the 16-byte chunk number exclusive-or the bits from 7 up.
+template <int kSpan>
+__device__ __forceinline__ uint32_t swz(uint32_t at) {
+  constexpr uint32_t m = kSpan == 128 ? 7u : kSpan == 64 ? 3u : 1u;
+  return at ^ (((at >> 7) & m) << 4);
+}
+// Shared-memory matrix descriptor: start, leading and stride byte offsets in units of 16 bytes,
+// version 1, swizzle mode (2: 128 bytes, 4: 64, 6: 32). K-major operands: rows of the swizzle span,
+// 8-row atoms `sbo` apart. MN-major operands: k rows of the span (8 of them an atom, atoms `sbo`
+// apart), spans of consecutive m or n `lbo` apart.
+template <int kSpan>
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+  constexpr uint64_t mode = kSpan == 128 ? 2 : kSpan == 64 ? 4 : 6;
+  return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(lbo >> 4) << 16) |
+         (static_cast<uint64_t>(sbo >> 4) << 32) | (1ull << 46) | (mode << 61);
+}
+// Instruction descriptor: fp32 accumulator; A and B e4m3 (kind::f8f6f4) or fp16 (kind::f16), both
+// format 0; bits 15, 16: A, B are MN-major
+__host__ __device__ constexpr uint32_t attn_idesc(int M, int N, bool mn_major) {
+  return (1u << 4) | (mn_major ? 3u << 15 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) |
+         (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// ------------------------------------------------------------------ the line of tiles
+
+struct Item {   // one (sequence, key head, row tile)
+  int b, h, rt;
+  int len, n;      // tokens before the new ones; new ones
+  bool ok;         // lengths fit
+  int end;         // first slot that no row sees
+  int tiles;
+};
+
+template <int NT>
+__device__ __forceinline__ int item_end(const AttnArgs &p, int len, int n, bool ok, int rt) {
+  if (!ok || n == 0) return 0;
+  if (p.RT == 1 || p.a.mask) return len + n;
+  const long long first = static_cast<long long>(rt) * NT / p.G;
+  if (first >= n) return 0;   // padding
+  const long long last = (static_cast<long long>(rt) * NT + NT - 1) / p.G;
+  return len + static_cast<int>(last + 1 < n ? last + 1 : n);
+}
+__device__ __forceinline__ int tiles_for(int end) { return end > kTile ? (end + kTile - 1) / kTile : 1; }
+
+// tiles of one key head of sequence b
+template <int NT>
+__device__ __forceinline__ int head_tiles(const AttnArgs &p, int b) {
+  int len, n;
+  const bool ok = kv_lengths(p.a, b, len, n);
+  int s = 0;
+  for (int rt = 0; rt < p.RT; ++rt) s += tiles_for(item_end<NT>(p, len, n, ok, rt));
+  return s;
+}
+template <int NT>
+__device__ __forceinline__ void item_load(const AttnArgs &p, Item &x) {
+  x.ok = kv_lengths(p.a, x.b, x.len, x.n);
+  x.end = item_end<NT>(p, x.len, x.n, x.ok, x.rt);
+  x.tiles = tiles_for(x.end);
+}
+template <int NT>
+__device__ __forceinline__ void item_next(const AttnArgs &p, Item &x) {
+  if (++x.rt == p.RT) {
+    x.rt = 0;
+    if (++x.h == p.a.Hkv) {
+      x.h = 0;
+      ++x.b;
+    }
+  }
+  if (x.b < p.a.B) item_load<NT>(p, x);
+}
+__device__ __forceinline__ int range_start(long long T, int c, int G) {
+  return static_cast<int>(T * c / G);
+}
+
+// The CTA's range [t0, t1) of the line and its first item; called by all threads. Thread t sums
+// the sequences of its own contiguous share; the thread whose share holds t0 finds it there.
+struct LocateScratch {
+  int b0, skip0;
+  int warp_sum[20];
+};
+template <int NT, int kThreads>
+__device__ void locate(const AttnArgs &p, LocateScratch &sm, int &t0, int &t1, Item &x, int &skip) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int share = (p.a.B + kThreads - 1) / kThreads;
+  const int lo = min(p.a.B, tid * share), hi = min(p.a.B, lo + share);
+  int mine = 0;
+  for (int b = lo; b < hi; ++b) mine += head_tiles<NT>(p, b) * p.a.Hkv;
+  int incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) sm.warp_sum[warp] = incl;
+  __syncthreads();
+  int before = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += sm.warp_sum[w];
+    total += sm.warp_sum[w];
+  }
+  t0 = range_start(total, blockIdx.x, gridDim.x);
+  t1 = range_start(total, blockIdx.x + 1, gridDim.x);
+  int at = before + incl - mine;
+  if (t0 >= at && t0 < at + mine) {
+    int b = lo;
+    for (;; ++b) {
+      const int n = head_tiles<NT>(p, b) * p.a.Hkv;
+      if (t0 < at + n) break;
+      at += n;
+    }
+    sm.b0 = b;
+    sm.skip0 = t0 - at;
+  }
+  __syncthreads();
+  if (t0 >= t1) return;
+  x.b = sm.b0;
+  x.rt = 0;
+  skip = sm.skip0;
+  const int per_head = head_tiles<NT>(p, x.b);
+  x.h = skip / per_head;
+  skip -= x.h * per_head;
+  item_load<NT>(p, x);
+  while (skip >= x.tiles) {
+    skip -= x.tiles;
+    ++x.rt;
+    item_load<NT>(p, x);
+  }
+}
+// What the join needs to know of the CTA's range: its first item and the item's tiles before it,
+// the item's tiles, and the range.
+__device__ __forceinline__ void publish_range(const AttnArgs &p, const Item &x, int skip, int t0,
+                                              int t1) {
+  if (t0 < t1) p.start[blockIdx.x] = make_int4(x.b, x.h, x.rt, skip);
+  p.start[gridDim.x + blockIdx.x] = make_int4(t0 < t1 ? x.tiles : 0, t0, t1, 0);
+}
+
+// ------------------------------------------------------------------ operands
+
+// Rows 0 .. NT - 1 of the item as e4m3 terms in shared memory (D / 8 lanes a row), each in units of a
+// power of two that puts its largest element in [2^7, 2^8); qs[n] undoes it. Two terms hold bf16's 8
+// significant bits exactly down to 2^-9 of the unit, three fp16's 11. Blocks of kBlock rows, each
+// term of a block a K-major operand; rows past the item's are zero.
+template <typename T, int D, int NT, int kBlock, int kTerms, int kThreads>
+__device__ __forceinline__ void load_queries(const AttnArgs &p, const Item &x, int tid, uint8_t *sq,
+                                             float *qs) {
+  constexpr int kLanes = D / 8, kRows = kThreads / kLanes;
+  const int sub = tid % kLanes, row0 = tid / kLanes;
+#pragma unroll 4
+  for (int n0 = 0; n0 < NT; n0 += kRows) {
+    const int n = n0 + row0;
+    if (n >= NT) break;   // whole warps: a warp's rows are 2 or 4
+    const long long r = static_cast<long long>(x.rt) * NT + n;
+    const int i = static_cast<int>(r / p.G), g = static_cast<int>(r - static_cast<long long>(i) * p.G);
+    float f[8];
+    if (i < x.n && x.ok) {
+      const T *src = static_cast<const T *>(p.q) +
+                     (static_cast<long long>(x.b) * p.a.N + i) * p.q_stride +
+                     (static_cast<long long>(x.h) * p.G + g) * D + sub * 8;
+      vec_to_floats<T>(__ldg(reinterpret_cast<const uint4 *>(src)), f);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = 0.f;
+    }
+    float m = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m = fmax_nan(m, fabsf(f[e]));
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1) m = fmax_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const int e = max(static_cast<int>(__float_as_uint(m) >> 23), 27);   // exponent, at least -100
+    const float mul = __uint_as_float(static_cast<uint32_t>(127 + 127 + 7 - e) << 23);
+    if (sub == 0) qs[n] = m < INFINITY ? __uint_as_float(static_cast<uint32_t>(e - 7) << 23) : NAN;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) f[k] *= mul;
+    uint8_t *blk = sq + n / kBlock * (kTerms * kBlock * D);
+#pragma unroll
+    for (int t = 0; t < kTerms; ++t) {
+      const uint2 w = floats_to_e4m3(f, 1.f);
+      *reinterpret_cast<uint2 *>(blk + t * (kBlock * D) + swz<D>(n % kBlock * D + sub * 8)) = w;
+      if (t + 1 < kTerms) {
+        float g8[8];
+        e4m3_to_floats(w, g8);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) f[k] -= g8[k];   // exact
+      }
+    }
+  }
+}
+
+// V's bytes of a tile, on their way to fp16: 16 bytes a lane and step, whole rows side by side.
+template <int D, int kThreads> struct Widen {
+  static constexpr int kLanes = D / 16;             // lanes of a token
+  static constexpr int kRows = kThreads / kLanes;   // tokens a step
+  static constexpr int kSteps = kTile / kRows;
+};
+template <int D, int kThreads>
+__device__ __forceinline__ void fetch_values(const uint8_t *sv, int gtid, int valid,
+                                             uint4 (&w)[Widen<D, kThreads>::kSteps]) {
+  using W = Widen<D, kThreads>;
+#pragma unroll
+  for (int u = 0; u < W::kSteps; ++u) {
+    const int t = u * W::kRows + gtid / W::kLanes;
+    w[u] = *reinterpret_cast<const uint4 *>(sv + t * D + gtid % W::kLanes * 16);
+    if (t >= valid) w[u] = make_uint4(0, 0, 0, 0);
+  }
+}
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) {   // bit 7 of each NaN byte
+  return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+}
+// The values as fp16 rows of 64 dims (128 bytes, swizzled). NaN codes become zero and mark their
+// token: the weights of the rows that see it then turn NaN instead (a NaN operand would reach the
+// rows that do not): `mark`(token) is called for each.
+template <int D, int kThreads, typename Mark>
+__device__ __forceinline__ bool widen(uint4 (&w)[Widen<D, kThreads>::kSteps], uint8_t *out, int gtid,
+                                      Mark mark) {
+  using W = Widen<D, kThreads>;
+  const int c = gtid % W::kLanes, row0 = gtid / W::kLanes;
+  uint32_t any = 0;
+#pragma unroll
+  for (int u = 0; u < W::kSteps; ++u)
+    any |= nan_codes(w[u].x) | nan_codes(w[u].y) | nan_codes(w[u].z) | nan_codes(w[u].w);
+  if (any) {
+#pragma unroll
+    for (int u = 0; u < W::kSteps; ++u) {
+      const uint32_t hx = nan_codes(w[u].x), hy = nan_codes(w[u].y), hz = nan_codes(w[u].z),
+                     hw = nan_codes(w[u].w);
+      w[u].x &= ~((hx >> 7) * 255u);
+      w[u].y &= ~((hy >> 7) * 255u);
+      w[u].z &= ~((hz >> 7) * 255u);
+      w[u].w &= ~((hw >> 7) * 255u);
+      if (hx | hy | hz | hw) mark(u * W::kRows + row0);
+    }
+  }
+  // 64 dims (4 lanes) a block of kTile rows; the second block's lanes store their halves the other
+  // way round, so that eight neighbours never meet in a bank
+  uint8_t *blk = out + (c >> 2) * (kTile * 128);
+  const bool flip = (c >> 2) & 1;
+#pragma unroll
+  for (int u = 0; u < W::kSteps; ++u) {
+    const int t = u * W::kRows + row0;
+    const uint4 lo = make_uint4(e4m3_to_half2(w[u].x & 0xffffu), e4m3_to_half2(w[u].x >> 16),
+                                e4m3_to_half2(w[u].y & 0xffffu), e4m3_to_half2(w[u].y >> 16));
+    const uint4 hi = make_uint4(e4m3_to_half2(w[u].z & 0xffffu), e4m3_to_half2(w[u].z >> 16),
+                                e4m3_to_half2(w[u].w & 0xffffu), e4m3_to_half2(w[u].w >> 16));
+    const uint32_t a0 = swz<128>(t * 128 + (c & 3) * 32), a1 = swz<128>(t * 128 + (c & 3) * 32 + 16);
+    *reinterpret_cast<uint4 *>(blk + (flip ? a1 : a0)) = flip ? hi : lo;
+    *reinterpret_cast<uint4 *>(blk + (flip ? a0 : a1)) = flip ? lo : hi;
+  }
+  return any != 0;
+}
+
+// ------------------------------------------------------------------ the join
+
+// Joins the parts of the items that cross ranges. Block (c, rows): the item that range c begins
+// inside of, if c is the first range to do so; one warp per row.
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(256) kv_attention_join(const __grid_constant__ AttnArgs p,
+                                                         int ctas) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  constexpr int kBlocks = NT / 8;
+  const int c = 1 + blockIdx.x / kBlocks;
+  const int n = (blockIdx.x % kBlocks) * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  // (written by other CTAs: read from L2)
+  auto empty = [&](int at) {
+    const int4 e = __ldcg(p.start + at);
+    return e.y >= e.z;
+  };
+  const int4 d = __ldcg(p.start + ctas + c);           // tiles of its first item, t0, t1
+  if (d.y >= d.z) return;
+  const int4 s = __ldcg(p.start + c);
+  const int begin = d.y - s.w, end = begin + d.x;   // the item's tiles on the line
+  if (s.w == 0) return;
+  // the range with the tile before: the item's first part, or another block's item
+  int first = c - 1;   // (ranges may be empty when there are few tiles)
+  while (empty(ctas + first)) --first;
+  if (begin < __ldcg(p.start + ctas + first).y) return;
+  const long long r = static_cast<long long>(s.z) * NT + n;
+  const int i = static_cast<int>(r / p.G), g = static_cast<int>(r - static_cast<long long>(i) * p.G);
+  if (i >= p.a.N) return;
+  float m = -INFINITY;
+  for (int k = first; k < ctas; ++k) {
+    const int4 e = __ldcg(p.start + ctas + k);
+    if (e.y >= end) break;
+    if (e.y >= e.z) continue;
+    m = fmax_nan(m, __ldcg(p.part_lse + (2LL * k + (k == first ? 1 : 0)) * NT + n));
+  }
+  constexpr int E = D / 32;
+  float acc[E], sum = 0.f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+  if (m != -INFINITY)
+    for (int k = first; k < ctas; ++k) {
+      const int4 e = __ldcg(p.start + ctas + k);
+      if (e.y >= end) break;
+      if (e.y >= e.z) continue;
+      const long long part = (2LL * k + (k == first ? 1 : 0)) * NT + n;
+      const float w = ex2(__ldcg(p.part_lse + part) - m);
+      sum += w;
+      const float *o = p.part_o + part * D + lane * E;
+#pragma unroll
+      for (int q = 0; q < E; ++q) acc[q] = __fmaf_rn(w, __ldcg(o + q), acc[q]);
+    }
+  int len, nn;
+  const bool ok = kv_lengths(p.a, s.x, len, nn);
+  const bool pad = ok && i >= nn;
+  const float f = pad || m == -INFINITY ? 0.f : 1.f / sum;
+  const long long at = (static_cast<long long>(s.x) * p.a.N + i) * p.a.Hq +
+                       static_cast<long long>(s.y) * p.G + g;
+  T *o = static_cast<T *>(p.out) + at * D + lane * E;
+#pragma unroll
+  for (int q = 0; q < E; q += 2)
+    *reinterpret_cast<uint32_t *>(o + q) =
+        pad ? 0u : pack_pair(acc[q] * f, acc[q + 1] * f, T());
+  if (p.lse && lane == 0)
+    p.lse[at] = pad || m == -INFINITY ? -INFINITY : (m + log2f(sum)) * kLn2;
+}
+
+// ------------------------------------------------------------------ launch
+
+
+inline PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> fn{nullptr};
+  PFN_cuTensorMapEncodeTiled_v12000 f = fn.load(std::memory_order_acquire);
+  if (!f) {
+    void *ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000,
+                                         cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess || !ptr)
+      return nullptr;
+    f = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+    fn.store(f, std::memory_order_release);
+  }
+  return f;
+}
+
+// [rows, D] bytes, boxes of one page of one head
+inline bool make_map(CUtensorMap *m, const void *base, long long rows, int D, int page, bool swizzle) {
+  const auto enc = encode_fn();
+  if (!enc) return false;
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(D)};
+  cuuint32_t box[2] = {static_cast<cuuint32_t>(D), static_cast<cuuint32_t>(page)};
+  cuuint32_t es[2] = {1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE,
+             !swizzle ? CU_TENSOR_MAP_SWIZZLE_NONE
+                      : D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// `ctas` CTAs' parts of NT rows in the workspace, and the launch that joins them.
+inline void plan_parts(AttnArgs &p, char *ws, int NT) {
+  p.start = reinterpret_cast<int4 *>(ws);
+  p.part_lse = reinterpret_cast<float *>(ws + 2 * kMaxCtas * sizeof(int4));
+  p.part_o = p.part_lse + 2 * kMaxCtas * NT;
+  const long long rows = static_cast<long long>(p.a.N) * p.G;
+  p.RT = static_cast<int>((rows + NT - 1) / NT);
+}
+template <typename T, int D, int NT>
+cudaError_t launch_join(const AttnArgs &p, int ctas, cudaStream_t stream) {
+  if (ctas == 1) return cudaSuccess;
+  return launch_kv(kv_attention_join<T, D, NT>, static_cast<long long>(ctas - 1) * (NT / 8), 256, 0,
+                   stream, p, ctas);
+}
+// raises a kernel's shared-memory limit once per device
+template <typename K>
+cudaError_t allow_smem(K kernel, int bytes, std::atomic<bool> (&ready)[64]) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 64 && ready[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev < 64) ready[dev].store(true, std::memory_order_release);
+  return e;
+}
+
+}  // namespace attn
+
+// the kernel for items of more than 32 query rows (spec_kv_attention_rows.cu)
+cudaError_t launch_attention_rows(attn::AttnArgs &p, int dtype, const CUtensorMap &mk,
+                                  const CUtensorMap &mv, int ctas, char *ws, cudaStream_t stream);
+
+}  // namespace specv
