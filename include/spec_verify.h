@@ -365,8 +365,8 @@ int spec_kv_append(const spec_kv_cache_t *cache, const int32_t *page_table, int 
  * Scores, statistics and sums are held in fp32 and the softmax weights are rounded to fp16 before
  * their product with the values. A query that sees no token (an empty mask row of an empty
  * sequence, or padding) gets zeros and lse = -inf. What lies in slots that no query of the
- * sequence sees is not used, NaN included. A NaN in a query, key or value reaches every element
- * of the queries that see it.
+ * sequence sees is not used, NaN included; a NaN in a query, key or value reaches the outputs of
+ * the queries that see it and no others.
  *   workspace  at least spec_kv_attention_workspace_bytes(B, N, q_heads, kv_heads, head_dim) bytes
  * In the data: a bad length makes every output of the sequence NaN, a bad page number those of the
  * queries that see a token of the page; both set *status. A wait inside the kernel that gives up

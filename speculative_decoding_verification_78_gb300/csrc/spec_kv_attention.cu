@@ -87,7 +87,7 @@ struct Cfg {
 struct __align__(16) Small {   // the small parts of shared memory; arrays of NT follow
   uint64_t full[4], empty[4], sfull[2], pfull[2], pfree[2], qfull, done;
   float ks[4][8], vs[4][8];
-  uint8_t vnan[2][kTile];      // by group: the token's values hold NaN (see widen)
+  uint8_t vnan[2][kTile];      // by group: the token's values hold NaN (see scrub_values)
   uint32_t tmem;
   LocateScratch loc;
 };
@@ -253,13 +253,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   if (tid < 2 * kTile) sm.vnan[tid / kTile][tid % kTile] = 0;
   if (warp == kMma) tmem_alloc(&sm.tmem, F::kTmem);
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  int t0 = 0, t1 = 0, skip = 0;
+  int t0 = 0, t1 = 0, total = 0, skip = 0;
   Item x{};
   tc::fence_before_sync();
-  locate<F::NT, kAttnThreads>(p, sm.loc, t0, t1, x, skip);
+  locate<F::NT, kAttnThreads>(p, sm.loc, t0, t1, total, x, skip);
   tc::fence_after_sync();
   const uint32_t tmem = sm.tmem;
-  if (tid == 0) publish_range(p, x, skip, t0, t1);
+  if (tid == 0) publish_range(p, x, skip, t0, t1, total);
   bool ok = true;   // false after a wait gave up: no further waits, and no further work is issued
   if (warp == kProducer) {
     int it = 0;
@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     }
     // the last copies of each stage land before the CTA may end
     for (int k = max(0, it - F::S); k < it; ++k)
-      if (!tc::mbar_wait(&sm.full[k % F::S], (k / F::S) & 1)) ok = false;
+      if (!wait_for(&sm.full[k % F::S], (k / F::S) & 1)) ok = false;
   } else if (warp == kMma) {
     // The whole warp walks the tiles and one elected lane issues: inside a branch of one lane the
     // descriptors are not known to be uniform, and issuing a tile's 16 MMAs took 1400 clocks.
@@ -423,7 +423,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         fetch_values<F::D, kGroupThreads>(smem + s * 2 * F::kSideBytes + F::kSideBytes, gtid, x.end - slot0, w);
         const float ks = sm.ks[s][row >> p.a.page_shift], vs = sm.vs[s][row >> p.a.page_shift];
         wait(&sm.pfree[grp], (use & 1) ^ 1);
-        const bool nan = widen<F::D, kGroupThreads>(w, sv16, gtid, [&](int at) { vnan[at] = 1; });
+        const bool masked = slot0 + kTile > min(x.len, x.end);
+        const bool nan = masked && scrub_values<F::D, kGroupThreads>(
+                                       w, gtid, [&](int at) { vnan[at] = 1; });
+        widen<F::D, kGroupThreads>(w, sv16, gtid);
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.empty[s]);
         // a NaN scale (a bad page) makes the scores of its tokens NaN through lvs, and only those:
@@ -445,7 +448,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           tk.from = static_cast<int>(
               min(static_cast<long long>(F::NT),
                   static_cast<long long>(j) * p.G - static_cast<long long>(x.rt) * F::NT));
-        const bool masked = slot0 + kTile > min(x.len, x.end);
         wait(&sm.sfull[grp], use & 1);
         tc::fence_after_sync();
         bool again = false;

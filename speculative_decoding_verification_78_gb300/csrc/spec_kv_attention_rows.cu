@@ -10,14 +10,14 @@
 // its reference, its sum and its query's unit are registers; what differs by token, the page scales,
 // is constant over 16 columns (pages hold at least 16 tokens). P is written back to tensor memory,
 // over the scores it came from, as the fp16 operand of the second MMA: nothing of the softmax passes
-// through shared memory, which the operands of the MMAs already load. V is widened to fp16 by four
+// through shared memory, which the operands of the MMAs already load. V is widened to fp16 by eight
 // warps of their own, once for all rows of the CTA.
 //
-// Two groups of four softmax warps work half a step apart, so that the tensor cores have one group's
+// Two groups of eight softmax warps (two for each 32 rows, half of the tile's tokens each) work half a
+// step apart, so that the tensor cores have one group's
 // MMAs while the other group exponentiates: with more than 128 rows each group has 128 rows of its
 // own and both take every tile; with fewer, the groups take the tiles in turn and are joined at the
-// end of the item. Unit u of a segment belongs to group u & 1; the MMA warp issues scores(u), then
-// values(u - 1).
+// end of the item. Unit u of a segment belongs to group u & 1; one warp issues the scores, another the values.
 //
 // What bounds it: a 256-row tile of 128 tokens (D = 128) is 2048 clocks of MMA (two e4m3 terms cost
 // what one 16-bit operand would) and 1024 of ex2.
@@ -29,12 +29,14 @@ using namespace attn;
 
 namespace {
 
-constexpr int kSoftWarps = 8;            // two groups of four
+constexpr int kGroupWarps = 8;                        // two for each 32 rows: half of the tokens each
+constexpr int kSoftWarps = 2 * kGroupWarps;
 constexpr int kSoftThreads = 32 * kSoftWarps;
-constexpr int kWidenWarp = kSoftWarps;   // four warps widen V
-constexpr int kWidenThreads = 128;
-constexpr int kProducer = kSoftWarps + 4, kMma = kProducer + 1;
-constexpr int kRowsThreads = 32 * (kMma + 1);
+constexpr int kWidenWarp = kSoftWarps, kWidenWarps = 8;   // warps that widen V
+constexpr int kWidenThreads = 32 * kWidenWarps;
+constexpr int kProducer = kWidenWarp + kWidenWarps;       // copies; then the two MMA warps
+constexpr int kScores = kProducer + 1, kValues = kProducer + 2;
+constexpr int kRowsThreads = 32 * (kValues + 2);   // one idle warp: register shares go by four warps
 constexpr float kBias = 8.f;        // a new reference puts the row's largest weight at 2^8 ...
 constexpr float kTrigger = 15.f;    // ... and is taken when one exceeds 2^15 (fp16 ends at 2^16)
 
@@ -44,6 +46,25 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, u
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
       "r"(a), "l"(b), "r"(idesc), "r"(acc));
+}
+// Registers: 896 threads start with 72 each; the softmax warps, which hold a half row's weights, take
+// more, which the others give up (512 x 96 + 384 x 40 = 896 x 72).
+__device__ __forceinline__ void regs_take() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
+}
+__device__ __forceinline__ void regs_give() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+}
+// barrier of the two warps that share rows: true in both if `p` was in any of their threads
+__device__ __forceinline__ bool pair_any(int id, bool p) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, %2, 64, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(p)), "r"(id)
+      : "memory");
+  return r != 0;
 }
 __device__ __forceinline__ void rows_sync() {   // the softmax threads
   asm volatile("bar.sync 1, %0;" ::"n"(kSoftThreads) : "memory");
@@ -74,13 +95,13 @@ struct __align__(16) RowsSmall {
   uint64_t qfull, done;
   float ks[4][8], vs[4][8];
   float4 page[2][8];             // by 16 tokens: scale log2(e) ks, log2 vs, 1 / vs
-  uint32_t vnan[2][4];           // tokens whose values hold NaN
+  uint32_t vnan[2][4];           // tokens whose values hold NaN (tiles with new tokens)
   uint32_t tmem;
   LocateScratch loc;
 };
-template <class F> constexpr int rows_smem() {   // + qs; groups that share rows: references, sums
-  return F::kOffSmall + static_cast<int>(sizeof(RowsSmall)) + F::NT * 4 +
-         (F::RTC == 1 ? 4 * 128 * 4 : 0);
+// + the queries' units, which, once read, leave their place to the row maxima [group][half][row]
+template <class F> constexpr int rows_smem() {
+  return F::kOffSmall + static_cast<int>(sizeof(RowsSmall)) + 512 * 4;
 }
 
 // Bits of the 32 slots from number `j0` among the new tokens on (negative: the cached ones, which
@@ -103,21 +124,21 @@ __device__ __forceinline__ uint32_t seen_bits(const AttnArgs &p, int b, int i, i
   return r;
 }
 
-// One row of the tile: weights against -nm, as fp16 pairs in h, and their sum over the value scales;
+// Half a row of the tile: weights against -nm, as fp16 pairs in h, and their sum over the value scales;
 // returns the largest exponent. The next 16 scores are on their way while these are worked on.
 template <bool kMasked>
 __device__ __forceinline__ float row_weights(uint32_t ts, const float4 *page, float qs, float nm,
-                                             const uint32_t (&see)[4], const uint32_t (&nan)[4],
-                                             uint32_t (&h)[64], float &sum) {
+                                             const uint32_t (&see)[2], const uint32_t (&nan)[2],
+                                             uint32_t (&h)[32], float &sum) {
   float big = -INFINITY;
   sum = 0.f;
   uint32_t s[2][16];
   tmem_ld(ts, s[0]);
 #pragma unroll
-  for (int c = 0; c < 8; ++c) {
+  for (int c = 0; c < 4; ++c) {
     uint32_t(&v)[16] = s[c & 1];
     tmem_wait(v);
-    if (c < 7) tmem_ld(ts + 16 * (c + 1), s[(c + 1) & 1]);
+    if (c < 3) tmem_ld(ts + 16 * (c + 1), s[(c + 1) & 1]);
     const float4 pg = page[c];
     const float k = pg.x * qs, d = pg.y + nm;
     const f32x2 k2 = pk2(k, k), d2 = pk2(d, d);
@@ -144,20 +165,19 @@ __device__ __forceinline__ float row_weights(uint32_t ts, const float4 *page, fl
   }
   return big;
 }
-// The largest y of the row's tile, without the reference.
+// The largest y of the half row, without the reference.
 template <bool kMasked>
 __device__ __forceinline__ float row_maximum(uint32_t ts, const float4 *page, float qs,
-                                             const uint32_t (&see)[4]) {
+                                             const uint32_t (&see)[2]) {
   float big = -INFINITY;
-#pragma unroll 2
-  for (int c = 0; c < 8; ++c) {
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
     uint32_t v[16];
     tmem_ld(ts + 16 * c, v);
     tmem_wait(v);
     const float4 pg = page[c];
     const float k = pg.x * qs;
-    const uint32_t bits = kMasked ? (c < 4 ? c < 2 ? see[0] : see[1] : c < 6 ? see[2] : see[3]) >> (16 * (c & 1))
-                                  : 0xffffu;
+    const uint32_t bits = kMasked ? (c < 2 ? see[0] : see[1]) >> (16 * (c & 1)) : 0xffffu;
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
       const float y = __fmaf_rn(__uint_as_float(v[e]), k, pg.y);
@@ -181,34 +201,36 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
   if (tid == 0) {
     for (int s = 0; s < F::S; ++s) {
       tc::mbar_init(&sm.full[s], 33);     // 32 lanes' scales and the byte count
-      tc::mbar_init(&sm.empty[s], 1 + 4); // the score MMAs; the widening warps
+      tc::mbar_init(&sm.empty[s], 1 + kWidenWarps);   // the score MMAs; the widening warps
     }
     for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(&sm.vfull[i], 4);
+      tc::mbar_init(&sm.vfull[i], kWidenWarps);
       tc::mbar_init(&sm.vfree[i], 1);
       tc::mbar_init(&sm.sfull[i], 1);
-      tc::mbar_init(&sm.pfull[i], 4);
+      tc::mbar_init(&sm.pfull[i], kGroupWarps);
       tc::mbar_init(&sm.ofull[i], 1);
     }
     tc::mbar_init(&sm.qfull, 1);
-    tc::mbar_init(&sm.done, 1);
+    tc::mbar_init(&sm.done, 2);
     tc::mbar_fence_init();
   }
-  if (warp == kMma) tmem_alloc(&sm.tmem, 512);
+  if (warp == kScores) tmem_alloc(&sm.tmem, 512);
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  int t0 = 0, t1 = 0, skip = 0;
+  int t0 = 0, t1 = 0, total = 0, skip = 0;
   Item x{};
   tc::fence_before_sync();
-  locate<NT, kRowsThreads>(p, sm.loc, t0, t1, x, skip);
+  locate<NT, kRowsThreads>(p, sm.loc, t0, t1, total, x, skip);
   tc::fence_after_sync();
   const uint32_t tmem = sm.tmem;
-  if (tid == 0) publish_range(p, x, skip, t0, t1);
+  if (tid == 0) publish_range(p, x, skip, t0, t1, total);
   bool ok = true;   // false after a wait gave up: no further waits, and no further work is issued
   auto wait = [&](uint64_t *bar, int parity) {   // whole warps
     ok = ok && wait_for(bar, parity);
     ok = __all_sync(0xffffffffu, ok);
   };
+  // (in each role's own branch: where branches meet, the smaller share would hold for the code after)
   if (warp == kProducer) {
+    regs_give();
     int it = 0;
     const int per_tile = kTile >> p.a.page_shift;
     for (int t = t0; t < t1 && ok;) {
@@ -255,69 +277,64 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     }
     // the last copies of each stage land before the CTA may end
     for (int k = max(0, it - F::S); k < it; ++k)
-      if (!tc::mbar_wait(&sm.full[k % F::S], (k / F::S) & 1)) ok = false;
-  } else if (warp == kMma) {
-    // the whole warp walks the units, one elected lane issues
+      if (!wait_for(&sm.full[k % F::S], (k / F::S) & 1)) ok = false;
+  } else if (warp == kScores || warp == kValues) {
+    regs_give();
+    // The whole warp walks the units and one elected lane issues. Scores and values have a warp each,
+    // so that one's waiting and issuing hides behind the other's MMAs; scores(u) also waits for
+    // values(u - 2), whose P lies where its scores go.
     constexpr uint32_t id_s = attn_idesc(128, kTile, false);
     constexpr uint32_t id_o = (1u << 4) | (1u << 16) | (static_cast<uint32_t>(D >> 3) << 17) |
                               (static_cast<uint32_t>(128 >> 4) << 24);   // B MN-major
     const uint32_t base = tc::saddr(smem);
-    // unit u of a segment whose first tile is number `it` of the range
-    auto scores = [&](int u, int it, bool last) {
-      const int g = u & 1, tile = it + (F::RTC == 2 ? u >> 1 : u);
-      const uint64_t da = smem_desc<D>(
-          base + F::kOffQ + (F::RTC == 2 ? g * F::kTerms * F::kQBytes : 0), 16, 8 * D);
-      const uint64_t db = smem_desc<D>(base + tile % F::S * 2 * F::kSideBytes, 16, 8 * D);
-      const uint32_t d = tmem + F::kColS + g * 128;
-      if (elect_one()) {
-#pragma unroll
-        for (int term = 0; term < F::kTerms; ++term)
-#pragma unroll
-          for (int kk = 0; kk < D / 32; ++kk)   // 32 dims of e4m3: 32 bytes on
-            mma_f8(d, da + term * (F::kQBytes / 16) + 2 * kk, db + 2 * kk, id_s, (term | kk) != 0);
-        if (last) mma_commit(&sm.empty[tile % F::S]);
-        mma_commit(&sm.sfull[g]);
-      }
-      __syncwarp();
-    };
-    auto values = [&](int u, int it, bool first, bool last) {
-      const int g = u & 1, tile = it + (F::RTC == 2 ? u >> 1 : u);
-      const uint64_t db = smem_desc<128>(base + F::kOffV16 + (tile & 1) * F::kVfBytes,
-                                         D > 64 ? kTile * 128 : 0, 1024);
-      const uint32_t d = tmem + F::kColO + g * D, a = tmem + F::kColS + g * 128;
-      if (elect_one()) {
-#pragma unroll
-        for (int kk = 0; kk < kTile / 16; ++kk)   // 16 tokens: 8 columns of pairs
-          mma_f16_ts(d, a + 8 * kk, db + kk * (16 * 128 / 16), id_o, !(first && kk == 0));
-        if (last) mma_commit(&sm.vfree[tile & 1]);
-        mma_commit(&sm.ofull[g]);
-      }
-      __syncwarp();
-    };
     int it = 0, seg = 0;
-    int uses[2] = {0, 0};   // units of each group so far
+    uint32_t phase = 0;   // bit g: parity of group g's next unit
     for (int t = t0; t < t1 && ok; ++seg) {
       const int cnt = min(x.tiles - skip, t1 - t);
-      wait(&sm.qfull, seg & 1);
-      tc::fence_after_sync();
       const int units = F::RTC * cnt;
-      for (int u = 0; u <= units && ok; ++u) {
-        if (u < units) {
-          const int tile = it + (F::RTC == 2 ? u >> 1 : u);
-          if (F::RTC == 1 || !(u & 1)) wait(&sm.full[tile % F::S], (tile / F::S) & 1);
+      if (warp == kScores) wait(&sm.qfull, seg & 1);
+      for (int u = 0; u < units && ok; ++u) {
+        const int g = u & 1, tile = it + (F::RTC == 2 ? u >> 1 : u);
+        const bool last = F::RTC == 1 || g;   // of the tile's units
+        if (warp == kScores) {
+          if (F::RTC == 1 || !g) ok = ok && wait_for(&sm.full[tile % F::S], (tile / F::S) & 1);
+          wait(&sm.ofull[g], (phase >> g & 1) ^ 1);
           if (!ok) break;
           tc::fence_after_sync();
-          scores(u, it, F::RTC == 1 || (u & 1));
-        }
-        if (u > 0) {
-          const int w = u - 1, g = w & 1, tile = it + (F::RTC == 2 ? w >> 1 : w);
-          if (F::RTC == 1 || !g) wait(&sm.vfull[tile & 1], (tile >> 1) & 1);
-          wait(&sm.pfull[g], uses[g] & 1);
+          const uint64_t da = smem_desc<D>(
+              base + F::kOffQ + (F::RTC == 2 ? g * F::kTerms * F::kQBytes : 0), 16, 8 * D);
+          const uint64_t db = smem_desc<D>(base + tile % F::S * 2 * F::kSideBytes, 16, 8 * D);
+          const uint32_t d = tmem + F::kColS + g * 128;
+          if (elect_one()) {
+#pragma unroll
+            for (int term = 0; term < F::kTerms; ++term)
+#pragma unroll
+              for (int kk = 0; kk < D / 32; ++kk)   // 32 dims of e4m3: 32 bytes on
+                mma_f8(d, da + term * (F::kQBytes / 16) + 2 * kk, db + 2 * kk, id_s,
+                       (term | kk) != 0);
+            if (last) mma_commit(&sm.empty[tile % F::S]);
+            mma_commit(&sm.sfull[g]);
+          }
+        } else {
+          if (F::RTC == 1 || !g) ok = ok && wait_for(&sm.vfull[tile & 1], (tile >> 1) & 1);
+          wait(&sm.pfull[g], phase >> g & 1);
           if (!ok) break;
-          ++uses[g];
           tc::fence_after_sync();
-          values(w, it, w < 2, F::RTC == 1 || g);
+          // (N = D dims: one or two blocks of 64)
+          const uint64_t db = smem_desc<128>(base + F::kOffV16 + (tile & 1) * F::kVfBytes,
+                                             D > 64 ? kTile * 128 : 0, 1024);
+          const uint32_t d = tmem + F::kColO + g * D, a = tmem + F::kColS + g * 128;
+          const uint32_t later = u < 2 ? 0u : 1u;   // the group's first unit of the segment starts O
+          if (elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < kTile / 16; ++kk)   // 16 tokens: 8 columns of pairs
+              mma_f16_ts(d, a + 8 * kk, db + kk * (16 * 128 / 16), id_o, kk ? 1u : later);
+            if (last) mma_commit(&sm.vfree[tile & 1]);
+            mma_commit(&sm.ofull[g]);
+          }
         }
+        __syncwarp();
+        phase ^= 1u << g;
       }
       it += cnt;
       t += cnt;
@@ -327,7 +344,10 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     if (elect_one()) mma_commit(&sm.done);   // every MMA issued has completed before the CTA may end
     if (!wait_for(&sm.done, 0)) ok = false;
     __syncwarp();
+  } else if (warp > kValues) {
+    regs_give();
   } else if (warp >= kWidenWarp) {
+    regs_give();
     const int wtid = tid - 32 * kWidenWarp;
     int it = 0;
     for (int t = t0; t < t1;) {
@@ -339,26 +359,24 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         uint4 w[Widen<D, kWidenThreads>::kSteps];
         fetch_values<D, kWidenThreads>(smem + s * 2 * F::kSideBytes + F::kSideBytes, wtid,
                                        x.end - slot0, w);
-        float ks = 0.f, vs = 0.f;
-        const bool used = wtid < 8 && slot0 + 16 * wtid < x.end;   // else no scale was copied
-        if (used) {
-          ks = sm.ks[s][16 * wtid >> p.a.page_shift];
-          vs = sm.vs[s][16 * wtid >> p.a.page_shift];
-        }
-        wait(&sm.vfree[buf], ((it >> 1) & 1) ^ 1);
-        if (wtid < 4) sm.vnan[buf][wtid] = 0;
-        if (wtid < 8) {
+        float4 page = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (wtid < 8 && slot0 + 16 * wtid < x.end) {   // (else no scale was copied)
+          const float ks = sm.ks[s][16 * wtid >> p.a.page_shift];
+          const float vs = sm.vs[s][16 * wtid >> p.a.page_shift];
           // a NaN scale (a bad page) makes its tokens' scores NaN through log2 vs; 1 / vs multiplies
           // the zero weights of the rows that do not see them too, so it stays finite
           const float vse = vs < kMinValueScale ? kMinValueScale : vs;
-          sm.page[buf][wtid] = used ? make_float4(ks * p.scale2, __log2f(vse),
-                                                  vs == vs ? __frcp_rn(vse) : 1.f, 0.f)
-                                    : make_float4(0.f, 0.f, 0.f, 0.f);
+          page = make_float4(ks * p.scale2, __log2f(vse), vs == vs ? __frcp_rn(vse) : 1.f, 0.f);
         }
-        widen_sync();
-        widen<D, kWidenThreads>(w, smem + F::kOffV16 + buf * F::kVfBytes, wtid, [&](int at) {
-          atomicOr(&sm.vnan[buf][at >> 5], 1u << (at & 31));
-        });
+        wait(&sm.vfree[buf], ((it >> 1) & 1) ^ 1);
+        if (wtid < 8) sm.page[buf][wtid] = page;
+        if (slot0 + kTile > min(x.len, x.end)) {
+          if (wtid < 4) sm.vnan[buf][wtid] = 0;
+          widen_sync();
+          scrub_values<D, kWidenThreads>(
+              w, wtid, [&](int at) { atomicOr(&sm.vnan[buf][at >> 5], 1u << (at & 31)); });
+        }
+        widen<D, kWidenThreads>(w, smem + F::kOffV16 + buf * F::kVfBytes, wtid);
         fence_async();
         __syncwarp();
         if (lane == 0) {
@@ -371,11 +389,18 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       if (t < t1) item_next<NT>(p, x);
     }
   } else {
-    const int grp = warp >> 2, quad = warp & 3;
+    regs_take();
+    const int grp = warp / kGroupWarps, half = warp >> 2 & 1, quad = warp & 3;
     const int lrow = quad * 32 + lane;                        // row of the MMA tile
     const int n = F::RTC == 2 ? grp * 128 + lrow : lrow;      // row of the item's tile
+    const int pair = 4 + grp * 4 + quad;                      // barrier of the two warps with these rows
     const uint32_t tlane = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-    const uint32_t ts = tlane + F::kColS + grp * 128;
+    const uint32_t ts = tlane + F::kColS + grp * 128;         // the row's scores
+    // what the two halves (and, at the end, the groups) of a row tell each other: [group][half][row].
+    // The
+    // queries' place is free once every score has been taken.
+    float *share = reinterpret_cast<float *>(smem + F::kOffQ);
+    float *top = qs + grp * 256;
     int it = 0, use = 0;   // tiles so far; this group's units so far
     for (int t = t0; t < t1;) {
       const int cnt = min(x.tiles - skip, t1 - t);
@@ -384,11 +409,12 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       fence_async();
       rows_sync();
       if (tid == 0) mbar_arrive(&sm.qfull);
-      const long long r = static_cast<long long>(x.rt) * NT + n;
-      const int i = static_cast<int>(r / p.G), gq = static_cast<int>(r - static_cast<long long>(i) * p.G);
+      const unsigned r = static_cast<unsigned>(x.rt) * NT + n;
+      const int i = static_cast<int>(r / p.G), gq = static_cast<int>(r - static_cast<unsigned>(i) * p.G);
       const bool live = i < x.n && x.ok;
       const bool idle = !__any_sync(0xffffffffu, live);   // no row of this warp: nothing to weigh
       const float q = qs[n];
+      rows_sync();   // `top` takes its place
       float nm = kNoRef, l = 0.f;
       const int step = F::RTC == 2 ? 1 : 2;
       const int k0 = F::RTC == 2 ? 0 : grp;
@@ -396,27 +422,32 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         const int tile = it + k, buf = tile & 1;
         const int slot0 = (skip + k) * kTile;
         const bool edge = slot0 + kTile > min(x.len, x.end);
-        uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};
+        uint32_t see[2] = {~0u, ~0u};
         if (edge)
 #pragma unroll
-          for (int w = 0; w < 4; ++w)
-            see[w] = live ? seen_bits(p, x.b, i, slot0 + 32 * w - x.len, x.n) : 0u;
+          for (int w = 0; w < 2; ++w)
+            see[w] = live ? seen_bits(p, x.b, i, slot0 + 64 * half + 32 * w - x.len, x.n) : 0u;
         wait(&sm.vfull[buf], (tile >> 1) & 1);   // its page scales and NaN marks
-        uint32_t nan[4];
-        *reinterpret_cast<uint4 *>(nan) = *reinterpret_cast<const uint4 *>(sm.vnan[buf]);
-        const bool masked = edge || (nan[0] | nan[1] | nan[2] | nan[3]) != 0;
-        const float4 *page = sm.page[buf];
+        uint32_t nan[2] = {0, 0};
+        if (edge) {
+          nan[0] = sm.vnan[buf][2 * half];
+          nan[1] = sm.vnan[buf][2 * half + 1];
+        }
+        const float4 *page = sm.page[buf] + 4 * half;
         wait(&sm.sfull[grp], use & 1);
         tc::fence_after_sync();
         if (!idle) {
-          uint32_t h[64];
+          uint32_t h[32];
           float sum = 0.f;
           bool fresh = __any_sync(0xffffffffu, nm == kNoRef);   // a row's first tile, mostly
 #pragma unroll 1
           for (;;) {
-            if (fresh) {   // new references
-              const float m = masked ? row_maximum<true>(ts, page, q, see)
-                                     : row_maximum<false>(ts, page, q, see);
+            if (fresh) {   // new references: the larger of the halves' maxima
+              const float mine = edge ? row_maximum<true>(ts + 64 * half, page, q, see)
+                                      : row_maximum<false>(ts + 64 * half, page, q, see);
+              top[half * 128 + lrow] = mine;
+              pair_any(pair, false);
+              const float m = fmaxf(mine, top[(half ^ 1) * 128 + lrow]);
               const bool grow = m + nm > kTrigger;
               const float now = grow ? kBias - m : nm;
               const float f = grow ? ex2(now - nm) : 1.f;   // 2^(m_old - m_new)
@@ -424,7 +455,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
               l *= f;
               if (k > k0)   // the group's earlier value MMAs completed before these scores
 #pragma unroll 1
-                for (int c = 0; c < D; c += 16) {
+                for (int c = half * (D / 2); c < half * (D / 2) + D / 2; c += 16) {
                   uint32_t o[16];
                   tmem_ld(tlane + F::kColO + grp * D + c, o);
                   tmem_wait(o);
@@ -433,18 +464,19 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
                   tmem_st(tlane + F::kColO + grp * D + c, o);
                 }
             }
-            const float big = masked ? row_weights<true>(ts, page, q, nm, see, nan, h, sum)
-                                     : row_weights<false>(ts, page, q, nm, see, nan, h, sum);
-            if (fresh || !__any_sync(0xffffffffu, big > kTrigger)) break;
+            const float big = edge ? row_weights<true>(ts + 64 * half, page, q, nm, see, nan, h, sum)
+                                   : row_weights<false>(ts + 64 * half, page, q, nm, see, nan, h, sum);
+            // (also: both halves have read their scores, which P is about to overwrite)
+            if (!pair_any(pair, !fresh && big > kTrigger)) break;
             fresh = true;
           }
           l += sum;
 #pragma unroll
-          for (int c = 0; c < 64; c += 16) {
+          for (int c = 0; c < 32; c += 16) {
             uint32_t v[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) v[e] = h[c + e];
-            tmem_st(ts + c, v);
+            tmem_st(ts + 32 * half + c, v);
           }
           asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         }
@@ -458,29 +490,31 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       const long long part = 2LL * blockIdx.x + (skip == 0 ? 1 : 0);
       if (use > 0) wait(&sm.ofull[grp], (use - 1) & 1);
       tc::fence_after_sync();
+      rows_sync();   // every MMA of the item has completed: the queries' place is free
+      float *mine = share + (grp * 2 + half) * 256;
+      mine[lrow] = l;
+      mine[128 + lrow] = nm;
+      rows_sync();
+      auto sum_of = [&](int g) { return share[g * 512 + lrow] + share[g * 512 + 256 + lrow]; };
       float f0 = 0.f, f1 = 0.f;   // what the accumulator(s) are multiplied by
       float lse2;
       if constexpr (F::RTC == 2) {
-        lse2 = l == 0.f ? -INFINITY : log2f(l) - nm;
-        f0 = l == 0.f ? 0.f : 1.f / l;
+        const float total = sum_of(grp);
+        lse2 = total == 0.f ? -INFINITY : log2f(total) - nm;
+        f0 = total == 0.f ? 0.f : 1.f / total;
       } else {
-        float *merge = qs + NT;   // [group][reference, sum][row]
-        merge[grp * 256 + lrow] = nm;
-        merge[grp * 256 + 128 + lrow] = l;
-        rows_sync();   // and both groups' value MMAs have completed
-        tc::fence_after_sync();
-        const float nmo = merge[(grp ^ 1) * 256 + lrow], lo = merge[(grp ^ 1) * 256 + 128 + lrow];
-        const float m = fminf(nm, nmo);   // -m of the larger reference
-        const float w = ex2(m - nm), wo = ex2(m - nmo);
-        const float total = grp ? lo * wo + l * w : l * w + lo * wo;
+        const float n0 = share[128 + lrow], n1 = share[512 + 128 + lrow];
+        const float l0 = sum_of(0), l1 = sum_of(1);
+        const float m = fminf(n0, n1);   // -m of the larger reference
+        const float w0 = ex2(m - n0), w1 = ex2(m - n1);
+        const float total = l0 * w0 + l1 * w1;
         const float inv = total == 0.f ? 0.f : 1.f / total;
         lse2 = total == 0.f ? -INFINITY : log2f(total) - m;
-        const float fm = l == 0.f ? 0.f * inv : w * inv, fo = lo == 0.f ? 0.f * inv : wo * inv;
-        f0 = grp ? fo : fm;
-        f1 = grp ? fm : fo;
+        f0 = l0 == 0.f ? 0.f * inv : w0 * inv;   // (0 NaN is NaN)
+        f1 = l1 == 0.f ? 0.f * inv : w1 * inv;
       }
       if (!x.ok) lse2 = f0 = NAN;
-      if (i < p.a.N && (F::RTC == 2 || grp == 0)) {
+      if (i < p.a.N && half == 0 && (F::RTC == 2 || grp == 0)) {
         if (!whole)
           p.part_lse[part * NT + n] = lse2;
         else if (p.lse)
@@ -488,14 +522,15 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
                 static_cast<long long>(x.h) * p.G + gq] = live || !x.ok ? lse2 * kLn2 : -INFINITY;
       }
       const bool zero = x.ok && !live;   // padding
-      // both groups' halves of the dims when they share rows, else all of the group's own
-      const int d0 = F::RTC == 2 ? 0 : grp * (D / 2), d1 = F::RTC == 2 ? D : d0 + D / 2;
+      // the dims shared out over the warps with these rows: two, or four when the groups share them
+      constexpr int kDims = F::RTC == 2 ? D / 2 : D / 4;
+      const int d0 = (F::RTC == 2 ? half : grp * 2 + half) * kDims;
       using T = typename F::T;
       T *out = static_cast<T *>(p.out) + ((static_cast<long long>(x.b) * p.a.N + i) * p.a.Hq +
                                           static_cast<long long>(x.h) * p.G + gq) * D;
       float *po = p.part_o + (part * NT + n) * D;
 #pragma unroll 1
-      for (int c = d0; c < d1; c += 16) {
+      for (int c = d0; c < d0 + kDims; c += 16) {
         uint32_t o[16], o1[16];
         tmem_ld(tlane + F::kColO + (F::RTC == 2 ? grp * D : 0) + c, o);
         if (F::RTC == 1) tmem_ld(tlane + F::kColO + D + c, o1);
@@ -525,7 +560,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       }
       if (!x.ok && tid == 0) set_status(p.a.status, SPEC_ERR_LENGTH);
       tc::fence_before_sync();
-      rows_sync();   // every accumulator is read and every score MMA done before the next item
+      rows_sync();   // every accumulator and `share` are read before the next item writes
       t += cnt;
       skip = 0;
       if (t < t1) item_next<NT>(p, x);
@@ -534,7 +569,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
   if (!ok) set_status(p.a.status, SPEC_ERR_TIMEOUT);
   tc::fence_before_sync();
   __syncthreads();
-  if (warp == kMma) {
+  if (warp == kScores) {
     tc::fence_after_sync();
     tmem_free(tmem, 512);
   }

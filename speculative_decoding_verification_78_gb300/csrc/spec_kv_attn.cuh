@@ -144,9 +144,14 @@ __device__ __forceinline__ bool elect_one() {
       : "=r"(r));
   return r != 0;
 }
-// tc::mbar_wait whose usual case, a phase that has completed, costs no call
+// tc::mbar_wait in line: no call, whose registers would be kept free around every wait
 __device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity) {
-  return tc::mbar_try(bar, parity) || tc::mbar_wait(bar, parity);
+  if (tc::mbar_try(bar, parity)) return true;
+  const unsigned long long t0 = tc::now_ns();
+#pragma unroll 1
+  while (!tc::mbar_try(bar, parity))
+    if (tc::now_ns() - t0 > tc::kWaitNs) return false;
+  return true;
 }
 __device__ __forceinline__ void fence_async() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -190,10 +195,10 @@ template <int NT>
 __device__ __forceinline__ int item_end(const AttnArgs &p, int len, int n, bool ok, int rt) {
   if (!ok || n == 0) return 0;
   if (p.RT == 1 || p.a.mask) return len + n;
-  const long long first = static_cast<long long>(rt) * NT / p.G;
+  const int first = static_cast<int>(static_cast<unsigned>(rt) * NT / p.G);
   if (first >= n) return 0;   // padding
-  const long long last = (static_cast<long long>(rt) * NT + NT - 1) / p.G;
-  return len + static_cast<int>(last + 1 < n ? last + 1 : n);
+  const int last = static_cast<int>((static_cast<unsigned>(rt) * NT + NT - 1) / p.G);
+  return len + min(last + 1, n);
 }
 __device__ __forceinline__ int tiles_for(int end) { return end > kTile ? (end + kTile - 1) / kTile : 1; }
 
@@ -223,8 +228,12 @@ __device__ __forceinline__ void item_next(const AttnArgs &p, Item &x) {
   }
   if (x.b < p.a.B) item_load<NT>(p, x);
 }
-__device__ __forceinline__ int range_start(long long T, int c, int G) {
-  return static_cast<int>(T * c / G);
+// Range c of G of a line of T tiles begins at floor(T c / G); range_of: the range that holds tile t.
+__device__ __forceinline__ int range_start(int T, int c, int G) {
+  return static_cast<int>(static_cast<unsigned long long>(T) * c / G);
+}
+__device__ __forceinline__ int range_of(int T, int t, int G) {
+  return static_cast<int>((static_cast<unsigned long long>(t + 1) * G + T - 1) / T) - 1;
 }
 
 // The CTA's range [t0, t1) of the line and its first item; called by all threads. Thread t sums
@@ -234,7 +243,8 @@ struct LocateScratch {
   int warp_sum[20];
 };
 template <int NT, int kThreads>
-__device__ void locate(const AttnArgs &p, LocateScratch &sm, int &t0, int &t1, Item &x, int &skip) {
+__device__ void locate(const AttnArgs &p, LocateScratch &sm, int &t0, int &t1, int &total, Item &x,
+                       int &skip) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int share = (p.a.B + kThreads - 1) / kThreads;
   const int lo = min(p.a.B, tid * share), hi = min(p.a.B, lo + share);
@@ -248,7 +258,8 @@ __device__ void locate(const AttnArgs &p, LocateScratch &sm, int &t0, int &t1, I
   }
   if (lane == 31) sm.warp_sum[warp] = incl;
   __syncthreads();
-  int before = 0, total = 0;
+  int before = 0;
+  total = 0;
 #pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) {
     if (w < warp) before += sm.warp_sum[w];
@@ -283,11 +294,11 @@ __device__ void locate(const AttnArgs &p, LocateScratch &sm, int &t0, int &t1, I
   }
 }
 // What the join needs to know of the CTA's range: its first item and the item's tiles before it,
-// the item's tiles, and the range.
+// the item's tiles, the range, and the length of the line.
 __device__ __forceinline__ void publish_range(const AttnArgs &p, const Item &x, int skip, int t0,
-                                              int t1) {
+                                              int t1, int total) {
   if (t0 < t1) p.start[blockIdx.x] = make_int4(x.b, x.h, x.rt, skip);
-  p.start[gridDim.x + blockIdx.x] = make_int4(t0 < t1 ? x.tiles : 0, t0, t1, 0);
+  p.start[gridDim.x + blockIdx.x] = make_int4(t0 < t1 ? x.tiles : 0, t0, t1, total);
 }
 
 // ------------------------------------------------------------------ operands
@@ -300,43 +311,52 @@ template <typename T, int D, int NT, int kBlock, int kTerms, int kThreads>
 __device__ __forceinline__ void load_queries(const AttnArgs &p, const Item &x, int tid, uint8_t *sq,
                                              float *qs) {
   constexpr int kLanes = D / 8, kRows = kThreads / kLanes;
+  constexpr int kSteps = (NT + kRows - 1) / kRows, kAhead = kSteps < 4 ? kSteps : 4;
   const int sub = tid % kLanes, row0 = tid / kLanes;
-#pragma unroll 4
-  for (int n0 = 0; n0 < NT; n0 += kRows) {
-    const int n = n0 + row0;
-    if (n >= NT) break;   // whole warps: a warp's rows are 2 or 4
-    const long long r = static_cast<long long>(x.rt) * NT + n;
-    const int i = static_cast<int>(r / p.G), g = static_cast<int>(r - static_cast<long long>(i) * p.G);
-    float f[8];
-    if (i < x.n && x.ok) {
-      const T *src = static_cast<const T *>(p.q) +
-                     (static_cast<long long>(x.b) * p.a.N + i) * p.q_stride +
-                     (static_cast<long long>(x.h) * p.G + g) * D + sub * 8;
-      vec_to_floats<T>(__ldg(reinterpret_cast<const uint4 *>(src)), f);
-    } else {
+  const T *base = static_cast<const T *>(p.q) +
+                  static_cast<long long>(x.b) * p.a.N * p.q_stride +
+                  static_cast<long long>(x.h) * p.G * D + sub * 8;
+#pragma unroll 1
+  for (int n0 = row0; n0 < NT; n0 += kAhead * kRows) {   // whole warps: a warp's rows are 2 or 4
+    uint4 raw[kAhead];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = 0.f;
+    for (int u = 0; u < kAhead; ++u) {
+      const int n = n0 + u * kRows;
+      const unsigned r = static_cast<unsigned>(x.rt) * NT + n;
+      const unsigned i = r / p.G, g = r - i * p.G;
+      raw[u] = make_uint4(0, 0, 0, 0);
+      if (n < NT && static_cast<int>(i) < x.n && x.ok)
+        raw[u] = __ldg(reinterpret_cast<const uint4 *>(
+            base + static_cast<long long>(i) * p.q_stride + static_cast<long long>(g) * D));
     }
-    float m = 0.f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) m = fmax_nan(m, fabsf(f[e]));
+    for (int u = 0; u < kAhead; ++u) {
+      const int n = n0 + u * kRows;
+      if (n >= NT) break;
+      float f[8];
+      vec_to_floats<T>(raw[u], f);
+      float m = 0.f;
 #pragma unroll
-    for (int o = kLanes / 2; o > 0; o >>= 1) m = fmax_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const int e = max(static_cast<int>(__float_as_uint(m) >> 23), 27);   // exponent, at least -100
-    const float mul = __uint_as_float(static_cast<uint32_t>(127 + 127 + 7 - e) << 23);
-    if (sub == 0) qs[n] = m < INFINITY ? __uint_as_float(static_cast<uint32_t>(e - 7) << 23) : NAN;
+      for (int e = 0; e < 8; ++e) m = fmax_nan(m, fabsf(f[e]));
 #pragma unroll
-    for (int k = 0; k < 8; ++k) f[k] *= mul;
-    uint8_t *blk = sq + n / kBlock * (kTerms * kBlock * D);
+      for (int o = kLanes / 2; o > 0; o >>= 1) m = fmax_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+      const int e = max(static_cast<int>(__float_as_uint(m) >> 23), 27);   // exponent, at least -100
+      const float mul = __uint_as_float(static_cast<uint32_t>(127 + 127 + 7 - e) << 23);
+      if (sub == 0)
+        qs[n] = m < INFINITY ? __uint_as_float(static_cast<uint32_t>(e - 7) << 23) : NAN;
 #pragma unroll
-    for (int t = 0; t < kTerms; ++t) {
-      const uint2 w = floats_to_e4m3(f, 1.f);
-      *reinterpret_cast<uint2 *>(blk + t * (kBlock * D) + swz<D>(n % kBlock * D + sub * 8)) = w;
-      if (t + 1 < kTerms) {
-        float g8[8];
-        e4m3_to_floats(w, g8);
+      for (int k = 0; k < 8; ++k) f[k] *= mul;
+      uint8_t *blk = sq + n / kBlock * (kTerms * kBlock * D);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) f[k] -= g8[k];   // exact
+      for (int t = 0; t < kTerms; ++t) {
+        const uint2 w = floats_to_e4m3(f, 1.f);
+        *reinterpret_cast<uint2 *>(blk + t * (kBlock * D) + swz<D>(n % kBlock * D + sub * 8)) = w;
+        if (t + 1 < kTerms) {
+          float g8[8];
+          e4m3_to_floats(w, g8);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) f[k] -= g8[k];   // exact
+        }
       }
     }
   }
@@ -362,32 +382,39 @@ __device__ __forceinline__ void fetch_values(const uint8_t *sv, int gtid, int va
 __device__ __forceinline__ uint32_t nan_codes(uint32_t w) {   // bit 7 of each NaN byte
   return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
 }
-// The values as fp16 rows of 64 dims (128 bytes, swizzled). NaN codes become zero and mark their
-// token: the weights of the rows that see it then turn NaN instead (a NaN operand would reach the
-// rows that do not): `mark`(token) is called for each.
+// NaN codes made zero; `mark`(token) is called for each token that had one. Returns whether any had.
+// For tiles that not every row sees whole: there the weights of the rows that do see such a token are
+// made NaN instead, since a NaN operand would reach the rows that do not (0 NaN is NaN). Where every
+// row sees every token the operand may stay NaN.
 template <int D, int kThreads, typename Mark>
-__device__ __forceinline__ bool widen(uint4 (&w)[Widen<D, kThreads>::kSteps], uint8_t *out, int gtid,
-                                      Mark mark) {
+__device__ __forceinline__ bool scrub_values(uint4 (&w)[Widen<D, kThreads>::kSteps], int gtid,
+                                             Mark mark) {
   using W = Widen<D, kThreads>;
-  const int c = gtid % W::kLanes, row0 = gtid / W::kLanes;
   uint32_t any = 0;
 #pragma unroll
   for (int u = 0; u < W::kSteps; ++u)
     any |= nan_codes(w[u].x) | nan_codes(w[u].y) | nan_codes(w[u].z) | nan_codes(w[u].w);
-  if (any) {
+  if (!any) return false;
 #pragma unroll
-    for (int u = 0; u < W::kSteps; ++u) {
-      const uint32_t hx = nan_codes(w[u].x), hy = nan_codes(w[u].y), hz = nan_codes(w[u].z),
-                     hw = nan_codes(w[u].w);
-      w[u].x &= ~((hx >> 7) * 255u);
-      w[u].y &= ~((hy >> 7) * 255u);
-      w[u].z &= ~((hz >> 7) * 255u);
-      w[u].w &= ~((hw >> 7) * 255u);
-      if (hx | hy | hz | hw) mark(u * W::kRows + row0);
-    }
+  for (int u = 0; u < W::kSteps; ++u) {
+    const uint32_t hx = nan_codes(w[u].x), hy = nan_codes(w[u].y), hz = nan_codes(w[u].z),
+                   hw = nan_codes(w[u].w);
+    w[u].x &= ~((hx >> 7) * 255u);
+    w[u].y &= ~((hy >> 7) * 255u);
+    w[u].z &= ~((hz >> 7) * 255u);
+    w[u].w &= ~((hw >> 7) * 255u);
+    if (hx | hy | hz | hw) mark(u * W::kRows + gtid / W::kLanes);
   }
-  // 64 dims (4 lanes) a block of kTile rows; the second block's lanes store their halves the other
-  // way round, so that eight neighbours never meet in a bank
+  return true;
+}
+// The values as fp16 rows of 64 dims (128 bytes, swizzled): 64 dims (4 lanes) a block of kTile rows;
+// the second block's lanes store their halves the other way round, so that eight neighbours never
+// meet in a bank.
+template <int D, int kThreads>
+__device__ __forceinline__ void widen(const uint4 (&w)[Widen<D, kThreads>::kSteps], uint8_t *out,
+                                      int gtid) {
+  using W = Widen<D, kThreads>;
+  const int c = gtid % W::kLanes, row0 = gtid / W::kLanes;
   uint8_t *blk = out + (c >> 2) * (kTile * 128);
   const bool flip = (c >> 2) & 1;
 #pragma unroll
@@ -401,74 +428,87 @@ __device__ __forceinline__ bool widen(uint4 (&w)[Widen<D, kThreads>::kSteps], ui
     *reinterpret_cast<uint4 *>(blk + (flip ? a1 : a0)) = flip ? hi : lo;
     *reinterpret_cast<uint4 *>(blk + (flip ? a0 : a1)) = flip ? lo : hi;
   }
-  return any != 0;
 }
 
 // ------------------------------------------------------------------ the join
 
-// Joins the parts of the items that cross ranges. Block (c, rows): the item that range c begins
-// inside of, if c is the first range to do so; one warp per row.
+// Joins the parts of the items that cross ranges, in the order of the line. Block (c, rows): the item
+// that range c begins inside of, if c is the first range to do so; one warp per row. The ranges are
+// arithmetic, so every load but the first two waits for nothing but those.
 template <typename T, int D, int NT>
 __global__ void __launch_bounds__(256) kv_attention_join(const __grid_constant__ AttnArgs p,
                                                          int ctas) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  constexpr int kBlocks = NT / 8;
+  constexpr int kBlocks = NT / 8, E = D / 32;
   const int c = 1 + blockIdx.x / kBlocks;
   const int n = (blockIdx.x % kBlocks) * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   // (written by other CTAs: read from L2)
-  auto empty = [&](int at) {
-    const int4 e = __ldcg(p.start + at);
-    return e.y >= e.z;
-  };
-  const int4 d = __ldcg(p.start + ctas + c);           // tiles of its first item, t0, t1
-  if (d.y >= d.z) return;
-  const int4 s = __ldcg(p.start + c);
-  const int begin = d.y - s.w, end = begin + d.x;   // the item's tiles on the line
-  if (s.w == 0) return;
-  // the range with the tile before: the item's first part, or another block's item
-  int first = c - 1;   // (ranges may be empty when there are few tiles)
-  while (empty(ctas + first)) --first;
-  if (begin < __ldcg(p.start + ctas + first).y) return;
-  const long long r = static_cast<long long>(s.z) * NT + n;
-  const int i = static_cast<int>(r / p.G), g = static_cast<int>(r - static_cast<long long>(i) * p.G);
+  const int4 s = __ldcg(p.start + c);          // its first item: b, h, row tile, tiles before
+  const int4 d = __ldcg(p.start + ctas + c);   // that item's tiles, t0, t1, all tiles
+  if (d.y >= d.z || s.w == 0) return;
+  const int total = d.w, begin = d.y - s.w, end = begin + d.x;   // the item's tiles on the line
+  const int first = range_of(total, begin, ctas);
+  // with fewer tiles than ranges each part is a tile
+  const int parts = total >= ctas ? range_of(total, end - 1, ctas) - first + 1 : d.x;
+  auto cta = [&](int k) { return total >= ctas ? first + k : range_of(total, begin + k, ctas); };
+  if (c != cta(1)) return;   // another block's
+  const unsigned r = static_cast<unsigned>(s.z) * NT + n;
+  const int i = static_cast<int>(r / p.G), g = static_cast<int>(r - static_cast<unsigned>(i) * p.G);
   if (i >= p.a.N) return;
-  float m = -INFINITY;
-  for (int k = first; k < ctas; ++k) {
-    const int4 e = __ldcg(p.start + ctas + k);
-    if (e.y >= end) break;
-    if (e.y >= e.z) continue;
-    m = fmax_nan(m, __ldcg(p.part_lse + (2LL * k + (k == first ? 1 : 0)) * NT + n));
-  }
-  constexpr int E = D / 32;
-  float acc[E], sum = 0.f;
+  int len, nn;
+  const bool pad = kv_lengths(p.a, s.x, len, nn) && i >= nn;
+  float m = -INFINITY, sum = 0.f, acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
-  if (m != -INFINITY)
-    for (int k = first; k < ctas; ++k) {
-      const int4 e = __ldcg(p.start + ctas + k);
-      if (e.y >= end) break;
-      if (e.y >= e.z) continue;
-      const long long part = (2LL * k + (k == first ? 1 : 0)) * NT + n;
-      const float w = ex2(__ldcg(p.part_lse + part) - m);
-      sum += w;
-      const float *o = p.part_o + part * D + lane * E;
-#pragma unroll
-      for (int q = 0; q < E; ++q) acc[q] = __fmaf_rn(w, __ldcg(o + q), acc[q]);
+  for (int k0 = 0; k0 < parts; k0 += 32) {   // 32 parts at a time, a lane each for their weights
+    const int k = k0 + lane;
+    long long part = 0;
+    float v = -INFINITY;
+    if (k < parts) {
+      part = (2LL * cta(k) + (k == 0 ? 1 : 0)) * NT + n;
+      v = __ldcg(p.part_lse + part);
     }
-  int len, nn;
-  const bool ok = kv_lengths(p.a, s.x, len, nn);
-  const bool pad = ok && i >= nn;
-  const float f = pad || m == -INFINITY ? 0.f : 1.f / sum;
+    float top = v;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmax_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+    top = fmax_nan(top, m);
+    const float ref = top == -INFINITY ? 0.f : top;
+    const float w = ex2(v - ref), old = ex2(m - ref);
+    m = top;
+    float s32 = w;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s32 += __shfl_xor_sync(0xffffffffu, s32, o);
+    sum = sum * old + s32;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] *= old;
+    const int cnt = min(32, parts - k0);
+#pragma unroll 4
+    for (int j = 0; j < cnt; ++j) {
+      const float wj = __shfl_sync(0xffffffffu, w, j);
+      const float *o = p.part_o + __shfl_sync(0xffffffffu, part, j) * D + lane * E;
+      if constexpr (E == 4) {
+        const float4 q = __ldcg(reinterpret_cast<const float4 *>(o));
+        acc[0] = __fmaf_rn(wj, q.x, acc[0]);
+        acc[1] = __fmaf_rn(wj, q.y, acc[1]);
+        acc[2] = __fmaf_rn(wj, q.z, acc[2]);
+        acc[3] = __fmaf_rn(wj, q.w, acc[3]);
+      } else {
+        const float2 q = __ldcg(reinterpret_cast<const float2 *>(o));
+        acc[0] = __fmaf_rn(wj, q.x, acc[0]);
+        acc[1] = __fmaf_rn(wj, q.y, acc[1]);
+      }
+    }
+  }
+  const bool none = pad || m == -INFINITY;
+  const float f = 1.f / sum;
   const long long at = (static_cast<long long>(s.x) * p.a.N + i) * p.a.Hq +
                        static_cast<long long>(s.y) * p.G + g;
   T *o = static_cast<T *>(p.out) + at * D + lane * E;
 #pragma unroll
   for (int q = 0; q < E; q += 2)
-    *reinterpret_cast<uint32_t *>(o + q) =
-        pad ? 0u : pack_pair(acc[q] * f, acc[q + 1] * f, T());
-  if (p.lse && lane == 0)
-    p.lse[at] = pad || m == -INFINITY ? -INFINITY : (m + log2f(sum)) * kLn2;
+    *reinterpret_cast<uint32_t *>(o + q) = none ? 0u : pack_pair(acc[q] * f, acc[q + 1] * f, T());
+  if (p.lse && lane == 0) p.lse[at] = none ? -INFINITY : (m + log2f(sum)) * kLn2;
 }
 
 // ------------------------------------------------------------------ launch
