@@ -17,7 +17,7 @@
 // step apart, so that the tensor cores have one group's
 // MMAs while the other group exponentiates: with more than 128 rows each group has 128 rows of its
 // own and both take every tile; with fewer, the groups take the tiles in turn and are joined at the
-// end of the item. Unit u of a segment belongs to group u & 1; one warp issues the scores, another the values.
+// end of the item. Unit u of a segment belongs to group u & 1; 
 //
 // What bounds it: a 256-row tile of 128 tokens (D = 128) is 2048 clocks of MMA (two e4m3 terms cost
 // what one 16-bit operand would) and 1024 of ex2.
@@ -34,9 +34,8 @@ constexpr int kSoftWarps = 2 * kGroupWarps;
 constexpr int kSoftThreads = 32 * kSoftWarps;
 constexpr int kWidenWarp = kSoftWarps, kWidenWarps = 8;   // warps that widen V
 constexpr int kWidenThreads = 32 * kWidenWarps;
-constexpr int kProducer = kWidenWarp + kWidenWarps;       // copies; then the two MMA warps
-constexpr int kScores = kProducer + 1, kValues = kProducer + 2;
-constexpr int kRowsThreads = 32 * (kValues + 2);   // one idle warp: register shares go by four warps
+constexpr int kProducer = kWidenWarp + kWidenWarps, kMma = kProducer + 1;
+constexpr int kRowsThreads = 32 * (kMma + 3);   // two idle warps: register shares go by four warps
 constexpr float kBias = 8.f;        // a new reference puts the row's largest weight at 2^8 ...
 constexpr float kTrigger = 15.f;    // ... and is taken when one exceeds 2^15 (fp16 ends at 2^16)
 
@@ -211,10 +210,10 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       tc::mbar_init(&sm.ofull[i], 1);
     }
     tc::mbar_init(&sm.qfull, 1);
-    tc::mbar_init(&sm.done, 2);
+    tc::mbar_init(&sm.done, 1);
     tc::mbar_fence_init();
   }
-  if (warp == kScores) tmem_alloc(&sm.tmem, 512);
+  if (warp == kMma) tmem_alloc(&sm.tmem, 512);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   int t0 = 0, t1 = 0, total = 0, skip = 0;
   Item x{};
@@ -278,63 +277,67 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     // the last copies of each stage land before the CTA may end
     for (int k = max(0, it - F::S); k < it; ++k)
       if (!wait_for(&sm.full[k % F::S], (k / F::S) & 1)) ok = false;
-  } else if (warp == kScores || warp == kValues) {
+  } else if (warp == kMma) {
     regs_give();
-    // The whole warp walks the units and one elected lane issues. Scores and values have a warp each,
-    // so that one's waiting and issuing hides behind the other's MMAs; scores(u) also waits for
-    // values(u - 2), whose P lies where its scores go.
+    // The whole warp walks the units and one elected lane issues. values(u) is followed at once by
+    // scores(u + 2), whose scores go where values(u)'s P lies: MMAs run in the order of their issue,
+    // so a group's turn costs one hand-over in each direction.
     constexpr uint32_t id_s = attn_idesc(128, kTile, false);
     constexpr uint32_t id_o = (1u << 4) | (1u << 16) | (static_cast<uint32_t>(D >> 3) << 17) |
                               (static_cast<uint32_t>(128 >> 4) << 24);   // B MN-major
     const uint32_t base = tc::saddr(smem);
     int it = 0, seg = 0;
     uint32_t phase = 0;   // bit g: parity of group g's next unit
+    auto scores = [&](int u) {
+      const int g = u & 1, tile = it + (F::RTC == 2 ? u >> 1 : u);
+      if (F::RTC == 1 || !g) wait(&sm.full[tile % F::S], (tile / F::S) & 1);
+      if (!ok) return;
+      tc::fence_after_sync();
+      const uint64_t da = smem_desc<D>(
+          base + F::kOffQ + (F::RTC == 2 ? g * F::kTerms * F::kQBytes : 0), 16, 8 * D);
+      const uint64_t db = smem_desc<D>(base + tile % F::S * 2 * F::kSideBytes, 16, 8 * D);
+      const uint32_t d = tmem + F::kColS + g * 128;
+      if (elect_one()) {
+#pragma unroll
+        for (int term = 0; term < F::kTerms; ++term)
+#pragma unroll
+          for (int kk = 0; kk < D / 32; ++kk)   // 32 dims of e4m3: 32 bytes on
+            mma_f8(d, da + term * (F::kQBytes / 16) + 2 * kk, db + 2 * kk, id_s, (term | kk) != 0);
+        mma_commit(&sm.sfull[g]);
+        if (F::RTC == 1 || g) mma_commit(&sm.empty[tile % F::S]);
+      }
+      __syncwarp();
+    };
+    auto values = [&](int u) {
+      const int g = u & 1, tile = it + (F::RTC == 2 ? u >> 1 : u);
+      wait(&sm.pfull[g], phase >> g & 1);
+      if (F::RTC == 1 || !g) wait(&sm.vfull[tile & 1], (tile >> 1) & 1);
+      if (!ok) return;
+      phase ^= 1u << g;
+      tc::fence_after_sync();
+      // (N = D dims: one or two blocks of 64)
+      const uint64_t db = smem_desc<128>(base + F::kOffV16 + (tile & 1) * F::kVfBytes,
+                                         D > 64 ? kTile * 128 : 0, 1024);
+      const uint32_t d = tmem + F::kColO + g * D, a = tmem + F::kColS + g * 128;
+      const uint32_t later = u < 2 ? 0u : 1u;   // the group's first unit of the segment starts O
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < kTile / 16; ++kk)   // 16 tokens: 8 columns of pairs
+          mma_f16_ts(d, a + 8 * kk, db + kk * (16 * 128 / 16), id_o, kk ? 1u : later);
+        if (F::RTC == 1 || g) mma_commit(&sm.vfree[tile & 1]);
+        mma_commit(&sm.ofull[g]);
+      }
+      __syncwarp();
+    };
     for (int t = t0; t < t1 && ok; ++seg) {
       const int cnt = min(x.tiles - skip, t1 - t);
       const int units = F::RTC * cnt;
-      if (warp == kScores) wait(&sm.qfull, seg & 1);
+      wait(&sm.qfull, seg & 1);
+      if (ok) scores(0);
+      if (ok && units > 1) scores(1);
       for (int u = 0; u < units && ok; ++u) {
-        const int g = u & 1, tile = it + (F::RTC == 2 ? u >> 1 : u);
-        const bool last = F::RTC == 1 || g;   // of the tile's units
-        if (warp == kScores) {
-          if (F::RTC == 1 || !g) ok = ok && wait_for(&sm.full[tile % F::S], (tile / F::S) & 1);
-          wait(&sm.ofull[g], (phase >> g & 1) ^ 1);
-          if (!ok) break;
-          tc::fence_after_sync();
-          const uint64_t da = smem_desc<D>(
-              base + F::kOffQ + (F::RTC == 2 ? g * F::kTerms * F::kQBytes : 0), 16, 8 * D);
-          const uint64_t db = smem_desc<D>(base + tile % F::S * 2 * F::kSideBytes, 16, 8 * D);
-          const uint32_t d = tmem + F::kColS + g * 128;
-          if (elect_one()) {
-#pragma unroll
-            for (int term = 0; term < F::kTerms; ++term)
-#pragma unroll
-              for (int kk = 0; kk < D / 32; ++kk)   // 32 dims of e4m3: 32 bytes on
-                mma_f8(d, da + term * (F::kQBytes / 16) + 2 * kk, db + 2 * kk, id_s,
-                       (term | kk) != 0);
-            if (last) mma_commit(&sm.empty[tile % F::S]);
-            mma_commit(&sm.sfull[g]);
-          }
-        } else {
-          if (F::RTC == 1 || !g) ok = ok && wait_for(&sm.vfull[tile & 1], (tile >> 1) & 1);
-          wait(&sm.pfull[g], phase >> g & 1);
-          if (!ok) break;
-          tc::fence_after_sync();
-          // (N = D dims: one or two blocks of 64)
-          const uint64_t db = smem_desc<128>(base + F::kOffV16 + (tile & 1) * F::kVfBytes,
-                                             D > 64 ? kTile * 128 : 0, 1024);
-          const uint32_t d = tmem + F::kColO + g * D, a = tmem + F::kColS + g * 128;
-          const uint32_t later = u < 2 ? 0u : 1u;   // the group's first unit of the segment starts O
-          if (elect_one()) {
-#pragma unroll
-            for (int kk = 0; kk < kTile / 16; ++kk)   // 16 tokens: 8 columns of pairs
-              mma_f16_ts(d, a + 8 * kk, db + kk * (16 * 128 / 16), id_o, kk ? 1u : later);
-            if (last) mma_commit(&sm.vfree[tile & 1]);
-            mma_commit(&sm.ofull[g]);
-          }
-        }
-        __syncwarp();
-        phase ^= 1u << g;
+        values(u);
+        if (ok && u + 2 < units) scores(u + 2);
       }
       it += cnt;
       t += cnt;
@@ -344,7 +347,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     if (elect_one()) mma_commit(&sm.done);   // every MMA issued has completed before the CTA may end
     if (!wait_for(&sm.done, 0)) ok = false;
     __syncwarp();
-  } else if (warp > kValues) {
+  } else if (warp > kMma) {
     regs_give();
   } else if (warp >= kWidenWarp) {
     regs_give();
@@ -569,7 +572,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
   if (!ok) set_status(p.a.status, SPEC_ERR_TIMEOUT);
   tc::fence_before_sync();
   __syncthreads();
-  if (warp == kScores) {
+  if (warp == kMma) {
     tc::fence_after_sync();
     tmem_free(tmem, 512);
   }
