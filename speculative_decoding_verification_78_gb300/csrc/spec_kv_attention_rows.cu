@@ -96,7 +96,6 @@ struct __align__(16) RowsSmall {
   float4 page[2][8];             // by 16 tokens: scale log2(e) ks, log2 vs, 1 / vs
   uint32_t vnan[2][4];           // tokens whose values hold NaN (tiles with new tokens)
   uint32_t tmem;
-  LocateScratch loc;
 };
 // + the queries' units, which, once read, leave their place to the row maxima [group][half][row]
 template <class F> constexpr int rows_smem() {
@@ -218,7 +217,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
   int t0 = 0, t1 = 0, total = 0, skip = 0;
   Item x{};
   tc::fence_before_sync();
-  locate<NT, kRowsThreads>(p, sm.loc, t0, t1, total, x, skip);
+  locate<NT, kRowsThreads>(p, *reinterpret_cast<LocateScratch *>(smem + F::kOffQ), t0, t1, total, x, skip);
   tc::fence_after_sync();
   const uint32_t tmem = sm.tmem;
   if (tid == 0) publish_range(p, x, skip, t0, t1, total);
@@ -503,16 +502,16 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       float lse2;
       if constexpr (F::RTC == 2) {
         const float total = sum_of(grp);
-        lse2 = total == 0.f ? -INFINITY : log2f(total) - nm;
-        f0 = total == 0.f ? 0.f : 1.f / total;
+        lse2 = total == 0.f ? -INFINITY : __log2f(total) - nm;
+        f0 = total == 0.f ? 0.f : __frcp_rn(total);
       } else {
         const float n0 = share[128 + lrow], n1 = share[512 + 128 + lrow];
         const float l0 = sum_of(0), l1 = sum_of(1);
         const float m = fminf(n0, n1);   // -m of the larger reference
         const float w0 = ex2(m - n0), w1 = ex2(m - n1);
         const float total = l0 * w0 + l1 * w1;
-        const float inv = total == 0.f ? 0.f : 1.f / total;
-        lse2 = total == 0.f ? -INFINITY : log2f(total) - m;
+        const float inv = total == 0.f ? 0.f : __frcp_rn(total);
+        lse2 = total == 0.f ? -INFINITY : __log2f(total) - m;
         f0 = l0 == 0.f ? 0.f * inv : w0 * inv;   // (0 NaN is NaN)
         f1 = l1 == 0.f ? 0.f * inv : w1 * inv;
       }
@@ -532,7 +531,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       T *out = static_cast<T *>(p.out) + ((static_cast<long long>(x.b) * p.a.N + i) * p.a.Hq +
                                           static_cast<long long>(x.h) * p.G + gq) * D;
       float *po = p.part_o + (part * NT + n) * D;
-#pragma unroll 1
+#pragma unroll 2
       for (int c = d0; c < d0 + kDims; c += 16) {
         uint32_t o[16], o1[16];
         tmem_ld(tlane + F::kColO + (F::RTC == 2 ? grp * D : 0) + c, o);

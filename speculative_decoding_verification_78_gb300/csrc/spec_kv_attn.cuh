@@ -226,7 +226,13 @@ __device__ __forceinline__ void item_next(const AttnArgs &p, Item &x) {
       ++x.b;
     }
   }
-  if (x.b < p.a.B) item_load<NT>(p, x);
+  if (x.b >= p.a.B) return;
+  if (x.h == 0 && x.rt == 0) {   // another sequence
+    item_load<NT>(p, x);
+  } else if (p.RT > 1) {
+    x.end = item_end<NT>(p, x.len, x.n, x.ok, x.rt);
+    x.tiles = tiles_for(x.end);
+  }
 }
 // Range c of G of a line of T tiles begins at floor(T c / G); range_of: the range that holds tile t.
 __device__ __forceinline__ int range_start(int T, int c, int G) {
@@ -240,7 +246,7 @@ __device__ __forceinline__ int range_of(int T, int t, int G) {
 // the sequences of its own contiguous share; the thread whose share holds t0 finds it there.
 struct LocateScratch {
   int b0, skip0;
-  int warp_sum[20];
+  int warp_sum[32];
 };
 template <int NT, int kThreads>
 __device__ void locate(const AttnArgs &p, LocateScratch &sm, int &t0, int &t1, int &total, Item &x,
@@ -279,10 +285,11 @@ __device__ void locate(const AttnArgs &p, LocateScratch &sm, int &t0, int &t1, i
     sm.skip0 = t0 - at;
   }
   __syncthreads();
-  if (t0 >= t1) return;
   x.b = sm.b0;
   x.rt = 0;
   skip = sm.skip0;
+  __syncthreads();   // the scratch may be put to other use
+  if (t0 >= t1) return;
   const int per_head = head_tiles<NT>(p, x.b);
   x.h = skip / per_head;
   skip -= x.h * per_head;
