@@ -139,7 +139,7 @@ struct RopeArgs {
   const int32_t *positions;     // [B, N] or null
   int rows, R, pairs;
   int touched;                  // pages one sequence's new tokens can touch
-  long long q_vecs;             // B * N * Hq * D / 8
+  int vec4;                     // rope is 16-byte aligned
 };
 
 cudaError_t launch_kv_append(const KvArgs &a, const RopeArgs &r, int dtype, cudaStream_t stream);

@@ -111,7 +111,7 @@ int spec_kv_append(const spec_kv_cache_t *cache, const int32_t *page_table, int 
   r.R = rope_dim;
   r.pairs = interleaved != 0;
   r.touched = (N + a.page - 2) / a.page + 1;
-  r.q_vecs = static_cast<long long>(B) * N * q_heads * (a.D / 8);
+  r.vec4 = aligned(rope, 16);
   return launch_result(launch_kv_append(a, r, dtype, static_cast<cudaStream_t>(stream)));
 }
 

@@ -1,19 +1,21 @@
-// spec_kv_append.cu -- new tokens into the paged e4m3 cache: keys rotated by their positions, one
-// power-of-two scale for each page and head, queries rotated beside them.
+// spec_kv_append.cu -- new tokens into the paged e4m3 cache (keys rotated by their positions, one
+// power-of-two scale for each page and head, queries rotated beside them), and the accepted path of a
+// verified tree moved to the front of the new tokens' slots.
 //
-// One CTA per page that a sequence's new tokens touch, head, and side (keys or values): the CTA
-// holds the page's new rows in registers (one read of 2 bytes an element), reduces their largest
-// magnitude, and writes them as e4m3 at the page's scale (one byte an element), so the scale costs
-// no second pass. A page that held tokens has them stored again only when its scale grows. Further
-// CTAs rotate the queries. Nothing here is a contraction: HBM bounds long calls, latency short ones.
+// Appending reads 2 bytes an element and writes 1 (keys, values) or 2 (queries): HBM bounds long calls,
+// latency short ones. The scale costs no second pass: a CTA holds a page's new rows of one head in
+// registers, reduces their largest magnitude and writes them. It takes several heads of the page in
+// turn (the next head's rows on their way meanwhile), so that the cosines and sines of its tokens,
+// twice a head's bytes, are loaded once for all of them; calls with few pages give each head a CTA. The
+// queries' warps take up to four head groups of a token on the same cosines and sines. A page that held
+// tokens has them stored again only when its scale grows.
 #include "spec_kv.cuh"
 
 namespace specv {
 
 namespace {
 
-constexpr int kAppendThreads = 256;
-constexpr int kQVecs = 4;   // query vectors (8 elements) per thread
+constexpr int kQIters = 4;    // head groups of a task
 
 // The position of new token i of sequence b; a position outside the table is reported and read as 0.
 __device__ __forceinline__ int kv_position(const KvArgs &a, const RopeArgs &r, int b, int i,
@@ -36,82 +38,135 @@ __device__ __forceinline__ int kv_position(const KvArgs &a, const RopeArgs &r, i
   return static_cast<int>(pos);
 }
 
-// Elements d0 .. d0 + 7 of one head's row of a token (at `row`), rotated by table row `pos`.
-// Halves: the partner of element j < R/2 is j + R/2, eight of which are a vector of their own
-// (R is a multiple of 16). Pairs: both partners lie in the vector.
-template <typename T>
-__device__ __forceinline__ void load_rotated(const RopeArgs &r, const T *row, int d0, int pos,
-                                             float (&f)[8]) {
-  vec_to_floats<T>(__ldg(reinterpret_cast<const uint4 *>(row + d0)), f);
-  if (d0 >= r.R) return;
-  const float *cs = r.rope + static_cast<long long>(pos) * r.R;
-  const int half = r.R / 2;
-  if (r.pairs) {
-    // R / 2 is a multiple of 8 and d0 / 2 of 4: 16-byte aligned when the table is; the table is
-    // only known to be 4-byte aligned, so scalar loads
+// A head's row is D / 16 units of two vectors of 8 elements. Unit u < R / 16 rotates by the cosines and
+// sines 8 u .. 8 u + 7: its vectors are 8 u and R / 2 + 8 u (halves: partners), or 16 u and 16 u + 8
+// (interleaved pairs: partners side by side). The others are what is left, two vectors side by side.
+struct Unit {
+  int a, b;    // first elements of its vectors
+  bool turn;
+};
+__device__ __forceinline__ Unit unit_of(const RopeArgs &r, int u, bool rotate) {
+  Unit x;
+  x.turn = rotate && u < r.R / 16;
+  if (x.turn && !r.pairs) {
+    x.a = 8 * u;
+    x.b = r.R / 2 + 8 * u;
+  } else {
+    x.a = 16 * u;
+    x.b = 16 * u + 8;
+  }
+  return x;
+}
+struct Angles {
+  float c[8], s[8];
+};
+__device__ __forceinline__ void load_angles(const RopeArgs &r, int pos, int u, Angles &t) {
+  const float *row = r.rope + static_cast<long long>(pos) * r.R + 8 * u;
+  if (r.vec4) {   // (R is a multiple of 16, so rows and halves are aligned when the table is)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float c = __ldg(cs + d0 / 2 + i), s = __ldg(cs + half + d0 / 2 + i);
-      const float x = f[2 * i], y = f[2 * i + 1];
-      f[2 * i] = __fmaf_rn(x, c, -(y * s));
-      f[2 * i + 1] = __fmaf_rn(y, c, x * s);
+    for (int i = 0; i < 8; i += 4) {
+      const float4 c = __ldg(reinterpret_cast<const float4 *>(row + i));
+      const float4 s = __ldg(reinterpret_cast<const float4 *>(row + r.R / 2 + i));
+      t.c[i] = c.x, t.c[i + 1] = c.y, t.c[i + 2] = c.z, t.c[i + 3] = c.w;
+      t.s[i] = s.x, t.s[i + 1] = s.y, t.s[i + 2] = s.z, t.s[i + 3] = s.w;
     }
   } else {
-    const bool up = d0 >= half;
-    const int j0 = up ? d0 - half : d0;
-    float g[8];
-    vec_to_floats<T>(__ldg(reinterpret_cast<const uint4 *>(row + (up ? j0 : j0 + half))), g);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float c = __ldg(cs + j0 + i), s = __ldg(cs + half + j0 + i);
-      f[i] = up ? __fmaf_rn(f[i], c, g[i] * s) : __fmaf_rn(f[i], c, -(g[i] * s));
+      t.c[i] = __ldg(row + i);
+      t.s[i] = __ldg(row + r.R / 2 + i);
+    }
+  }
+}
+__device__ __forceinline__ void rotate(const RopeArgs &r, const Angles &t, float (&f)[8],
+                                       float (&g)[8]) {
+  if (r.pairs) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float x = f[2 * i], y = f[2 * i + 1], z = g[2 * i], w = g[2 * i + 1];
+      f[2 * i] = __fmaf_rn(x, t.c[i], -(y * t.s[i]));
+      f[2 * i + 1] = __fmaf_rn(y, t.c[i], x * t.s[i]);
+      g[2 * i] = __fmaf_rn(z, t.c[4 + i], -(w * t.s[4 + i]));
+      g[2 * i + 1] = __fmaf_rn(w, t.c[4 + i], z * t.s[4 + i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float x = f[i], y = g[i];
+      f[i] = __fmaf_rn(x, t.c[i], -(y * t.s[i]));
+      g[i] = __fmaf_rn(y, t.c[i], x * t.s[i]);
     }
   }
 }
 
-// kV: vectors of 8 elements per thread that cover a page of one head
-template <typename T, int kV>
-__global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(KvArgs a, RopeArgs r) {
-  __shared__ float warp_max[kAppendThreads / 32];
+// One warp's queries: token `task / blocks`, up to kQIters groups of 32 / (D / 16) heads.
+template <typename T>
+__device__ __forceinline__ void append_queries(const KvArgs &a, const RopeArgs &r, long long task,
+                                               int lane) {
+  const int upr = a.D / 16, per = 32 / upr;   // units of a row; heads of a group
+  const int blocks = (a.Hq + per * kQIters - 1) / (per * kQIters);
+  const long long token = task / blocks;
+  if (token >= static_cast<long long>(a.B) * a.N) return;
+  const int h0 = static_cast<int>(task - token * blocks) * per * kQIters + lane / upr;
+  const int b = static_cast<int>(token / a.N);
+  const int i = static_cast<int>(token - static_cast<long long>(b) * a.N);
+  int len, n;
+  if (!kv_lengths(a, b, len, n) || i >= n) return;
+  const int u = lane % upr;
+  const Unit x = unit_of(r, u, true);
+  const T *src = static_cast<const T *>(r.q) + token * r.q_stride;
+  T *dst = static_cast<T *>(r.q_out) + token * a.Hq * a.D;
+  uint4 raw[kQIters][2];
+#pragma unroll
+  for (int k = 0; k < kQIters; ++k) {
+    const int h = h0 + k * per;
+    if (h < a.Hq) {
+      raw[k][0] = __ldg(reinterpret_cast<const uint4 *>(src + h * a.D + x.a));
+      raw[k][1] = __ldg(reinterpret_cast<const uint4 *>(src + h * a.D + x.b));
+    }
+  }
+  Angles t;
+  if (x.turn) load_angles(r, kv_position(a, r, b, i, len), u, t);
+  __syncwarp();   // q_out may be q: nothing of a row is stored before all of it is read
+#pragma unroll
+  for (int k = 0; k < kQIters; ++k) {
+    const int h = h0 + k * per;
+    if (h < a.Hq) {
+      if (x.turn) {
+        float f[8], g[8];
+        vec_to_floats<T>(raw[k][0], f);
+        vec_to_floats<T>(raw[k][1], g);
+        rotate(r, t, f, g);
+        raw[k][0] = floats_to_vec<T>(f);
+        raw[k][1] = floats_to_vec<T>(g);
+      }
+      *reinterpret_cast<uint4 *>(dst + h * a.D + x.a) = raw[k][0];
+      *reinterpret_cast<uint4 *>(dst + h * a.D + x.b) = raw[k][1];
+    }
+  }
+}
+
+// kU: units of a thread; kThreads * kU units cover a page of one head. Heads h0 .. h0 + hpc - 1 of a
+// page, keys or values; the CTAs from `kv_ctas` on rotate queries.
+template <typename T, int kU, int kThreads>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads)
+    kv_append_kernel(const __grid_constant__ KvArgs a, const __grid_constant__ RopeArgs r, int hpc,
+                     int kv_ctas) {
+  __shared__ float warp_max[2][kThreads / 32];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int tid = threadIdx.x;
-  const int dv = a.D / 8;   // vectors per row
-  const long long kv_ctas = 2LL * a.Hkv * r.touched * a.B;
-  if (blockIdx.x >= kv_ctas) {   // queries
-    const long long first = (blockIdx.x - kv_ctas) * kAppendThreads * kQVecs;
-    const T *q = static_cast<const T *>(r.q);
-    T *qo = static_cast<T *>(r.q_out);
-    float f[kQVecs][8];
-    long long at[kQVecs];
-#pragma unroll
-    for (int u = 0; u < kQVecs; ++u) {   // all loads before the stores: q_out may be q
-      const long long vec = first + u * kAppendThreads + tid;
-      at[u] = -1;
-      if (vec >= r.q_vecs) continue;
-      const long long rowh = vec / dv;   // (token, head)
-      const int d0 = static_cast<int>(vec - rowh * dv) * 8;
-      const long long token = rowh / a.Hq;
-      const int h = static_cast<int>(rowh - token * a.Hq);
-      const int b = static_cast<int>(token / a.N), i = static_cast<int>(token - static_cast<long long>(b) * a.N);
-      int len, n;
-      if (!kv_lengths(a, b, len, n) || i >= n) continue;
-      const int pos = r.R ? kv_position(a, r, b, i, len) : 0;
-      load_rotated<T>(r, q + token * r.q_stride + static_cast<long long>(h) * a.D, d0, pos, f[u]);
-      at[u] = vec * 8;
-    }
-    __syncwarp();   // a head's row is within one warp: nothing of it is stored before all is read
-#pragma unroll
-    for (int u = 0; u < kQVecs; ++u)
-      if (at[u] >= 0) *reinterpret_cast<uint4 *>(qo + at[u]) = floats_to_vec<T>(f[u]);
+  if (static_cast<int>(blockIdx.x) >= kv_ctas) {
+    const long long task = static_cast<long long>(blockIdx.x - kv_ctas) * (kThreads / 32) + (tid >> 5);
+    append_queries<T>(a, r, task, tid & 31);
     return;
   }
-  // one page of one head: keys (side 0) or values
-  long long x = blockIdx.x;
+  unsigned x = blockIdx.x;
   const int side = static_cast<int>(x & 1);
   x >>= 1;
-  const int h = static_cast<int>(x % a.Hkv);
-  x /= a.Hkv;
+  const unsigned groups = (a.Hkv + hpc - 1) / hpc;
+  const int h0 = static_cast<int>(x % groups) * hpc;
+  x /= groups;
   const int pi = static_cast<int>(x % r.touched);
   const int b = static_cast<int>(x / r.touched);
   int len, n;
@@ -128,198 +183,262 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(KvArgs a, Rop
     if (tid == 0) set_status(a.status, SPEC_ERR_PAGE);
     return;
   }
+  const int upr = a.D / 16;
+  const bool turning = side == 0 && r.R > 0;
   const T *src = static_cast<const T *>(side ? r.v : r.k);
   const long long stride = side ? r.v_stride : r.k_stride;
-  const bool turn = side == 0 && r.R > 0;
-  const long long head = static_cast<long long>(page) * a.Hkv + h;
-  float *scale = (side ? a.v_scale : a.k_scale) + head;
-  uint8_t *dst = (side ? a.v : a.k) + (head << a.page_shift) * a.D;
-  const bool held = from > p0;
-  const float old = held ? *scale : 0.f;
-  float f[kV][8];
-  float amax = 0.f;
-  bool finite = true;
+  Unit un[kU];
+  int row[kU];        // of the page, or -1: nothing of this thread's
+  const T *at[kU];
+  Angles t[kU];
 #pragma unroll
-  for (int u = 0; u < kV; ++u) {
-    const int vec = u * kAppendThreads + tid;
-    const int row = vec / dv, d0 = (vec - row * dv) * 8, t = p0 + row;
-    if (row < a.page && t >= from && t < to) {
-      const int i = t - len;
-      const long long token = static_cast<long long>(b) * a.N + i;
-      const T *at = src + token * stride + static_cast<long long>(h) * a.D;
-      if (turn)
-        load_rotated<T>(r, at, d0, kv_position(a, r, b, i, len), f[u]);
-      else
-        vec_to_floats<T>(__ldg(reinterpret_cast<const uint4 *>(at + d0)), f[u]);
+  for (int k = 0; k < kU; ++k) {
+    const int id = k * kThreads + tid;
+    row[k] = id / upr;
+    un[k] = unit_of(r, id - row[k] * upr, turning);
+    const int slot = p0 + row[k];
+    at[k] = src + (static_cast<long long>(b) * a.N + (slot - len)) * stride;
+    if (row[k] >= a.page) row[k] = -1;
+    if (row[k] >= 0 && un[k].turn && slot >= from && slot < to)
+      load_angles(r, kv_position(a, r, b, slot - len, len), id % upr, t[k]);
+  }
+  const int h1 = min(a.Hkv, h0 + hpc);
+  uint4 raw[kU][2];
+  auto fetch = [&](int h) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float m = fabsf(f[u][e]);
-        const bool ok = m < INFINITY;   // false for NaN too
-        finite = finite && ok;
-        amax = fmaxf(amax, ok ? m : 0.f);
+    for (int k = 0; k < kU; ++k) {
+      const int slot = p0 + row[k];
+      if (row[k] >= 0 && slot >= from && slot < to) {
+        raw[k][0] = __ldg(reinterpret_cast<const uint4 *>(at[k] + h * a.D + un[k].a));
+        raw[k][1] = __ldg(reinterpret_cast<const uint4 *>(at[k] + h * a.D + un[k].b));
       }
     }
+  };
+  fetch(h0);
+  const bool held = from > p0;
+  bool finite = true;
+  for (int h = h0; h < h1; ++h) {
+    const long long head = static_cast<long long>(page) * a.Hkv + h;
+    float *scale = (side ? a.v_scale : a.k_scale) + head;
+    uint8_t *dst = (side ? a.v : a.k) + (head << a.page_shift) * a.D;
+    const float old = held ? *scale : 0.f;
+    float f[kU][2][8];
+    float amax = 0.f;
+#pragma unroll
+    for (int k = 0; k < kU; ++k) {
+      const int slot = p0 + row[k];
+      if (row[k] >= 0 && slot >= from && slot < to) {
+        vec_to_floats<T>(raw[k][0], f[k][0]);
+        vec_to_floats<T>(raw[k][1], f[k][1]);
+        if (un[k].turn) rotate(r, t[k], f[k][0], f[k][1]);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const float m = fabsf(f[k][e >> 3][e & 7]);
+          const bool ok = m < INFINITY;   // false for NaN too
+          finite = finite && ok;
+          amax = fmaxf(amax, ok ? m : 0.f);
+        }
+      }
+    }
+    if (h + 1 < h1) fetch(h + 1);
+    // magnitudes order like their bit patterns
+    amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
+    float *wm = warp_max[h & 1];   // the other half may still be read for the head before
+    if ((tid & 31) == 0) wm[tid >> 5] = amax;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) amax = fmaxf(amax, wm[w]);
+    const float s = fmaxf(kv_scale_for(amax), old);
+    const float inv = 1.f / s;   // exact for a power of two
+#pragma unroll
+    for (int k = 0; k < kU; ++k) {
+      if (row[k] < 0) continue;
+      const int slot = p0 + row[k];
+      uint2 *oa = reinterpret_cast<uint2 *>(dst + row[k] * a.D + un[k].a);
+      uint2 *ob = reinterpret_cast<uint2 *>(dst + row[k] * a.D + un[k].b);
+      if (slot >= from && slot < to) {
+        const uint2 wa = floats_to_e4m3(f[k][0], inv), wb = floats_to_e4m3(f[k][1], inv);
+        if (un[k].b == un[k].a + 8) {   // side by side: 16 bytes
+          *reinterpret_cast<uint4 *>(oa) = make_uint4(wa.x, wa.y, wb.x, wb.y);
+        } else {
+          *oa = wa;
+          *ob = wb;
+        }
+      } else if (held && s != old && slot < from) {   // the rows the page held, at the new scale
+        float g[8];
+        e4m3_to_floats(*oa, g);
+        *oa = floats_to_e4m3(g, old / s);
+        e4m3_to_floats(*ob, g);
+        *ob = floats_to_e4m3(g, old / s);
+      }
+    }
+    if (tid == 0 && s != old) *scale = s;
   }
   if (!finite) set_status(a.status, SPEC_ERR_NONFINITE);
-  // magnitudes order like their bit patterns
-  amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
-  if ((tid & 31) == 0) warp_max[tid >> 5] = amax;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kAppendThreads / 32; ++w) amax = fmaxf(amax, warp_max[w]);
-  const float s = fmaxf(kv_scale_for(amax), old);
-  const float inv = 1.f / s;   // exact for a power of two
-#pragma unroll
-  for (int u = 0; u < kV; ++u) {
-    const int vec = u * kAppendThreads + tid;
-    const int row = vec / dv, d0 = (vec - row * dv) * 8, t = p0 + row;
-    uint2 *out = reinterpret_cast<uint2 *>(dst + row * a.D + d0);
-    if (row < a.page && t >= from && t < to) {
-      *out = floats_to_e4m3(f[u], inv);
-    } else if (held && s != old && t < from) {   // the rows the page held, at the new scale
-      float g[8];
-      e4m3_to_floats(*out, g);
-      *out = floats_to_e4m3(g, old / s);
-    }
-  }
-  if (tid == 0 && s != old) *scale = s;
+}
+
+template <typename T, int kU, int kThreads>
+cudaError_t launch_append(const KvArgs &a, const RopeArgs &r, int hpc, cudaStream_t stream) {
+  const int groups = (a.Hkv + hpc - 1) / hpc;
+  const long long kv = 2LL * groups * r.touched * a.B;
+  const int per = 32 / (a.D / 16) * kQIters;   // heads of a query task
+  const long long tasks = static_cast<long long>(a.B) * a.N * ((a.Hq + per - 1) / per);
+  const long long grid = kv + (tasks + kThreads / 32 - 1) / (kThreads / 32);
+  if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  return launch_kv(kv_append_kernel<T, kU, kThreads>, grid, kThreads, 0, stream, a, r, hpc,
+                   static_cast<int>(kv));
 }
 
 template <typename T>
-cudaError_t launch_append(const KvArgs &a, const RopeArgs &r, cudaStream_t stream) {
-  const long long grid = 2LL * a.Hkv * r.touched * a.B +
-                         (r.q_vecs + kAppendThreads * kQVecs - 1) / (kAppendThreads * kQVecs);
-  if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  const int vecs = a.page * a.D / 8;
-  if (vecs <= kAppendThreads)
-    return launch_kv(kv_append_kernel<T, 1>, grid, kAppendThreads, 0, stream, a, r);
-  if (vecs <= 2 * kAppendThreads)
-    return launch_kv(kv_append_kernel<T, 2>, grid, kAppendThreads, 0, stream, a, r);
-  if (vecs <= 4 * kAppendThreads)
-    return launch_kv(kv_append_kernel<T, 4>, grid, kAppendThreads, 0, stream, a, r);
-  return launch_kv(kv_append_kernel<T, 8>, grid, kAppendThreads, 0, stream, a, r);
+cudaError_t launch_append_for(const KvArgs &a, const RopeArgs &r, cudaStream_t stream) {
+  // heads of a CTA: as many as leave about four CTAs for each SM
+  int hpc = 1;
+  while (hpc < a.Hkv && 2LL * a.B * r.touched * ((a.Hkv + 2 * hpc - 1) / (2 * hpc)) >= 608) hpc *= 2;
+  const int units = a.page * a.D / 16;
+  if (units <= 256) return launch_append<T, 1, 256>(a, r, hpc, stream);
+  if (units <= 512) return launch_append<T, 2, 256>(a, r, hpc, stream);
+  return launch_append<T, 2, 512>(a, r, hpc, stream);
 }
 
 // ------------------------------------------------------------------ the accepted path
 //
-// One CTA per layer, sequence, head and side. The path's nodes increase and node k of it is at
-// least k, so moving rows forward in the order of k never overwrites a row still to be moved. Page
-// by page of the destination: the rows that move there are read into registers (dequantised),
-// their largest magnitude raises the page's scale if it must, the rest of the page is stored again
-// when it did, and the rows are written.
-__global__ void __launch_bounds__(kAppendThreads)
-    kv_commit_kernel(KvArgs a, const int32_t *path_nodes, const int32_t *accept_len,
-                     int32_t *out_lens) {
-  __shared__ float warp_max[kAppendThreads / 32];
+// One warp per layer, sequence, head and side; a few rows of 64 or 128 bytes move, so the call is all
+// latency, and many small tasks at once hide it (one CTA each, a page in registers, took 127 us for
+// 32 trees in 32 layers of 8 heads). The path's nodes increase and node k of it is at least k, so moving
+// rows forward in the order of k never overwrites a row still to be moved. Page by page of the
+// destination: the largest magnitude of the rows that move there raises the page's scale if it must,
+// the page is stored again when it did, and the rows are moved.
+constexpr int kCommitWarps = 4;
+
+__global__ void __launch_bounds__(32 * kCommitWarps)
+    kv_commit_kernel(const __grid_constant__ KvArgs a, const int32_t *path_nodes,
+                     const int32_t *accept_len, int32_t *out_lens, long long tasks) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int tid = threadIdx.x;
-  long long x = blockIdx.x;
+  const int lane = threadIdx.x & 31;
+  long long x = static_cast<long long>(blockIdx.x) * kCommitWarps + (threadIdx.x >> 5);
+  if (x >= tasks) return;
   const int side = static_cast<int>(x & 1);
   x >>= 1;
   const int h = static_cast<int>(x % a.Hkv);
   x /= a.Hkv;
   const int b = static_cast<int>(x % a.B);
   const long long layer = x / a.B;
-  const bool first = side == 0 && h == 0 && layer == 0;
   const int len = __ldg(a.seq_lens + b), acc = __ldg(accept_len + b);
   const int32_t *path = path_nodes + static_cast<long long>(b) * a.N;
   bool bad = acc < -1 || acc >= a.N;
-  if (!bad)
-    for (int k = tid; k <= acc; k += kAppendThreads) {
+  bool moves = false;
+  int top = 0;   // the path's last node
+  if (!bad) {
+    for (int k = lane; k <= acc; k += 32) {
       const int p = __ldg(path + k);
       bad = bad || (k == 0 ? p != 0 : p <= __ldg(path + k - 1)) || p >= a.N;
+      moves = moves || p != k;
+      top = max(top, p);
     }
-  bad = __syncthreads_or(bad) != 0;
-  const long long last = bad || acc < 0 ? 0 : static_cast<long long>(len) + __ldg(path + acc);
-  const bool len_ok = len >= 0 && last < (static_cast<long long>(a.pps) << a.page_shift);
-  if (first && tid == 0) {
+  }
+  bad = __any_sync(0xffffffffu, bad);
+  moves = __any_sync(0xffffffffu, moves);
+  top = __reduce_max_sync(0xffffffffu, top);
+  const bool len_ok = len >= 0 && (bad || acc < 0 ||
+                                   static_cast<long long>(len) + top <
+                                       (static_cast<long long>(a.pps) << a.page_shift));
+  if (side == 0 && h == 0 && layer == 0 && lane == 0) {
     if (!len_ok) set_status(a.status, SPEC_ERR_LENGTH);
     if (bad) set_status(a.status, SPEC_ERR_PATH);
     out_lens[b] = len_ok && !bad ? len + acc + 1 : len;
   }
-  if (!len_ok || bad || acc < 1) return;
-  const int dv = a.D / 8;
+  if (!len_ok || bad || !moves) return;
+  const int dv = a.D / 8, per = 32 / dv;   // lanes of a row; rows at a time
+  const int sub = lane / dv, d0 = lane % dv * 8;
   const long long layer_heads = layer * a.num_pages * a.Hkv;
   float *scales = (side ? a.v_scale : a.k_scale) + layer_heads;
   uint8_t *pool = (side ? a.v : a.k) + (layer_heads << a.page_shift) * a.D;
   for (int local = len >> a.page_shift; (local << a.page_shift) <= len + acc; ++local) {
     const int p0 = local << a.page_shift;
+    const int k0 = max(0, p0 - len), k1 = min(acc + 1, p0 + a.page - len);   // path nodes that end here
     int page;
     if (!kv_page(a, b, local, page)) {
-      if (tid == 0) set_status(a.status, SPEC_ERR_PAGE);
+      if (lane == 0) set_status(a.status, SPEC_ERR_PAGE);
       continue;
     }
     const long long head = static_cast<long long>(page) * a.Hkv + h;
     uint8_t *dst = pool + (head << a.page_shift) * a.D;
     const float old = scales[head];
-    float f[8][8];   // up to 128 rows of 128 elements: 8 vectors a thread
-    uint32_t moves = 0;
-    float amax = 0.f;
-#pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const int vec = u * kAppendThreads + tid;
-      const int row = vec / dv, d0 = (vec - row * dv) * 8, k = p0 + row - len;
-      if (row >= a.page || k < 0 || k > acc) continue;
-      const int from = len + __ldg(path + k);
-      if (from == p0 + row) continue;
+    float s = old;   // the page's scale
+    // node k's row, dequantised; false if it stays where it is or its page is bad
+    auto source = [&](int k, float (&f)[8]) {
+      if (k >= k1) return false;
+      const int node = __ldg(path + k);
+      if (node == k) return false;
+      const int slot = len + node;
       int spage;
-      if (!kv_page(a, b, from >> a.page_shift, spage)) {
+      if (!kv_page(a, b, slot >> a.page_shift, spage)) {
         set_status(a.status, SPEC_ERR_PAGE);
-        continue;
+        return false;
       }
       const long long shead = static_cast<long long>(spage) * a.Hkv + h;
-      const float ss = scales[shead];
       e4m3_to_floats(*reinterpret_cast<const uint2 *>(
-                         pool + ((shead << a.page_shift) + (from & (a.page - 1))) * a.D + d0),
-                     f[u]);
-      moves |= 1u << u;
+                         pool + ((shead << a.page_shift) + (slot & (a.page - 1))) * a.D + d0),
+                     f);
+      const float m = spage == page ? s : scales[shead];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        f[u][e] *= ss;
-        const float m = fabsf(f[u][e]);
-        amax = fmaxf(amax, m < INFINITY ? m : 0.f);
-      }
+      for (int e = 0; e < 8; ++e) f[e] *= m;
+      return true;
+    };
+    float f[8];
+    float amax = 0.f;
+    bool any = false, mine = false;
+    for (int k = k0; k < k1; k += per) {
+      mine = source(k + sub, f);
+      any = any || mine;
+      if (mine)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float m = fabsf(f[e]);
+          amax = fmaxf(amax, m < INFINITY ? m : 0.f);
+        }
     }
-    if (!__syncthreads_or(moves != 0)) continue;
+    if (!__any_sync(0xffffffffu, any)) continue;
     amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
-    if ((tid & 31) == 0) warp_max[tid >> 5] = amax;
-    __syncthreads();   // every source row is in registers
-#pragma unroll
-    for (int w = 0; w < kAppendThreads / 32; ++w) amax = fmaxf(amax, warp_max[w]);
-    const float s = fmaxf(kv_scale_for(amax), old);
-    const float inv = 1.f / s;
-#pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const int vec = u * kAppendThreads + tid;
-      const int row = vec / dv, d0 = (vec - row * dv) * 8;
-      if (row >= a.page) continue;
-      uint2 *out = reinterpret_cast<uint2 *>(dst + row * a.D + d0);
-      if (moves >> u & 1u) {
-        *out = floats_to_e4m3(f[u], inv);
-      } else if (s != old) {
+    s = fmaxf(kv_scale_for(amax), old);
+    if (s != old) {   // the page at its new scale, rows still to be moved from it too
+      __syncwarp();
+      for (int r = sub; r < a.page; r += per) {
+        uint2 *at = reinterpret_cast<uint2 *>(dst + r * a.D + d0);
         float g[8];
-        e4m3_to_floats(*out, g);
-        *out = floats_to_e4m3(g, old / s);
+        e4m3_to_floats(*at, g);
+        *at = floats_to_e4m3(g, old / s);
       }
+      if (lane == 0) scales[head] = s;
+      __syncwarp();
     }
-    if (tid == 0 && s != old) scales[head] = s;
-    __syncthreads();   // the next page may read rows of this one
+    const float inv = 1.f / s;
+    const bool kept = k1 - k0 <= per && s == old;   // the rows are still in the registers
+    for (int k = k0; k < k1; k += per) {
+      if (!kept) mine = source(k + sub, f);
+      __syncwarp();   // every row of the step is read before any is written
+      if (mine)
+        *reinterpret_cast<uint2 *>(dst + (len + k + sub - p0) * a.D + d0) = floats_to_e4m3(f, inv);
+      __syncwarp();
+    }
   }
 }
 
 }  // namespace
 
 cudaError_t launch_kv_append(const KvArgs &a, const RopeArgs &r, int dtype, cudaStream_t stream) {
-  return dtype == SPEC_BF16 ? launch_append<__nv_bfloat16>(a, r, stream)
-                            : launch_append<__half>(a, r, stream);
+  return dtype == SPEC_BF16 ? launch_append_for<__nv_bfloat16>(a, r, stream)
+                            : launch_append_for<__half>(a, r, stream);
 }
 
 cudaError_t launch_kv_commit(const KvArgs &a, int layers, const int32_t *path,
                              const int32_t *accept, int32_t *out_lens, cudaStream_t stream) {
-  const long long grid = 2LL * a.Hkv * a.B * layers;
+  const long long tasks = 2LL * a.Hkv * a.B * layers;
+  const long long grid = (tasks + kCommitWarps - 1) / kCommitWarps;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  return launch_kv(kv_commit_kernel, grid, kAppendThreads, 0, stream, a, path, accept, out_lens);
+  return launch_kv(kv_commit_kernel, grid, 32 * kCommitWarps, 0, stream, a, path, accept, out_lens,
+                   tasks);
 }
 
 }  // namespace specv
