@@ -7,7 +7,7 @@
 // registers, reduces their largest magnitude and writes them. It takes several heads of the page in
 // turn (the next head's rows on their way meanwhile), so that the cosines and sines of its tokens,
 // twice a head's bytes, are loaded once for all of them; calls with few pages give each head a CTA. The
-// queries' warps take up to four head groups of a token on the same cosines and sines. A page that held
+// queries' warps take up to eight head groups of a token on the same cosines and sines. A page that held
 // tokens has them stored again only when its scale grows.
 #include "spec_kv.cuh"
 
@@ -15,7 +15,7 @@ namespace specv {
 
 namespace {
 
-constexpr int kQIters = 4;    // head groups of a task
+constexpr int kQIters = 8;   // head groups of a query task
 
 // The position of new token i of sequence b; a position outside the table is reported and read as 0.
 __device__ __forceinline__ int kv_position(const KvArgs &a, const RopeArgs &r, int b, int i,
@@ -149,7 +149,7 @@ __device__ __forceinline__ void append_queries(const KvArgs &a, const RopeArgs &
 // kU: units of a thread; kThreads * kU units cover a page of one head. Heads h0 .. h0 + hpc - 1 of a
 // page, keys or values; the CTAs from `kv_ctas` on rotate queries.
 template <typename T, int kU, int kThreads>
-__global__ void __launch_bounds__(kThreads, 1024 / kThreads)
+__global__ void __launch_bounds__(kThreads, 512 / kThreads)
     kv_append_kernel(const __grid_constant__ KvArgs a, const __grid_constant__ RopeArgs r, int hpc,
                      int kv_ctas) {
   __shared__ float warp_max[2][kThreads / 32];
@@ -291,9 +291,9 @@ cudaError_t launch_append(const KvArgs &a, const RopeArgs &r, int hpc, cudaStrea
 
 template <typename T>
 cudaError_t launch_append_for(const KvArgs &a, const RopeArgs &r, cudaStream_t stream) {
-  // heads of a CTA: as many as leave about four CTAs for each SM
+  // heads of a CTA: as many as leave about two CTAs for each SM
   int hpc = 1;
-  while (hpc < a.Hkv && 2LL * a.B * r.touched * ((a.Hkv + 2 * hpc - 1) / (2 * hpc)) >= 608) hpc *= 2;
+  while (hpc < a.Hkv && 2LL * a.B * r.touched * ((a.Hkv + 2 * hpc - 1) / (2 * hpc)) >= 304) hpc *= 2;
   const int units = a.page * a.D / 16;
   if (units <= 256) return launch_append<T, 1, 256>(a, r, hpc, stream);
   if (units <= 512) return launch_append<T, 2, 256>(a, r, hpc, stream);

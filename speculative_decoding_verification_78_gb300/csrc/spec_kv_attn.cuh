@@ -440,16 +440,20 @@ __device__ __forceinline__ void widen(const uint4 (&w)[Widen<D, kThreads>::kStep
 // ------------------------------------------------------------------ the join
 
 // Joins the parts of the items that cross ranges, in the order of the line. Block (c, rows): the item
-// that range c begins inside of, if c is the first range to do so; one warp per row. The ranges are
-// arithmetic, so every load but the first two waits for nothing but those.
+// that range c begins inside of, if c is the first range to do so; kJoinRows rows a warp, whose loads
+// overlap. The ranges are arithmetic, so every load but the first two waits for nothing but those.
+constexpr int kJoinRows = 4, kJoinBlockRows = 8 * kJoinRows;
+
 template <typename T, int D, int NT>
 __global__ void __launch_bounds__(256) kv_attention_join(const __grid_constant__ AttnArgs p,
                                                          int ctas) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  constexpr int kBlocks = NT / 8, E = D / 32;
+  constexpr int kRows = NT < kJoinBlockRows ? NT / 8 : kJoinRows;   // of a warp
+  constexpr int kBlocks = NT / (8 * kRows), E = D / 32;
   const int c = 1 + blockIdx.x / kBlocks;
-  const int n = (blockIdx.x % kBlocks) * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int n0 = (blockIdx.x % kBlocks) * 8 * kRows + (threadIdx.x >> 5) * kRows;
+  const int lane = threadIdx.x & 31;
   // (written by other CTAs: read from L2)
   const int4 s = __ldcg(p.start + c);          // its first item: b, h, row tile, tiles before
   const int4 d = __ldcg(p.start + ctas + c);   // that item's tiles, t0, t1, all tiles
@@ -460,62 +464,78 @@ __global__ void __launch_bounds__(256) kv_attention_join(const __grid_constant__
   const int parts = total >= ctas ? range_of(total, end - 1, ctas) - first + 1 : d.x;
   auto cta = [&](int k) { return total >= ctas ? first + k : range_of(total, begin + k, ctas); };
   if (c != cta(1)) return;   // another block's
-  const unsigned r = static_cast<unsigned>(s.z) * NT + n;
-  const int i = static_cast<int>(r / p.G), g = static_cast<int>(r - static_cast<unsigned>(i) * p.G);
-  if (i >= p.a.N) return;
+  const unsigned r0 = static_cast<unsigned>(s.z) * NT + n0;
+  if (r0 >= static_cast<unsigned>(p.a.N) * p.G) return;
   int len, nn;
-  const bool pad = kv_lengths(p.a, s.x, len, nn) && i >= nn;
-  float m = -INFINITY, sum = 0.f, acc[E];
+  const bool ok = kv_lengths(p.a, s.x, len, nn);
+  float m[kRows], sum[kRows], acc[kRows][E];
 #pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+  for (int q = 0; q < kRows; ++q) {
+    m[q] = -INFINITY;
+    sum[q] = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[q][e] = 0.f;
+  }
   for (int k0 = 0; k0 < parts; k0 += 32) {   // 32 parts at a time, a lane each for their weights
     const int k = k0 + lane;
-    long long part = 0;
-    float v = -INFINITY;
-    if (k < parts) {
-      part = (2LL * cta(k) + (k == 0 ? 1 : 0)) * NT + n;
-      v = __ldcg(p.part_lse + part);
+    const long long part = k < parts ? (2LL * cta(k) + (k == 0 ? 1 : 0)) * NT + n0 : 0;
+    float v[kRows], w[kRows];
+#pragma unroll
+    for (int q = 0; q < kRows; ++q) v[q] = k < parts ? __ldcg(p.part_lse + part + q) : -INFINITY;
+#pragma unroll
+    for (int q = 0; q < kRows; ++q) {
+      float top = v[q];
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) top = fmax_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+      top = fmax_nan(top, m[q]);
+      const float ref = top == -INFINITY ? 0.f : top;
+      w[q] = ex2(v[q] - ref);
+      const float old = ex2(m[q] - ref);
+      m[q] = top;
+      float all = w[q];
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+      sum[q] = sum[q] * old + all;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[q][e] *= old;
     }
-    float top = v;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmax_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
-    top = fmax_nan(top, m);
-    const float ref = top == -INFINITY ? 0.f : top;
-    const float w = ex2(v - ref), old = ex2(m - ref);
-    m = top;
-    float s32 = w;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s32 += __shfl_xor_sync(0xffffffffu, s32, o);
-    sum = sum * old + s32;
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] *= old;
     const int cnt = min(32, parts - k0);
-#pragma unroll 4
+#pragma unroll 2
     for (int j = 0; j < cnt; ++j) {
-      const float wj = __shfl_sync(0xffffffffu, w, j);
       const float *o = p.part_o + __shfl_sync(0xffffffffu, part, j) * D + lane * E;
-      if constexpr (E == 4) {
-        const float4 q = __ldcg(reinterpret_cast<const float4 *>(o));
-        acc[0] = __fmaf_rn(wj, q.x, acc[0]);
-        acc[1] = __fmaf_rn(wj, q.y, acc[1]);
-        acc[2] = __fmaf_rn(wj, q.z, acc[2]);
-        acc[3] = __fmaf_rn(wj, q.w, acc[3]);
-      } else {
-        const float2 q = __ldcg(reinterpret_cast<const float2 *>(o));
-        acc[0] = __fmaf_rn(wj, q.x, acc[0]);
-        acc[1] = __fmaf_rn(wj, q.y, acc[1]);
+#pragma unroll
+      for (int q = 0; q < kRows; ++q) {
+        const float wj = __shfl_sync(0xffffffffu, w[q], j);
+        if constexpr (E == 4) {
+          const float4 x = __ldcg(reinterpret_cast<const float4 *>(o + q * D));
+          acc[q][0] = __fmaf_rn(wj, x.x, acc[q][0]);
+          acc[q][1] = __fmaf_rn(wj, x.y, acc[q][1]);
+          acc[q][2] = __fmaf_rn(wj, x.z, acc[q][2]);
+          acc[q][3] = __fmaf_rn(wj, x.w, acc[q][3]);
+        } else {
+          const float2 x = __ldcg(reinterpret_cast<const float2 *>(o + q * D));
+          acc[q][0] = __fmaf_rn(wj, x.x, acc[q][0]);
+          acc[q][1] = __fmaf_rn(wj, x.y, acc[q][1]);
+        }
       }
     }
   }
-  const bool none = pad || m == -INFINITY;
-  const float f = 1.f / sum;
-  const long long at = (static_cast<long long>(s.x) * p.a.N + i) * p.a.Hq +
-                       static_cast<long long>(s.y) * p.G + g;
-  T *o = static_cast<T *>(p.out) + at * D + lane * E;
 #pragma unroll
-  for (int q = 0; q < E; q += 2)
-    *reinterpret_cast<uint32_t *>(o + q) = none ? 0u : pack_pair(acc[q] * f, acc[q + 1] * f, T());
-  if (p.lse && lane == 0) p.lse[at] = none ? -INFINITY : (m + log2f(sum)) * kLn2;
+  for (int q = 0; q < kRows; ++q) {
+    const unsigned r = r0 + q;
+    const int i = static_cast<int>(r / p.G), g = static_cast<int>(r - static_cast<unsigned>(i) * p.G);
+    if (i >= p.a.N) break;
+    const bool none = (ok && i >= nn) || m[q] == -INFINITY;   // padding, or nothing seen
+    const float f = 1.f / sum[q];
+    const long long at = (static_cast<long long>(s.x) * p.a.N + i) * p.a.Hq +
+                         static_cast<long long>(s.y) * p.G + g;
+    T *o = static_cast<T *>(p.out) + at * D + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; e += 2)
+      *reinterpret_cast<uint32_t *>(o + e) =
+          none ? 0u : pack_pair(acc[q][e] * f, acc[q][e + 1] * f, T());
+    if (p.lse && lane == 0) p.lse[at] = none ? -INFINITY : (m[q] + log2f(sum[q])) * kLn2;
+  }
 }
 
 // ------------------------------------------------------------------ launch
@@ -564,7 +584,8 @@ inline void plan_parts(AttnArgs &p, char *ws, int NT) {
 template <typename T, int D, int NT>
 cudaError_t launch_join(const AttnArgs &p, int ctas, cudaStream_t stream) {
   if (ctas == 1) return cudaSuccess;
-  return launch_kv(kv_attention_join<T, D, NT>, static_cast<long long>(ctas - 1) * (NT / 8), 256, 0,
+  constexpr int kBlocks = NT < kJoinBlockRows ? 1 : NT / kJoinBlockRows;
+  return launch_kv(kv_attention_join<T, D, NT>, static_cast<long long>(ctas - 1) * kBlocks, 256, 0,
                    stream, p, ctas);
 }
 // raises a kernel's shared-memory limit once per device
