@@ -158,7 +158,9 @@ def dtype_flag(t: torch.Tensor) -> int:
 
 def _stream(stream):
     if stream is None:
-        stream = torch.cuda.current_stream()
+        # the raw handle of torch.cuda.current_stream(), without building the Stream object (several
+        # microseconds of a call)
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()))
     if isinstance(stream, torch.cuda.Stream):
         return ctypes.c_void_p(stream.cuda_stream)
     return ctypes.c_void_p(int(stream))
@@ -400,12 +402,14 @@ class KVCache:
         ptrs = [_ptr(t).value if t.numel() else 0 for t in (k, v, k_scale, v_scale)]
         page = self.num_pages * self.kv_heads
         steps = [page * self.page_size * self.head_dim] * 2 + [page * 4] * 2
-        self._structs = [SpecKVCache(*(p + i * s for p, s in zip(ptrs, steps)), self.num_pages,
-                                     self.page_size, self.kv_heads, self.head_dim)
+        # (pointers to) the spec_kv_cache_t of each layer
+        self._structs = [ctypes.pointer(SpecKVCache(*(p + i * s for p, s in zip(ptrs, steps)),
+                                                    self.num_pages, self.page_size, self.kv_heads,
+                                                    self.head_dim))
                          for i in range(self.layers)]
 
     def struct(self, layer=0):
-        """The spec_kv_cache_t of one layer."""
+        """A pointer to the spec_kv_cache_t of one layer."""
         if not 0 <= layer < self.layers:
             raise ValueError(f"layer {layer} of a cache of {self.layers}")
         return self._structs[layer]
@@ -425,7 +429,7 @@ def _tokens(t, name, B, N, heads, D, dtype):
     and whose tokens lie evenly apart."""
     if not isinstance(t, torch.Tensor) or t.dtype != dtype:
         raise TypeError(f"{name}: expected a {dtype} tensor")
-    if tuple(t.shape) != (B, N, heads, D):
+    if t.shape != (B, N, heads, D):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(B, N, heads, D)}")
     if not t.numel():
         return None, heads * D
@@ -439,17 +443,30 @@ def _tokens(t, name, B, N, heads, D, dtype):
     return t.data_ptr(), step
 
 
+def _operand(t, name, numel, dtype):
+    """The pointer of a contiguous device tensor of `numel` elements of `dtype` (None stays None):
+    _expect and _ptr in one pass."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.numel() != numel:
+        _expect(t, name, numel, (dtype,))
+    if not t.is_contiguous() or not t.is_cuda:
+        return _ptr(t)   # raises, or an empty tensor
+    return t.data_ptr() or None
+
+
+_I32, _F32 = torch.int32, torch.float32
+
+
 def _kv_shared(page_table, seq_lens, new_lens, mask, status, B, N):
+    """Checks what every KV call takes; returns (pages_per_seq, the five pointers)."""
     if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2 or \
             page_table.shape[0] != B:
         raise ValueError(f"page_table must be a [{B}, pages] tensor")
-    i32 = (torch.int32,)
-    _expect(page_table, "page_table", page_table.numel(), i32)
-    _expect(seq_lens, "seq_lens", B, i32)
-    _expect(new_lens, "new_lens", B, i32)
-    _expect(mask, "mask", B * N * ((N + 31) // 32), i32)
-    _expect(status, "status", 1, i32)
-    return page_table.shape[1]
+    return (page_table.shape[1], _operand(page_table, "page_table", page_table.numel(), _I32),
+            _operand(seq_lens, "seq_lens", B, _I32), _operand(new_lens, "new_lens", B, _I32),
+            _operand(mask, "mask", B * N * ((N + 31) // 32), _I32),
+            _operand(status, "status", 1, _I32))
 
 
 def spec_kv_append(cache, layer, page_table, seq_lens, new_lens, k, v, q, q_out, rope, interleaved,
@@ -459,27 +476,27 @@ def spec_kv_append(cache, layer, page_table, seq_lens, new_lens, k, v, q, q_out,
     rope [rows, rope_dim] fp32 or None; mask_words [B, N, ceil(N/32)] int32 or None."""
     flag = _kv_dtype(k, "k")
     B, N = k.shape[:2]
-    D = cache.head_dim
-    pps = _kv_shared(page_table, seq_lens, new_lens, mask_words, status, B, N)
-    kp, ks = _tokens(k, "k", B, N, cache.kv_heads, D, k.dtype)
-    vp, vs = _tokens(v, "v", B, N, cache.kv_heads, D, k.dtype)
-    heads, qp, qs = 0, None, D
+    D, dtype = cache.head_dim, k.dtype
+    pps, table, lens, news, mask, st = _kv_shared(page_table, seq_lens, new_lens, mask_words, status,
+                                                  B, N)
+    kp, ks = _tokens(k, "k", B, N, cache.kv_heads, D, dtype)
+    vp, vs = _tokens(v, "v", B, N, cache.kv_heads, D, dtype)
+    heads, qp, qs, qo = 0, None, D, None
     if q is not None:
         heads = q.shape[2] if q.dim() == 4 else -1
-        qp, qs = _tokens(q, "q", B, N, heads, D, k.dtype)
-        _expect(q_out, "q_out", q.numel(), (k.dtype,))
+        qp, qs = _tokens(q, "q", B, N, heads, D, dtype)
+        qo = _operand(q_out, "q_out", q.numel(), dtype)
     rows = width = 0
+    rp = None
     if rope is not None:
         if not isinstance(rope, torch.Tensor) or rope.dim() != 2:
             raise ValueError("rope must be a [rows, rope_dim] tensor")
         rows, width = rope.shape
-        _expect(rope, "rope", rows * width, (torch.float32,))
-    _expect(positions, "positions", B * N, (torch.int32,))
+        rp = _operand(rope, "rope", rows * width, _F32)
+    pos = _operand(positions, "positions", B * N, _I32)
     return load_library().spec_kv_append(
-        ctypes.byref(cache.struct(layer)), _ptr(page_table), pps, _ptr(seq_lens), _ptr(new_lens), B,
-        N, kp, ks, vp, vs, qp, qs, heads, _ptr(q_out) if q is not None else None, flag, _ptr(rope),
-        rows, width, int(bool(interleaved)), _ptr(positions), _ptr(mask_words), _ptr(status),
-        _stream(stream))
+        cache.struct(layer), table, pps, lens, news, B, N, kp, ks, vp, vs, qp, qs, heads, qo, flag,
+        rp, rows, width, int(bool(interleaved)), pos, mask, st, _stream(stream))
 
 
 def spec_kv_attention_workspace_bytes(B: int, N: int, q_heads: int, kv_heads: int,
@@ -495,13 +512,12 @@ def spec_kv_attention(cache, layer, page_table, seq_lens, new_lens, q, scale, ma
     B, N, heads, D = q.shape
     if D != cache.head_dim:
         raise ValueError(f"q: head_dim {D}, the cache's is {cache.head_dim}")
-    pps = _kv_shared(page_table, seq_lens, new_lens, mask_words, status, B, N)
+    pps, table, lens, news, mask, st = _kv_shared(page_table, seq_lens, new_lens, mask_words, status,
+                                                  B, N)
     qp, qs = _tokens(q, "q", B, N, heads, D, q.dtype)
-    _expect(out, "out", q.numel(), (q.dtype,))
-    _expect(lse, "lse", B * N * heads, (torch.float32,))
     return load_library().spec_kv_attention(
-        ctypes.byref(cache.struct(layer)), _ptr(page_table), pps, _ptr(seq_lens), _ptr(new_lens), B,
-        N, qp, qs, heads, flag, float(scale), _ptr(mask_words), _ptr(out), _ptr(lse), _ptr(status),
+        cache.struct(layer), table, pps, lens, news, B, N, qp, qs, heads, flag, float(scale), mask,
+        _operand(out, "out", q.numel(), q.dtype), _operand(lse, "lse", B * N * heads, _F32), st,
         _ptr(workspace), _nbytes(workspace), _stream(stream))
 
 
@@ -512,14 +528,12 @@ def spec_kv_commit(cache, page_table, seq_lens, path_nodes, accept_len, out_lens
     if not isinstance(path_nodes, torch.Tensor) or path_nodes.dim() != 2:
         raise ValueError("path_nodes must be a [B, N] tensor")
     B, N = path_nodes.shape
-    i32 = (torch.int32,)
-    pps = _kv_shared(page_table, seq_lens, None, None, status, B, N)
-    _expect(path_nodes, "path_nodes", B * N, i32)
-    _expect(accept_len, "accept_len", B, i32)
-    _expect(out_lens, "out_lens", B, i32)
+    pps, table, lens, _, _, st = _kv_shared(page_table, seq_lens, None, None, status, B, N)
     return load_library().spec_kv_commit(
-        ctypes.byref(cache.struct(0)), cache.layers, _ptr(page_table), pps, _ptr(seq_lens), B, N,
-        _ptr(path_nodes), _ptr(accept_len), _ptr(out_lens), _ptr(status), _stream(stream))
+        cache.struct(0), cache.layers, table, pps, lens, B, N,
+        _operand(path_nodes, "path_nodes", B * N, _I32),
+        _operand(accept_len, "accept_len", B, _I32), _operand(out_lens, "out_lens", B, _I32), st,
+        _stream(stream))
 
 
 # ------------------------------------------------------------------ conveniences (allocation)
