@@ -47,12 +47,13 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, u
       "r"(a), "l"(b), "r"(idesc), "r"(acc));
 }
 // Registers: 896 threads start with 72 each; the softmax warps, which hold a half row's weights, take
-// more, which the others give up (512 x 96 + 384 x 40 = 896 x 72).
+// more, which the others give up (512 x 80 + 384 x 56 < 896 x 72). At 96 and 40 the copies' and MMAs'
+// warps spilled, which is on every tile's path: 212 us for 167 (32 trees of 64 nodes, 32 key heads).
 __device__ __forceinline__ void regs_take() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 80;");
 }
 __device__ __forceinline__ void regs_give() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
 }
 // barrier of the two warps that share rows: true in both if `p` was in any of their threads
 __device__ __forceinline__ bool pair_any(int id, bool p) {
@@ -84,22 +85,26 @@ struct RowsCfg {
   static constexpr int kOffV16 = S * 2 * kSideBytes;
   static constexpr int kOffQ = kOffV16 + 2 * kVfBytes;
   static constexpr int kOffSmall = kOffQ + RTC * kTerms * kQBytes;
+  // A tile's page constants give way to those of kPages tiles later, which the producer writes when the
+  // scores of the tile S before those are done, so after the values of at least two tiles more.
+  static constexpr int kPages = RTC == 2 ? 4 : 8;
+  static_assert(S + (RTC == 2 ? 2 : 3) <= kPages, "page constants are read by then");
   static constexpr uint32_t kColS = 0, kColO = 256;      // tensor memory: S of each group, O of each
 };
 
 struct __align__(16) RowsSmall {
   uint64_t full[4], empty[4];    // stages
   uint64_t vfull[2], vfree[2];   // widened V
+  uint64_t cfull[8];             // page constants
   uint64_t sfull[2], pfull[2], ofull[2];   // by group
   uint64_t qfull, done;
-  float ks[4][8], vs[4][8];
-  float4 page[2][8];             // by 16 tokens: scale log2(e) ks, log2 vs, 1 / vs
   uint32_t vnan[2][4];           // tokens whose values hold NaN (tiles with new tokens)
   uint32_t tmem;
 };
+// + by tile and 16 tokens the page constants (scale log2(e) ks, log2 vs, 1 / vs) of the last kPages tiles;
 // + the queries' units, which, once read, leave their place to the row maxima [group][half][row]
 template <class F> constexpr int rows_smem() {
-  return F::kOffSmall + static_cast<int>(sizeof(RowsSmall)) + 512 * 4;
+  return F::kOffSmall + static_cast<int>(sizeof(RowsSmall)) + 512 * 4 + F::kPages * 8 * 16;
 }
 
 // Bits of the 32 slots from number `j0` among the new tokens on (negative: the cached ones, which
@@ -192,13 +197,14 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
                              const __grid_constant__ AttnArgs p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   RowsSmall &sm = *reinterpret_cast<RowsSmall *>(smem + F::kOffSmall);
-  float *qs = reinterpret_cast<float *>(smem + F::kOffSmall + sizeof(RowsSmall));
+  float4 *pages = reinterpret_cast<float4 *>(smem + F::kOffSmall + sizeof(RowsSmall));
+  float *qs = reinterpret_cast<float *>(pages + F::kPages * 8);
   constexpr int NT = F::NT, D = F::D;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int s = 0; s < F::S; ++s) {
-      tc::mbar_init(&sm.full[s], 33);     // 32 lanes' scales and the byte count
+      tc::mbar_init(&sm.full[s], 1);
       tc::mbar_init(&sm.empty[s], 1 + kWidenWarps);   // the score MMAs; the widening warps
     }
     for (int i = 0; i < 2; ++i) {
@@ -208,6 +214,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       tc::mbar_init(&sm.pfull[i], kGroupWarps);
       tc::mbar_init(&sm.ofull[i], 1);
     }
+    for (int i = 0; i < F::kPages; ++i) tc::mbar_init(&sm.cfull[i], 1);
     tc::mbar_init(&sm.qfull, 1);
     tc::mbar_init(&sm.done, 1);
     tc::mbar_fence_init();
@@ -233,20 +240,31 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     const int per_tile = kTile >> p.a.page_shift;
     for (int t = t0; t < t1 && ok;) {
       const int cnt = min(x.tiles - skip, t1 - t);
-      // the page number of this lane's page in tile k of the segment (0 past the end)
+      // this lane's page of tile k of the segment: its number (0 past the end), and its scales, which
+      // are on their way while the tile before waits for room
       const int32_t *table = p.a.page_table + static_cast<long long>(x.b) * p.a.pps;
-      auto page_of = [&](int k) {
-        const int slot = (skip + k) * kTile + (lane << p.a.page_shift);
-        return lane < per_tile && slot < x.end ? __ldg(table + (slot >> p.a.page_shift)) : 0;
+      auto wanted = [&](int k) {
+        return lane < per_tile && (skip + k) * kTile + (lane << p.a.page_shift) < x.end;
       };
-      int next = page_of(0);
+      auto page_of = [&](int k) {
+        return k < cnt && wanted(k) ? __ldg(table + (skip + k) * per_tile + lane) : 0;
+      };
+      auto valid = [&](int page) { return page >= 0 && page < p.a.num_pages; };
+      int page = page_of(0), next = page_of(1);
+      auto scales_of = [&](int pg, bool want) {
+        const int head = pg * p.a.Hkv + x.h;
+        return want && valid(pg) ? make_float2(__ldg(p.a.k_scale + head), __ldg(p.a.v_scale + head))
+                                 : make_float2(NAN, NAN);   // what reads a bad page is NaN
+      };
+      float2 sc = scales_of(page, wanted(0));
       for (int k = 0; k < cnt && ok; ++k, ++it) {
         const int s = it % F::S;
-        const int slot = (skip + k) * kTile + (lane << p.a.page_shift);
-        const bool want = lane < per_tile && slot < x.end;
-        const int page = next;
-        if (k + 1 < cnt) next = page_of(k + 1);   // on its way while this tile waits for room
-        const bool good = want && page >= 0 && page < p.a.num_pages;
+        const bool want = wanted(k), good = want && valid(page);
+        const float2 now = sc;
+        const int cur = page;
+        page = next;
+        next = page_of(k + 2);
+        sc = scales_of(page, k + 1 < cnt && wanted(k + 1));
         if (want && !good) set_status(p.a.status, SPEC_ERR_PAGE);
         const uint32_t goods = __ballot_sync(0xffffffffu, good);
         wait(&sm.empty[s], ((it / F::S) & 1) ^ 1);
@@ -255,19 +273,24 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
           tc::mbar_expect_tx(&sm.full[s], __popc(goods) * 2 * (D << p.a.page_shift));
         __syncwarp();
         if (good) {
-          const int head = page * p.a.Hkv + x.h;
-          const int row = head << p.a.page_shift;
+          const int row = (cur * p.a.Hkv + x.h) << p.a.page_shift;
           const uint32_t dst = tc::saddr(smem + s * 2 * F::kSideBytes) +
                                (lane << p.a.page_shift) * D;
           tma_load_2d(dst, &map_k, 0, row, &sm.full[s]);
           tma_load_2d(dst + F::kSideBytes, &map_v, 0, row, &sm.full[s]);
-          copy4(&sm.ks[s][lane], p.a.k_scale + head);
-          copy4(&sm.vs[s][lane], p.a.v_scale + head);
-          mbar_arrive_copies(&sm.full[s]);
-        } else {
-          if (want) sm.ks[s][lane] = sm.vs[s][lane] = NAN;   // what reads the page is NaN
-          mbar_arrive(&sm.full[s]);
         }
+        if (lane < per_tile) {
+          // a NaN scale makes its tokens' scores NaN through log2 vs; 1 / vs multiplies the zero weights
+          // of the rows that do not see them too, so it stays finite, as everything past the end
+          const float vse = now.y < kMinValueScale ? kMinValueScale : now.y;
+          const float4 c = want ? make_float4(now.x * p.scale2, __log2f(vse),
+                                              now.y == now.y ? __frcp_rn(vse) : 1.f, 0.f)
+                                : make_float4(0.f, 0.f, 0.f, 0.f);
+          const int chunks = 8 / per_tile;
+          for (int e = 0; e < chunks; ++e) pages[it % F::kPages * 8 + lane * chunks + e] = c;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.cfull[it % F::kPages]);
       }
       t += cnt;
       skip = 0;
@@ -361,17 +384,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         uint4 w[Widen<D, kWidenThreads>::kSteps];
         fetch_values<D, kWidenThreads>(smem + s * 2 * F::kSideBytes + F::kSideBytes, wtid,
                                        x.end - slot0, w);
-        float4 page = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (wtid < 8 && slot0 + 16 * wtid < x.end) {   // (else no scale was copied)
-          const float ks = sm.ks[s][16 * wtid >> p.a.page_shift];
-          const float vs = sm.vs[s][16 * wtid >> p.a.page_shift];
-          // a NaN scale (a bad page) makes its tokens' scores NaN through log2 vs; 1 / vs multiplies
-          // the zero weights of the rows that do not see them too, so it stays finite
-          const float vse = vs < kMinValueScale ? kMinValueScale : vs;
-          page = make_float4(ks * p.scale2, __log2f(vse), vs == vs ? __frcp_rn(vse) : 1.f, 0.f);
-        }
         wait(&sm.vfree[buf], ((it >> 1) & 1) ^ 1);
-        if (wtid < 8) sm.page[buf][wtid] = page;
         if (slot0 + kTile > min(x.len, x.end)) {
           if (wtid < 4) sm.vnan[buf][wtid] = 0;
           widen_sync();
@@ -404,6 +417,9 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     float *share = reinterpret_cast<float *>(smem + F::kOffQ);
     float *top = qs + grp * 256;
     int it = 0, use = 0;   // tiles so far; this group's units so far
+    auto look = [&](uint64_t *bar, int parity) {   // a lane's wait
+      if (!tc::mbar_try(bar, parity) && ok) ok = wait_for(bar, parity);
+    };
     for (int t = t0; t < t1;) {
       const int cnt = min(x.tiles - skip, t1 - t);
       load_queries<typename F::T, D, NT, 128, F::kTerms, kSoftThreads>(p, x, tid, smem + F::kOffQ,
@@ -429,19 +445,21 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
 #pragma unroll
           for (int w = 0; w < 2; ++w)
             see[w] = live ? seen_bits(p, x.b, i, slot0 + 64 * half + 32 * w - x.len, x.n) : 0u;
-        wait(&sm.vfull[buf], (tile >> 1) & 1);   // its page scales and NaN marks
         uint32_t nan[2] = {0, 0};
         if (edge) {
+          look(&sm.vfull[buf], (tile >> 1) & 1);
           nan[0] = sm.vnan[buf][2 * half];
           nan[1] = sm.vnan[buf][2 * half + 1];
         }
-        const float4 *page = sm.page[buf] + 4 * half;
-        wait(&sm.sfull[grp], use & 1);
+        const float4 *page = pages + (tile % F::kPages * 8 + 4 * half);
+        look(&sm.cfull[tile % F::kPages], (tile / F::kPages) & 1);
+        look(&sm.sfull[grp], use & 1);
+        __syncwarp();
         tc::fence_after_sync();
         if (!idle) {
           uint32_t h[32];
           float sum = 0.f;
-          bool fresh = __any_sync(0xffffffffu, nm == kNoRef);   // a row's first tile, mostly
+          bool fresh = k == k0;   // (a row that sees its first token later asks for it by its weights)
 #pragma unroll 1
           for (;;) {
             if (fresh) {   // new references: the larger of the halves' maxima
