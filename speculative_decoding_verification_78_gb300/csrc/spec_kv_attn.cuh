@@ -208,6 +208,7 @@ __device__ __forceinline__ int head_tiles(const AttnArgs &p, int b) {
   int len, n;
   const bool ok = kv_lengths(p.a, b, len, n);
   int s = 0;
+#pragma unroll 1
   for (int rt = 0; rt < p.RT; ++rt) s += tiles_for(item_end<NT>(p, len, n, ok, rt));
   return s;
 }
@@ -247,14 +248,17 @@ __device__ __forceinline__ int range_of(int T, int t, int G) {
 struct LocateScratch {
   int b0, skip0;
   int warp_sum[32];
+  Item x;
+  int t0, t1, total, skip;
 };
 template <int NT, int kThreads>
-__device__ void locate(const AttnArgs &p, LocateScratch &sm, int &t0, int &t1, int &total, Item &x,
-                       int &skip) {
+__device__ __forceinline__ void locate(const AttnArgs &p, LocateScratch &sm, int &t0, int &t1,
+                                       int &total, Item &x, int &skip) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int share = (p.a.B + kThreads - 1) / kThreads;
   const int lo = min(p.a.B, tid * share), hi = min(p.a.B, lo + share);
   int mine = 0;
+#pragma unroll 1
   for (int b = lo; b < hi; ++b) mine += head_tiles<NT>(p, b) * p.a.Hkv;
   int incl = mine;
 #pragma unroll
@@ -264,41 +268,59 @@ __device__ void locate(const AttnArgs &p, LocateScratch &sm, int &t0, int &t1, i
   }
   if (lane == 31) sm.warp_sum[warp] = incl;
   __syncthreads();
-  int before = 0;
-  total = 0;
-#pragma unroll
+  int before = 0, all = 0;
+#pragma unroll 1
   for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) before += sm.warp_sum[w];
-    total += sm.warp_sum[w];
+    const int v = sm.warp_sum[w];
+    if (w < warp) before += v;
+    all += v;
   }
-  t0 = range_start(total, blockIdx.x, gridDim.x);
-  t1 = range_start(total, blockIdx.x + 1, gridDim.x);
+  const int first = range_start(all, blockIdx.x, gridDim.x);
   int at = before + incl - mine;
-  if (t0 >= at && t0 < at + mine) {
+  if (first >= at && first < at + mine) {
     int b = lo;
+#pragma unroll 1
     for (;; ++b) {
       const int n = head_tiles<NT>(p, b) * p.a.Hkv;
-      if (t0 < at + n) break;
+      if (first < at + n) break;
       at += n;
     }
     sm.b0 = b;
-    sm.skip0 = t0 - at;
+    sm.skip0 = first - at;
   }
   __syncthreads();
-  x.b = sm.b0;
-  x.rt = 0;
-  skip = sm.skip0;
-  __syncthreads();   // the scratch may be put to other use
-  if (t0 >= t1) return;
-  const int per_head = head_tiles<NT>(p, x.b);
-  x.h = skip / per_head;
-  skip -= x.h * per_head;
-  item_load<NT>(p, x);
-  while (skip >= x.tiles) {
-    skip -= x.tiles;
-    ++x.rt;
-    item_load<NT>(p, x);
+  // one thread works out the item; all take it from shared memory, so that nothing of the search stays
+  // in (or is spilled from) the registers of the roles that follow
+  if (tid == 0) {
+    sm.t0 = first;
+    sm.t1 = range_start(all, blockIdx.x + 1, gridDim.x);
+    sm.total = all;
+    Item y{};
+    int left = 0;
+    if (sm.t0 < sm.t1) {
+      y.b = sm.b0;
+      left = sm.skip0;
+      const int per_head = head_tiles<NT>(p, y.b);
+      y.h = left / per_head;
+      left -= y.h * per_head;
+      item_load<NT>(p, y);
+#pragma unroll 1
+      while (left >= y.tiles) {
+        left -= y.tiles;
+        ++y.rt;
+        item_load<NT>(p, y);
+      }
+    }
+    sm.x = y;
+    sm.skip = left;
   }
+  __syncthreads();
+  x = sm.x;
+  t0 = sm.t0;
+  t1 = sm.t1;
+  total = sm.total;
+  skip = sm.skip;
+  __syncthreads();   // the scratch may be put to other use
 }
 // What the join needs to know of the CTA's range: its first item and the item's tiles before it,
 // the item's tiles, the range, and the length of the line.
