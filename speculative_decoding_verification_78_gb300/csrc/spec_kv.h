@@ -1,4 +1,4 @@
-// spec_kv.cuh -- what the KV-cache kernels share: arguments, e4m3 and 16-bit element access, page
+// spec_kv.h -- what the KV-cache kernels share: arguments, e4m3 and 16-bit element access, page
 // scales, and launches.
 #pragma once
 

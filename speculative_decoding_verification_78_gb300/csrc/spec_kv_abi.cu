@@ -2,7 +2,7 @@
 // dispatch to the kernels.
 #include <math.h>
 
-#include "spec_kv.cuh"
+#include "spec_kv.h"
 #include "spec_verify.h"
 
 using namespace specv;

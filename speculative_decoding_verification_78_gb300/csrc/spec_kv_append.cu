@@ -9,7 +9,7 @@
 // twice a head's bytes, are loaded once for all of them; calls with few pages give each head a CTA. The
 // queries' warps take up to eight head groups of a token on the same cosines and sines. A page that held
 // tokens has them stored again only when its scale grows.
-#include "spec_kv.cuh"
+#include "spec_kv.h"
 
 namespace specv {
 
@@ -252,7 +252,8 @@ __global__ void __launch_bounds__(kThreads, 512 / kThreads)
     const float inv = 1.f / s;   // exact for a power of two
 #pragma unroll
     for (int k = 0; k < kU; ++k) {
-      if (row[k] < 0) continue;
+      if (row[k] < 0 || !SPEC_CHECK(a, row[k] < a.page && head < static_cast<long long>(a.num_pages) * a.Hkv))
+        continue;
       const int slot = p0 + row[k];
       uint2 *oa = reinterpret_cast<uint2 *>(dst + row[k] * a.D + un[k].a);
       uint2 *ob = reinterpret_cast<uint2 *>(dst + row[k] * a.D + un[k].b);
@@ -418,7 +419,7 @@ __global__ void __launch_bounds__(32 * kCommitWarps)
     for (int k = k0; k < k1; k += per) {
       if (!kept) mine = source(k + sub, f);
       __syncwarp();   // every row of the step is read before any is written
-      if (mine)
+      if (mine && SPEC_CHECK(a, len + k + sub >= p0 && len + k + sub < p0 + a.page))
         *reinterpret_cast<uint2 *>(dst + (len + k + sub - p0) * a.D + d0) = floats_to_e4m3(f, inv);
       __syncwarp();
     }

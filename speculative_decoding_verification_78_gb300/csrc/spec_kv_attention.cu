@@ -9,7 +9,7 @@
 // denominator adds, so bytes of pages with unlike scales meet in one accumulator.
 //
 // Orientation. Tokens, of which there are always many, lie along the MMA's 128 rows, and the query
-// rows (1 to 128 of them, padded to 16) along its columns: S^T = K Q^T, O^T = V^T P^T. Both cost
+// rows (1 to 32 of them, padded to 16) along its columns: S^T = K Q^T, O^T = V^T P^T. Both cost
 // tensor time in proportion to the query rows that exist. K's e4m3 bytes are an MMA operand as TMA
 // lands them: Q is the sum of 2 (bf16) or 3 (fp16) e4m3 terms, whose products accumulate in the
 // same fp32 accumulator (two terms hold bf16's 8 significant bits exactly down to 2^-9 of the
@@ -26,7 +26,15 @@
 // tile) items form one line, CTA c of G takes tiles [T c / G, T (c+1) / G). An item inside one
 // CTA's range is written directly; the parts of one that crosses ranges go to the workspace (at
 // most two per CTA), and a second kernel joins them in order, so results do not depend on timing.
-#include "spec_kv_attn.cuh"
+//
+// What bounds it: HBM, which it does not quite fill. 64 sequences of about 15000 tokens, one new token,
+// 32 query and 8 key heads of 128: 321 us for 1.95 GB, 6.07 TB/s (90 % of the measured copy rate). A
+// tile's chain (wait, widen, scores, weights, barrier) takes a group about 3600 clocks, which two groups
+// in turn hide but for a tenth; issuing the 16 MMAs takes their own warp 950 of a tile's 1650. With one
+// group 607 us; with the MMAs issued from a branch of one lane, where their descriptors are not known to
+// be uniform, 503 us. Tried and not kept: the query terms as columns side by side (8 MMAs fewer, the terms
+// added by the softmax: 362 against 333 us), the page constants worked out by the copying warp (407).
+#include "spec_kv_attn.h"
 
 namespace specv {
 
@@ -72,9 +80,8 @@ struct Cfg {
   static constexpr int EC = NT / 4;                      // columns of a thread in the epilogue
   static constexpr int ECH = EC < 16 ? EC : 16;
   static constexpr int kSideBytes = kTile * D;           // K or V of a stage
-  static constexpr int kPSpan = NT >= 64 ? 128 : 2 * NT; // bytes of a row of P
-  static constexpr int kPBlocks = NT > 64 ? NT / 64 : 1;
-  static constexpr int kPBytes = kTile * kPSpan * kPBlocks;
+  static constexpr int kPSpan = 2 * NT;                  // bytes of a row of P
+  static constexpr int kPBytes = kTile * kPSpan;
   static constexpr int kVfBytes = kTile * D * 2;
   static constexpr int kQBytes = NT * D;                 // one term
   static constexpr int kOffV16 = S * 2 * kSideBytes;
@@ -181,8 +188,7 @@ __device__ __forceinline__ bool weigh(const AttnArgs &p, const Item &x, const To
       }
     }
     const int n = col0 + c0;
-    const uint32_t at = swz<F::kPSpan>(row * F::kPSpan + (n % (F::kPSpan / 2)) * 2);
-    *reinterpret_cast<uint4 *>(sp + (n / (F::kPSpan / 2)) * (kTile * F::kPSpan) + at) =
+    *reinterpret_cast<uint4 *>(sp + swz<F::kPSpan>(row * F::kPSpan + n * 2)) =
         make_uint4(h[0], h[1], h[2], h[3]);
   }
   return big > kTrigger;
@@ -337,7 +343,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       const uint64_t da = smem_desc<128>(base + F::kOffV16 + grp * F::kVfBytes,
                                          F::D > 64 ? kTile * 128 : 0, 1024);
       const uint64_t db = smem_desc<F::kPSpan>(base + F::kOffP + grp * F::kPBytes,
-                                               kTile * F::kPSpan, 8 * F::kPSpan);
+                                               16, 8 * F::kPSpan);
       const uint32_t d = tmem + (2 + grp) * F::NT;
       if (elect_one()) {
 #pragma unroll
@@ -571,6 +577,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             const float f0 = fac[n], f1 = fac[F::NT + n];
             const float v = (f0 == 0.f ? 0.f : __uint_as_float(o[c]) * f0) +
                             (f1 == 0.f ? 0.f : __uint_as_float(o1[c]) * f1);
+            if (!SPEC_CHECK(p.a, n < F::NT && part < 2LL * gridDim.x && x.b < p.a.B)) continue;
             if (!whole) {
               p.part_o[(part * F::NT + n) * F::D + row] = v;
             } else {

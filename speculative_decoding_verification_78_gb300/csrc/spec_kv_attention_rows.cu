@@ -14,14 +14,24 @@
 // warps of their own, once for all rows of the CTA.
 //
 // Two groups of eight softmax warps (two for each 32 rows, half of the tile's tokens each) work half a
-// step apart, so that the tensor cores have one group's
-// MMAs while the other group exponentiates: with more than 128 rows each group has 128 rows of its
-// own and both take every tile; with fewer, the groups take the tiles in turn and are joined at the
-// end of the item. Unit u of a segment belongs to group u & 1; 
+// step apart, so that the tensor cores have one group's MMAs while the other group exponentiates: with
+// more than 128 rows each group has 128 rows of its own and both take every tile; with fewer, the groups
+// take the tiles in turn and are joined at the end of the item. Unit u of a segment belongs to group
+// u & 1; values(u) and then scores(u + 2) are issued as soon as its weights are there.
 //
-// What bounds it: a 256-row tile of 128 tokens (D = 128) is 2048 clocks of MMA (two e4m3 terms cost
-// what one 16-bit operand would) and 1024 of ex2.
-#include "spec_kv_attn.cuh"
+// What bounds it (D = 128, measured with clock counters): a 256-row tile of 128 tokens costs 2460 clocks
+// of MMA (two e4m3 terms cost what one 16-bit operand would: 2048 at the nominal rate; the operands of
+// both MMAs, V's widening and the copies want about 2400 clocks of shared-memory bandwidth) and 1380 of
+// weights (345 clocks a warp for 64 scores of 32 rows: ex2 256 of them). A group's turn is longer than
+// either, about 3600: its weights, a hand-over to the MMA warp, its MMAs behind the other group's, a
+// hand-over back. 32 trees of 64 nodes, four query heads a key head, 8192 tokens: 250 us, 1030 TFLOP/s;
+// with one MMA warp waiting for each hand-over in turn 294 us, with full rows per thread 367 us. Dropping
+// the second e4m3 term, half of the value MMAs or the widening (wrong results, for timing only) gains
+// 3 to 10 % each: no one part bounds it.
+// Tried and not kept: three stages of K and V for 256 rows (265 us), scores and values issued by two warps
+// (294), the next item's queries posted before the accumulators are read (262), tiles widened by two lots
+// of four warps (267), all 64 scores of a thread loaded at once (276).
+#include "spec_kv_attn.h"
 
 namespace specv {
 
@@ -556,7 +566,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         if (F::RTC == 1) tmem_ld(tlane + F::kColO + D + c, o1);
         tmem_wait(o);
         if (F::RTC == 1) tmem_wait(o1);
-        if (i < p.a.N) {
+        if (i < p.a.N && SPEC_CHECK(p.a, n < NT && part < 2LL * gridDim.x && x.b < p.a.B && gq < p.G)) {
           float v[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {

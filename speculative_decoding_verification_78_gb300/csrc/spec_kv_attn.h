@@ -1,4 +1,4 @@
-// spec_kv_attn.cuh -- what the two attention kernels share: tensor-core and barrier helpers, the line
+// spec_kv_attn.h -- what the two attention kernels share: tensor-core and barrier helpers, the line
 // of 128-token tiles and its even cut over the SMs, queries as e4m3 terms, values widened to fp16, and
 // the join of the parts of an item that several CTAs worked on.
 #pragma once
@@ -7,7 +7,7 @@
 
 #include <atomic>
 
-#include "spec_kv.cuh"
+#include "spec_kv.h"
 #include "spec_tc.cuh"
 
 namespace specv {

@@ -621,3 +621,109 @@ def test_verify_step(sv):
     o1, _, _ = sv.kv_attention(plain, table, last, qp[:, 3:].contiguous())
     err = (out[:, 8].float() - o1[:, 0].float()).abs().max()
     assert float(err) < 2.0 ** -4
+
+
+def test_example():
+    """The example's steps run, accept some drafts, and repeat themselves token for token."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        "verify_step.py")
+    spec = importlib.util.spec_from_file_location("verify_step", path)
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    emitted, lens, status = ex.run(steps=2, batch=2, nodes=8, layers=2)
+    assert int(status.item()) == 0
+    assert all(len(e) >= 3 for e in emitted) and any(len(e) > 3 for e in emitted)
+    again, lens2, _ = ex.run(steps=2, batch=2, nodes=8, layers=2)
+    assert again == emitted and torch.equal(lens, lens2)
+
+
+# ------------------------------------------------------------------ large offsets, streams, checks
+
+def test_offsets_past_32_bits(sv):
+    """A pool of more than 4 GiB a side: pages at its far end."""
+    Hkv, D, page, pages = 8, 128, 128, 33000
+    assert pages * Hkv * page * D > 1 << 32
+    cache = sv.new_kv_cache(pages, Hkv, D, page)
+    small = sv.new_kv_cache(8, Hkv, D, page)
+    rng = np.random.default_rng(71)
+    lens = torch.tensor([0, 0], dtype=torch.int32, device="cuda")
+    far = torch.tensor([[32999, 32768], [16384, 32991]], dtype=torch.int32, device="cuda")
+    near = torch.tensor([[0, 3], [5, 1]], dtype=torch.int32, device="cuda")
+    x = rand16(rng, (2, 200, 16 + 2 * Hkv, D), torch.bfloat16)
+    q, k, v = x.split([16, Hkv, Hkv], 2)
+    out = []
+    for c, t in ((cache, far), (small, near)):
+        qo, st = sv.kv_append(c, t, lens, k, v, q=q)
+        o, lse, st = sv.kv_attention(c, t, lens, qo, return_lse=True, status=st)
+        now = lens + 150
+        path = torch.full((2, 50), -1, dtype=torch.int32, device="cuda")
+        path[:, :3] = torch.tensor([0, 20, 49], dtype=torch.int32)
+        new, st = sv.kv_commit(c, t, now, path, torch.full((2,), 2, dtype=torch.int32, device="cuda"),
+                               status=st)
+        o1, _, st = sv.kv_attention(c, t, new - 1, q[:, :1].contiguous(), status=st)
+        assert int(st.item()) == 0
+        out.append((o, lse, new, o1))
+    for a, b in zip(*out):
+        assert torch.equal(a, b)
+
+
+def test_two_streams_at_once(sv):
+    """Calls in flight on two streams, each with its own workspace."""
+    cs = [Case(72 + i, [3000 + 500 * i, 700, 90], 5, 2, 128, 64) for i in range(2)]
+    qs = [rand16(c.rng, (3, 5, 8 * (i + 1), 128), torch.bfloat16) for i, c in enumerate(cs)]
+    want = [check_attention(sv, c, q)[0] for c, q in zip(cs, qs)]
+    args = [(c.cache(sv), *c.dev("table", "lens"), q) for c, q in zip(cs, qs)]
+    streams = [torch.cuda.Stream() for _ in cs]
+    ws = [sv.new_attention_workspace(3, 5, q.shape[2], 2, 128) for q in qs]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(10):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(sv.kv_attention(*args[i], workspace=ws[i])[0])
+    torch.cuda.synchronize()
+    for g, w in zip(got, want):
+        for o in g:
+            assert torch.equal(o, w)
+
+
+def test_checked_build(sv):
+    """The checked build (indices range-checked) reports nothing and gives the same results."""
+    import speculative_decoding_verification_78_gb300._binding as bnd
+    plain, checked = bnd.load_library(), bnd.load_library(checked=True)
+    saved = bnd.load_library
+    results = []
+    for lib in (plain, checked):
+        bnd.load_library = lambda checked=False, lib=lib: lib
+        try:
+            out = []
+            for N, Hq, dtype, tree in ((1, 8, torch.bfloat16, False), (9, 8, torch.float16, True),
+                                       (40, 16, torch.bfloat16, True), (70, 4, torch.bfloat16, False)):
+                c = Case(81 + N, [0, 77, 600], N, 2, 128, 32)
+                cache = c.cache(sv)
+                table, lens = c.dev("table", "lens")
+                words = tree_words(c.rng, 3, N, sv) if tree else None
+                x = rand16(c.rng, (3, N, Hq + 4, 128), dtype)
+                q, k, v = x.split([Hq, 2, 2], 2)
+                rope = torch.from_numpy(rope_table(800, 128)).cuda()
+                qo, st = sv.kv_append(cache, table, lens, k, v, q=q, rope=rope, mask=words)
+                o, lse, st = sv.kv_attention(cache, table, lens, qo, mask=words, return_lse=True,
+                                             status=st)
+                path = torch.full((3, N), -1, dtype=torch.int32, device="cuda")
+                acc = min(N - 1, 1)
+                path[:, 0] = 0
+                if acc:
+                    path[:, 1] = N - 1
+                new, st = sv.kv_commit(cache, table, lens, path,
+                                       torch.full((3,), acc, dtype=torch.int32, device="cuda"),
+                                       status=st)
+                torch.cuda.synchronize()
+                assert int(st.item()) == 0
+                out += [qo, o, lse, new, cache.k.view(torch.uint8), cache.k_scale]
+            results.append(out)
+        finally:
+            bnd.load_library = saved
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
