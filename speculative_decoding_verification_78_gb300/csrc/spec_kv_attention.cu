@@ -408,8 +408,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     };
     for (int t = t0; t < t1;) {
       const int cnt = min(x.tiles - skip, t1 - t);
-      load_queries<typename F::T, F::D, F::NT, F::NT, F::kTerms, kSoftThreads>(p, x, tid,
-                                                                               smem + F::kOffQ, qs);
+      load_queries<typename F::T, F::D, F::NT, F::NT, F::kTerms, kSoftThreads>(
+          p, x, RowMap::of<F::NT>(p, x.rt), F::NT, tid, smem + F::kOffQ, qs);
       if (tid < F::NT) {
         nm[tid] = nm[F::NT + tid] = kNoRef;
         const long long i = (static_cast<long long>(x.rt) * F::NT + tid) / p.G;

@@ -212,6 +212,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
   constexpr int NT = F::NT, D = F::D;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // warps of 32 MMA rows that any item uses; the softmax warps of the others take no part in the tiles
+  const int quads = F::RTC == 2 ? 4 : static_cast<int>((static_cast<unsigned>(p.a.N) * p.G + 31) / 32);
   if (tid == 0) {
     for (int s = 0; s < F::S; ++s) {
       tc::mbar_init(&sm.full[s], 1);
@@ -221,7 +223,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       tc::mbar_init(&sm.vfull[i], kWidenWarps);
       tc::mbar_init(&sm.vfree[i], 1);
       tc::mbar_init(&sm.sfull[i], 1);
-      tc::mbar_init(&sm.pfull[i], kGroupWarps);
+      tc::mbar_init(&sm.pfull[i], 2 * quads);
       tc::mbar_init(&sm.ofull[i], 1);
     }
     for (int i = 0; i < F::kPages; ++i) tc::mbar_init(&sm.cfull[i], 1);
@@ -239,9 +241,10 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
   const uint32_t tmem = sm.tmem;
   if (tid == 0) publish_range(p, x, skip, t0, t1, total);
   bool ok = true;   // false after a wait gave up: no further waits, and no further work is issued
-  auto wait = [&](uint64_t *bar, int parity) {   // whole warps
-    ok = ok && wait_for(bar, parity);
-    ok = __all_sync(0xffffffffu, ok);
+  // A lane's wait; after one that gave up its lane waits no more but keeps step with its warp, whose
+  // loops end by their counts (an `ok` agreed on by vote cost each hand-over about 60 clocks).
+  auto wait = [&](uint64_t *bar, int parity) {
+    if (!tc::mbar_try(bar, parity) && ok) ok = wait_for(bar, parity);
   };
   // (in each role's own branch: where branches meet, the smaller share would hold for the code after)
   if (warp == kProducer) {
@@ -278,7 +281,10 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         if (want && !good) set_status(p.a.status, SPEC_ERR_PAGE);
         const uint32_t goods = __ballot_sync(0xffffffffu, good);
         wait(&sm.empty[s], ((it / F::S) & 1) ^ 1);
-        if (!ok) break;
+        if (!__all_sync(0xffffffffu, ok)) {   // no copy into a place that may be in use
+          ok = false;
+          break;
+        }
         if (lane == 0)
           tc::mbar_expect_tx(&sm.full[s], __popc(goods) * 2 * (D << p.a.page_shift));
         __syncwarp();
@@ -323,7 +329,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     auto scores = [&](int u) {
       const int g = u & 1, tile = it + (F::RTC == 2 ? u >> 1 : u);
       if (F::RTC == 1 || !g) wait(&sm.full[tile % F::S], (tile / F::S) & 1);
-      if (!ok) return;
+      __syncwarp();
       tc::fence_after_sync();
       const uint64_t da = smem_desc<D>(
           base + F::kOffQ + (F::RTC == 2 ? g * F::kTerms * F::kQBytes : 0), 16, 8 * D);
@@ -344,7 +350,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       const int g = u & 1, tile = it + (F::RTC == 2 ? u >> 1 : u);
       wait(&sm.pfull[g], phase >> g & 1);
       if (F::RTC == 1 || !g) wait(&sm.vfull[tile & 1], (tile >> 1) & 1);
-      if (!ok) return;
+      __syncwarp();
       phase ^= 1u << g;
       tc::fence_after_sync();
       // (N = D dims: one or two blocks of 64)
@@ -361,15 +367,15 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       }
       __syncwarp();
     };
-    for (int t = t0; t < t1 && ok; ++seg) {
+    for (int t = t0; t < t1; ++seg) {
       const int cnt = min(x.tiles - skip, t1 - t);
       const int units = F::RTC * cnt;
       wait(&sm.qfull, seg & 1);
-      if (ok) scores(0);
-      if (ok && units > 1) scores(1);
-      for (int u = 0; u < units && ok; ++u) {
+      scores(0);
+      if (units > 1) scores(1);
+      for (int u = 0; u < units; ++u) {
         values(u);
-        if (ok && u + 2 < units) scores(u + 2);
+        if (u + 2 < units) scores(u + 2);
       }
       it += cnt;
       t += cnt;
@@ -395,6 +401,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         fetch_values<D, kWidenThreads>(smem + s * 2 * F::kSideBytes + F::kSideBytes, wtid,
                                        x.end - slot0, w);
         wait(&sm.vfree[buf], ((it >> 1) & 1) ^ 1);
+        __syncwarp();
         if (slot0 + kTile > min(x.len, x.end)) {
           if (wtid < 4) sm.vnan[buf][wtid] = 0;
           widen_sync();
@@ -427,29 +434,31 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     float *share = reinterpret_cast<float *>(smem + F::kOffQ);
     float *top = qs + grp * 256;
     int it = 0, use = 0;   // tiles so far; this group's units so far
-    auto look = [&](uint64_t *bar, int parity) {   // a lane's wait
-      if (!tc::mbar_try(bar, parity) && ok) ok = wait_for(bar, parity);
-    };
     for (int t = t0; t < t1;) {
       const int cnt = min(x.tiles - skip, t1 - t);
-      load_queries<typename F::T, D, NT, 128, F::kTerms, kSoftThreads>(p, x, tid, smem + F::kOffQ,
-                                                                       qs);
+      const RowMap map = RowMap::of<NT>(p, x.rt);
+      // rows in use, up to whole warps; the others hold what they held: nothing reads their scores
+      const long long used = x.ok ? static_cast<long long>(x.n) * p.G - static_cast<long long>(x.rt) * NT : 0;
+      const int fill = static_cast<int>(max(0LL, min(static_cast<long long>(NT), (used + 31) / 32 * 32)));
+      load_queries<typename F::T, D, NT, 128, F::kTerms, kSoftThreads>(p, x, map, fill, tid,
+                                                                       smem + F::kOffQ, qs);
       fence_async();
       rows_sync();
       if (tid == 0) mbar_arrive(&sm.qfull);
-      const unsigned r = static_cast<unsigned>(x.rt) * NT + n;
-      const int i = static_cast<int>(r / p.G), gq = static_cast<int>(r - static_cast<unsigned>(i) * p.G);
+      int i, gq;
+      map.row(n, i, gq);
       const bool live = i < x.n && x.ok;
       const bool idle = !__any_sync(0xffffffffu, live);   // no row of this warp: nothing to weigh
       const float q = qs[n];
       rows_sync();   // `top` takes its place
       float nm = kNoRef, l = 0.f;
+      const int plain = min(x.len, x.end) - kTile;   // tiles from slots past this on need masks
       const int step = F::RTC == 2 ? 1 : 2;
       const int k0 = F::RTC == 2 ? 0 : grp;
-      for (int k = k0; k < cnt; k += step, ++use) {
+      for (int k = quad < quads ? k0 : cnt; k < cnt; k += step, ++use) {
         const int tile = it + k, buf = tile & 1;
         const int slot0 = (skip + k) * kTile;
-        const bool edge = slot0 + kTile > min(x.len, x.end);
+        const bool edge = slot0 > plain;
         uint32_t see[2] = {~0u, ~0u};
         if (edge)
 #pragma unroll
@@ -457,13 +466,13 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
             see[w] = live ? seen_bits(p, x.b, i, slot0 + 64 * half + 32 * w - x.len, x.n) : 0u;
         uint32_t nan[2] = {0, 0};
         if (edge) {
-          look(&sm.vfull[buf], (tile >> 1) & 1);
+          wait(&sm.vfull[buf], (tile >> 1) & 1);
           nan[0] = sm.vnan[buf][2 * half];
           nan[1] = sm.vnan[buf][2 * half + 1];
         }
         const float4 *page = pages + (tile % F::kPages * 8 + 4 * half);
-        look(&sm.cfull[tile % F::kPages], (tile / F::kPages) & 1);
-        look(&sm.sfull[grp], use & 1);
+        wait(&sm.cfull[tile % F::kPages], (tile / F::kPages) & 1);
+        wait(&sm.sfull[grp], use & 1);
         __syncwarp();
         tc::fence_after_sync();
         if (!idle) {
@@ -501,13 +510,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
             fresh = true;
           }
           l += sum;
-#pragma unroll
-          for (int c = 0; c < 32; c += 16) {
-            uint32_t v[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) v[e] = h[c + e];
-            tmem_st(ts + 32 * half + c, v);
-          }
+          tmem_st(ts + 32 * half, h);
           asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         }
         tc::fence_before_sync();
@@ -518,7 +521,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       // The item's (or its part's) result.
       const bool whole = skip == 0 && cnt == x.tiles;
       const long long part = 2LL * blockIdx.x + (skip == 0 ? 1 : 0);
-      if (use > 0) wait(&sm.ofull[grp], (use - 1) & 1);
+      if (use > 0) wait(&sm.ofull[grp], (use - 1) & 1);   // (a warp without rows reads nothing)
+      __syncwarp();
       tc::fence_after_sync();
       rows_sync();   // every MMA of the item has completed: the queries' place is free
       float *mine = share + (grp * 2 + half) * 256;
@@ -559,6 +563,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       T *out = static_cast<T *>(p.out) + ((static_cast<long long>(x.b) * p.a.N + i) * p.a.Hq +
                                           static_cast<long long>(x.h) * p.G + gq) * D;
       float *po = p.part_o + (part * NT + n) * D;
+      if (__any_sync(0xffffffffu, i < p.a.N))   // (whole warps)
 #pragma unroll 2
       for (int c = d0; c < d0 + kDims; c += 16) {
         uint32_t o[16], o1[16];

@@ -131,6 +131,18 @@ __device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&v)[16])
       "r"(taddr)
       : "memory");
 }
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, "
+      "%10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
+      "%28, %29, %30, %31};" ::"r"(v[0]),
+      "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]),
+      "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]),
+      "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]),
+      "r"(v[29]), "r"(v[30]), "r"(v[31]), "r"(taddr)
+      : "memory");
+}
 __device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
   f32x2 r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
@@ -332,13 +344,38 @@ __device__ __forceinline__ void publish_range(const AttnArgs &p, const Item &x, 
 
 // ------------------------------------------------------------------ operands
 
+// The token and query head of row n < 256 of a row tile: one division for the tile, then an exact
+// quotient of small numbers ((t + 1/2) / G is 1/2G away from an integer at least, the product's error
+// below 2^-8 / G for t < 2^15).
+struct RowMap {
+  int i0, g0, G;
+  float inv;
+  template <int NT>
+  static __device__ __forceinline__ RowMap of(const AttnArgs &p, int rt) {
+    RowMap m;
+    const unsigned r = static_cast<unsigned>(rt) * NT;
+    m.G = p.G;
+    m.i0 = static_cast<int>(r / p.G);
+    m.g0 = static_cast<int>(r - static_cast<unsigned>(m.i0) * p.G);
+    m.inv = __frcp_rn(static_cast<float>(p.G));
+    return m;
+  }
+  __device__ __forceinline__ void row(int n, int &i, int &g) const {
+    const int t = g0 + n;
+    const int d = static_cast<int>((static_cast<float>(t) + 0.5f) * inv);
+    i = i0 + d;
+    g = t - d * G;
+  }
+};
+
 // Rows 0 .. NT - 1 of the item as e4m3 terms in shared memory (D / 8 lanes a row), each in units of a
 // power of two that puts its largest element in [2^7, 2^8); qs[n] undoes it. Two terms hold bf16's 8
 // significant bits exactly down to 2^-9 of the unit, three fp16's 11. Blocks of kBlock rows, each
-// term of a block a K-major operand; rows past the item's are zero.
+// term of a block a K-major operand; of the NT rows the first `rows` (a multiple of 16) are written, zero
+// past the item's.
 template <typename T, int D, int NT, int kBlock, int kTerms, int kThreads>
-__device__ __forceinline__ void load_queries(const AttnArgs &p, const Item &x, int tid, uint8_t *sq,
-                                             float *qs) {
+__device__ __forceinline__ void load_queries(const AttnArgs &p, const Item &x, const RowMap &map,
+                                             int rows, int tid, uint8_t *sq, float *qs) {
   constexpr int kLanes = D / 8, kRows = kThreads / kLanes;
   constexpr int kSteps = (NT + kRows - 1) / kRows, kAhead = kSteps < 4 ? kSteps : 4;
   const int sub = tid % kLanes, row0 = tid / kLanes;
@@ -346,22 +383,22 @@ __device__ __forceinline__ void load_queries(const AttnArgs &p, const Item &x, i
                   static_cast<long long>(x.b) * p.a.N * p.q_stride +
                   static_cast<long long>(x.h) * p.G * D + sub * 8;
 #pragma unroll 1
-  for (int n0 = row0; n0 < NT; n0 += kAhead * kRows) {   // whole warps: a warp's rows are 2 or 4
+  for (int n0 = row0; n0 < rows; n0 += kAhead * kRows) {   // whole warps: a warp's rows are 2 or 4
     uint4 raw[kAhead];
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       const int n = n0 + u * kRows;
-      const unsigned r = static_cast<unsigned>(x.rt) * NT + n;
-      const unsigned i = r / p.G, g = r - i * p.G;
+      int i, g;
+      map.row(n, i, g);
       raw[u] = make_uint4(0, 0, 0, 0);
-      if (n < NT && static_cast<int>(i) < x.n && x.ok)
+      if (n < rows && i < x.n && x.ok)
         raw[u] = __ldg(reinterpret_cast<const uint4 *>(
             base + static_cast<long long>(i) * p.q_stride + static_cast<long long>(g) * D));
     }
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       const int n = n0 + u * kRows;
-      if (n >= NT) break;
+      if (n >= rows) break;
       float f[8];
       vec_to_floats<T>(raw[u], f);
       float m = 0.f;
