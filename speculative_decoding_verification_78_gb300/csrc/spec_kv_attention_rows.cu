@@ -44,8 +44,9 @@ constexpr int kSoftWarps = 2 * kGroupWarps;
 constexpr int kSoftThreads = 32 * kSoftWarps;
 constexpr int kWidenWarp = kSoftWarps, kWidenWarps = 8;   // warps that widen V
 constexpr int kWidenThreads = 32 * kWidenWarps;
-constexpr int kProducer = kWidenWarp + kWidenWarps, kMma = kProducer + 1;
-constexpr int kRowsThreads = 32 * (kMma + 3);   // two idle warps: register shares go by four warps
+constexpr int kCopyK = kWidenWarp + kWidenWarps, kMma = kCopyK + 1, kCopyV = kCopyK + 2,
+              kConsts = kCopyK + 3;
+constexpr int kRowsThreads = 32 * (kConsts + 1);
 constexpr float kBias = 8.f;        // a new reference puts the row's largest weight at 2^8 ...
 constexpr float kTrigger = 15.f;    // ... and is taken when one exceeds 2^15 (fp16 ends at 2^16)
 
@@ -95,7 +96,7 @@ struct RowsCfg {
   static constexpr int kOffV16 = S * 2 * kSideBytes;
   static constexpr int kOffQ = kOffV16 + 2 * kVfBytes;
   static constexpr int kOffSmall = kOffQ + RTC * kTerms * kQBytes;
-  // A tile's page constants give way to those of kPages tiles later, which the producer writes when the
+  // A tile's page constants give way to those of kPages tiles later, which are written when the
   // scores of the tile S before those are done, so after the values of at least two tiles more.
   static constexpr int kPages = RTC == 2 ? 4 : 8;
   static_assert(S + (RTC == 2 ? 2 : 3) <= kPages, "page constants are read by then");
@@ -105,7 +106,7 @@ struct RowsCfg {
 struct __align__(16) RowsSmall {
   uint64_t full[4], empty[4];    // stages
   uint64_t vfull[2], vfree[2];   // widened V
-  uint64_t cfull[8];             // page constants
+  uint64_t cfull[8], room[8];    // page constants; the keys' warp has room for the tile
   uint64_t sfull[2], pfull[2], ofull[2];   // by group
   uint64_t qfull, done;
   uint32_t vnan[2][4];           // tokens whose values hold NaN (tiles with new tokens)
@@ -216,7 +217,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
   const int quads = F::RTC == 2 ? 4 : static_cast<int>((static_cast<unsigned>(p.a.N) * p.G + 31) / 32);
   if (tid == 0) {
     for (int s = 0; s < F::S; ++s) {
-      tc::mbar_init(&sm.full[s], 1);
+      tc::mbar_init(&sm.full[s], 2);          // the keys' and the values' byte counts
       tc::mbar_init(&sm.empty[s], 1 + kWidenWarps);   // the score MMAs; the widening warps
     }
     for (int i = 0; i < 2; ++i) {
@@ -227,6 +228,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       tc::mbar_init(&sm.ofull[i], 1);
     }
     for (int i = 0; i < F::kPages; ++i) tc::mbar_init(&sm.cfull[i], 1);
+    for (int i = 0; i < 8; ++i) tc::mbar_init(&sm.room[i], 1);
     tc::mbar_init(&sm.qfull, 1);
     tc::mbar_init(&sm.done, 1);
     tc::mbar_fence_init();
@@ -247,37 +249,32 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     if (!tc::mbar_try(bar, parity) && ok) ok = wait_for(bar, parity);
   };
   // (in each role's own branch: where branches meet, the smaller share would hold for the code after)
-  if (warp == kProducer) {
+  if (warp == kCopyK || warp == kCopyV) {
     regs_give();
-    int it = 0;
+    // One warp copies the keys' pages, one the values', a third works out the page constants. One warp for
+    // all of it took 2290 clocks a tile of 16-token pages (the copies 1250 of them), more than the rest
+    // of the tile: 58.5 us for 52.3 (64 chains of 6, 16 query heads on 2, 4000 tokens). Where pages are
+    // larger or rows more, the copies wait for room and it makes no difference.
+    const bool keys = warp == kCopyK;
+    const CUtensorMap *map = keys ? &map_k : &map_v;
     const int per_tile = kTile >> p.a.page_shift;
+    const uint32_t lane_dst =
+        tc::saddr(smem) + (keys ? 0 : F::kSideBytes) + (lane << p.a.page_shift) * D;
+    int it = 0;
     for (int t = t0; t < t1 && ok;) {
       const int cnt = min(x.tiles - skip, t1 - t);
-      // this lane's page of tile k of the segment: its number (0 past the end), and its scales, which
-      // are on their way while the tile before waits for room
+      // this lane's page of the next tile: its number, on its way while the tile before waits for room
       const int32_t *table = p.a.page_table + static_cast<long long>(x.b) * p.a.pps;
-      auto wanted = [&](int k) {
-        return lane < per_tile && (skip + k) * kTile + (lane << p.a.page_shift) < x.end;
-      };
-      auto page_of = [&](int k) {
-        return k < cnt && wanted(k) ? __ldg(table + (skip + k) * per_tile + lane) : 0;
-      };
-      auto valid = [&](int page) { return page >= 0 && page < p.a.num_pages; };
-      int page = page_of(0), next = page_of(1);
-      auto scales_of = [&](int pg, bool want) {
-        const int head = pg * p.a.Hkv + x.h;
-        return want && valid(pg) ? make_float2(__ldg(p.a.k_scale + head), __ldg(p.a.v_scale + head))
-                                 : make_float2(NAN, NAN);   // what reads a bad page is NaN
-      };
-      float2 sc = scales_of(page, wanted(0));
-      for (int k = 0; k < cnt && ok; ++k, ++it) {
-        const int s = it % F::S;
-        const bool want = wanted(k), good = want && valid(page);
-        const float2 now = sc;
-        const int cur = page;
-        page = next;
-        next = page_of(k + 2);
-        sc = scales_of(page, k + 1 < cnt && wanted(k + 1));
+      const int pages_end = (x.end + p.a.page - 1) >> p.a.page_shift;
+      int at = skip * per_tile + lane;   // place in the table
+      auto page_of = [&]() { return lane < per_tile && at < pages_end ? __ldg(table + at) : -1; };
+      int next = page_of();
+      for (int k = 0; k < cnt; ++k, ++it) {
+        const int s = it % F::S, page = next;
+        const bool want = lane < per_tile && at < pages_end;
+        at += per_tile;
+        next = page_of();
+        const bool good = page >= 0 && page < p.a.num_pages;
         if (want && !good) set_status(p.a.status, SPEC_ERR_PAGE);
         const uint32_t goods = __ballot_sync(0xffffffffu, good);
         wait(&sm.empty[s], ((it / F::S) & 1) ^ 1);
@@ -285,28 +282,14 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
           ok = false;
           break;
         }
-        if (lane == 0)
-          tc::mbar_expect_tx(&sm.full[s], __popc(goods) * 2 * (D << p.a.page_shift));
-        __syncwarp();
-        if (good) {
-          const int row = (cur * p.a.Hkv + x.h) << p.a.page_shift;
-          const uint32_t dst = tc::saddr(smem + s * 2 * F::kSideBytes) +
-                               (lane << p.a.page_shift) * D;
-          tma_load_2d(dst, &map_k, 0, row, &sm.full[s]);
-          tma_load_2d(dst + F::kSideBytes, &map_v, 0, row, &sm.full[s]);
-        }
-        if (lane < per_tile) {
-          // a NaN scale makes its tokens' scores NaN through log2 vs; 1 / vs multiplies the zero weights
-          // of the rows that do not see them too, so it stays finite, as everything past the end
-          const float vse = now.y < kMinValueScale ? kMinValueScale : now.y;
-          const float4 c = want ? make_float4(now.x * p.scale2, __log2f(vse),
-                                              now.y == now.y ? __frcp_rn(vse) : 1.f, 0.f)
-                                : make_float4(0.f, 0.f, 0.f, 0.f);
-          const int chunks = 8 / per_tile;
-          for (int e = 0; e < chunks; ++e) pages[it % F::kPages * 8 + lane * chunks + e] = c;
+        if (lane == 0) {
+          tc::mbar_expect_tx(&sm.full[s], __popc(goods) * (D << p.a.page_shift));
+          if (keys) mbar_arrive(&sm.room[it & 7]);
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.cfull[it % F::kPages]);
+        if (good)
+          tma_load_2d(lane_dst + s * 2 * F::kSideBytes, map, 0,
+                      (page * p.a.Hkv + x.h) << p.a.page_shift, &sm.full[s]);
       }
       t += cnt;
       skip = 0;
@@ -315,6 +298,54 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     // the last copies of each stage land before the CTA may end
     for (int k = max(0, it - F::S); k < it; ++k)
       if (!wait_for(&sm.full[k % F::S], (k / F::S) & 1)) ok = false;
+  } else if (warp == kConsts) {
+    regs_give();
+    // The page constants of every tile, from scales asked for two tiles before, once the keys' warp has
+    // room for the tile (it is at most S tiles ahead: a stage is free only when its tile's constants were
+    // read, so the eight `room` barriers are never a round off).
+    const int per_tile = kTile >> p.a.page_shift, chunks = 1 << (p.a.page_shift - 4);
+    int it = 0;
+    for (int t = t0; t < t1;) {
+      const int cnt = min(x.tiles - skip, t1 - t);
+      const int32_t *table = p.a.page_table + static_cast<long long>(x.b) * p.a.pps;
+      const int pages_end = (x.end + p.a.page - 1) >> p.a.page_shift;
+      int at = skip * per_tile + lane;
+      const int stop = (skip + cnt) * per_tile;
+      auto page_of = [&](int place) {
+        return lane < per_tile && place < pages_end && place < stop ? __ldg(table + place) : -1;
+      };
+      auto scales_of = [&](int page) {
+        const int head = page * p.a.Hkv + x.h;
+        return page >= 0 && page < p.a.num_pages
+                   ? make_float2(__ldg(p.a.k_scale + head), __ldg(p.a.v_scale + head))
+                   : make_float2(NAN, NAN);   // what reads a bad page is NaN
+      };
+      const int second = page_of(at + per_tile);
+      int next = page_of(at + 2 * per_tile);
+      float2 sc = scales_of(page_of(at)), sc1 = scales_of(second);
+      for (int k = 0; k < cnt; ++k, ++it) {
+        const float2 now = sc;
+        const bool want = lane < per_tile && at < pages_end;
+        sc = sc1;
+        sc1 = scales_of(next);
+        at += per_tile;
+        next = page_of(at + 2 * per_tile);
+        // a NaN scale makes its tokens' scores NaN through log2 vs; 1 / vs multiplies the zero weights of
+        // the rows that do not see them too, so it stays finite, as everything past the end
+        const float vse = now.y < kMinValueScale ? kMinValueScale : now.y;
+        const float4 c = want ? make_float4(now.x * p.scale2, __log2f(vse),
+                                            now.y == now.y ? __frcp_rn(vse) : 1.f, 0.f)
+                              : make_float4(0.f, 0.f, 0.f, 0.f);
+        wait(&sm.room[it & 7], (it >> 3) & 1);
+        if (lane < per_tile)
+          for (int e = 0; e < chunks; ++e) pages[it % F::kPages * 8 + lane * chunks + e] = c;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.cfull[it % F::kPages]);
+      }
+      t += cnt;
+      skip = 0;
+      if (t < t1) item_next<NT>(p, x);
+    }
   } else if (warp == kMma) {
     regs_give();
     // The whole warp walks the units and one elected lane issues. values(u) is followed at once by
@@ -385,8 +416,6 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     if (elect_one()) mma_commit(&sm.done);   // every MMA issued has completed before the CTA may end
     if (!wait_for(&sm.done, 0)) ok = false;
     __syncwarp();
-  } else if (warp > kMma) {
-    regs_give();
   } else if (warp >= kWidenWarp) {
     regs_give();
     const int wtid = tid - 32 * kWidenWarp;
