@@ -30,7 +30,8 @@
 // 3 to 10 % each: no one part bounds it.
 // Tried and not kept: three stages of K and V for 256 rows (265 us), scores and values issued by two warps
 // (294), the next item's queries posted before the accumulators are read (262), tiles widened by two lots
-// of four warps (267), all 64 scores of a thread loaded at once (276).
+// of four warps (267), all 64 scores of a thread loaded at once (276), the next item's queries asked for
+// in L2 some tiles ahead (253: reading them is not what an item's start waits for).
 #include "spec_kv_attn.h"
 
 namespace specv {
@@ -421,7 +422,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     const int wtid = tid - 32 * kWidenWarp;
     int it = 0;
     for (int t = t0; t < t1;) {
-      const int cnt = min(x.tiles - skip, t1 - t);
+      const int cnt = min(x.tiles - skip, t1 - t), full = seen_by_all<NT>(p, x);
       for (int k = 0; k < cnt; ++k, ++it) {
         const int s = it % F::S, buf = it & 1;
         const int slot0 = (skip + k) * kTile;
@@ -431,7 +432,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
                                        x.end - slot0, w);
         wait(&sm.vfree[buf], ((it >> 1) & 1) ^ 1);
         __syncwarp();
-        if (slot0 + kTile > min(x.len, x.end)) {
+        if (slot0 + kTile > full) {
           if (wtid < 4) sm.vnan[buf][wtid] = 0;
           widen_sync();
           scrub_values<D, kWidenThreads>(
@@ -481,7 +482,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       const float q = qs[n];
       rows_sync();   // `top` takes its place
       float nm = kNoRef, l = 0.f;
-      const int plain = min(x.len, x.end) - kTile;   // tiles from slots past this on need masks
+      const int plain = seen_by_all<NT>(p, x) - kTile;   // tiles from slots past this on need masks
       const int step = F::RTC == 2 ? 1 : 2;
       const int k0 = F::RTC == 2 ? 0 : grp;
       for (int k = quad < quads ? k0 : cnt; k < cnt; k += step, ++use) {

@@ -212,6 +212,13 @@ __device__ __forceinline__ int item_end(const AttnArgs &p, int len, int n, bool 
   const int last = static_cast<int>((static_cast<unsigned>(rt) * NT + NT - 1) / p.G);
   return len + min(last + 1, n);
 }
+// The slots below it are seen by every row of the item that has a token: what lies past the first
+// token's place may be hidden from some.
+template <int NT>
+__device__ __forceinline__ int seen_by_all(const AttnArgs &p, const Item &x) {
+  const int first = static_cast<int>(static_cast<unsigned>(x.rt) * NT / p.G);
+  return min(x.len + (p.a.mask ? 0 : first + 1), x.end);
+}
 __device__ __forceinline__ int tiles_for(int end) { return end > kTile ? (end + kTile - 1) / kTile : 1; }
 
 // tiles of one key head of sequence b
