@@ -143,8 +143,8 @@ __device__ __forceinline__ uint32_t seen_bits(const AttnArgs &p, int b, int i, i
 // returns the largest exponent. The next 16 scores are on their way while these are worked on.
 template <bool kMasked>
 __device__ __forceinline__ float row_weights(uint32_t ts, const float4 *page, float qs, float nm,
-                                             const uint32_t (&see)[2], const uint32_t (&nan)[2],
-                                             uint32_t (&h)[32], float &sum) {
+                                             const uint32_t (&see)[2], uint32_t (&h)[32],
+                                             float &sum) {
   float big = -INFINITY;
   sum = 0.f;
   uint32_t s[2][16];
@@ -164,8 +164,6 @@ __device__ __forceinline__ float row_weights(uint32_t ts, const float4 *page, fl
       up2(fma2(pk2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), k2, d2), y0, y1);
       if (kMasked) {
         const int at = 16 * c + e;
-        if (nan[at >> 5] >> (at & 31) & 1u) y0 = NAN;
-        if (nan[at >> 5] >> (at & 31) & 2u) y1 = NAN;
         if (!(see[at >> 5] >> (at & 31) & 1u)) y0 = -INFINITY;
         if (!(see[at >> 5] >> (at & 31) & 2u)) y1 = -INFINITY;
       }
@@ -494,12 +492,6 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
 #pragma unroll
           for (int w = 0; w < 2; ++w)
             see[w] = live ? seen_bits(p, x.b, i, slot0 + 64 * half + 32 * w - x.len, x.n) : 0u;
-        uint32_t nan[2] = {0, 0};
-        if (edge) {
-          wait(&sm.vfull[buf], (tile >> 1) & 1);
-          nan[0] = sm.vnan[buf][2 * half];
-          nan[1] = sm.vnan[buf][2 * half + 1];
-        }
         const float4 *page = pages + (tile % F::kPages * 8 + 4 * half);
         wait(&sm.cfull[tile % F::kPages], (tile / F::kPages) & 1);
         wait(&sm.sfull[grp], use & 1);
@@ -533,13 +525,17 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
                   tmem_st(tlane + F::kColO + grp * D + c, o);
                 }
             }
-            const float big = edge ? row_weights<true>(ts + 64 * half, page, q, nm, see, nan, h, sum)
-                                   : row_weights<false>(ts + 64 * half, page, q, nm, see, nan, h, sum);
+            const float big = edge ? row_weights<true>(ts + 64 * half, page, q, nm, see, h, sum)
+                                   : row_weights<false>(ts + 64 * half, page, q, nm, see, h, sum);
             // (also: both halves have read their scores, which P is about to overwrite)
             if (!pair_any(pair, !fresh && big > kTrigger)) break;
             fresh = true;
           }
           l += sum;
+          if (edge) {   // values with NaN went into the product as zeros: the rows that see them are NaN
+            wait(&sm.vfull[buf], (tile >> 1) & 1);
+            if ((sm.vnan[buf][2 * half] & see[0]) | (sm.vnan[buf][2 * half + 1] & see[1])) l = NAN;
+          }
           tmem_st(ts + 32 * half, h);
           asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         }
@@ -594,7 +590,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
                                           static_cast<long long>(x.h) * p.G + gq) * D;
       float *po = p.part_o + (part * NT + n) * D;
       if (__any_sync(0xffffffffu, i < p.a.N))   // (whole warps)
-#pragma unroll 2
+#pragma unroll
       for (int c = d0; c < d0 + kDims; c += 16) {
         uint32_t o[16], o1[16];
         tmem_ld(tlane + F::kColO + (F::RTC == 2 ? grp * D : 0) + c, o);
