@@ -356,30 +356,38 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     const uint32_t base = tc::saddr(smem);
     int it = 0, seg = 0;
     uint32_t phase = 0;   // bit g: parity of group g's next unit
-    auto scores = [&](int u) {
-      const int g = u & 1, tile = it + (F::RTC == 2 ? u >> 1 : u);
-      if (F::RTC == 1 || !g) wait(&sm.full[tile % F::S], (tile / F::S) & 1);
-      __syncwarp();
-      tc::fence_after_sync();
+    auto tile_of = [&](int u) { return it + (F::RTC == 2 ? u >> 1 : u); };
+    auto keys_there = [&](int u) {
+      const int tile = tile_of(u);
+      if (F::RTC == 1 || !(u & 1)) wait(&sm.full[tile % F::S], (tile / F::S) & 1);
+    };
+    auto scores = [&](int u) {   // one lane
+      const int g = u & 1, tile = tile_of(u);
       const uint64_t da = smem_desc<D>(
           base + F::kOffQ + (F::RTC == 2 ? g * F::kTerms * F::kQBytes : 0), 16, 8 * D);
       const uint64_t db = smem_desc<D>(base + tile % F::S * 2 * F::kSideBytes, 16, 8 * D);
       const uint32_t d = tmem + F::kColS + g * 128;
-      if (elect_one()) {
 #pragma unroll
-        for (int term = 0; term < F::kTerms; ++term)
+      for (int term = 0; term < F::kTerms; ++term)
 #pragma unroll
-          for (int kk = 0; kk < D / 32; ++kk)   // 32 dims of e4m3: 32 bytes on
-            mma_f8(d, da + term * (F::kQBytes / 16) + 2 * kk, db + 2 * kk, id_s, (term | kk) != 0);
-        mma_commit(&sm.sfull[g]);
-        if (F::RTC == 1 || g) mma_commit(&sm.empty[tile % F::S]);
-      }
+        for (int kk = 0; kk < D / 32; ++kk)   // 32 dims of e4m3: 32 bytes on
+          mma_f8(d, da + term * (F::kQBytes / 16) + 2 * kk, db + 2 * kk, id_s, (term | kk) != 0);
+      mma_commit(&sm.sfull[g]);
+      if (F::RTC == 1 || g) mma_commit(&sm.empty[tile % F::S]);
+    };
+    auto first_scores = [&](int u) {
+      keys_there(u);
+      __syncwarp();
+      tc::fence_after_sync();
+      if (elect_one()) scores(u);
       __syncwarp();
     };
-    auto values = [&](int u) {
-      const int g = u & 1, tile = it + (F::RTC == 2 ? u >> 1 : u);
-      wait(&sm.pfull[g], phase >> g & 1);
+    // everything else is waited for before the weights, as a rule the last to come
+    auto values = [&](int u, bool last) {
+      const int g = u & 1, tile = tile_of(u);
       if (F::RTC == 1 || !g) wait(&sm.vfull[tile & 1], (tile >> 1) & 1);
+      if (!last) keys_there(u + 2);
+      wait(&sm.pfull[g], phase >> g & 1);
       __syncwarp();
       phase ^= 1u << g;
       tc::fence_after_sync();
@@ -393,7 +401,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         for (int kk = 0; kk < kTile / 16; ++kk)   // 16 tokens: 8 columns of pairs
           mma_f16_ts(d, a + 8 * kk, db + kk * (16 * 128 / 16), id_o, kk ? 1u : later);
         if (F::RTC == 1 || g) mma_commit(&sm.vfree[tile & 1]);
-        mma_commit(&sm.ofull[g]);
+        if (F::RTC == 1 || last) mma_commit(&sm.ofull[g]);
+        if (!last) scores(u + 2);
       }
       __syncwarp();
     };
@@ -401,11 +410,10 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       const int cnt = min(x.tiles - skip, t1 - t);
       const int units = F::RTC * cnt;
       wait(&sm.qfull, seg & 1);
-      scores(0);
-      if (units > 1) scores(1);
+      first_scores(0);
+      if (units > 1) first_scores(1);
       for (int u = 0; u < units; ++u) {
-        values(u);
-        if (u + 2 < units) scores(u + 2);
+        values(u, u + 2 >= units);
       }
       it += cnt;
       t += cnt;
@@ -461,7 +469,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     // queries' place is free once every score has been taken.
     float *share = reinterpret_cast<float *>(smem + F::kOffQ);
     float *top = qs + grp * 256;
-    int it = 0, use = 0;   // tiles so far; this group's units so far
+    int it = 0, use = 0, ends = 0;   // tiles so far; this group's units and commits to `ofull` so far
     for (int t = t0; t < t1;) {
       const int cnt = min(x.tiles - skip, t1 - t);
       const RowMap map = RowMap::of<NT>(p, x.rt);
@@ -547,7 +555,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       // The item's (or its part's) result.
       const bool whole = skip == 0 && cnt == x.tiles;
       const long long part = 2LL * blockIdx.x + (skip == 0 ? 1 : 0);
-      if (use > 0) wait(&sm.ofull[grp], (use - 1) & 1);   // (a warp without rows reads nothing)
+      if (F::RTC == 2 || use > 0) wait(&sm.ofull[grp], F::RTC == 2 ? ends++ & 1 : (use - 1) & 1);
       __syncwarp();
       tc::fence_after_sync();
       rows_sync();   // every MMA of the item has completed: the queries' place is free
