@@ -152,11 +152,11 @@ __device__ __forceinline__ float row_weights(uint32_t ts, const float4 *page, fl
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
     uint32_t(&v)[16] = s[c & 1];
-    tmem_wait(v);
-    if (c < 3) tmem_ld(ts + 16 * (c + 1), s[(c + 1) & 1]);
     const float4 pg = page[c];
     const float k = pg.x * qs, d = pg.y + nm;
     const f32x2 k2 = pk2(k, k), d2 = pk2(d, d);
+    tmem_wait(v);
+    if (c < 3) tmem_ld(ts + 16 * (c + 1), s[(c + 1) & 1]);
     f32x2 acc = pk2(0.f, 0.f);
 #pragma unroll
     for (int e = 0; e < 16; e += 2) {
@@ -187,8 +187,8 @@ __device__ __forceinline__ float row_maximum(uint32_t ts, const float4 *page, fl
   for (int c = 0; c < 4; ++c) {
     uint32_t v[16];
     tmem_ld(ts + 16 * c, v);
-    tmem_wait(v);
     const float4 pg = page[c];
+    tmem_wait(v);
     const float k = pg.x * qs;
     const uint32_t bits = kMasked ? (c < 2 ? see[0] : see[1]) >> (16 * (c & 1)) : 0xffffu;
 #pragma unroll
