@@ -78,25 +78,59 @@ __device__ __forceinline__ void load_angles(const RopeArgs &r, int pos, int u, A
     }
   }
 }
+// x c + y s with one product rounded; within 1.5 units in the last place of the sum, whatever cancels
+// (Kahan's, with the product's error); or as a 32-bit number that rounds to fewer bits as the exact sum does.
+enum Turn { kRounded, kClose, kExact };
+template <Turn kTurn>
+__device__ __forceinline__ float turned(float x, float c, float y, float s) {
+  const float w = y * s;
+  if (kTurn == kRounded) return __fmaf_rn(x, c, w);
+  const float ew = __fmaf_rn(y, s, -w);
+  if (kTurn == kClose) return __fadd_rn(__fmaf_rn(x, c, w), ew);
+  // both products with their errors (Dekker's, by FMA), the sum of the products with its (Knuth's)
+  const float p = x * c, ep = __fmaf_rn(x, c, -p);
+  const float sum = __fadd_rn(p, w), part = __fsub_rn(sum, p);
+  const float es = __fadd_rn(__fsub_rn(p, __fsub_rn(sum, part)), __fsub_rn(w, part));
+  const float err = __fadd_rn(es, __fadd_rn(ep, ew)), r = __fadd_rn(sum, err);
+  if (!(fabsf(r) < INFINITY)) return sum;   // (the errors of an infinite sum are NaN)
+  // a border is never met by rounding to it: what was rounded off moves such a number by a unit
+  const float rest = __fsub_rn(err, __fsub_rn(r, sum));
+  const int bits = __float_as_int(r);
+  return (bits & 0x7ffff) || rest == 0.f ? r
+                                         : __int_as_float(bits + ((rest > 0.f) == (r > 0.f) ? 1 : -1));
+}
+template <Turn kTurn>
 __device__ __forceinline__ void rotate(const RopeArgs &r, const Angles &t, float (&f)[8],
                                        float (&g)[8]) {
   if (r.pairs) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float x = f[2 * i], y = f[2 * i + 1], z = g[2 * i], w = g[2 * i + 1];
-      f[2 * i] = __fmaf_rn(x, t.c[i], -(y * t.s[i]));
-      f[2 * i + 1] = __fmaf_rn(y, t.c[i], x * t.s[i]);
-      g[2 * i] = __fmaf_rn(z, t.c[4 + i], -(w * t.s[4 + i]));
-      g[2 * i + 1] = __fmaf_rn(w, t.c[4 + i], z * t.s[4 + i]);
+      f[2 * i] = turned<kTurn>(x, t.c[i], -y, t.s[i]);
+      f[2 * i + 1] = turned<kTurn>(y, t.c[i], x, t.s[i]);
+      g[2 * i] = turned<kTurn>(z, t.c[4 + i], -w, t.s[4 + i]);
+      g[2 * i + 1] = turned<kTurn>(w, t.c[4 + i], z, t.s[4 + i]);
     }
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float x = f[i], y = g[i];
-      f[i] = __fmaf_rn(x, t.c[i], -(y * t.s[i]));
-      g[i] = __fmaf_rn(y, t.c[i], x * t.s[i]);
+      f[i] = turned<kTurn>(x, t.c[i], -y, t.s[i]);
+      g[i] = turned<kTurn>(y, t.c[i], x, t.s[i]);
     }
   }
+}
+
+// Keys are rounded to 4 significant bits next, where a sum that is off by a unit or two in the last place
+// puts about one element in a million on the other side of a border. Borders are multiples of 2^19 units,
+// so a thread that holds a number within 4 units of one (one thread in 4000) turns its 16 again exactly.
+// In a graph, 8 x 4096 tokens of 8 key and 32 query heads: 142 us, 136 without, 164 with every sum exact.
+__device__ __forceinline__ bool near_border(const float (&f)[2][8]) {
+  uint32_t least = 8;
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    least = min(least, (__float_as_uint(f[i >> 3][i & 7]) + 4u) & 0x7ffffu);
+  return least < 8;
 }
 
 // One warp's queries: token `task / blocks`, up to kQIters groups of 32 / (D / 16) heads.
@@ -136,7 +170,7 @@ __device__ __forceinline__ void append_queries(const KvArgs &a, const RopeArgs &
         float f[8], g[8];
         vec_to_floats<T>(raw[k][0], f);
         vec_to_floats<T>(raw[k][1], g);
-        rotate(r, t, f, g);
+        rotate<kRounded>(r, t, f, g);
         raw[k][0] = floats_to_vec<T>(f);
         raw[k][1] = floats_to_vec<T>(g);
       }
@@ -230,7 +264,14 @@ __global__ void __launch_bounds__(kThreads, 512 / kThreads)
       if (row[k] >= 0 && slot >= from && slot < to) {
         vec_to_floats<T>(raw[k][0], f[k][0]);
         vec_to_floats<T>(raw[k][1], f[k][1]);
-        if (un[k].turn) rotate(r, t[k], f[k][0], f[k][1]);
+        if (un[k].turn) {
+          rotate<kClose>(r, t[k], f[k][0], f[k][1]);
+          if (near_border(f[k])) {
+            vec_to_floats<T>(raw[k][0], f[k][0]);
+            vec_to_floats<T>(raw[k][1], f[k][1]);
+            rotate<kExact>(r, t[k], f[k][0], f[k][1]);
+          }
+        }
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           const float m = fabsf(f[k][e >> 3][e & 7]);

@@ -404,6 +404,28 @@ def test_append(sv, dtype, N, Hq, Hkv, D, page, R, pairs):
     check_append(sv, c, Hq, dtype, R, pairs, packed=N % 2 == 1)
 
 
+@pytest.mark.parametrize("pairs", [False, True])
+def test_append_keys_are_the_exact_rotation_rounded_once(sv, pairs):
+    """Four million keys: every byte is the e4m3 value nearest to the exact rotation (ties to even)."""
+    B, N, Hkv, D, page = 4, 512, 16, 128, 64
+    rng = np.random.default_rng(17 + pairs)
+    cache = sv.new_kv_cache(B * N // page, Hkv, D, page)
+    table = torch.arange(B * N // page, dtype=torch.int32).view(B, -1).cuda()
+    k = rand16(rng, (B, N, Hkv, D), torch.bfloat16)
+    rope = rope_table(N, D)
+    sv.kv_append(cache, table, torch.zeros(B, dtype=torch.int32, device="cuda"), k, k,
+                 rope=torch.from_numpy(rope).cuda(), interleaved=pairs)
+    codes, scales = cache.k.view(torch.uint8).cpu().numpy()[0], cache.k_scale.cpu().numpy()[0]
+    x = f64(k)
+    for b in range(B):
+        y = np.stack([ref.rotated(x[b, i], rope, i, pairs) for i in range(N)])
+        y = y.reshape(N // page, page, Hkv, D).transpose(0, 2, 1, 3)   # as the pages lie
+        at = slice(b * N // page, (b + 1) * N // page)
+        z = y / scales[at][:, :, None, None]
+        step = 2 * ref.half_step(z)
+        np.testing.assert_array_equal(ref.E4M3[codes[at]], np.rint(z / step) * step)
+
+
 @pytest.mark.parametrize("N", [2, 33, 64])
 def test_append_tree_positions(sv, N):
     c = Case(N, [0, 10, 64, 100], N, 2, 128, 64)
