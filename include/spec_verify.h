@@ -320,7 +320,8 @@ typedef struct {
 
 /*
  * Appends N new tokens to each of B sequences: rotates the keys by their positions, stores keys and
- * values as e4m3 with one power-of-two scale for each page and head, and rotates the queries.
+ * values as e4m3 with one power-of-two scale for each page and head, and rotates the queries. A new
+ * key is its exact rotation by the table's numbers, rounded once (to nearest, ties to even).
  *
  *   rotation  of dims j < rope_dim by row `position` of rope [rope_rows, rope_dim] fp32, whose first
  *             rope_dim / 2 columns are the cosines and the others the sines (c_j, s_j):

@@ -28,12 +28,14 @@
 // most two per CTA), and a second kernel joins them in order, so results do not depend on timing.
 //
 // What bounds it: HBM, which it does not quite fill. 64 sequences of about 15000 tokens, one new token,
-// 32 query and 8 key heads of 128: 321 us for 1.95 GB, 6.07 TB/s (90 % of the measured copy rate). A
+// 32 query and 8 key heads of 128: 322 us for 1.95 GB, 6.05 TB/s (90 % of the measured copy rate). A
 // tile's chain (wait, widen, scores, weights, barrier) takes a group about 3600 clocks, which two groups
 // in turn hide but for a tenth; issuing the 16 MMAs takes their own warp 950 of a tile's 1650. With one
 // group 607 us; with the MMAs issued from a branch of one lane, where their descriptors are not known to
 // be uniform, 503 us. Tried and not kept: the query terms as columns side by side (8 MMAs fewer, the terms
-// added by the softmax: 362 against 333 us), the page constants worked out by the copying warp (407).
+// added by the softmax: 362 against 333 us), the page constants worked out by the copying warp (407), scores
+// two tiles ahead of the values with the weights before the widening (390: a stage is held longer than
+// four of them last), waits without a vote, as the kernel for many rows has them (354: spills).
 #include "spec_kv_attn.h"
 
 namespace specv {

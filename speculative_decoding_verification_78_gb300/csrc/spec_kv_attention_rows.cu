@@ -19,19 +19,24 @@
 // take the tiles in turn and are joined at the end of the item. Unit u of a segment belongs to group
 // u & 1; values(u) and then scores(u + 2) are issued as soon as its weights are there.
 //
-// What bounds it (D = 128, measured with clock counters): a 256-row tile of 128 tokens costs 2460 clocks
+// What bounds it (D = 128, measured with clock counters): a 256-row tile of 128 tokens costs 2100 clocks
 // of MMA (two e4m3 terms cost what one 16-bit operand would: 2048 at the nominal rate; the operands of
 // both MMAs, V's widening and the copies want about 2400 clocks of shared-memory bandwidth) and 1380 of
 // weights (345 clocks a warp for 64 scores of 32 rows: ex2 256 of them). A group's turn is longer than
-// either, about 3600: its weights, a hand-over to the MMA warp, its MMAs behind the other group's, a
-// hand-over back. 32 trees of 64 nodes, four query heads a key head, 8192 tokens: 250 us, 1030 TFLOP/s;
-// with one MMA warp waiting for each hand-over in turn 294 us, with full rows per thread 367 us. Dropping
-// the second e4m3 term, half of the value MMAs or the widening (wrong results, for timing only) gains
-// 3 to 10 % each: no one part bounds it.
-// Tried and not kept: three stages of K and V for 256 rows (265 us), scores and values issued by two warps
-// (294), the next item's queries posted before the accumulators are read (262), tiles widened by two lots
-// of four warps (267), all 64 scores of a thread loaded at once (276), the next item's queries asked for
-// in L2 some tiles ahead (253: reading them is not what an item's start waits for).
+// either, about 3500: its weights (1340, the other group's beside them), the store, a hand-over to the
+// MMA warp, its MMAs (1050) behind the other group's, a hand-over back; an item's start and end cost
+// another 20000. 32 trees of 64 nodes, four query heads a key head, 8192 tokens: 233 us with the join,
+// 1100 TFLOP/s; with full rows per thread 367 us, with one MMA warp waiting for each hand-over in turn
+// 294 us, with spills in the epilogue 251, with the MMA warp asking for the keys after the weights and
+// issuing values and scores apart 244. No one part bounds it: dropping the second e4m3 term, half of the
+// value MMAs or the widening (wrong results, for timing only) gained 3 to 10 % each.
+// Tried and not kept (us against what was there then): three stages of K and V for 256 rows (265 for 262),
+// scores and values issued by two warps (294 for 262), the next item's queries posted before the
+// accumulators are read (262 for 250), tiles widened by two lots of four warps (267 for 262), all 64
+// scores of a thread loaded at once (276 for 262) or 32 (263 for 245), the next item's queries asked for
+// in L2 some tiles ahead (253 for 251), results turned round in shared memory to store whole lines (no
+// change), with up to 64 rows the second group on the warps of the other 64 lanes (149 for 155 at best,
+// before what joining its accumulators would cost).
 #include "spec_kv_attn.h"
 
 namespace specv {
@@ -59,8 +64,8 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, u
       "r"(a), "l"(b), "r"(idesc), "r"(acc));
 }
 // Registers: 896 threads start with 72 each; the softmax warps, which hold a half row's weights, take
-// more, which the others give up (512 x 80 + 384 x 56 < 896 x 72). At 96 and 40 the copies' and MMAs'
-// warps spilled, which is on every tile's path: 212 us for 167 (32 trees of 64 nodes, 32 key heads).
+// more, which the others give up (512 x 80 + 384 x 56 < 896 x 72). At 88 and 48 the widening, copying and
+// MMA warps spill, which is on every tile's path: 272 us for 245 (long trees), 179 for 155 (short ones).
 __device__ __forceinline__ void regs_take() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 80;");
 }
@@ -465,8 +470,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     const uint32_t tlane = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     const uint32_t ts = tlane + F::kColS + grp * 128;         // the row's scores
     // what the two halves (and, at the end, the groups) of a row tell each other: [group][half][row].
-    // The
-    // queries' place is free once every score has been taken.
+    // The queries' place is free once every score has been taken.
     float *share = reinterpret_cast<float *>(smem + F::kOffQ);
     float *top = qs + grp * 256;
     int it = 0, use = 0, ends = 0;   // tiles so far; this group's units and commits to `ofull` so far
