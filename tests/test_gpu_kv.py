@@ -221,6 +221,48 @@ def test_attention_nan_in_unseen_slots(sv):
         assert torch.equal(l2[0, :7], lse[0, :7])
 
 
+@pytest.mark.parametrize("N,Hq", [(40, 4), (40, 8), (70, 8)])
+@pytest.mark.parametrize("side", [0, 1])
+def test_attention_nan_node_of_many_rows(sv, N, Hq, side):
+    """A node whose key or value is NaN: the queries that see it are NaN, the others as before."""
+    c = Case(N + Hq, [50, 300], N, 2, 128, 64)
+    words = tree_words(c.rng, 2, N, sv)
+    q = rand16(c.rng, (2, N, Hq, 128), torch.bfloat16)
+    out, lse = check_attention(sv, c, q, words)
+    node = 5
+    sees = torch.from_numpy(ref.mask_bits(words.cpu().numpy(), N)[1, :, node]).cuda()
+    assert bool(sees.any()) and not bool(sees.all())
+    slot = int(c.lens[1]) + node
+    c.pool[side][0, c.table[1, slot // 64], :, slot % 64] = 0x7f
+    table, lens = c.dev("table", "lens")
+    o2, l2, st = sv.kv_attention(c.cache(sv), table, lens, q, mask=words, return_lse=True)
+    assert int(st.item()) == 0
+    assert bool(o2[1, sees].isnan().all())
+    assert torch.equal(o2[1, ~sees], out[1, ~sees]) and torch.equal(o2[0], out[0])
+    assert torch.equal(l2[1, ~sees], lse[1, ~sees]) and torch.equal(l2[0], lse[0])
+
+
+@pytest.mark.parametrize("N,Hq,D", [(300, 4, 128), (520, 8, 64)])
+def test_attention_nan_value_in_a_prompt(sv, N, Hq, D):
+    """A prompt's token whose value has one NaN: that dim of the queries from it on is NaN (all of their
+    dims may be), the queries before it are as before."""
+    c = Case(N + D, [70, 5], N, 1, D, 64)
+    q = rand16(c.rng, (2, N, Hq, D), torch.bfloat16)
+    table, lens = c.dev("table", "lens")
+    out, lse, _ = sv.kv_attention(c.cache(sv), table, lens, q, return_lse=True)
+    for token in (0, 10, 200):
+        slot = int(c.lens[0]) + token
+        at = (0, c.table[0, slot // 64], 0, slot % 64, 3)
+        keep = c.pool[1][at]
+        c.pool[1][at] = 0x7f
+        o2, l2, st = sv.kv_attention(c.cache(sv), table, lens, q, return_lse=True)
+        c.pool[1][at] = keep
+        assert int(st.item()) == 0
+        assert bool(o2[0, token:, :, 3].isnan().all())
+        assert torch.equal(o2[0, :token], out[0, :token]) and torch.equal(o2[1], out[1])
+        assert torch.equal(l2[0, :token], lse[0, :token]) and torch.equal(l2[1], lse[1])
+
+
 def test_attention_nan_query_stays_in_its_row(sv):
     c = Case(14, [100, 30], 3, 2, 128, 16)
     q = rand16(c.rng, (2, 3, 4, 128), torch.bfloat16)
