@@ -10,7 +10,7 @@
 // its reference, its sum and its query's unit are registers; what differs by token, the page scales,
 // is constant over 16 columns (pages hold at least 16 tokens). P is written back to tensor memory,
 // over the scores it came from, as the fp16 operand of the second MMA: nothing of the softmax passes
-// through shared memory, which the operands of the MMAs already load. V is widened to fp16 by eight
+// through shared memory, which the operands of the MMAs already load. V is widened to fp16 by four
 // warps of their own, once for all rows of the CTA.
 //
 // Two groups of eight softmax warps (two for each 32 rows, half of the tile's tokens each) work half a
@@ -25,8 +25,9 @@
 // weights (345 clocks a warp for 64 scores of 32 rows: ex2 256 of them). A group's turn is longer than
 // either, about 3500: its weights (1340, the other group's beside them), the store, a hand-over to the
 // MMA warp, its MMAs (1050) behind the other group's, a hand-over back; an item's start and end cost
-// another 20000. 32 trees of 64 nodes, four query heads a key head, 8192 tokens: 233 us with the join,
-// 1100 TFLOP/s; with full rows per thread 367 us, with one MMA warp waiting for each hand-over in turn
+// another 20000. 32 trees of 64 nodes, four query heads a key head, 8192 tokens: 240 us with the join,
+// 1070 TFLOP/s (233 in the form these clocks were taken of, see the registers below); at the steps before
+// it with full rows per thread 367 us, with one MMA warp waiting for each hand-over in turn
 // 294 us, with spills in the epilogue 251, with the MMA warp asking for the keys after the weights and
 // issuing values and scores apart 244. No one part bounds it: dropping the second e4m3 term, half of the
 // value MMAs or the widening (wrong results, for timing only) gained 3 to 10 % each.
@@ -48,10 +49,16 @@ namespace {
 constexpr int kGroupWarps = 8;                        // two for each 32 rows: half of the tokens each
 constexpr int kSoftWarps = 2 * kGroupWarps;
 constexpr int kSoftThreads = 32 * kSoftWarps;
-constexpr int kWidenWarp = kSoftWarps, kWidenWarps = 8;   // warps that widen V
+constexpr int kWidenWarp = kSoftWarps, kWidenWarps = 4;   // warps that widen V
 constexpr int kWidenThreads = 32 * kWidenWarps;
 constexpr int kCopyK = kWidenWarp + kWidenWarps, kMma = kCopyK + 1, kCopyV = kCopyK + 2,
               kConsts = kCopyK + 3;
+// 24 warps of 80 registers, all that an SM has. Moving registers from the other roles to the softmax warps
+// (setmaxnreg) is not open to them: the copying, constants and MMA warps make up one warpgroup, whose four
+// warps have to execute the same instruction, and with one instruction before their branches the compiler
+// spills 460 bytes for 50. In a graph, us (64 chains of 6 / 32 trees / the same over 8192 tokens / two
+// prompts): 49 / 165 / 240 / 246; eight widening warps, 72 registers a thread: 52 / 167 / 249 / 255; those
+// with an instruction in each role's branch, which is undefined: 48 / 152 / 233 / 237.
 constexpr int kRowsThreads = 32 * (kConsts + 1);
 constexpr float kBias = 8.f;        // a new reference puts the row's largest weight at 2^8 ...
 constexpr float kTrigger = 15.f;    // ... and is taken when one exceeds 2^15 (fp16 ends at 2^16)
@@ -62,15 +69,6 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, u
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
       "r"(a), "l"(b), "r"(idesc), "r"(acc));
-}
-// Registers: 896 threads start with 72 each; the softmax warps, which hold a half row's weights, take
-// more, which the others give up (512 x 80 + 384 x 56 < 896 x 72). At 88 and 48 the widening, copying and
-// MMA warps spill, which is on every tile's path: 272 us for 245 (long trees), 179 for 155 (short ones).
-__device__ __forceinline__ void regs_take() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 80;");
-}
-__device__ __forceinline__ void regs_give() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
 }
 // barrier of the two warps that share rows: true in both if `p` was in any of their threads
 __device__ __forceinline__ bool pair_any(int id, bool p) {
@@ -252,9 +250,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
   auto wait = [&](uint64_t *bar, int parity) {
     if (!tc::mbar_try(bar, parity) && ok) ok = wait_for(bar, parity);
   };
-  // (in each role's own branch: where branches meet, the smaller share would hold for the code after)
   if (warp == kCopyK || warp == kCopyV) {
-    regs_give();
     // One warp copies the keys' pages, one the values', a third works out the page constants. One warp for
     // all of it took 2290 clocks a tile of 16-token pages (the copies 1250 of them), more than the rest
     // of the tile: 58.5 us for 52.3 (64 chains of 6, 16 query heads on 2, 4000 tokens). Where pages are
@@ -303,7 +299,6 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     for (int k = max(0, it - F::S); k < it; ++k)
       if (!wait_for(&sm.full[k % F::S], (k / F::S) & 1)) ok = false;
   } else if (warp == kConsts) {
-    regs_give();
     // The page constants of every tile, from scales asked for two tiles before, once the keys' warp has
     // room for the tile (it is at most S tiles ahead: a stage is free only when its tile's constants were
     // read, so the eight `room` barriers are never a round off).
@@ -351,7 +346,6 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       if (t < t1) item_next<NT>(p, x);
     }
   } else if (warp == kMma) {
-    regs_give();
     // The whole warp walks the units and one elected lane issues. values(u) is followed at once by
     // scores(u + 2), whose scores go where values(u)'s P lies: MMAs run in the order of their issue,
     // so a group's turn costs one hand-over in each direction.
@@ -429,7 +423,6 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     if (!wait_for(&sm.done, 0)) ok = false;
     __syncwarp();
   } else if (warp >= kWidenWarp) {
-    regs_give();
     const int wtid = tid - 32 * kWidenWarp;
     int it = 0;
     for (int t = t0; t < t1;) {
@@ -462,7 +455,6 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       if (t < t1) item_next<NT>(p, x);
     }
   } else {
-    regs_take();
     const int grp = warp / kGroupWarps, half = warp >> 2 & 1, quad = warp & 3;
     const int lrow = quad * 32 + lane;                        // row of the MMA tile
     const int n = F::RTC == 2 ? grp * 128 + lrow : lrow;      // row of the item's tile

@@ -463,22 +463,21 @@ template <int D, int kThreads, typename Mark>
 __device__ __forceinline__ bool scrub_values(uint4 (&w)[Widen<D, kThreads>::kSteps], int gtid,
                                              Mark mark) {
   using W = Widen<D, kThreads>;
-  uint32_t any = 0;
-#pragma unroll
-  for (int u = 0; u < W::kSteps; ++u)
-    any |= nan_codes(w[u].x) | nan_codes(w[u].y) | nan_codes(w[u].z) | nan_codes(w[u].w);
-  if (!any) return false;
+  bool any = false;
 #pragma unroll
   for (int u = 0; u < W::kSteps; ++u) {
     const uint32_t hx = nan_codes(w[u].x), hy = nan_codes(w[u].y), hz = nan_codes(w[u].z),
                    hw = nan_codes(w[u].w);
-    w[u].x &= ~((hx >> 7) * 255u);
-    w[u].y &= ~((hy >> 7) * 255u);
-    w[u].z &= ~((hz >> 7) * 255u);
-    w[u].w &= ~((hw >> 7) * 255u);
-    if (hx | hy | hz | hw) mark(u * W::kRows + gtid / W::kLanes);
+    if (hx | hy | hz | hw) {
+      w[u].x &= ~((hx >> 7) * 255u);
+      w[u].y &= ~((hy >> 7) * 255u);
+      w[u].z &= ~((hz >> 7) * 255u);
+      w[u].w &= ~((hw >> 7) * 255u);
+      mark(u * W::kRows + gtid / W::kLanes);
+      any = true;
+    }
   }
-  return true;
+  return any;
 }
 // The values as fp16 rows of 64 dims (128 bytes, swizzled): 64 dims (4 lanes) a block of kTile rows;
 // the second block's lanes store their halves the other way round, so that eight neighbours never
