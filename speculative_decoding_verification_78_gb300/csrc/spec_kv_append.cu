@@ -155,8 +155,9 @@ __device__ __forceinline__ void append_queries(const KvArgs &a, const RopeArgs &
   for (int k = 0; k < kQIters; ++k) {
     const int h = h0 + k * per;
     if (h < a.Hq) {
-      raw[k][0] = __ldg(reinterpret_cast<const uint4 *>(src + h * a.D + x.a));
-      raw[k][1] = __ldg(reinterpret_cast<const uint4 *>(src + h * a.D + x.b));
+      // (plain loads: where q_out is q, the read-only path is not open to them)
+      raw[k][0] = *reinterpret_cast<const uint4 *>(src + h * a.D + x.a);
+      raw[k][1] = *reinterpret_cast<const uint4 *>(src + h * a.D + x.b);
     }
   }
   Angles t;

@@ -19,3 +19,14 @@ def test_no_kernel_moves_registers_between_roles():
     roles are single warps, so none of them may use it."""
     for name in sorted(os.listdir(CSRC)):
         assert "setmaxnreg" not in source(name), name
+
+
+def test_queries_rotated_in_place_are_not_read_as_constants():
+    """q_out may be q: the read-only path (__ldg) is defined only for memory that the kernel does not
+    write."""
+    text = source("spec_kv_append.cu")
+    body = text[text.index("void append_queries("):text.index("kv_append_kernel(")]
+    reads = re.findall(r"raw\[k\]\[[01]\] = ([^;]*src[^;]*);", body)
+    assert len(reads) == 2
+    for r in reads:
+        assert "__ldg" not in r, r
