@@ -8,6 +8,8 @@ missing, every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
+import inspect
 import os
 import threading
 
@@ -538,6 +540,37 @@ def spec_kv_commit(cache, page_table, seq_lens, path_nodes, accept_len, out_lens
 
 # ------------------------------------------------------------------ conveniences (allocation)
 
+def _torch_stream(stream):
+    """The torch stream of what `stream` may be: one of torch's, or a cudaStream_t."""
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    handle = int(stream)   # 0 and 1: the legacy default stream
+    return torch.cuda.ExternalStream(handle) if handle > 1 else torch.cuda.default_stream()
+
+
+def _allocates(call):
+    """A wrapper that allocates does so on the stream it is given: there an initial value is in place
+    before the call starts, and what the wrapper drops when it returns (a workspace) is not handed out
+    again before the call has ended. What it returns may be used, and dropped, on the stream that is
+    current in the caller."""
+    at = list(inspect.signature(call).parameters).index("stream")
+
+    @functools.wraps(call)
+    def on_its_stream(*args, **kw):
+        stream = args[at] if len(args) > at else kw.get("stream")
+        if stream is None:
+            return call(*args, **kw)
+        here = torch.cuda.current_stream()
+        with torch.cuda.stream(_torch_stream(stream)):
+            out = call(*args, **kw)
+        for t in out:
+            if t is not None and t.is_cuda:
+                t.record_stream(here)
+        return out
+
+    return on_its_stream
+
+
 def new_workspace(B: int, rows_per_b: int, V: int, dtype: int, device=None) -> torch.Tensor:
     """A workspace tensor large enough for the given call shape (scratch; never needs zeroing)."""
     n = spec_workspace_bytes(B, rows_per_b, V, dtype)
@@ -551,6 +584,7 @@ def check(code: int, where: str) -> None:
         raise SpecError(code, where)
 
 
+@_allocates
 def verify_chain(target_logits, draft_logits, draft_tokens, uniforms, temperature,
                  workspace=None, stream=None):
     """Allocates the outputs and runs spec_verify_chain. Returns (accept_len, out_tokens,
@@ -567,6 +601,7 @@ def verify_chain(target_logits, draft_logits, draft_tokens, uniforms, temperatur
     return acc, out, st
 
 
+@_allocates
 def verify_tree(target_logits, parents, node_tokens, workspace=None, stream=None):
     """Allocates the outputs and runs spec_verify_tree. Returns (accept_len, path_nodes,
     out_tokens, status) device tensors."""
@@ -583,6 +618,7 @@ def verify_tree(target_logits, parents, node_tokens, workspace=None, stream=None
     return acc, path, out, st
 
 
+@_allocates
 def verify_tree_sample(target_logits, draft_logits, parents, node_tokens, uniforms, temperature,
                        workspace=None, stream=None):
     """Allocates the outputs and runs spec_verify_tree_sample. Returns (accept_len, path_nodes,
@@ -601,6 +637,7 @@ def verify_tree_sample(target_logits, draft_logits, parents, node_tokens, unifor
     return acc, path, out, st
 
 
+@_allocates
 def verify_chain_lmhead(hidden_t, head_t, hidden_d, head_d, draft_tokens, uniforms,
                         temperature, workspace=None, stream=None):
     """Allocates the outputs and runs spec_verify_chain_lmhead. Returns (accept_len, out_tokens,
@@ -624,6 +661,7 @@ def verify_chain_lmhead(hidden_t, head_t, hidden_d, head_d, draft_tokens, unifor
     return acc, out, st, lt, ld
 
 
+@_allocates
 def probs(logits, temperature, workspace=None, stream=None):
     """Allocates the output and runs spec_probs. Returns (probs fp32, status)."""
     V = logits.shape[-1]
@@ -637,6 +675,7 @@ def probs(logits, temperature, workspace=None, stream=None):
     return out, st
 
 
+@_allocates
 def sample(logits, temperature, uniforms=None, workspace=None, stream=None):
     """Allocates the output and runs spec_sample. Returns (tokens [rows] int32, status)."""
     V = logits.shape[-1]
@@ -650,6 +689,7 @@ def sample(logits, temperature, uniforms=None, workspace=None, stream=None):
     return out, st
 
 
+@_allocates
 def topk(logits, k, workspace=None, stream=None):
     """Allocates the output and runs spec_topk. Returns (indices [rows, k] int32, status)."""
     V = logits.shape[-1]
@@ -663,6 +703,7 @@ def topk(logits, k, workspace=None, stream=None):
     return out, st
 
 
+@_allocates
 def tree_mask(parents, stream=None):
     """Allocates the output and runs spec_tree_mask. Returns (mask words [B, N, W] int32 holding
     the uint32 bit patterns, status)."""
@@ -691,6 +732,7 @@ def new_attention_workspace(B, N, q_heads, kv_heads, head_dim, device=None) -> t
     return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
 
 
+@_allocates
 def kv_append(cache, page_table, seq_lens, k, v, q=None, rope=None, layer=0, interleaved=False,
               positions=None, mask=None, new_lens=None, q_out=None, status=None, stream=None):
     """Appends the new tokens' keys (rotated) and values to one layer of the cache and rotates the
@@ -704,6 +746,7 @@ def kv_append(cache, page_table, seq_lens, k, v, q=None, rope=None, layer=0, int
     return q_out, status
 
 
+@_allocates
 def kv_attention(cache, page_table, seq_lens, q, scale=None, mask=None, layer=0, new_lens=None,
                  out=None, workspace=None, status=None, return_lse=False, stream=None):
     """Attention of the new tokens over one layer of the cache, which already holds them
@@ -724,6 +767,7 @@ def kv_attention(cache, page_table, seq_lens, q, scale=None, mask=None, layer=0,
     return out, lse, status
 
 
+@_allocates
 def kv_commit(cache, page_table, seq_lens, path_nodes, accept_len, out_lens=None, status=None,
               stream=None):
     """Keeps the accepted paths of verified trees in every layer of the cache (spec_kv_commit).
