@@ -364,7 +364,9 @@ int spec_kv_append(const spec_kv_cache_t *cache, const int32_t *page_table, int 
  *   out  [B, N, q_heads, head_dim] the same type, contiguous
  *   lse  [B, N, q_heads] fp32 or NULL: the natural logarithm of the softmax's denominator
  * Scores, statistics and sums are held in fp32 and the softmax weights are rounded to fp16 before
- * their product with the values. A query that sees no token (an empty mask row of an empty
+ * their product with the values. The value scales of the pages that a query sees lie within a factor
+ * of 2^80 of each other (smaller ones than 2^-80, zero too, count as 2^-80); key scales are any
+ * finite numbers. A query that sees no token (an empty mask row of an empty
  * sequence, or padding) gets zeros and lse = -inf. What lies in slots that no query of the
  * sequence sees is not used, NaN included; a NaN in a query, key or value reaches the outputs of
  * the queries that see it and no others.

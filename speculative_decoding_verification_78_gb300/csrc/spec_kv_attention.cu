@@ -197,9 +197,11 @@ __device__ __forceinline__ bool weigh(const AttnArgs &p, const Item &x, const To
 }
 
 // Before a tile is taken again: the largest y of each of this thread's columns over the warp's 32
-// tokens, to wmax[column], and what the first attempt added to l taken off again. (That leaves at
-// most 2^-24 of the weight taken off, which stays in the new sum anyway; where it was infinite, the
-// old sum is less than 2^-100 of the new one. A NaN stays.)
+// tokens, to wmax[column], and what the first attempt added to l, by the same expression, taken off
+// again. (That leaves at most half a unit of the sum, which the new sum is not smaller than. Where the sum
+// was infinite the old one is dropped: with value scales within 2^80 of each other each weight in it is
+// below 2^-32 of the new one's, for y passed m by 128, or by 48 and more where 1 / vs is what passed the
+// range. A NaN stays.)
 template <class F>
 __device__ __forceinline__ void retract(const AttnArgs &p, const Item &x, const Token &t, uint32_t ts,
                                         int col0, const float *qs, const float *nm, const int *tok,
@@ -209,20 +211,25 @@ __device__ __forceinline__ void retract(const AttnArgs &p, const Item &x, const 
     uint32_t s[F::CH];
     tmem_ld(ts + c0, s);
     tmem_wait(s);
-    float y[F::CH];
+    float y[F::CH];   // without the reference
+    float w[F::CH];   // as the first attempt weighed it
 #pragma unroll
     for (int c = 0; c < F::CH; ++c) {
       const int n = col0 + c0 + c;
-      y[c] = __fmaf_rn(__uint_as_float(s[c]) * t.ks2, qs[n], t.lvs);
-      if (!sees<F>(p, x, t, n, tok)) y[c] = -INFINITY;
+      const float z = __uint_as_float(s[c]) * t.ks2;
+      y[c] = __fmaf_rn(z, qs[n], t.lvs);
+      w[c] = ex2(__fmaf_rn(z, qs[n], __fadd_rn(nm[n], t.lvs)));
+      if (!sees<F>(p, x, t, n, tok)) {
+        y[c] = -INFINITY;
+        w[c] = 0.f;
+      }
     }
 #pragma unroll
     for (int c = 0; c < F::CH; c += 2) {
-      const int n = col0 + c0 + c;
       float l0, l1;
       up2(l[(c0 + c) / 2], l0, l1);
-      l0 = l0 == INFINITY ? 0.f : l0 - ex2(y[c] + nm[n]) * t.ivs;
-      l1 = l1 == INFINITY ? 0.f : l1 - ex2(y[c + 1] + nm[n + 1]) * t.ivs;
+      l0 = l0 == INFINITY ? 0.f : __fmaf_rn(-w[c], t.ivs, l0);
+      l1 = l1 == INFINITY ? 0.f : __fmaf_rn(-w[c + 1], t.ivs, l1);
       l[(c0 + c) / 2] = pk2(l0, l1);
       if (y[c] != y[c]) y[c] = -INFINITY;
       if (y[c + 1] != y[c + 1]) y[c + 1] = -INFINITY;

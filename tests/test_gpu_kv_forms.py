@@ -50,3 +50,43 @@ def test_scratch_of_a_call_on_another_stream(sv, raw):
         if code == 0:
             assert torch.equal(out, want) and torch.equal(lse, wlse)
         assert all(bool((j == 0x3f).all()) for j in junk)
+
+
+# ------------------------------------------------------------------ references that rise
+
+@pytest.mark.parametrize("G", [16, 32])
+def test_a_row_whose_reference_rises_leaves_the_others_sums(sv, G):
+    """Rows share tiles with one whose scores rise by more than 2^7 a tile, so that every tile is weighed
+    twice. What the first time added to the others' sums is taken off again to half a unit of the sum: of
+    6 tiles a group at most 3.5 x 2^-24, 2^-21.7 of a base-2 logarithm, which is held in steps of 2^-18 (the
+    values' scale is 2^70): at most one row in 13 may show it, and one in 8 is let pass."""
+    B, Hkv, D, page, tiles = 19, 8, 64, 64, 12
+    n = 128 * tiles
+    rng = np.random.default_rng(G)
+    k = np.zeros((B, n, Hkv, D), np.float32)
+    k[..., 1:] = rng.integers(-8, 9, (B, 1, Hkv, D - 1))   # every token the same but for dim 0
+    k[..., 0] = (np.arange(n) // 128)[None, :, None]
+    pages = B * n // page
+
+    def pool(x):   # [B, n, Hkv, D] -> pages in order
+        x = x.reshape(pages, page, Hkv, D).transpose(0, 2, 1, 3)
+        return torch.from_numpy(np.ascontiguousarray(x)).cuda().to(kv.E4)
+
+    v = pool(rng.integers(-8, 9, k.shape).astype(np.float32))
+    one = torch.ones(pages, Hkv, device="cuda")
+    cache = sv.KVCache(pool(k), v, one, one * 2.0 ** 70)
+    table = torch.arange(pages, dtype=torch.int32, device="cuda").view(B, -1)
+    lens = torch.full((B,), n - 1, dtype=torch.int32, device="cuda")
+    q = rand16(rng, (B, 1, Hkv * G, D), torch.bfloat16, 0.05)
+    q[..., 0] = 0
+    lses = []
+    for rising in (0.0, 16.0):
+        r = q.clone()
+        r[:, :, ::G] = 0
+        r[:, :, ::G, 0] = rising
+        _, lse, st = sv.kv_attention(cache, table, lens, r, scale=1.0, return_lse=True)
+        assert int(st.item()) == 0
+        lses.append(lse.view(-1, G)[:, 1:])
+    assert bool(torch.isfinite(lses[0]).all())
+    differ = float((lses[0] != lses[1]).float().mean())
+    assert differ <= 1 / 8, differ
