@@ -371,6 +371,8 @@ int spec_kv_append(const spec_kv_cache_t *cache, const int32_t *page_table, int 
  * sequence sees is not used, NaN included; a NaN in a query, key or value reaches the outputs of
  * the queries that see it and no others.
  *   workspace  at least spec_kv_attention_workspace_bytes(B, N, q_heads, kv_heads, head_dim) bytes
+ * Limits: N * G < 2^31 and B * kv_heads * ceil(N * G / R) * ceil(pages_per_seq * page_size / 128) < 2^31,
+ * with R = 16, 32, 128 or 256, the first that holds N * G or else 256 (q_heads <= 16 * 1024).
  * In the data: a bad length makes every output of the sequence NaN, a bad page number those of the
  * queries that see a token of the page; both set *status. A wait inside the kernel that gives up
  * (after 2 s) sets *status to SPEC_ERR_TIMEOUT.

@@ -149,5 +149,10 @@ cudaError_t launch_kv_attention(const KvArgs &a, const void *q, long long q_stri
                                 float scale, void *out, float *lse, void *ws,
                                 cudaStream_t stream);
 size_t kv_attention_workspace(int B, int N, int Hq, int Hkv, int D);
+// Query rows of a tile, for calls with `rows` of them a key head: up to 32 along the columns of an MMA, more
+// along its lanes. (What each costs is measured at the two kernels.)
+inline int kv_row_tile(long long rows) {
+  return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 128 ? 128 : 256;
+}
 
 }  // namespace specv

@@ -2,6 +2,8 @@
 // dispatch to the kernels.
 #include <math.h>
 
+#include <initializer_list>
+
 #include "spec_kv.h"
 #include "spec_verify.h"
 
@@ -135,11 +137,17 @@ int spec_kv_attention(const spec_kv_cache_t *cache, const int32_t *page_table, i
   const size_t need = spec_kv_attention_workspace_bytes(B, N, q_heads, a.Hkv, a.D);
   if (need == 0) return SPEC_ERR_SHAPE;
   if (!stride_ok(q_stride, q_heads, a.D) || !isfinite(scale)) return SPEC_ERR_SHAPE;
-  // work is counted in 128-token tiles of one row tile and key head, in 31 bits
-  const long long tiles = (static_cast<long long>(pages_per_seq) * a.page + 127) / 128;
-  const long long rows = (static_cast<long long>(N) * (q_heads / a.Hkv) + 15) / 16;
-  if (rows >= (1LL << 27) || static_cast<double>(B) * a.Hkv * rows * tiles >= 2147483648.0)
-    return SPEC_ERR_SHAPE;
+  // rows, and the 128-token tiles of all sequences, key heads and row tiles, are counted in 31 bits
+  const long long limit = 1LL << 31;
+  const long long rows = static_cast<long long>(N) * (q_heads / a.Hkv);
+  if (rows >= limit) return SPEC_ERR_SHAPE;
+  const int height = kv_row_tile(rows);
+  long long tiles = (static_cast<long long>(pages_per_seq) * a.page + 127) / 128;   // < 2^23
+  for (const long long f : {(rows + height - 1) / height, static_cast<long long>(a.Hkv),
+                            static_cast<long long>(B)}) {
+    tiles *= f;   // both below 2^31
+    if (tiles >= limit) return SPEC_ERR_SHAPE;
+  }
   if (!q || !out || !workspace) return SPEC_ERR_NULL;
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(workspace, 16))
     return SPEC_ERR_ALIGN;

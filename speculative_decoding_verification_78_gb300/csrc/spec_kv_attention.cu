@@ -645,8 +645,7 @@ cudaError_t launch_columns(bool wide, AttnArgs &p, const CUtensorMap &mk, const 
 }  // namespace
 
 size_t kv_attention_workspace(int B, int N, int Hq, int Hkv, int D) {
-  const long long rows = static_cast<long long>(N) * (Hq / Hkv);
-  const size_t nt = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 128 ? 128 : 256;
+  const size_t nt = kv_row_tile(static_cast<long long>(N) * (Hq / Hkv));
   return 2 * kMaxCtas * (sizeof(int4) + nt * sizeof(float) * (1 + D));
 }
 
@@ -678,8 +677,8 @@ cudaError_t launch_kv_attention(const KvArgs &a, const void *q, long long q_stri
   const int ctas = sms < kMaxCtas ? sms : kMaxCtas;
   const long long query_rows = static_cast<long long>(a.N) * p.G;
   char *w = static_cast<char *>(ws);
-  if (query_rows > 32) return launch_attention_rows(p, dtype, mk, mv, ctas, w, stream);
-  const bool wide = query_rows > 16;
+  if (kv_row_tile(query_rows) > 32) return launch_attention_rows(p, dtype, mk, mv, ctas, w, stream);
+  const bool wide = kv_row_tile(query_rows) == 32;
   if (dtype == SPEC_BF16)
     return a.D == 64 ? launch_columns<__nv_bfloat16, 64>(wide, p, mk, mv, ctas, w, stream)
                      : launch_columns<__nv_bfloat16, 128>(wide, p, mk, mv, ctas, w, stream);

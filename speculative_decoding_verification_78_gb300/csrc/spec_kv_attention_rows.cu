@@ -658,7 +658,7 @@ cudaError_t launch_cfg(AttnArgs &p, const CUtensorMap &mk, const CUtensorMap &mv
 template <typename T, int D>
 cudaError_t launch_rows(AttnArgs &p, const CUtensorMap &mk, const CUtensorMap &mv, int ctas,
                         char *ws, cudaStream_t stream) {
-  if (static_cast<long long>(p.a.N) * p.G > 128)
+  if (kv_row_tile(static_cast<long long>(p.a.N) * p.G) == 256)
     return launch_cfg<RowsCfg<T, D, 2, 2>>(p, mk, mv, ctas, ws, stream);
   return launch_cfg<RowsCfg<T, D, 1, 3>>(p, mk, mv, ctas, ws, stream);
 }
