@@ -393,6 +393,10 @@ class KVCache:
         if not isinstance(k, torch.Tensor) or k.dim() not in (4, 5):
             raise ValueError("k must be a [layers, num_pages, kv_heads, page_size, head_dim] "
                              "tensor (or one layer of it)")
+        for t, name, shape in ((v, "v", k.shape), (k_scale, "k_scale", k.shape[:-2]),
+                               (v_scale, "v_scale", k.shape[:-2])):
+            if not isinstance(t, torch.Tensor) or t.shape != shape:
+                raise ValueError(f"{name} must be a {list(shape)} tensor beside k {list(k.shape)}")
         if k.dim() == 4:
             k, v, k_scale, v_scale = (t[None] for t in (k, v, k_scale, v_scale))
         self.layers, self.num_pages, self.kv_heads, self.page_size, self.head_dim = k.shape

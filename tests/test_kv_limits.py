@@ -25,3 +25,20 @@ def test_attention_tiles_in_31_bits(sv, N, most):   # noqa: F811
     (dict(B=1, N=1 << 20, qh=8 * 2048, qs=8 * 2048 * 128, pps=1), -2)])
 def test_long_prompts_are_taken(sv, shape, code):   # noqa: F811
     assert _attend(sv, _cache(sv, kv_heads=8), wsb=16, **shape) == code
+
+
+@pytest.mark.parametrize("layers", [None, 3])
+@pytest.mark.parametrize("bad", ["v", "k_scale", "v_scale", "v layers", "scale layers", "none"])
+def test_cache_of_mixed_layouts(sv, layers, bad):   # noqa: F811
+    """Values and scales in another order than the keys have as many elements, but lie elsewhere."""
+    lead = () if layers is None else (layers,)
+    k = torch.zeros(*lead, 10, 2, 64, 128, dtype=torch.uint8)
+    s = torch.ones(*lead, 10, 2)
+    swap = lambda t, a, b: t.transpose(a, b).contiguous()
+    args = {"v": (k, swap(k, -3, -2), s, s), "k_scale": (k, k, swap(s, -2, -1), s),
+            "v_scale": (k, k, s, swap(s, -2, -1)), "v layers": (k, k.flatten(0, 1), s, s),
+            "scale layers": (k, k, s, s.flatten()), "none": (k, None, s, s)}[bad]
+    with pytest.raises(ValueError, match="beside k"):
+        sv.KVCache(*args)
+    with pytest.raises(ValueError, match="device tensor"):   # as it should lie
+        sv.KVCache(k, k, s, s)
