@@ -309,7 +309,8 @@ int spec_tree_mask(const int32_t *parents, int B, int N, uint32_t *mask_words, i
  *   mask_words [B, N, ceil(N / 32)] from spec_tree_mask, or NULL for a chain
  * Limits: head_dim 64 or 128; page_size 16, 32, 64 or 128; kv_heads 1 .. 1024;
  * num_pages * kv_heads * page_size < 2^31; pages_per_seq * page_size < 2^30; 1 <= N <= 2^20 (with
- * mask_words: SPEC_MAX_NODES); B >= 0. k and v are 16-byte aligned.
+ * mask_words: SPEC_MAX_NODES); B >= 0 (B == 0 does nothing, its tensors may be NULL). k and v are
+ * 16-byte aligned.
  * A page that is written belongs to one sequence; full pages may be shared by any number.
  */
 typedef struct {

@@ -21,7 +21,7 @@ constexpr int kMaxHeads = 1024;
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 // The checks every call makes of the cache and the batch, shape before pointers, and the
-// arguments they share.
+// arguments they share. The tensors of an empty batch may be null: torch gives them no address.
 int kv_common(KvArgs &a, const spec_kv_cache_t *c, const int32_t *page_table, int pps,
               const int32_t *seq_lens, const int32_t *new_lens, int B, int N,
               const uint32_t *mask_words, int32_t *status) {
@@ -35,7 +35,8 @@ int kv_common(KvArgs &a, const spec_kv_cache_t *c, const int32_t *page_table, in
     return SPEC_ERR_SHAPE;
   if (static_cast<long long>(pps) * c->page_size >= (1LL << 30)) return SPEC_ERR_SHAPE;
   if (mask_words && N > SPEC_MAX_NODES) return SPEC_ERR_SHAPE;
-  if (!c->k || !c->v || !c->k_scale || !c->v_scale || !page_table || !seq_lens || !status)
+  if (!c->k || !c->v || !c->k_scale || !c->v_scale || !status ||
+      (B > 0 && (!page_table || !seq_lens)))
     return SPEC_ERR_NULL;
   if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 4) ||
       !aligned(c->v_scale, 4) || !aligned(page_table, 4) || !aligned(seq_lens, 4) ||
@@ -89,13 +90,13 @@ int spec_kv_append(const spec_kv_cache_t *cache, const int32_t *page_table, int 
     return SPEC_ERR_SHAPE;
   if (rope_dim < 0 || rope_dim > a.D || rope_dim % 16 || (rope_dim > 0 && rope_rows < 1))
     return SPEC_ERR_SHAPE;
-  if (!k || !v || (q_heads > 0 && (!q || !q_out)) || (rope_dim > 0 && !rope))
+  if ((B > 0 && (!k || !v || (q_heads > 0 && (!q || !q_out)))) || (rope_dim > 0 && !rope))
     return SPEC_ERR_NULL;
   if (!aligned(k, 16) || !aligned(v, 16) || !aligned(rope, 4) || !aligned(positions, 4) ||
       (q_heads > 0 && (!aligned(q, 16) || !aligned(q_out, 16))))
     return SPEC_ERR_ALIGN;
   // rotating in place needs the output's layout
-  if (q_heads > 0 && q == q_out && q_stride != static_cast<int64_t>(q_heads) * a.D)
+  if (q_heads > 0 && q && q == q_out && q_stride != static_cast<int64_t>(q_heads) * a.D)
     return SPEC_ERR_SHAPE;
   if (B == 0) return SPEC_OK;
   a.Hq = q_heads;
@@ -148,7 +149,7 @@ int spec_kv_attention(const spec_kv_cache_t *cache, const int32_t *page_table, i
     tiles *= f;   // both below 2^31
     if (tiles >= limit) return SPEC_ERR_SHAPE;
   }
-  if (!q || !out || !workspace) return SPEC_ERR_NULL;
+  if ((B > 0 && (!q || !out)) || !workspace) return SPEC_ERR_NULL;
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(workspace, 16))
     return SPEC_ERR_ALIGN;
   if (workspace_bytes < need) return SPEC_ERR_WORKSPACE;
@@ -167,10 +168,10 @@ int spec_kv_commit(const spec_kv_cache_t *cache, int layers, const int32_t *page
                            status);
   if (rc != SPEC_OK) return rc;
   if (layers < 1 || N > SPEC_MAX_NODES) return SPEC_ERR_SHAPE;
-  if (!path_nodes || !accept_len || !out_lens) return SPEC_ERR_NULL;
+  if (B > 0 && (!path_nodes || !accept_len || !out_lens)) return SPEC_ERR_NULL;
   if (!aligned(path_nodes, 4) || !aligned(accept_len, 4) || !aligned(out_lens, 4))
     return SPEC_ERR_ALIGN;
-  if (out_lens == seq_lens) return SPEC_ERR_SHAPE;
+  if (out_lens && out_lens == seq_lens) return SPEC_ERR_SHAPE;
   if (B == 0) return SPEC_OK;
   return launch_result(launch_kv_commit(a, layers, path_nodes, accept_len, out_lens,
                                         static_cast<cudaStream_t>(stream)));

@@ -90,3 +90,17 @@ def test_a_row_whose_reference_rises_leaves_the_others_sums(sv, G):
     assert bool(torch.isfinite(lses[0]).all())
     differ = float((lses[0] != lses[1]).float().mean())
     assert differ <= 1 / 8, differ
+
+
+def test_an_empty_batch(sv):
+    cache = sv.new_kv_cache(4, 2, 64, 16)
+    before = cache.k.view(torch.uint8).clone()
+    table = torch.empty(0, 2, dtype=torch.int32, device="cuda")
+    lens = torch.empty(0, dtype=torch.int32, device="cuda")
+    x = torch.empty(0, 3, 8, 64, dtype=torch.bfloat16, device="cuda")
+    q, st = sv.kv_append(cache, table, lens, x[:, :, :2], x[:, :, :2], q=x)
+    out, lse, st = sv.kv_attention(cache, table, lens, q, return_lse=True, status=st)
+    new, st = sv.kv_commit(cache, table, lens, torch.empty(0, 3, dtype=torch.int32, device="cuda"), lens, status=st)
+    assert int(st.item()) == 0
+    assert (q.shape, out.shape, lse.shape, new.shape) == (x.shape, x.shape, x.shape[:3], lens.shape)
+    assert torch.equal(cache.k.view(torch.uint8), before)

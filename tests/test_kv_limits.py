@@ -42,3 +42,18 @@ def test_cache_of_mixed_layouts(sv, layers, bad):   # noqa: F811
         sv.KVCache(*args)
     with pytest.raises(ValueError, match="device tensor"):   # as it should lie
         sv.KVCache(k, k, s, s)
+
+
+def test_an_empty_batch_has_no_tensors(sv):   # noqa: F811
+    """B = 0 does nothing, and torch gives empty tensors no address: only the cache and the status are
+    asked for."""
+    none = dict(B=0, table=None, lens=None)
+    assert _append(sv, k=None, v=None, q=None, qo=None, **none) == sv.SPEC_OK
+    assert _attend(sv, q=None, out=None, **none) == sv.SPEC_OK
+    assert _commit(sv, path=None, acc=None, out=None, **none) == sv.SPEC_OK
+    for call in (_append, _attend, _commit):
+        assert call(sv, _cache(sv, k=None), B=0) == sv.SPEC_ERR_NULL
+        assert call(sv, B=0, status=None) == sv.SPEC_ERR_NULL
+        assert call(sv, B=0, N=0) == sv.SPEC_ERR_SHAPE
+        assert call(sv, B=0, lens=FAKE + 1) == sv.SPEC_ERR_ALIGN
+    assert _attend(sv, B=0, wsb=16) == sv.SPEC_ERR_WORKSPACE
