@@ -10,8 +10,9 @@
  * "Circularity Check"). Falcon verifies a tree of drafts in one pass under greedy decoding
  * ("Falcon: Faster and Parallel Inference of Large Language Models through Enhanced
  * Semi-Autoregressive Drafting and Custom-Designed Decoding Tree", pith.science review,
- * "What carries the argument", Figure 3, Figure 4). This library is that verify step and
- * nothing else: the draft and target models are the caller's.
+ * "What carries the argument", Figure 3, Figure 4). This library is that verify step and what
+ * stands next to it in a step: the drafter's sampler and top-n, the tree-attention mask, the LM head of
+ * a chain, and the target's paged KV cache (append, attention, commit). The models are the caller's.
  *
  * Common rules for every entry point
  *   - All pointers except `stream` and `workspace`'s host-side size are DEVICE pointers on the
@@ -364,11 +365,13 @@ int spec_kv_append(const spec_kv_cache_t *cache, const int32_t *page_table, int 
  *   q    [B, N, q_heads, head_dim] SPEC_BF16 or SPEC_F16, tokens q_stride elements apart
  *   out  [B, N, q_heads, head_dim] the same type, contiguous
  *   lse  [B, N, q_heads] fp32 or NULL: the natural logarithm of the softmax's denominator
- * Scores, statistics and sums are held in fp32 and the softmax weights are rounded to fp16 before
- * their product with the values. The value scales of the pages that a query sees lie within a factor
- * of 2^80 of each other (smaller ones than 2^-80, zero too, count as 2^-80); key scales are any
- * finite numbers. A query that sees no token (an empty mask row of an empty
- * sequence, or padding) gets zeros and lse = -inf. What lies in slots that no query of the
+ * Scores, statistics and sums are held in fp32. Two things are rounded to fewer bits: the softmax
+ * weights, to fp16, before their product with the values; and queries, which are cut into e4m3 terms
+ * (bf16 two: exact for elements of at least 2^-9 of the row's largest; fp16 three: 2^-6), to 2^-17 of the
+ * row's largest element. The value scales of the pages that a query sees lie within a factor of 2^80 of
+ * each other (smaller ones than 2^-80, zero too, count as 2^-80); key scales are any finite numbers. A
+ * query that sees no token (an empty mask row of an empty sequence, or padding) gets zeros and
+ * lse = -inf. What lies in slots that no query of the
  * sequence sees is not used, NaN included; a NaN in a query, key or value reaches the outputs of
  * the queries that see it and no others.
  *   workspace  at least spec_kv_attention_workspace_bytes(B, N, q_heads, kv_heads, head_dim) bytes

@@ -113,7 +113,7 @@ template <typename T> __device__ __forceinline__ uint4 floats_to_vec(const float
 }
 
 // Launches `kernel` on `stream` as a programmatic dependent of what precedes it there: it may be
-// scheduled while that drains, and every kernel here waits (griddepcontrol.wait) before it
+// scheduled while that drains, so a kernel launched by it waits (griddepcontrol.wait) before it
 // touches memory.
 template <typename... P, typename... A>
 inline cudaError_t launch_kv(void (*kernel)(P...), long long grid, int threads, size_t smem,

@@ -13,7 +13,8 @@
 // tensor time in proportion to the query rows that exist. K's e4m3 bytes are an MMA operand as TMA
 // lands them: Q is the sum of 2 (bf16) or 3 (fp16) e4m3 terms, whose products accumulate in the
 // same fp32 accumulator (two terms hold bf16's 8 significant bits exactly down to 2^-9 of the
-// row's power-of-two unit; three fp16's 11). P is fp16 (11 bits; e4m3 terms would flush weights
+// row's largest element, three fp16's 11 down to 2^-6; smaller elements are off by at most 2^-17
+// of the largest). P is fp16 (11 bits; e4m3 terms would flush weights
 // below 2^-18 of the reference, which a long context of small weights adds up), so V's bytes are
 // widened to fp16, exactly, on their way through the softmax threads.
 //
@@ -35,7 +36,8 @@
 // be uniform, 503 us. Tried and not kept: the query terms as columns side by side (8 MMAs fewer, the terms
 // added by the softmax: 362 against 333 us), the page constants worked out by the copying warp (407), scores
 // two tiles ahead of the values with the weights before the widening (390: a stage is held longer than
-// four of them last), waits without a vote, as the kernel for many rows has them (354: spills).
+// four of them last), waits without a vote, as the kernel for many rows has them (354: more spills). At 96
+// registers, what 18 warps leave, all forms but that of 16 columns and 64 dims spill 40 to 44 bytes.
 #include "spec_kv_attn.h"
 
 namespace specv {
@@ -267,7 +269,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   }
   if (tid < 2 * kTile) sm.vnan[tid / kTile][tid % kTile] = 0;
   if (warp == kMma) tmem_alloc(&sm.tmem, F::kTmem);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   int t0 = 0, t1 = 0, total = 0, skip = 0;
   Item x{};
   tc::fence_before_sync();
@@ -629,7 +630,8 @@ cudaError_t launch_cfg(AttnArgs &p, const CUtensorMap &mk, const CUtensorMap &mv
   cudaError_t e = allow_smem(kv_attention_kernel<F>, smem, ready);
   if (e != cudaSuccess) return e;
   plan_parts(p, ws, F::NT);
-  // a plain stream-ordered launch: nearly all of an SM's shared memory is one CTA's
+  // In plain stream order, so the kernel waits for nothing itself; it lets its join be scheduled early.
+  // (Not measured: a launch as a programmatic dependent, whose set-up would run under the kernel before.)
   kv_attention_kernel<F><<<ctas, kAttnThreads, smem, stream>>>(mk, mv, p);
   e = cudaGetLastError();
   return e != cudaSuccess ? e : launch_join<typename F::T, F::D, F::NT>(p, ctas, stream);

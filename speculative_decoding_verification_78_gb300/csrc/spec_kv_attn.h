@@ -377,7 +377,8 @@ struct RowMap {
 
 // Rows 0 .. NT - 1 of the item as e4m3 terms in shared memory (D / 8 lanes a row), each in units of a
 // power of two that puts its largest element in [2^7, 2^8); qs[n] undoes it. Two terms hold bf16's 8
-// significant bits exactly down to 2^-9 of the unit, three fp16's 11. Blocks of kBlock rows, each
+// significant bits exactly for elements from 2^-2 on, three fp16's 11 from 2 on; below that they are off by
+// at most 2^-10, half the smallest e4m3 value. Blocks of kBlock rows, each
 // term of a block a K-major operand; of the NT rows the first `rows` (a multiple of 16) are written, zero
 // past the item's.
 template <typename T, int D, int NT, int kBlock, int kTerms, int kThreads>
