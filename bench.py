@@ -171,8 +171,9 @@ def measured_tensor_peaks():
 
 def kernel_source_hash():
     """Hash of the sources that define the verify kernels and their launches (the C ABI's host
-    checks, the static-scratch entry point and the LM-head GEMM's tensor-core helpers do not
-    change what those kernels read or write)."""
+    checks, the static-scratch entry point, the LM-head GEMM's tensor-core helpers and the KV
+    cache, all of whose files are spec_kv*.cu and spec_kv*.h, do not change what those kernels
+    read or write)."""
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "speculative_decoding_verification_78_gb300", "csrc")
     for f in sorted(os.listdir(csrc)):
