@@ -354,3 +354,21 @@ def test_append_rotation_table_off_16_bytes(sv, shift):
         out.append((q, cache.k.view(torch.uint8), cache.v.view(torch.uint8), cache.k_scale, cache.v_scale))
     for a, b in zip(*out):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("sizes", [(-64, 16), (-70, 8), (0, 80)])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("N,Hq", FORMS)
+def test_attention_value_scales_as_far_apart_as_allowed(sv, N, Hq, D, sizes):
+    """Pages of two value scales 2^78 to 2^80 apart, in runs of random lengths: the small ones' values vanish
+    beside the others', but their weights count. (bf16, whose range holds the outputs of either.)"""
+    c = Case(1000 + N + D, [1100, 300, 128], N, 2, D, 16)
+    for b in range(3):
+        at = 0
+        while at < c.pps:
+            run = int(c.rng.integers(1, 40))
+            pick = c.rng.integers(0, 2, 2)
+            for h in range(2):
+                c.scale[1][0, np.maximum(c.table[b, at:at + run], 0), h] = 2.0 ** sizes[pick[h]]
+            at += run
+    check_attention(sv, c, rand16(c.rng, (3, N, Hq, D), torch.bfloat16))
