@@ -72,6 +72,8 @@ typedef enum { SPEC_F32 = 0, SPEC_BF16 = 1, SPEC_F16 = 2 } spec_dtype_t;   /* F1
 #define SPEC_ERR_POSITION (-27)  /* KV cache: a token's position is outside the rotation table */
 #define SPEC_ERR_PATH (-28)      /* KV cache: accept_len outside [-1, N), or path nodes that do
                                     not increase from node 0 within [0, N)                    */
+#define SPEC_ERR_NO_PAGE (-29)   /* KV cache: the pool has no free page left for a sequence       */
+#define SPEC_ERR_REFS (-30)      /* KV cache: a page was given back more often than it was held   */
 #define SPEC_ERR_CHECK (-24)     /* checked build only (libspec_verify_checked.so): an index the
                                     kernels computed fell outside its buffer; the access was
                                     skipped. Never seen from a correct library.               */
@@ -81,6 +83,10 @@ typedef enum { SPEC_F32 = 0, SPEC_BF16 = 1, SPEC_F16 = 2 } spec_dtype_t;   /* F1
 #define SPEC_LMHEAD_MAX_V (1 << 19)   /* vocabulary size of spec_verify_chain_lmhead          */
 #define SPEC_MAX_GAMMA 255     /* draft length of the chain                                  */
 #define SPEC_MAX_NODES 1024    /* nodes per candidate tree                                   */
+#define SPEC_MAX_BEAMS 64      /* beams of a batch row                                       */
+#define SPEC_MAX_BEST 64       /* candidates that spec_beam_select returns for a batch row   */
+#define SPEC_MAX_STATES 8      /* tensors of one spec_beam_reorder call                      */
+#define SPEC_MAX_SEQS 8192     /* sequences of a call that deals with pages                  */
 
 /*
  * Bytes of workspace needed by a call over B batch rows of `rows_per_b` logits rows of V
@@ -277,6 +283,49 @@ int spec_topk(const void *logits, int dtype, int rows, int V, int k, int32_t *ou
               int32_t *status, void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * Beam search: the n best continuations of the K beams of each of B sequences, over all beams and the whole
+ * vocabulary (for a beam of drafts, or of a draft tree's branches: spec_topk with the beams' scores).
+ * Candidate (k, v) has the score
+ *   scores[b, k] + logits[b, k, v] - log sum_j exp(logits[b, k, j])
+ * tokens, parents and out_scores [b, 0..n) are the best of them, the largest score first, equal scores by
+ * beam, then by token: v, the row b * K + k (what spec_beam_reorder and spec_kv_fork take as parents) and the
+ * score. The order is that of the scores in exact arithmetic (two whose difference is not 0 but below 1e-9 may
+ * be taken for each other); out_scores are within 4e-6 of them, rounded to fp32.
+ *   - A beam whose score is -inf is not in use: it has no candidates, and its logits are not read.
+ *   - A beam with done[b, k] != 0 has ended: its one candidate is pad_token at its own score, and its logits
+ *     are not read. (done NULL: none has.)
+ *   - Entries past the last candidate: token and parent -1, score -inf.
+ *   - A NaN or +inf score, or an invalid logits row of a beam in use, makes the whole batch row -1 with NaN
+ *     scores and sets *status (SPEC_ERR_NONFINITE).
+ *   logits [B, K, V] dtype     scores [B, K] fp32     done [B, K] int32 or NULL
+ *   tokens, parents [B, n] int32 out     out_scores [B, n] fp32 out (apart from scores)
+ *   workspace  at least spec_beam_workspace_bytes(B, K, V, dtype) bytes (scratch)
+ * Limits: 1 <= K <= SPEC_MAX_BEAMS, 1 <= n <= SPEC_MAX_BEST, 1 <= V <= SPEC_MAX_V, 0 <= pad_token < V, B >= 0
+ * (B == 0 does nothing); units of 4 KB of a row's logits are counted in 31 bits over all rows.
+ */
+size_t spec_beam_workspace_bytes(int B, int K, int V, int dtype);
+int spec_beam_select(const void *logits, int dtype, const float *scores, const int32_t *done,
+                     int pad_token, int B, int K, int V, int n, int32_t *tokens, int32_t *parents,
+                     float *out_scores, int32_t *status, void *workspace, size_t workspace_bytes,
+                     void *stream);
+
+/*
+ * Reorders what belongs to the beams (token histories, hidden or recurrent states) by their parents:
+ *   out[c, :] = in[parents[c], :]   for c = 0 .. rows_out - 1, and zeros where parents[c] is -1
+ * for `count` tensors of rows_in and rows_out rows of row_bytes bytes, one after another. Any other parent
+ * outside [0, rows_in) counts as -1 and sets *status (SPEC_ERR_PARENT). No out may overlap an in.
+ * Limits: 1 <= count <= SPEC_MAX_STATES, row_bytes >= 1, rows_in, rows_out >= 0, rows_out * count < 2^31,
+ * rows * row_bytes < 2^62. (The KV cache is reordered by spec_kv_fork.)
+ */
+typedef struct {
+  const void *in;
+  void *out;
+  int64_t row_bytes;
+} spec_state_t;
+int spec_beam_reorder(const spec_state_t *states, int count, const int32_t *parents, int rows_in,
+                      int rows_out, int32_t *status, void *stream);
+
+/*
  * Tree-attention mask of B candidate trees (Falcon review, Figure 3, "SAR decoding tree
  * attention": every node attends to itself and its ancestors): with W = ceil(N / 32), bit j % 32
  * of mask_words[b, i, j / 32] is set iff node j is node i or an ancestor of node i. Parents as
@@ -404,6 +453,79 @@ int spec_kv_commit(const spec_kv_cache_t *cache, int layers, const int32_t *page
                    int pages_per_seq, const int32_t *seq_lens, int B, int N,
                    const int32_t *path_nodes, const int32_t *accept_len, int32_t *out_lens,
                    int32_t *status, void *stream);
+
+/*
+ * The pages of a cache. refs [num_pages] int32, zero at first, counts the places of page tables that hold a
+ * page: a page with 0 is free, and nothing else says so. In these calls a negative entry of a page table is a
+ * place without a page (the other calls read entries only where a sequence has tokens). All layers share
+ * pages and counts. Whoever needs a page gets the lowest free one, in the order of sequences and of places,
+ * so the results do not depend on timing. `cache` gives the sizes (and, where contents move, layer 0's
+ * memory; layers lie one after another as for spec_kv_commit). Tables may share pages; the rows of one call's
+ * table do not overlap. B and C are at most SPEC_MAX_SEQS.
+ *   workspace  at least spec_kv_pages_workspace_bytes(num_pages, B) bytes (scratch; of spec_kv_fork: C for B)
+ * In the data: a bad length (SPEC_ERR_LENGTH) leaves the sequence as it is; an entry of num_pages or more
+ * (SPEC_ERR_PAGE) counts as none; a page that is given back though nothing holds it stays free (SPEC_ERR_REFS).
+ */
+size_t spec_kv_pages_workspace_bytes(int num_pages, int B);
+
+/*
+ * Free pages for the slots seq_lens[b] .. seq_lens[b] + new_lens[b] - 1 (new_lens NULL: N each) that have
+ * none: page_table [B, pages_per_seq] and refs are brought up to date. A sequence gets all that it needs or
+ * nothing: served are those whose needs and those of all sequences before them fit into the free pages
+ * (a sequence that needs none always is); the others set *status (SPEC_ERR_NO_PAGE).
+ *   granted [B] int32 out: new_lens[b], or 0 for a sequence that was not served or whose lengths are bad
+ *           (so it may be the new_lens of spec_kv_append and spec_kv_attention)
+ * A new page's contents are left as they were. Limits: 1 <= N <= 2^20.
+ */
+int spec_kv_reserve(const spec_kv_cache_t *cache, int32_t *refs, int32_t *page_table, int pages_per_seq,
+                    const int32_t *seq_lens, const int32_t *new_lens, int B, int N, int32_t *granted,
+                    int32_t *status, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Gives back what B sequences of seq_lens[b] tokens do not need any more: pages all of whose slots t are
+ * behind the window of the next token (t <= seq_lens[b] - window) and not among the first `sinks`, and pages
+ * past the last token (reserved, not used). Limits: window >= 1 (2^30 or more: nothing is behind it),
+ * sinks >= 0.
+ */
+int spec_kv_trim(const spec_kv_cache_t *cache, int32_t *refs, int32_t *page_table, int pages_per_seq,
+                 const int32_t *seq_lens, int B, int window, int sinks, int32_t *status, void *stream);
+
+/*
+ * Ends sequences: those with ended[b] != 0 (NULL: all) give back their pages; their table entries become -1
+ * and their lengths 0. (Lengths are not read: any table is fine.)
+ */
+int spec_kv_free(const spec_kv_cache_t *cache, int32_t *refs, int32_t *page_table, int pages_per_seq,
+                 int32_t *seq_lens, const int32_t *ended, int B, int32_t *status, void *stream);
+
+/*
+ * C new sequences that continue from B given ones: child c has the tokens of parents[c]. Full pages are
+ * shared. The last page, if it is not full, is copied in all layers into a free page (its first tokens and
+ * its scales: the rows behind them keep what they held), because a page that is written belongs to one
+ * sequence. With release != 0 the parents end (a beam search's step): each gives back its pages, the first of
+ * its children takes over its last page uncopied, and pages that this frees are there for the copies of the
+ * others. page_table is not changed: with release it is void after the call.
+ *   parents [C] int32: -1 for none (an empty child: length 0); any other value outside [0, B) sets *status
+ *           (SPEC_ERR_PARENT) and the child's length to -1, as a parent with a bad length does
+ *   page_table_out [C, pages_per_seq], lens_out [C] int32 out, apart from page_table and seq_lens
+ * Places past the last token have no page in a child. A child for whose copy no page is left has no pages and
+ * the length -1 (SPEC_ERR_NO_PAGE); copies are served in the order of the children.
+ */
+int spec_kv_fork(const spec_kv_cache_t *cache, int layers, int32_t *refs, const int32_t *page_table,
+                 int pages_per_seq, const int32_t *seq_lens, int B, const int32_t *parents, int C,
+                 int release, int32_t *page_table_out, int32_t *lens_out, int32_t *status,
+                 void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Moves the pages in use to the front of the pool, so that pages live[0] .. num_pages - 1 are free: of the
+ * pages from live[0] on, the i-th in use moves (contents in all layers, scales and count) to the i-th free one
+ * below. The entries of page_table follow.
+ *   page_map [num_pages] int32 out: where each page's contents are now, -1 for a page that was free (for other
+ *            tables of the same pool)
+ *   live     [1] int32 out: pages in use
+ */
+int spec_kv_compact(const spec_kv_cache_t *cache, int layers, int32_t *refs, int32_t *page_table,
+                    int pages_per_seq, int B, int32_t *page_map, int32_t *live, int32_t *status,
+                    void *workspace, size_t workspace_bytes, void *stream);
 
 /* Static text for any SPEC_* code ("unknown status" otherwise). */
 const char *spec_status_string(int code);

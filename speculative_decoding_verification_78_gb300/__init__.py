@@ -22,4 +22,9 @@ from ._binding import (  # noqa: F401
     spec_last_cuda_error, spec_cuda_error_string, spec_selftest_bounded_wait,
     SPEC_F16, SPEC_ERR_LENGTH, SPEC_ERR_PAGE, SPEC_ERR_POSITION, SPEC_ERR_PATH, KVCache,
     SpecKVCache, kv_append, kv_attention, kv_commit, new_attention_workspace, new_kv_cache,
-    spec_kv_append, spec_kv_attention, spec_kv_attention_workspace_bytes, spec_kv_commit)
+    spec_kv_append, spec_kv_attention, spec_kv_attention_workspace_bytes, spec_kv_commit,
+    SPEC_ERR_NO_PAGE, SPEC_ERR_REFS, SPEC_MAX_BEAMS, SPEC_MAX_BEST, SPEC_MAX_SEQS, SPEC_MAX_STATES,
+    SpecState, beam_reorder, beam_select, kv_compact, kv_fork, kv_free, kv_reserve, kv_trim,
+    new_beam_workspace, new_page_refs, new_pages_workspace, spec_beam_reorder, spec_beam_select,
+    spec_beam_workspace_bytes, spec_kv_compact, spec_kv_fork, spec_kv_free,
+    spec_kv_pages_workspace_bytes, spec_kv_reserve, spec_kv_trim)

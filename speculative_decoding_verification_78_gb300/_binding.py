@@ -28,7 +28,9 @@ SPEC_ERR_NONFINITE, SPEC_ERR_TOKEN, SPEC_ERR_PARENT, SPEC_ERR_CHECK = -20, -21, 
 SPEC_ERR_TIMEOUT = -23
 SPEC_ERR_LENGTH, SPEC_ERR_PAGE, SPEC_ERR_POSITION, SPEC_ERR_PATH = -25, -26, -27, -28
 SPEC_MAX_V, SPEC_MAX_GAMMA, SPEC_MAX_NODES = 1 << 20, 255, 1024
+SPEC_ERR_NO_PAGE, SPEC_ERR_REFS = -29, -30
 SPEC_LMHEAD_MAX_V = 1 << 19
+SPEC_MAX_BEAMS, SPEC_MAX_BEST, SPEC_MAX_STATES, SPEC_MAX_SEQS = 64, 64, 8, 8192
 
 # every symbol include/spec_verify.h declares
 EXPORTS = ("spec_workspace_bytes", "spec_workspace_init", "spec_verify_chain",
@@ -37,7 +39,10 @@ EXPORTS = ("spec_workspace_bytes", "spec_workspace_init", "spec_verify_chain",
            "spec_last_cuda_error", "spec_cuda_error_string",
            "spec_launch_shape", "spec_verify_chain_static", "spec_sample", "spec_topk",
            "spec_tree_mask", "spec_selftest_bounded_wait", "spec_kv_append",
-           "spec_kv_attention_workspace_bytes", "spec_kv_attention", "spec_kv_commit")
+           "spec_kv_attention_workspace_bytes", "spec_kv_attention", "spec_kv_commit",
+           "spec_beam_workspace_bytes", "spec_beam_select", "spec_beam_reorder",
+           "spec_kv_pages_workspace_bytes", "spec_kv_reserve", "spec_kv_trim", "spec_kv_free",
+           "spec_kv_fork", "spec_kv_compact")
 SPEC_MAX_TOPK = 16
 SPEC_STATIC_SCRATCH_BYTES = 4 << 20
 SPEC_CALL_CHAIN, SPEC_CALL_TREE, SPEC_CALL_PROBS = 0, 1, 2
@@ -53,6 +58,11 @@ class SpecKVCache(ctypes.Structure):
                 ("v_scale", ctypes.c_void_p), ("num_pages", ctypes.c_int32),
                 ("page_size", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
                 ("head_dim", ctypes.c_int32)]
+
+
+class SpecState(ctypes.Structure):
+    """spec_state_t: one tensor that spec_beam_reorder reorders."""
+    _fields_ = [("in_", ctypes.c_void_p), ("out", ctypes.c_void_p), ("row_bytes", ctypes.c_int64)]
 
 
 class SpecError(RuntimeError):
@@ -129,6 +139,26 @@ def load_library(checked: bool = False):
         lib.spec_kv_attention.restype = i32
         lib.spec_kv_commit.argtypes = [cache, i32, vp, i32, vp, i32, i32, vp, vp, vp, vp, vp]
         lib.spec_kv_commit.restype = i32
+        lib.spec_beam_workspace_bytes.argtypes = [i32, i32, i32, i32]
+        lib.spec_beam_workspace_bytes.restype = sz
+        lib.spec_beam_select.argtypes = [vp, i32, vp, vp, i32, i32, i32, i32, i32, vp, vp, vp, vp, vp,
+                                         sz, vp]
+        lib.spec_beam_select.restype = i32
+        lib.spec_beam_reorder.argtypes = [ctypes.POINTER(SpecState), i32, vp, i32, i32, vp, vp]
+        lib.spec_beam_reorder.restype = i32
+        lib.spec_kv_pages_workspace_bytes.argtypes = [i32, i32]
+        lib.spec_kv_pages_workspace_bytes.restype = sz
+        lib.spec_kv_reserve.argtypes = [cache, vp, vp, i32, vp, vp, i32, i32, vp, vp, vp, sz, vp]
+        lib.spec_kv_reserve.restype = i32
+        lib.spec_kv_trim.argtypes = [cache, vp, vp, i32, vp, i32, i32, i32, vp, vp]
+        lib.spec_kv_trim.restype = i32
+        lib.spec_kv_free.argtypes = [cache, vp, vp, i32, vp, vp, i32, vp, vp]
+        lib.spec_kv_free.restype = i32
+        lib.spec_kv_fork.argtypes = [cache, i32, vp, vp, i32, vp, i32, vp, i32, i32, vp, vp, vp, vp, sz,
+                                     vp]
+        lib.spec_kv_fork.restype = i32
+        lib.spec_kv_compact.argtypes = [cache, i32, vp, vp, i32, i32, vp, vp, vp, vp, sz, vp]
+        lib.spec_kv_compact.restype = i32
         if checked:
             _checked_lib = lib
         else:
@@ -542,6 +572,124 @@ def spec_kv_commit(cache, page_table, seq_lens, path_nodes, accept_len, out_lens
         _stream(stream))
 
 
+# ------------------------------------------------------------------ the pages of a cache
+
+def _workspace(t):
+    """(pointer, bytes) of a uint8 workspace."""
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.is_contiguous():
+        return t.data_ptr(), t.numel() * t.element_size()
+    return _ptr(t), _nbytes(t)
+
+
+def spec_kv_pages_workspace_bytes(num_pages: int, B: int) -> int:
+    return int(load_library().spec_kv_pages_workspace_bytes(num_pages, B))
+
+
+def _kv_pages(cache, refs, page_table, seq_lens, status):
+    """Checks what the calls on pages take; returns (B, pages_per_seq, the pointers of refs, the table,
+    the lengths and the status)."""
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+        raise ValueError("page_table must be a [B, pages] tensor")
+    B, pps = page_table.shape
+    return (B, pps, _operand(refs, "refs", cache.num_pages, _I32),
+            _operand(page_table, "page_table", B * pps, _I32),
+            _operand(seq_lens, "seq_lens", B, _I32), _operand(status, "status", 1, _I32))
+
+
+def spec_kv_reserve(cache, refs, page_table, seq_lens, new_lens, N, granted, status, workspace,
+                    stream=None) -> int:
+    """refs [num_pages], page_table [B, pages] (changed), seq_lens, granted [B], new_lens [B] or None
+    int32; workspace uint8 (scratch)."""
+    B, pps, rp, table, lens, st = _kv_pages(cache, refs, page_table, seq_lens, status)
+    return load_library().spec_kv_reserve(
+        cache.struct(0), rp, table, pps, lens, _operand(new_lens, "new_lens", B, _I32), B, int(N),
+        _operand(granted, "granted", B, _I32), st, *_workspace(workspace), _stream(stream))
+
+
+def spec_kv_trim(cache, refs, page_table, seq_lens, window, sinks, status, stream=None) -> int:
+    """refs [num_pages], page_table [B, pages] int32 (both changed), seq_lens [B] int32."""
+    B, pps, rp, table, lens, st = _kv_pages(cache, refs, page_table, seq_lens, status)
+    return load_library().spec_kv_trim(cache.struct(0), rp, table, pps, lens, B, int(window), int(sinks),
+                                       st, _stream(stream))
+
+
+def spec_kv_free(cache, refs, page_table, seq_lens, ended, status, stream=None) -> int:
+    """refs [num_pages], page_table [B, pages], seq_lens [B] int32 (all changed); ended [B] int32 or
+    None."""
+    B, pps, rp, table, lens, st = _kv_pages(cache, refs, page_table, seq_lens, status)
+    return load_library().spec_kv_free(cache.struct(0), rp, table, pps, lens,
+                                       _operand(ended, "ended", B, _I32), B, st, _stream(stream))
+
+
+def spec_kv_fork(cache, refs, page_table, seq_lens, parents, release, page_table_out, lens_out, status,
+                 workspace, stream=None) -> int:
+    """parents, lens_out [C] and page_table_out [C, pages] int32 beside page_table [B, pages], seq_lens
+    [B]; refs changed; every layer of the cache."""
+    B, pps, rp, table, lens, st = _kv_pages(cache, refs, page_table, seq_lens, status)
+    if not isinstance(parents, torch.Tensor) or parents.dtype != _I32:
+        raise TypeError("parents must be an int32 tensor")
+    C = parents.numel()
+    return load_library().spec_kv_fork(
+        cache.struct(0), cache.layers, rp, table, pps, lens, B, _operand(parents, "parents", C, _I32), C,
+        int(bool(release)), _operand(page_table_out, "page_table_out", C * pps, _I32),
+        _operand(lens_out, "lens_out", C, _I32), st, *_workspace(workspace), _stream(stream))
+
+
+def spec_kv_compact(cache, refs, page_table, page_map, live, status, workspace, stream=None) -> int:
+    """refs [num_pages], page_table [B, pages] int32 (changed); page_map [num_pages], live [1] int32
+    out; every layer of the cache."""
+    B, pps, rp, table, _, st = _kv_pages(cache, refs, page_table, None, status)
+    return load_library().spec_kv_compact(
+        cache.struct(0), cache.layers, rp, table, pps, B,
+        _operand(page_map, "page_map", cache.num_pages, _I32), _operand(live, "live", 1, _I32), st,
+        *_workspace(workspace), _stream(stream))
+
+
+# ------------------------------------------------------------------ beams
+
+def spec_beam_workspace_bytes(B: int, K: int, V: int, dtype: int) -> int:
+    return int(load_library().spec_beam_workspace_bytes(B, K, V, dtype))
+
+
+def spec_beam_select(logits, scores, done, pad_token, n, tokens, parents, out_scores, status, workspace,
+                     stream=None) -> int:
+    """logits [B, K, V] (fp32 or bf16), scores [B, K] fp32, done [B, K] int32 or None; tokens, parents
+    [B, n] int32 and out_scores [B, n] fp32 out; workspace uint8 (scratch)."""
+    if not isinstance(logits, torch.Tensor) or logits.dim() != 3:
+        raise ValueError("logits must be a [B, K, V] tensor")
+    B, K, V = logits.shape
+    n = int(n)
+    return load_library().spec_beam_select(
+        _ptr(logits), dtype_flag(logits), _operand(scores, "scores", B * K, _F32),
+        _operand(done, "done", B * K, _I32), int(pad_token), B, K, V, n,
+        _operand(tokens, "tokens", B * n, _I32), _operand(parents, "parents", B * n, _I32),
+        _operand(out_scores, "out_scores", B * n, _F32), _operand(status, "status", 1, _I32),
+        *_workspace(workspace), _stream(stream))
+
+
+def spec_beam_reorder(states, parents, outs, status, stream=None) -> int:
+    """states: tensors [R, ...] of any types, contiguous; outs: the same with parents.numel() rows;
+    parents int32."""
+    if len(states) != len(outs) or not states:
+        raise ValueError("as many outputs as states, at least one")
+    if not isinstance(parents, torch.Tensor) or parents.dtype != _I32:
+        raise TypeError("parents must be an int32 tensor")
+    R, C = states[0].shape[0], parents.numel()
+    arr = (SpecState * len(states))()
+    for i, (t, o) in enumerate(zip(states, outs)):
+        if t.dim() < 1 or t.shape[0] != R or o.shape != (C, *t.shape[1:]) or o.dtype != t.dtype:
+            raise ValueError(f"state {i}: {tuple(t.shape)} {t.dtype} to {tuple(o.shape)} {o.dtype}, "
+                             f"with {R} rows to {C}")
+        for x in (t, o):
+            if x.numel() and not (x.is_cuda and x.is_contiguous()):
+                _ptr(x)   # raises
+        arr[i].in_, arr[i].out = t.data_ptr() or None, o.data_ptr() or None
+        arr[i].row_bytes = t[0].numel() * t.element_size() if R else \
+            o[0].numel() * o.element_size() if C else 1
+    return load_library().spec_beam_reorder(arr, len(states), _operand(parents, "parents", C, _I32), R, C,
+                                            _operand(status, "status", 1, _I32), _stream(stream))
+
+
 # ------------------------------------------------------------------ conveniences (allocation)
 
 def _torch_stream(stream):
@@ -783,3 +931,127 @@ def kv_commit(cache, page_table, seq_lens, path_nodes, accept_len, out_lens=None
     check(spec_kv_commit(cache, page_table, seq_lens, path_nodes, accept_len, out_lens, status,
                          stream), "spec_kv_commit")
     return out_lens, status
+
+
+def new_page_refs(cache) -> torch.Tensor:
+    """The counts of a cache whose pages are all free: zeros [num_pages] int32."""
+    return torch.zeros(cache.num_pages, dtype=torch.int32, device=cache.k.device)
+
+
+def new_pages_workspace(cache, sequences) -> torch.Tensor:
+    """A workspace for kv_reserve, kv_fork (sequences: the children) and kv_compact calls (scratch; never
+    needs zeroing)."""
+    n = spec_kv_pages_workspace_bytes(cache.num_pages, sequences)
+    if n == 0:
+        raise SpecError(SPEC_ERR_SHAPE, "spec_kv_pages_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=cache.k.device)
+
+
+def _status(status, device):
+    return torch.zeros(1, dtype=torch.int32, device=device) if status is None else status
+
+
+@_allocates
+def kv_reserve(cache, refs, page_table, seq_lens, N, new_lens=None, granted=None, workspace=None,
+               status=None, stream=None):
+    """Free pages for the next N tokens (or new_lens[b]) of each sequence, put into page_table and refs
+    (spec_kv_reserve). Returns (the tokens granted to each sequence, status)."""
+    if granted is None:
+        granted = torch.empty_like(seq_lens)
+    status = _status(status, seq_lens.device)
+    if workspace is None:
+        workspace = new_pages_workspace(cache, page_table.shape[0])
+    check(spec_kv_reserve(cache, refs, page_table, seq_lens, new_lens, N, granted, status, workspace,
+                          stream), "spec_kv_reserve")
+    return granted, status
+
+
+@_allocates
+def kv_trim(cache, refs, page_table, seq_lens, window=None, sinks=0, status=None, stream=None):
+    """Gives back the pages behind the window (None: none are) but for the sinks', and those past the last
+    token (spec_kv_trim). Returns (page_table, status)."""
+    status = _status(status, seq_lens.device)
+    check(spec_kv_trim(cache, refs, page_table, seq_lens, 1 << 30 if window is None else window, sinks,
+                       status, stream), "spec_kv_trim")
+    return page_table, status
+
+
+@_allocates
+def kv_free(cache, refs, page_table, seq_lens, ended=None, status=None, stream=None):
+    """Ends the sequences with ended[b] != 0 (None: all): their pages go back, their lengths become 0
+    (spec_kv_free). Returns (seq_lens, status)."""
+    status = _status(status, seq_lens.device)
+    check(spec_kv_free(cache, refs, page_table, seq_lens, ended, status, stream), "spec_kv_free")
+    return seq_lens, status
+
+
+@_allocates
+def kv_fork(cache, refs, page_table, seq_lens, parents, release=False, page_table_out=None, lens_out=None,
+            workspace=None, status=None, stream=None):
+    """Sequences that continue from parents[c], sharing full pages, in every layer of the cache
+    (spec_kv_fork); with release the parents end. Returns (page_table_out, lens_out, status)."""
+    C = parents.numel()
+    if page_table_out is None:
+        page_table_out = torch.empty((C, page_table.shape[1]), dtype=torch.int32, device=page_table.device)
+    if lens_out is None:
+        lens_out = torch.empty(C, dtype=torch.int32, device=page_table.device)
+    status = _status(status, page_table.device)
+    if workspace is None:
+        workspace = new_pages_workspace(cache, C)
+    check(spec_kv_fork(cache, refs, page_table, seq_lens, parents, release, page_table_out, lens_out,
+                       status, workspace, stream), "spec_kv_fork")
+    return page_table_out, lens_out, status
+
+
+@_allocates
+def kv_compact(cache, refs, page_table, page_map=None, live=None, workspace=None, status=None,
+               stream=None):
+    """Moves the pages in use to the front of the pool in every layer of the cache (spec_kv_compact).
+    Returns (page_map, the number of pages in use [1], status)."""
+    if page_map is None:
+        page_map = torch.empty_like(refs)
+    if live is None:
+        live = torch.empty(1, dtype=torch.int32, device=refs.device)
+    status = _status(status, refs.device)
+    if workspace is None:
+        workspace = new_pages_workspace(cache, page_table.shape[0])
+    check(spec_kv_compact(cache, refs, page_table, page_map, live, status, workspace, stream),
+          "spec_kv_compact")
+    return page_map, live, status
+
+
+def new_beam_workspace(B, K, V, dtype=torch.bfloat16, device=None) -> torch.Tensor:
+    """A workspace for beam_select calls of this shape (scratch; never needs zeroing)."""
+    n = spec_beam_workspace_bytes(B, K, V, SPEC_F32 if dtype == torch.float32 else SPEC_BF16)
+    if n == 0:
+        raise SpecError(SPEC_ERR_SHAPE, "spec_beam_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+
+
+@_allocates
+def beam_select(logits, scores, n=None, done=None, pad_token=0, workspace=None, status=None, stream=None):
+    """The n best (None: as many as beams) continuations of the beams of each batch row
+    (spec_beam_select). Returns (tokens [B, n], parents [B, n]: rows of [B * K], scores [B, n], status)."""
+    B, K, V = logits.shape
+    dev = logits.device
+    n = K if n is None else n
+    tokens, parents = (torch.empty((B, n), dtype=torch.int32, device=dev) for _ in range(2))
+    best = torch.empty((B, n), dtype=torch.float32, device=dev)
+    status = _status(status, dev)
+    if workspace is None:
+        workspace = new_beam_workspace(B, K, V, logits.dtype, dev)
+    check(spec_beam_select(logits, scores, done, pad_token, n, tokens, parents, best, status, workspace,
+                           stream), "spec_beam_select")
+    return tokens, parents, best, status
+
+
+@_allocates
+def beam_reorder(states, parents, outs=None, status=None, stream=None):
+    """What belongs to the beams (tensors [rows, ...]), by their parents (spec_beam_reorder). Returns
+    (the reordered tensors ..., status)."""
+    C = parents.numel()
+    if outs is None:
+        outs = [torch.empty((C, *t.shape[1:]), dtype=t.dtype, device=t.device) for t in states]
+    status = _status(status, parents.device)
+    check(spec_beam_reorder(states, parents, outs, status, stream), "spec_beam_reorder")
+    return (*outs, status)

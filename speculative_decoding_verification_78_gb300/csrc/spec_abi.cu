@@ -6,6 +6,7 @@
 #include <math.h>
 #include <stdint.h>
 
+#include "spec_beam.h"
 #include "spec_launch.h"
 #include "spec_verify.h"
 
@@ -579,6 +580,90 @@ const char *spec_cuda_error_string(int cuda_error) {
   return cudaGetErrorString(static_cast<cudaError_t>(cuda_error));
 }
 
+size_t spec_beam_workspace_bytes(int B, int K, int V, int dtype) {
+  if (B < 0 || K < 1 || K > SPEC_MAX_BEAMS || V < 1 || V > SPEC_MAX_V ||
+      (dtype != SPEC_F32 && dtype != SPEC_BF16))
+    return 0;
+  return align256(static_cast<size_t>(B > 0 ? B : 1) * K * beam_chunks(V, dtype) * sizeof(uint2));
+}
+
+int spec_beam_select(const void *logits, int dtype, const float *scores, const int32_t *done,
+                     int pad_token, int B, int K, int V, int n, int32_t *tokens, int32_t *parents,
+                     float *out_scores, int32_t *status, void *workspace, size_t workspace_bytes,
+                     void *stream) {
+  if (dtype != SPEC_F32 && dtype != SPEC_BF16) return SPEC_ERR_DTYPE;
+  if (B < 0 || K < 1 || K > SPEC_MAX_BEAMS || n < 1 || n > SPEC_MAX_BEST || V < 1 || V > SPEC_MAX_V ||
+      pad_token < 0 || pad_token >= V)
+    return SPEC_ERR_SHAPE;
+  const int C = beam_chunks(V, dtype);
+  const long long units = static_cast<long long>(B) * K * C;
+  if (units >= (1LL << 31) - 64) return SPEC_ERR_SHAPE;
+  if (B == 0) return SPEC_OK;
+  if (!logits || !scores || !tokens || !parents || !out_scores || !status || !workspace)
+    return SPEC_ERR_NULL;
+  if (!aligned(logits, elem_size(dtype)) || !aligned(scores, 4) || !aligned(done, 4) ||
+      !aligned(tokens, 4) || !aligned(parents, 4) || !aligned(out_scores, 4) || !aligned(status, 4) ||
+      !aligned(workspace, 16))
+    return SPEC_ERR_ALIGN;
+  if (scores == out_scores) return SPEC_ERR_SHAPE;
+  if (workspace_bytes < spec_beam_workspace_bytes(B, K, V, dtype)) return SPEC_ERR_WORKSPACE;
+  BeamArgs a{};
+  a.logits = logits;
+  a.scores = scores;
+  a.done = done;
+  a.tokens = tokens;
+  a.parents = parents;
+  a.out_scores = out_scores;
+  a.status = status;
+  a.part = static_cast<uint2 *>(workspace);
+  a.B = B;
+  a.K = K;
+  a.V = V;
+  a.C = C;
+  a.n = n;
+  a.pad = pad_token;
+  a.units = static_cast<int>(units);
+  const int sms = sm_count() > 0 ? sm_count() : 1;
+  return launch_result(launch_beam_select(dtype, a, sms, static_cast<cudaStream_t>(stream)));
+}
+
+int spec_beam_reorder(const spec_state_t *states, int count, const int32_t *parents, int rows_in,
+                      int rows_out, int32_t *status, void *stream) {
+  if (!states) return SPEC_ERR_NULL;
+  if (count < 1 || count > SPEC_MAX_STATES || rows_in < 0 || rows_out < 0) return SPEC_ERR_SHAPE;
+  if (static_cast<long long>(rows_out) * count >= 1LL << 31) return SPEC_ERR_SHAPE;
+  const long long most = rows_in > rows_out ? rows_in : rows_out;
+  for (int i = 0; i < count; ++i)
+    if (states[i].row_bytes < 1 || (most > 0 && states[i].row_bytes > (1LL << 62) / most))
+      return SPEC_ERR_SHAPE;
+  if (rows_out == 0) return SPEC_OK;
+  if (!parents || !status) return SPEC_ERR_NULL;
+  if (!aligned(parents, 4) || !aligned(status, 4)) return SPEC_ERR_ALIGN;
+  ReorderArgs a{};
+  for (int i = 0; i < count; ++i) {
+    const uintptr_t in = reinterpret_cast<uintptr_t>(states[i].in), bytes = states[i].row_bytes;
+    const uintptr_t out = reinterpret_cast<uintptr_t>(states[i].out);
+    if ((rows_in > 0 && !in) || !out) return SPEC_ERR_NULL;
+    for (int j = 0; j < count; ++j) {   // no output over an input or another output
+      const uintptr_t from = reinterpret_cast<uintptr_t>(states[j].in), len = states[j].row_bytes;
+      const uintptr_t to = reinterpret_cast<uintptr_t>(states[j].out);
+      if (rows_in > 0 && out < from + rows_in * len && from < out + rows_out * bytes) return SPEC_ERR_SHAPE;
+      if (i != j && out < to + rows_out * len && to < out + rows_out * bytes) return SPEC_ERR_SHAPE;
+    }
+    const uintptr_t all = in | out | bytes;
+    a.in[i] = static_cast<const char *>(states[i].in);
+    a.out[i] = static_cast<char *>(states[i].out);
+    a.bytes[i] = states[i].row_bytes;
+    a.grain[i] = all % 16 == 0 ? 16 : all % 8 == 0 ? 8 : all % 4 == 0 ? 4 : all % 2 == 0 ? 2 : 1;
+  }
+  a.parents = parents;
+  a.status = status;
+  a.states = count;
+  a.rows_in = rows_in;
+  a.rows_out = rows_out;
+  return launch_result(launch_beam_reorder(a, static_cast<cudaStream_t>(stream)));
+}
+
 const char *spec_status_string(int code) {
   switch (code) {
     case SPEC_OK: return "ok";
@@ -597,6 +682,8 @@ const char *spec_status_string(int code) {
     case SPEC_ERR_PAGE: return "a page number is outside [0, num_pages)";
     case SPEC_ERR_POSITION: return "a position is outside the rotation table";
     case SPEC_ERR_PATH: return "an accepted path is invalid";
+    case SPEC_ERR_NO_PAGE: return "no free page is left in the pool";
+    case SPEC_ERR_REFS: return "a page was given back more often than it was held";
     case SPEC_ERR_TIMEOUT: return "a bounded wait inside a kernel gave up";
     default: return "unknown status";
   }

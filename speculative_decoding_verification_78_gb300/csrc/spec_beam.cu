@@ -1,0 +1,562 @@
+// spec_beam.cu -- beam search's selection over beams and vocabulary, and the reordering of what belongs to
+// the beams.
+//
+// The mathematics. Candidate (k, v) of a batch row has the score s_k + l[k,v] - L_k, L_k = log sum_v e^l[k,v];
+// the n best are wanted, ordered by score, equal ones by beam and token. Two kernels, as for verification:
+// a stream kernel reads every logit once and leaves (maximum, sum) for each 4 KB unit of a row; a CTA a batch
+// row then picks units by their maxima and tokens from those units.
+//
+// Exactness. The order of two candidates of one beam is that of their logits, whatever L_k. Candidates of
+// different beams are compared by L_k from fp32 sums, whose error is bounded (kSlack); where two that matter
+// lie nearer than that, the L_k concerned are computed again to about 1e-10 and the selection is repeated. So
+// tokens and parents are those of exact arithmetic (but for scores closer than 1e-9). The sums are taken in
+// the order of the token numbers wherever a row lies in memory, so that beams with equal logits have equal L_k.
+#include "spec_beam.h"
+#include "spec_common.cuh"
+#include "spec_kv.h"
+
+namespace specv {
+
+namespace {
+
+constexpr int kFinishThreads = 512, kFinishWarps = kFinishThreads / 32;
+constexpr float kLog2eHi = 0x1.715476p+0f, kLog2eLo = 0x1.4ae0cp-26f;   // their sum: log2(e) to 2^-50
+constexpr float kLn2Hi = 0x1.62e43p-1f, kLn2Lo = -0x1.05c61p-29f;       // their sum: ln 2 to 2^-53
+constexpr double kLn2d = 0.69314718055994530942, kLog2ed = 1.44269504088896340736;
+// A unit whose maximum is below this in magnitude is summed against the integer R above its maximum's
+// logarithm: 2^(l log2 e - R), so that units are joined by powers of two. Beyond it (where R would not be an
+// exact fp32 integer with room for a fraction) against its maximum itself.
+constexpr float kPlainMax = 1048576.f;
+// Twice the bound of an fp32 sum's relative error: 2^-22 of ex2; two roundings of the exponent, 2^-24 |t| ln 2
+// each, |t| at most 21 on average (log2 of the largest vocabulary, and one); 25 roundings of sums.
+constexpr double kSlack = 8e-6;
+
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// ------------------------------------------------------------------ reading a row by token numbers
+
+// Elements g * EPV .. of the row as one vector, -inf past its end. Whole vectors of an unaligned row are put
+// together from the two aligned ones they lie in, where both lie inside the row.
+template <typename E>
+__device__ __forceinline__ uint4 load_group(const E *row, int V, int g) {
+  constexpr int kEPV = Elem<E>::kPerVec;
+  const int e0 = g * kEPV;
+  const uint32_t ni = Elem<E>::kNegInfWord;
+  uint4 r = make_uint4(ni, ni, ni, ni);
+  if (e0 >= V) return r;
+  const E *at = row + e0;
+  const unsigned mis = static_cast<unsigned>(reinterpret_cast<uintptr_t>(row) & 15u);
+  if (mis == 0) {
+    if (e0 + kEPV <= V) return ld_stream(reinterpret_cast<const uint4 *>(at));
+  } else if (e0 > 0 && e0 + 2 * kEPV <= V) {
+    const uint4 *p = reinterpret_cast<const uint4 *>(reinterpret_cast<uintptr_t>(at) - mis);
+    const uint4 a = __ldg(p), b = __ldg(p + 1);
+    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    const unsigned q = mis >> 2, sh = (mis & 3u) * 8u;
+    if (q & 1)
+#pragma unroll
+      for (int i = 0; i < 7; ++i) w[i] = w[i + 1];
+    if (q & 2)
+#pragma unroll
+      for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+    return make_uint4(__funnelshift_r(w[0], w[1], sh), __funnelshift_r(w[1], w[2], sh),
+                      __funnelshift_r(w[2], w[3], sh), __funnelshift_r(w[3], w[4], sh));
+  }
+  uint32_t w[4] = {ni, ni, ni, ni};
+#pragma unroll
+  for (int e = 0; e < kEPV; ++e)
+    if (e0 + e < V) {
+      const uint32_t bits = __float_as_uint(ld_elem<E>(at + e));
+      if (sizeof(E) == 4)
+        w[e] = bits;
+      else
+        w[e / 2] = (e & 1) ? (w[e / 2] & 0xffffu) | (bits & 0xffff0000u) : (w[e / 2] & 0xffff0000u) | (bits >> 16);
+    }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// What a beam contributes: nothing (score -inf), one candidate (at its end), or its row.
+enum BeamKind : int { kUnused = 0, kEnded = 1, kLive = 2, kBad = 3 };
+__device__ __forceinline__ int beam_kind(const BeamArgs &a, int row, float &s) {
+  s = __ldg(a.scores + row);
+  if (s == -INFINITY) return kUnused;
+  if (s != s || s == INFINITY) return kBad;
+  return a.done && __ldg(a.done + row) ? kEnded : kLive;
+}
+
+__device__ __forceinline__ float unit_ref(float m) { return ceilf(__fmul_rn(m, kLog2eHi)); }
+
+template <typename E>
+__global__ void __launch_bounds__(256, 4) beam_stream_kernel(const __grid_constant__ BeamArgs a) {
+  constexpr int kEPV = Elem<E>::kPerVec;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int lane = threadIdx.x & 31;
+  for (int unit = blockIdx.x * 8 + (threadIdx.x >> 5); unit < a.units; unit += 8 * gridDim.x) {
+    const int row_i = static_cast<int>(static_cast<unsigned>(unit) / static_cast<unsigned>(a.C));
+    const int chunk = unit - row_i * a.C;
+    float score;
+    if (beam_kind(a, row_i, score) != kLive) continue;
+    if (!SPEC_CHECK(a, row_i < a.B * a.K && chunk < a.C)) continue;
+    const E *row = static_cast<const E *>(a.logits) + static_cast<long long>(row_i) * a.V;
+    uint4 buf[kVPL];
+#pragma unroll
+    for (int j = 0; j < kVPL; ++j) buf[j] = load_group<E>(row, a.V, chunk * kUnitVecs + j * 32 + lane);
+    float m = unit_lane_max<E>(buf, -INFINITY, -INFINITY);
+    m = key_float(__reduce_max_sync(0xffffffffu, float_key(m)));
+    float s = 0.f;
+    if (m != -INFINITY) {
+      f32x2 acc[4] = {pk2(0.f, 0.f), pk2(0.f, 0.f), pk2(0.f, 0.f), pk2(0.f, 0.f)};
+      if (fabsf(m) < kPlainMax) {
+        const float R = unit_ref(m);
+        const f32x2 hi = pk2(kLog2eHi, kLog2eHi), lo = pk2(kLog2eLo, kLog2eLo), nr = pk2(-R, -R);
+#pragma unroll
+        for (int j = 0; j < kVPL; ++j)
+#pragma unroll
+          for (int e = 0; e < kEPV; e += 2) {
+            const f32x2 x = pk2(vec_elem<E>(buf[j], e), vec_elem<E>(buf[j], e + 1));
+            float t0, t1;
+            up2(fma2(x, lo, fma2(x, hi, nr)), t0, t1);
+            f32x2 &c = acc[(j * (kEPV / 2) + e / 2) & 3];
+            c = add2(c, pk2(ex2(t0), ex2(t1)));
+          }
+      } else {   // (NaN and +inf come here and leave NaN in the maximum's place)
+#pragma unroll
+        for (int j = 0; j < kVPL; ++j)
+#pragma unroll
+          for (int e = 0; e < kEPV; e += 2)
+            acc[(e / 2) & 3] = add2(acc[(e / 2) & 3], pk2(ex2_shift(vec_elem<E>(buf[j], e), m, kLog2eHi),
+                                                          ex2_shift(vec_elem<E>(buf[j], e + 1), m, kLog2eHi)));
+      }
+      float v0, v1;
+      up2(add2(add2(acc[0], acc[1]), add2(acc[2], acc[3])), v0, v1);
+      s = __fadd_rn(v0, v1);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, o));
+      if (m == INFINITY) m = NAN;
+    }
+    if (lane == 0) a.part[unit] = make_uint2(__float_as_uint(m), __float_as_uint(s));
+  }
+}
+
+// ------------------------------------------------------------------ an exponential to 1e-10
+
+// e^(x - M), x <= M, as a sum of two fp32 numbers. With x - M = d + dl exactly, t = (x - M) log2 e = n + f,
+// |f| <= 1/2: 2^n e^y with y = f ln 2 in two words; 1 + y + y^2/2 + y^3/6 in two words and the rest of
+// Taylor's series, below 7e-4, in one.
+__device__ __forceinline__ void exp_pair(float x, float M, float &hi, float &lo) {
+  const float d = __fsub_rn(x, M);
+  if (!(d > -87.f)) {
+    hi = lo = 0.f;
+    return;
+  }
+  const float bb = __fsub_rn(d, x);
+  const float dl = __fadd_rn(__fsub_rn(x, __fsub_rn(d, bb)), __fsub_rn(-M, bb));
+  const float t = __fmul_rn(d, kLog2eHi);
+  const float te = __fmaf_rn(dl, kLog2eHi, __fmaf_rn(d, kLog2eLo, __fmaf_rn(d, kLog2eHi, -t)));
+  const float n = rintf(t), f = __fsub_rn(t, n);
+  const float yh = __fmul_rn(f, kLn2Hi);
+  const float yl = __fmaf_rn(te, kLn2Hi, __fmaf_rn(f, kLn2Lo, __fmaf_rn(f, kLn2Hi, -yh)));
+  const float y2h = __fmul_rn(yh, yh);
+  const float y2l = __fmaf_rn(2.f * yh, yl, __fmaf_rn(yh, yh, -y2h));
+  const float y3h = __fmul_rn(y2h, yh);
+  const float y3l = __fmaf_rn(y2h, yl, __fmaf_rn(y2l, yh, __fmaf_rn(y2h, yh, -y3h)));
+  constexpr float kSixthHi = 0x1.555556p-3f, kSixthLo = -0x1.555556p-28f;
+  const float ch = __fmul_rn(y3h, kSixthHi);
+  const float cl = __fmaf_rn(y3l, kSixthHi, __fmaf_rn(y3h, kSixthLo, __fmaf_rn(y3h, kSixthHi, -ch)));
+  float q = 1.f / 3628800.f;
+  q = __fmaf_rn(q, yh, 1.f / 362880.f);
+  q = __fmaf_rn(q, yh, 1.f / 40320.f);
+  q = __fmaf_rn(q, yh, 1.f / 5040.f);
+  q = __fmaf_rn(q, yh, 1.f / 720.f);
+  q = __fmaf_rn(q, yh, 1.f / 120.f);
+  q = __fmaf_rn(q, yh, 1.f / 24.f);
+  const float rest = __fmul_rn(__fmul_rn(y2h, y2h), q);
+  // (each sum's second term is the smaller)
+  const float s1 = __fadd_rn(1.f, yh), e1 = __fsub_rn(yh, __fsub_rn(s1, 1.f));
+  const float h2 = 0.5f * y2h;
+  const float s2 = __fadd_rn(s1, h2), e2 = __fsub_rn(h2, __fsub_rn(s2, s1));
+  const float s3 = __fadd_rn(s2, ch), e3 = __fsub_rn(ch, __fsub_rn(s3, s2));
+  const float low = ((e1 + e2) + (e3 + yl)) + ((0.5f * y2l + cl) + rest);
+  const float scale = __uint_as_float(static_cast<uint32_t>(static_cast<int>(n) + 127) << 23);
+  hi = s3 * scale;
+  lo = low * scale;
+}
+
+// ------------------------------------------------------------------ selection
+
+// doubles as integers in the same order (no NaN)
+__device__ __forceinline__ unsigned long long order_of(double x) {
+  const unsigned long long b = static_cast<unsigned long long>(__double_as_longlong(x + 0.0));
+  return b >> 63 ? ~b : b | (1ull << 63);
+}
+__device__ __forceinline__ double from_order(unsigned long long k) {
+  return __longlong_as_double(static_cast<long long>(k >> 63 ? k & ~(1ull << 63) : ~k));
+}
+
+// A candidate: its score (as order_of; 0: none), beam, logit and place in the beam. Equal scores go by beam;
+// within one by logit (which may differ where 64 bits of score do not), then by place.
+struct Pick {
+  unsigned long long key;
+  float l;
+  int k, at;
+};
+__device__ __forceinline__ bool before(const Pick &x, const Pick &y) {
+  if (x.key != y.key) return x.key > y.key;
+  if (x.k != y.k) return x.k < y.k;
+  return x.l > y.l || (x.l == y.l && x.at < y.at);
+}
+__device__ __forceinline__ Pick warp_best(Pick p) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    Pick q;
+    q.key = __shfl_xor_sync(0xffffffffu, p.key, o);
+    q.l = __shfl_xor_sync(0xffffffffu, p.l, o);
+    q.k = __shfl_xor_sync(0xffffffffu, p.k, o);
+    q.at = __shfl_xor_sync(0xffffffffu, p.at, o);
+    if (before(q, p)) p = q;
+  }
+  return p;
+}
+__device__ __forceinline__ Pick no_pick() { return Pick{0, -INFINITY, 0x7fffffff, 0}; }
+
+struct FinishShared {
+  double log_sum[SPEC_MAX_BEAMS];   // L_k less the row's largest logit
+  float s[SPEC_MAX_BEAMS], top[SPEC_MAX_BEAMS];
+  int kind[SPEC_MAX_BEAMS], precise[SPEC_MAX_BEAMS], wanted[SPEC_MAX_BEAMS];
+  Pick warp[kFinishWarps], best;
+  int unit[SPEC_MAX_BEST];     // chosen units, in order
+  Pick head[SPEC_MAX_BEST];    // the best of each that is left; place: the token
+  double sum[kFinishWarps];
+  int bad, again;
+};
+
+template <typename E>
+struct Finish {
+  const BeamArgs &a;
+  FinishShared &sh;
+  const int b, tid, lane, warp;
+
+  __device__ __forceinline__ const E *row(int k) const {
+    return static_cast<const E *>(a.logits) + (static_cast<long long>(b) * a.K + k) * a.V;
+  }
+  __device__ __forceinline__ uint2 part(int u) const {
+    return __ldcg(a.part + static_cast<long long>(b) * a.K * a.C + u);
+  }
+  // unit u = k C + chunk of the batch row, by its largest candidate
+  __device__ __forceinline__ Pick unit_pick(int u) const {
+    const int k = u / a.C, chunk = u - k * a.C;
+    Pick p{0, 0.f, k, chunk};
+    if (sh.kind[k] == kEnded) {
+      if (chunk == 0) p.key = order_of(sh.s[k]);
+    } else if (sh.kind[k] == kLive) {
+      const float m = __uint_as_float(part(u).x);
+      p.l = m;
+      if (m > -INFINITY) p.key = order_of(score(k, m));
+    }
+    return p;
+  }
+  __device__ __forceinline__ double score(int k, float l) const {
+    return static_cast<double>(sh.s[k]) + ((static_cast<double>(l) - sh.top[k]) - sh.log_sum[k]);
+  }
+  // two candidates whose order the sums as they are do not tell: asks for better ones
+  __device__ __forceinline__ void compare(double x, int k, double y, int j) const {
+    if (k == j || (sh.precise[k] && sh.precise[j])) return;
+    const double gap = fabs(x - y);
+    if (gap == 0. || gap > kSlack) return;   // (0: beams with the same logits and scores)
+    if (!sh.precise[k]) sh.wanted[k] = 1;
+    if (!sh.precise[j]) sh.wanted[j] = 1;
+    sh.again = 1;
+  }
+
+  // L_k from the unit sums, a warp a beam
+  __device__ __forceinline__ void sums() const {
+    for (int k = warp; k < a.K; k += kFinishWarps) {
+      float s;
+      const int kind = beam_kind(a, b * a.K + k, s);
+      if (lane == 0) {
+        sh.kind[k] = kind;
+        sh.s[k] = s;
+        sh.precise[k] = kind != kLive;
+        sh.wanted[k] = 0;
+        sh.top[k] = 0.f;
+        sh.log_sum[k] = 0.;
+        if (kind == kBad) sh.bad = 1;
+      }
+      if (kind != kLive) continue;
+      float m = -INFINITY;
+      for (int c = lane; c < a.C; c += 32) m = fmax_nan(m, __uint_as_float(part(k * a.C + c).x));
+      m = key_float(__reduce_max_sync(0xffffffffu, float_key(m)));
+      if (m != m || m == -INFINITY) {
+        if (lane == 0) sh.bad = 1;
+        continue;
+      }
+      const bool plain = fabsf(m) < kPlainMax;
+      const float R = unit_ref(m);
+      double t = 0.;
+      for (int c = lane; c < a.C; c += 32) {
+        const uint2 w = part(k * a.C + c);
+        const float um = __uint_as_float(w.x);
+        const double us = static_cast<double>(__uint_as_float(w.y));
+        if (um == -INFINITY) continue;
+        if (plain && fabsf(um) < kPlainMax) {
+          const float e = unit_ref(um) - R;   // an integer
+          if (e > -1000.f) t += us * __longlong_as_double(static_cast<long long>(1023 + static_cast<int>(e)) << 52);
+        } else {
+          // from the unit's reference to its maximum, and from there to the row's
+          const double to_max = fabsf(um) < kPlainMax ? unit_ref(um) - um * kLog2ed : 0.;
+          t += us * exp2(to_max + (static_cast<double>(um) - m) * kLog2ed);
+        }
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+      if (lane == 0) {
+        sh.top[k] = m;
+        sh.log_sum[k] = (plain ? R * kLn2d - m : 0.) + log(t);
+      }
+    }
+  }
+
+  // L_k of one beam again, to about 1e-10, by the whole CTA
+  __device__ void precise_sum(int k) const {
+    const float M = sh.top[k];
+    float h = 0.f, l = 0.f;
+    for (int g = tid; g * Elem<E>::kPerVec < a.V; g += kFinishThreads) {
+      const uint4 v = load_group<E>(row(k), a.V, g);
+#pragma unroll
+      for (int e = 0; e < Elem<E>::kPerVec; ++e) {
+        float xh, xl;
+        exp_pair(vec_elem<E>(v, e), M, xh, xl);
+        const float s = __fadd_rn(h, xh), bb = __fsub_rn(s, h);
+        l = __fadd_rn(l, __fadd_rn(__fadd_rn(__fsub_rn(h, __fsub_rn(s, bb)), __fsub_rn(xh, bb)), xl));
+        h = s;
+      }
+    }
+    double t = static_cast<double>(h) + static_cast<double>(l);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    __syncthreads();
+    if (lane == 0) sh.sum[warp] = t;
+    __syncthreads();
+    if (tid == 0) {
+      double all = 0.;
+      for (int w = 0; w < kFinishWarps; ++w) all += sh.sum[w];
+      sh.log_sum[k] = log(all);
+      sh.precise[k] = 1;
+      sh.wanted[k] = 0;
+    }
+    __syncthreads();
+  }
+
+  // the best of this thread's units that ranks after `last`
+  __device__ __forceinline__ Pick next_unit(const Pick &last) const {
+    Pick best = no_pick();
+    for (int u = tid; u < a.K * a.C; u += kFinishThreads) {
+      const Pick p = unit_pick(u);
+      if (p.key && before(last, p) && before(p, best)) best = p;
+    }
+    return best;
+  }
+
+  // the best token of a chosen unit that ranks after (l, token); by one warp
+  __device__ __forceinline__ void next_token(int j, float last_l, int last_t) const {
+    const int u = sh.unit[j], k = u / a.C, chunk = u - k * a.C;
+    float l = -INFINITY;
+    int t = 0x7fffffff;
+    if (sh.kind[k] == kEnded) {
+      if (last_t < 0) {
+        l = 0.f;
+        t = a.pad;
+      }
+    } else {
+#pragma unroll
+      for (int v = 0; v < kVPL; ++v) {
+        const int g = chunk * kUnitVecs + v * 32 + lane;
+        const uint4 w = load_group<E>(row(k), a.V, g);
+#pragma unroll
+        for (int e = 0; e < Elem<E>::kPerVec; ++e) {
+          const float x = vec_elem<E>(w, e);
+          const int at = g * Elem<E>::kPerVec + e;
+          const bool after = x < last_l || (x == last_l && at > last_t);
+          if (x > -INFINITY && after && (x > l || (x == l && at < t))) {
+            l = x;
+            t = at;
+          }
+        }
+      }
+      const unsigned key = float_key(__fadd_rn(l, 0.f));
+      const unsigned top = __reduce_max_sync(0xffffffffu, key);
+      t = __reduce_min_sync(0xffffffffu, key == top ? t : 0x7fffffff);
+      l = key_float(top);
+    }
+    if (lane == 0) {
+      const bool some = t != 0x7fffffff;
+      sh.head[j] = Pick{!some ? 0 : sh.kind[k] == kEnded ? order_of(sh.s[k]) : order_of(score(k, l)), l, k, t};
+    }
+  }
+
+  // Chooses units and tokens, and writes the results; false if sums have to be improved first.
+  __device__ bool select() const {
+    // the n first units by their largest candidates: the n best candidates lie in them
+    Pick last{~0ull, 0.f, 0, 0};   // before all others
+    Pick mine = next_unit(last);
+    int units = 0;
+    for (; units < a.n; ++units) {
+      const Pick w = warp_best(mine);
+      if (lane == 0) sh.warp[warp] = w;
+      __syncthreads();
+      if (warp == 0) {
+        const Pick all = warp_best(lane < kFinishWarps ? sh.warp[lane] : no_pick());
+        if (lane == 0) {
+          sh.best = all;
+          if (units > 0 && all.key)
+            compare(from_order(last.key), last.k, from_order(all.key), all.k);
+        }
+      }
+      __syncthreads();
+      const Pick p = sh.best;
+      if (!p.key) break;
+      if (tid == 0) sh.unit[units] = p.k * a.C + p.at;
+      if (mine.k == p.k && mine.at == p.at) mine = next_unit(p);
+      last = p;
+    }
+    if (units == a.n) {
+      const double least = from_order(last.key);
+      for (int u = tid; u < a.K * a.C; u += kFinishThreads) {
+        const Pick p = unit_pick(u);
+        if (p.key && before(last, p)) compare(least, last.k, from_order(p.key), p.k);
+      }
+    }
+    __syncthreads();
+    if (sh.again) return false;
+    for (int j = warp; j < units; j += kFinishWarps) next_token(j, INFINITY, -1);
+    __syncthreads();
+    int32_t *tokens = a.tokens + static_cast<long long>(b) * a.n;
+    int32_t *parents = a.parents + static_cast<long long>(b) * a.n;
+    float *scores = a.out_scores + static_cast<long long>(b) * a.n;
+    double before_key = 0.;
+    int before_k = -1, found = 0;
+    for (; found < a.n; ++found) {
+      Pick p = no_pick();   // every warp finds the best head by itself
+      int j = 0;
+      for (int i = lane; i < units; i += 32)
+        if (sh.head[i].key && before(sh.head[i], p)) p = sh.head[i];
+      p = warp_best(p);
+      if (!p.key) break;
+      while (sh.unit[j] != p.k * a.C + (sh.kind[p.k] == kEnded ? 0 : p.at / (kUnitVecs * Elem<E>::kPerVec))) ++j;
+      const int k = p.k, token = p.at;
+      const float l = p.l;
+      const double x = from_order(p.key);
+      if (tid == 0) {
+        if (found > 0) compare(before_key, before_k, x, k);
+        tokens[found] = token;
+        parents[found] = b * a.K + k;
+        scores[found] = static_cast<float>(x);
+      }
+      before_key = x;
+      before_k = k;
+      __syncthreads();
+      if (warp == j % kFinishWarps) next_token(j, sh.kind[k] == kEnded ? -INFINITY : l, token);
+      __syncthreads();
+    }
+    if (found == a.n)
+      for (int j = tid; j < units; j += kFinishThreads)
+        if (sh.head[j].key) compare(before_key, before_k, from_order(sh.head[j].key), sh.head[j].k);
+    __syncthreads();
+    if (sh.again) return false;
+    for (int j = found + tid; j < a.n; j += kFinishThreads) {
+      tokens[j] = parents[j] = -1;
+      scores[j] = -INFINITY;
+    }
+    return true;
+  }
+};
+
+// One CTA a batch row.
+template <typename E>
+__global__ void __launch_bounds__(kFinishThreads, 1) beam_finish_kernel(const __grid_constant__ BeamArgs a) {
+  __shared__ FinishShared sh;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int tid = threadIdx.x, b = blockIdx.x;
+  const Finish<E> f{a, sh, b, tid, tid & 31, tid >> 5};
+  if (tid == 0) sh.bad = sh.again = 0;
+  __syncthreads();
+  f.sums();
+  __syncthreads();
+  if (sh.bad) {
+    if (tid == 0) set_status(a.status, SPEC_ERR_NONFINITE);
+    for (int j = tid; j < a.n; j += kFinishThreads) {
+      const long long at = static_cast<long long>(b) * a.n + j;
+      a.tokens[at] = a.parents[at] = -1;
+      a.out_scores[at] = NAN;
+    }
+    return;
+  }
+  while (!f.select()) {   // at most once a beam
+    __syncthreads();
+    if (tid == 0) sh.again = 0;
+    for (int k = 0; k < a.K; ++k)
+      if (sh.wanted[k]) f.precise_sum(k);
+    __syncthreads();
+  }
+}
+
+// ------------------------------------------------------------------ reordering
+
+// A CTA a (row, state): row c of each state from row parents[c] of the one before; zeros without a parent.
+template <typename W>
+__device__ __forceinline__ void copy_row(const char *from, char *to, long long bytes) {
+  const long long n = bytes / static_cast<long long>(sizeof(W));
+  for (long long i0 = threadIdx.x; i0 < n; i0 += 4 * 256) {
+    W w[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (i0 + u * 256 < n) w[u] = from ? reinterpret_cast<const W *>(from)[i0 + u * 256] : W{};
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (i0 + u * 256 < n) reinterpret_cast<W *>(to)[i0 + u * 256] = w[u];
+  }
+}
+
+__global__ void __launch_bounds__(256) beam_reorder_kernel(const __grid_constant__ ReorderArgs a) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int c = blockIdx.x / a.states, s = blockIdx.x - c * a.states;
+  const int p = __ldg(a.parents + c);
+  const bool ok = p >= 0 && p < a.rows_in;
+  if (!ok && p != -1 && threadIdx.x == 0) set_status(a.status, SPEC_ERR_PARENT);
+  const long long bytes = a.bytes[s];
+  const char *from = ok ? a.in[s] + p * bytes : nullptr;
+  char *to = a.out[s] + c * bytes;
+  switch (a.grain[s]) {
+    case 16: copy_row<uint4>(from, to, bytes); break;
+    case 8: copy_row<uint2>(from, to, bytes); break;
+    case 4: copy_row<uint32_t>(from, to, bytes); break;
+    case 2: copy_row<uint16_t>(from, to, bytes); break;
+    default: copy_row<uint8_t>(from, to, bytes);
+  }
+}
+
+template <typename E>
+cudaError_t launch_select(const BeamArgs &a, int sms, cudaStream_t stream) {
+  const int groups = (a.units + 7) / 8;
+  const cudaError_t e = launch_kv(beam_stream_kernel<E>, groups < 4 * sms ? groups : 4 * sms, 256, 0, stream, a);
+  return e != cudaSuccess ? e : launch_kv(beam_finish_kernel<E>, a.B, kFinishThreads, 0, stream, a);
+}
+
+}  // namespace
+
+cudaError_t launch_beam_select(int dtype, const BeamArgs &a, int sms, cudaStream_t stream) {
+  return dtype == SPEC_BF16 ? launch_select<uint16_t>(a, sms, stream) : launch_select<float>(a, sms, stream);
+}
+
+cudaError_t launch_beam_reorder(const ReorderArgs &a, cudaStream_t stream) {
+  return launch_kv(beam_reorder_kernel, static_cast<long long>(a.rows_out) * a.states, 256, 0, stream, a);
+}
+
+}  // namespace specv

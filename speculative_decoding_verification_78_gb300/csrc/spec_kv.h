@@ -142,6 +142,39 @@ struct RopeArgs {
   int vec4;                     // rope is 16-byte aligned
 };
 
+// Pages: counts of the places that hold them, and the table of the sequences concerned
+struct PageArgs {
+  int32_t *refs;             // [num_pages]
+  int32_t *table;            // [B, pps]; a negative entry: no page
+  const int32_t *seq_lens;   // [B]
+  int32_t *status;
+  int num_pages, page, page_shift, pps, B;
+};
+// All layers of a cache, for moving contents
+struct PoolArgs {
+  uint8_t *k, *v;
+  float *k_scale, *v_scale;
+  int num_pages, page, Hkv, D, layers;
+};
+struct ForkArgs {
+  const int32_t *parents;    // [C]
+  int32_t *table_out;        // [C, pps]
+  int32_t *lens_out;         // [C]
+  int32_t *count;            // copies to make: (page, its copy, rows)
+  int4 *copies;
+  int32_t *list;             // free pages
+  int C, release;
+};
+cudaError_t launch_kv_release(const PageArgs &a, const int32_t *ended, int32_t *lens, int window,
+                              int sinks, cudaStream_t stream);
+cudaError_t launch_kv_reserve(const PageArgs &a, const int32_t *new_lens, int N, int32_t *granted,
+                              void *ws, cudaStream_t stream);
+cudaError_t launch_kv_fork(const PageArgs &a, const PoolArgs &m, ForkArgs f, void *ws,
+                           cudaStream_t stream);
+cudaError_t launch_kv_compact(const PageArgs &a, const PoolArgs &m, int32_t *map, int32_t *live,
+                              void *ws, cudaStream_t stream);
+size_t kv_pages_workspace(int num_pages, int B);
+
 cudaError_t launch_kv_append(const KvArgs &a, const RopeArgs &r, int dtype, cudaStream_t stream);
 cudaError_t launch_kv_commit(const KvArgs &a, int layers, const int32_t *path,
                              const int32_t *accept, int32_t *out_lens, cudaStream_t stream);

@@ -69,6 +69,35 @@ bool stride_ok(int64_t stride, int heads, int D) {
   return stride >= static_cast<int64_t>(heads) * D && stride % 8 == 0 && stride < (1LL << 31);
 }
 
+// The checks of the calls that deal with pages: `refs`, and tables of at most SPEC_MAX_SEQS sequences
+int pages_common(PageArgs &g, KvArgs &a, const spec_kv_cache_t *c, int32_t *refs, int32_t *page_table,
+                 int pps, const int32_t *seq_lens, int B, int32_t *status) {
+  const int rc = kv_common(a, c, page_table, pps, seq_lens, nullptr, B, 1, nullptr, status);
+  if (rc != SPEC_OK) return rc;
+  if (B > SPEC_MAX_SEQS) return SPEC_ERR_SHAPE;
+  if (!refs) return SPEC_ERR_NULL;
+  if (!aligned(refs, 4)) return SPEC_ERR_ALIGN;
+  g = PageArgs{refs, page_table, seq_lens, status, a.num_pages, a.page, a.page_shift, pps, B};
+  return SPEC_OK;
+}
+
+int pages_workspace_ok(const void *workspace, size_t bytes, int num_pages, int B) {
+  if (!workspace) return SPEC_ERR_NULL;
+  if (!aligned(workspace, 16)) return SPEC_ERR_ALIGN;
+  return bytes < kv_pages_workspace(num_pages, B) ? SPEC_ERR_WORKSPACE : SPEC_OK;
+}
+
+PoolArgs pool_of(const KvArgs &a, int layers) {
+  return PoolArgs{a.k, a.v, a.k_scale, a.v_scale, a.num_pages, a.page, a.Hkv, a.D, layers};
+}
+
+bool apart(const void *p, const void *q, size_t n, size_t m) {   // n bytes from p, m from q
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return a + n <= b || b + m <= a;
+}
+
+constexpr int kMaxWindow = 1 << 30;   // past every slot
+
 }  // namespace
 
 extern "C" {
@@ -175,6 +204,97 @@ int spec_kv_commit(const spec_kv_cache_t *cache, int layers, const int32_t *page
   if (B == 0) return SPEC_OK;
   return launch_result(launch_kv_commit(a, layers, path_nodes, accept_len, out_lens,
                                         static_cast<cudaStream_t>(stream)));
+}
+
+size_t spec_kv_pages_workspace_bytes(int num_pages, int B) {
+  if (num_pages < 1 || B < 0 || B > SPEC_MAX_SEQS) return 0;
+  return kv_pages_workspace(num_pages, B);
+}
+
+int spec_kv_reserve(const spec_kv_cache_t *cache, int32_t *refs, int32_t *page_table, int pages_per_seq,
+                    const int32_t *seq_lens, const int32_t *new_lens, int B, int N, int32_t *granted,
+                    int32_t *status, void *workspace, size_t workspace_bytes, void *stream) {
+  PageArgs g;
+  KvArgs a;
+  int rc = pages_common(g, a, cache, refs, page_table, pages_per_seq, seq_lens, B, status);
+  if (rc != SPEC_OK) return rc;
+  if (N < 1 || N > kMaxNew) return SPEC_ERR_SHAPE;
+  if (B > 0 && !granted) return SPEC_ERR_NULL;
+  if (!aligned(granted, 4) || !aligned(new_lens, 4)) return SPEC_ERR_ALIGN;
+  if ((rc = pages_workspace_ok(workspace, workspace_bytes, a.num_pages, B)) != SPEC_OK) return rc;
+  if (B == 0) return SPEC_OK;
+  return launch_result(launch_kv_reserve(g, new_lens, N, granted, workspace,
+                                         static_cast<cudaStream_t>(stream)));
+}
+
+int spec_kv_trim(const spec_kv_cache_t *cache, int32_t *refs, int32_t *page_table, int pages_per_seq,
+                 const int32_t *seq_lens, int B, int window, int sinks, int32_t *status, void *stream) {
+  PageArgs g;
+  KvArgs a;
+  const int rc = pages_common(g, a, cache, refs, page_table, pages_per_seq, seq_lens, B, status);
+  if (rc != SPEC_OK) return rc;
+  if (window < 1 || sinks < 0) return SPEC_ERR_SHAPE;
+  if (B == 0) return SPEC_OK;
+  return launch_result(launch_kv_release(g, nullptr, nullptr, window < kMaxWindow ? window : kMaxWindow,
+                                         sinks < kMaxWindow ? sinks : kMaxWindow,
+                                         static_cast<cudaStream_t>(stream)));
+}
+
+int spec_kv_free(const spec_kv_cache_t *cache, int32_t *refs, int32_t *page_table, int pages_per_seq,
+                 int32_t *seq_lens, const int32_t *ended, int B, int32_t *status, void *stream) {
+  PageArgs g;
+  KvArgs a;
+  const int rc = pages_common(g, a, cache, refs, page_table, pages_per_seq, seq_lens, B, status);
+  if (rc != SPEC_OK) return rc;
+  if (!aligned(ended, 4)) return SPEC_ERR_ALIGN;
+  if (B == 0) return SPEC_OK;
+  return launch_result(launch_kv_release(g, ended, seq_lens, 0, 0, static_cast<cudaStream_t>(stream)));
+}
+
+int spec_kv_fork(const spec_kv_cache_t *cache, int layers, int32_t *refs, const int32_t *page_table,
+                 int pages_per_seq, const int32_t *seq_lens, int B, const int32_t *parents, int C,
+                 int release, int32_t *page_table_out, int32_t *lens_out, int32_t *status,
+                 void *workspace, size_t workspace_bytes, void *stream) {
+  PageArgs g;
+  KvArgs a;
+  // (the table is only read)
+  int rc = pages_common(g, a, cache, refs, const_cast<int32_t *>(page_table), pages_per_seq, seq_lens, B,
+                        status);
+  if (rc != SPEC_OK) return rc;
+  if (layers < 1 || C < 0 || C > SPEC_MAX_SEQS) return SPEC_ERR_SHAPE;
+  if (C > 0 && (!parents || !page_table_out || !lens_out)) return SPEC_ERR_NULL;
+  if (!aligned(parents, 4) || !aligned(page_table_out, 4) || !aligned(lens_out, 4)) return SPEC_ERR_ALIGN;
+  const size_t row = 4 * static_cast<size_t>(pages_per_seq);
+  if (B > 0 && C > 0 &&
+      (!apart(page_table, page_table_out, row * B, row * C) ||
+       !apart(seq_lens, lens_out, 4 * static_cast<size_t>(B), 4 * static_cast<size_t>(C))))
+    return SPEC_ERR_SHAPE;
+  if ((rc = pages_workspace_ok(workspace, workspace_bytes, a.num_pages, C)) != SPEC_OK) return rc;
+  if (C == 0 && (B == 0 || !release)) return SPEC_OK;
+  ForkArgs f{};
+  f.parents = parents;
+  f.table_out = page_table_out;
+  f.lens_out = lens_out;
+  f.C = C;
+  f.release = release != 0;
+  return launch_result(launch_kv_fork(g, pool_of(a, layers), f, workspace,
+                                      static_cast<cudaStream_t>(stream)));
+}
+
+int spec_kv_compact(const spec_kv_cache_t *cache, int layers, int32_t *refs, int32_t *page_table,
+                    int pages_per_seq, int B, int32_t *page_map, int32_t *live, int32_t *status,
+                    void *workspace, size_t workspace_bytes, void *stream) {
+  PageArgs g;
+  KvArgs a;
+  // (no lengths: a table entry is a page or none)
+  int rc = pages_common(g, a, cache, refs, page_table, pages_per_seq, page_table, B, status);
+  if (rc != SPEC_OK) return rc;
+  if (layers < 1) return SPEC_ERR_SHAPE;
+  if (!page_map || !live) return SPEC_ERR_NULL;
+  if (!aligned(page_map, 4) || !aligned(live, 4)) return SPEC_ERR_ALIGN;
+  if ((rc = pages_workspace_ok(workspace, workspace_bytes, a.num_pages, B)) != SPEC_OK) return rc;
+  return launch_result(launch_kv_compact(g, pool_of(a, layers), page_map, live, workspace,
+                                         static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"
