@@ -438,6 +438,21 @@ int spec_kv_attention(const spec_kv_cache_t *cache, const int32_t *page_table, i
                       void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * spec_kv_attention with a sliding window: a query at position p sees, of the slots t that it would see there,
+ * those with t > p - window (the last `window` positions, its own among them) and the first `sinks` slots
+ * (t < sinks), which stay visible. The position of new token i is its slot seq_lens[b] + i, or with mask_words
+ * seq_lens[b] + depth of node i (the bits of its row, less one); there window >= N, so that the window holds
+ * every ancestor among the new tokens. Pages without a slot that some query of the call sees are not read: their
+ * table entries may be -1 (spec_kv_trim). Work and traffic follow the slots that are seen.
+ * Everything else is as for spec_kv_attention, with the same workspace. Limits: window >= 1, sinks >= 0.
+ */
+int spec_kv_attention_window(const spec_kv_cache_t *cache, const int32_t *page_table, int pages_per_seq,
+                             const int32_t *seq_lens, const int32_t *new_lens, int B, int N,
+                             const void *q, int64_t q_stride, int q_heads, int dtype, float scale,
+                             const uint32_t *mask_words, int window, int sinks, void *out, float *lse,
+                             int32_t *status, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * Keeps the accepted path of B verified trees, in `layers` caches that lie one after another in
  * memory ([layers, num_pages, ...], scales too) and share page numbers: row
  * seq_lens[b] + path_nodes[b, k] moves to row seq_lens[b] + k for k = 0 .. accept_len[b], and

@@ -27,4 +27,4 @@ from ._binding import (  # noqa: F401
     SpecState, beam_reorder, beam_select, kv_compact, kv_fork, kv_free, kv_reserve, kv_trim,
     new_beam_workspace, new_page_refs, new_pages_workspace, spec_beam_reorder, spec_beam_select,
     spec_beam_workspace_bytes, spec_kv_compact, spec_kv_fork, spec_kv_free,
-    spec_kv_pages_workspace_bytes, spec_kv_reserve, spec_kv_trim)
+    spec_kv_pages_workspace_bytes, spec_kv_reserve, spec_kv_trim, spec_kv_attention_window)

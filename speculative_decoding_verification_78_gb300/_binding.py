@@ -40,6 +40,7 @@ EXPORTS = ("spec_workspace_bytes", "spec_workspace_init", "spec_verify_chain",
            "spec_launch_shape", "spec_verify_chain_static", "spec_sample", "spec_topk",
            "spec_tree_mask", "spec_selftest_bounded_wait", "spec_kv_append",
            "spec_kv_attention_workspace_bytes", "spec_kv_attention", "spec_kv_commit",
+           "spec_kv_attention_window",
            "spec_beam_workspace_bytes", "spec_beam_select", "spec_beam_reorder",
            "spec_kv_pages_workspace_bytes", "spec_kv_reserve", "spec_kv_trim", "spec_kv_free",
            "spec_kv_fork", "spec_kv_compact")
@@ -137,6 +138,9 @@ def load_library(checked: bool = False):
         lib.spec_kv_attention.argtypes = [cache, vp, i32, vp, vp, i32, i32, vp, i64, i32, i32, f32,
                                           vp, vp, vp, vp, vp, sz, vp]
         lib.spec_kv_attention.restype = i32
+        lib.spec_kv_attention_window.argtypes = [cache, vp, i32, vp, vp, i32, i32, vp, i64, i32, i32, f32,
+                                                 vp, i32, i32, vp, vp, vp, vp, sz, vp]
+        lib.spec_kv_attention_window.restype = i32
         lib.spec_kv_commit.argtypes = [cache, i32, vp, i32, vp, i32, i32, vp, vp, vp, vp, vp]
         lib.spec_kv_commit.restype = i32
         lib.spec_beam_workspace_bytes.argtypes = [i32, i32, i32, i32]
@@ -544,6 +548,19 @@ def spec_kv_attention(cache, layer, page_table, seq_lens, new_lens, q, scale, ma
                       status, workspace, stream=None) -> int:
     """q, out [B, N, q_heads, D] (bf16 or fp16); lse [B, N, q_heads] fp32 or None; workspace uint8
     (scratch); the others as for spec_kv_append."""
+    return _kv_attend("spec_kv_attention", cache, layer, page_table, seq_lens, new_lens, q, scale,
+                      mask_words, (), out, lse, status, workspace, stream)
+
+
+def spec_kv_attention_window(cache, layer, page_table, seq_lens, new_lens, q, scale, mask_words, window,
+                             sinks, out, lse, status, workspace, stream=None) -> int:
+    """spec_kv_attention over the last `window` positions and the first `sinks` tokens."""
+    return _kv_attend("spec_kv_attention_window", cache, layer, page_table, seq_lens, new_lens, q, scale,
+                      mask_words, (int(window), int(sinks)), out, lse, status, workspace, stream)
+
+
+def _kv_attend(name, cache, layer, page_table, seq_lens, new_lens, q, scale, mask_words, span, out, lse,
+               status, workspace, stream) -> int:
     flag = _kv_dtype(q, "q")
     B, N, heads, D = q.shape
     if D != cache.head_dim:
@@ -551,10 +568,10 @@ def spec_kv_attention(cache, layer, page_table, seq_lens, new_lens, q, scale, ma
     pps, table, lens, news, mask, st = _kv_shared(page_table, seq_lens, new_lens, mask_words, status,
                                                   B, N)
     qp, qs = _tokens(q, "q", B, N, heads, D, q.dtype)
-    return load_library().spec_kv_attention(
-        cache.struct(layer), table, pps, lens, news, B, N, qp, qs, heads, flag, float(scale), mask,
+    return getattr(load_library(), name)(
+        cache.struct(layer), table, pps, lens, news, B, N, qp, qs, heads, flag, float(scale), mask, *span,
         _operand(out, "out", q.numel(), q.dtype), _operand(lse, "lse", B * N * heads, _F32), st,
-        _ptr(workspace), _nbytes(workspace), _stream(stream))
+        *_workspace(workspace), _stream(stream))
 
 
 def spec_kv_commit(cache, page_table, seq_lens, path_nodes, accept_len, out_lens, status,
@@ -900,10 +917,14 @@ def kv_append(cache, page_table, seq_lens, k, v, q=None, rope=None, layer=0, int
 
 @_allocates
 def kv_attention(cache, page_table, seq_lens, q, scale=None, mask=None, layer=0, new_lens=None,
-                 out=None, workspace=None, status=None, return_lse=False, stream=None):
+                 out=None, workspace=None, status=None, return_lse=False, stream=None, window=None,
+                 sinks=0):
     """Attention of the new tokens over one layer of the cache, which already holds them
-    (spec_kv_attention). scale: 1 / sqrt(head_dim) by default. Returns (out, lse, status); lse is
-    None unless return_lse."""
+    (spec_kv_attention); with `window`, of the last `window` positions and the first `sinks` tokens
+    (spec_kv_attention_window). scale: 1 / sqrt(head_dim) by default. Returns (out, lse, status); lse
+    is None unless return_lse."""
+    if window is None and sinks:
+        raise ValueError("sinks are what stays visible outside a window: give a window")
     if out is None:
         out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     B, N, heads, D = q.shape
@@ -914,8 +935,13 @@ def kv_attention(cache, page_table, seq_lens, q, scale=None, mask=None, layer=0,
         workspace = new_attention_workspace(B, N, heads, cache.kv_heads, D, q.device)
     if scale is None:
         scale = D ** -0.5
-    check(spec_kv_attention(cache, layer, page_table, seq_lens, new_lens, q, scale, mask, out, lse,
-                            status, workspace, stream), "spec_kv_attention")
+    if window is None:
+        check(spec_kv_attention(cache, layer, page_table, seq_lens, new_lens, q, scale, mask, out, lse,
+                                status, workspace, stream), "spec_kv_attention")
+    else:
+        check(spec_kv_attention_window(cache, layer, page_table, seq_lens, new_lens, q, scale, mask,
+                                       window, sinks, out, lse, status, workspace, stream),
+              "spec_kv_attention_window")
     return out, lse, status
 
 

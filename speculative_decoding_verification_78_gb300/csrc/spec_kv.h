@@ -179,8 +179,8 @@ cudaError_t launch_kv_append(const KvArgs &a, const RopeArgs &r, int dtype, cuda
 cudaError_t launch_kv_commit(const KvArgs &a, int layers, const int32_t *path,
                              const int32_t *accept, int32_t *out_lens, cudaStream_t stream);
 cudaError_t launch_kv_attention(const KvArgs &a, const void *q, long long q_stride, int dtype,
-                                float scale, void *out, float *lse, void *ws,
-                                cudaStream_t stream);
+                                float scale, int window, int sinks, void *out, float *lse, void *ws,
+                                cudaStream_t stream);   // window 0: none
 size_t kv_attention_workspace(int B, int N, int Hq, int Hkv, int D);
 // Query rows of a tile, for calls with `rows` of them a key head: up to 32 along the columns of an MMA, more
 // along its lanes. (What each costs is measured at the two kernels.)

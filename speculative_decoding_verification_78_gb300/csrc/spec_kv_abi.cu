@@ -98,6 +98,43 @@ bool apart(const void *p, const void *q, size_t n, size_t m) {   // n bytes from
 
 constexpr int kMaxWindow = 1 << 30;   // past every slot
 
+// spec_kv_attention (window 0) and spec_kv_attention_window
+int attend(const spec_kv_cache_t *cache, const int32_t *page_table, int pages_per_seq,
+           const int32_t *seq_lens, const int32_t *new_lens, int B, int N, const void *q,
+           int64_t q_stride, int q_heads, int dtype, float scale, const uint32_t *mask_words,
+           int window, int sinks, void *out, float *lse, int32_t *status, void *workspace,
+           size_t workspace_bytes, void *stream) {
+  if (dtype != SPEC_BF16 && dtype != SPEC_F16) return SPEC_ERR_DTYPE;
+  KvArgs a;
+  // (a tree's new tokens lie within the window whole: their places are not their positions)
+  if (sinks < 0 || (window > 0 && mask_words && window < N)) return SPEC_ERR_SHAPE;
+  const int rc = kv_common(a, cache, page_table, pages_per_seq, seq_lens, new_lens, B, N,
+                           mask_words, status);
+  if (rc != SPEC_OK) return rc;
+  const size_t need = spec_kv_attention_workspace_bytes(B, N, q_heads, a.Hkv, a.D);
+  if (need == 0) return SPEC_ERR_SHAPE;
+  if (!stride_ok(q_stride, q_heads, a.D) || !isfinite(scale)) return SPEC_ERR_SHAPE;
+  // rows, and the 128-token tiles of all sequences, key heads and row tiles, are counted in 31 bits
+  const long long limit = 1LL << 31;
+  const long long rows = static_cast<long long>(N) * (q_heads / a.Hkv);
+  if (rows >= limit) return SPEC_ERR_SHAPE;
+  const int height = kv_row_tile(rows);
+  long long tiles = (static_cast<long long>(pages_per_seq) * a.page + 127) / 128;   // < 2^23
+  for (const long long f : {(rows + height - 1) / height, static_cast<long long>(a.Hkv),
+                            static_cast<long long>(B)}) {
+    tiles *= f;   // both below 2^31
+    if (tiles >= limit) return SPEC_ERR_SHAPE;
+  }
+  if ((B > 0 && (!q || !out)) || !workspace) return SPEC_ERR_NULL;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(workspace, 16))
+    return SPEC_ERR_ALIGN;
+  if (workspace_bytes < need) return SPEC_ERR_WORKSPACE;
+  if (B == 0) return SPEC_OK;
+  a.Hq = q_heads;
+  return launch_result(launch_kv_attention(a, q, q_stride, dtype, scale, window, sinks, out, lse,
+                                           workspace, static_cast<cudaStream_t>(stream)));
+}
+
 }  // namespace
 
 extern "C" {
@@ -159,33 +196,20 @@ int spec_kv_attention(const spec_kv_cache_t *cache, const int32_t *page_table, i
                       int64_t q_stride, int q_heads, int dtype, float scale,
                       const uint32_t *mask_words, void *out, float *lse, int32_t *status,
                       void *workspace, size_t workspace_bytes, void *stream) {
-  if (dtype != SPEC_BF16 && dtype != SPEC_F16) return SPEC_ERR_DTYPE;
-  KvArgs a;
-  const int rc = kv_common(a, cache, page_table, pages_per_seq, seq_lens, new_lens, B, N,
-                           mask_words, status);
-  if (rc != SPEC_OK) return rc;
-  const size_t need = spec_kv_attention_workspace_bytes(B, N, q_heads, a.Hkv, a.D);
-  if (need == 0) return SPEC_ERR_SHAPE;
-  if (!stride_ok(q_stride, q_heads, a.D) || !isfinite(scale)) return SPEC_ERR_SHAPE;
-  // rows, and the 128-token tiles of all sequences, key heads and row tiles, are counted in 31 bits
-  const long long limit = 1LL << 31;
-  const long long rows = static_cast<long long>(N) * (q_heads / a.Hkv);
-  if (rows >= limit) return SPEC_ERR_SHAPE;
-  const int height = kv_row_tile(rows);
-  long long tiles = (static_cast<long long>(pages_per_seq) * a.page + 127) / 128;   // < 2^23
-  for (const long long f : {(rows + height - 1) / height, static_cast<long long>(a.Hkv),
-                            static_cast<long long>(B)}) {
-    tiles *= f;   // both below 2^31
-    if (tiles >= limit) return SPEC_ERR_SHAPE;
-  }
-  if ((B > 0 && (!q || !out)) || !workspace) return SPEC_ERR_NULL;
-  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(workspace, 16))
-    return SPEC_ERR_ALIGN;
-  if (workspace_bytes < need) return SPEC_ERR_WORKSPACE;
-  if (B == 0) return SPEC_OK;
-  a.Hq = q_heads;
-  return launch_result(launch_kv_attention(a, q, q_stride, dtype, scale, out, lse, workspace,
-                                           static_cast<cudaStream_t>(stream)));
+  return attend(cache, page_table, pages_per_seq, seq_lens, new_lens, B, N, q, q_stride, q_heads, dtype,
+                scale, mask_words, 0, 0, out, lse, status, workspace, workspace_bytes, stream);
+}
+
+int spec_kv_attention_window(const spec_kv_cache_t *cache, const int32_t *page_table, int pages_per_seq,
+                             const int32_t *seq_lens, const int32_t *new_lens, int B, int N,
+                             const void *q, int64_t q_stride, int q_heads, int dtype, float scale,
+                             const uint32_t *mask_words, int window, int sinks, void *out, float *lse,
+                             int32_t *status, void *workspace, size_t workspace_bytes, void *stream) {
+  if (window < 1) return SPEC_ERR_SHAPE;
+  return attend(cache, page_table, pages_per_seq, seq_lens, new_lens, B, N, q, q_stride, q_heads, dtype,
+                scale, mask_words, window < kMaxWindow ? window : kMaxWindow,
+                sinks < kMaxWindow ? sinks : kMaxWindow, out, lse, status, workspace, workspace_bytes,
+                stream);
 }
 
 int spec_kv_commit(const spec_kv_cache_t *cache, int layers, const int32_t *page_table,

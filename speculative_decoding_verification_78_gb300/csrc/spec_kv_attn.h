@@ -32,6 +32,8 @@ struct AttnArgs {
                        // its tiles
   int G;               // query heads per key head
   int RT;              // row tiles
+  int window, sinks;   // (windowed kernels) a query at position p sees slots past p - window, and the first
+                       // `sinks`
 };
 
 // ------------------------------------------------------------------ tensor-core helpers
@@ -195,12 +197,20 @@ __host__ __device__ constexpr uint32_t attn_idesc(int M, int N, bool mn_major) {
 
 // ------------------------------------------------------------------ the line of tiles
 
-struct Item {   // one (sequence, key head, row tile)
+// With a window: the first slot of any row's window, and of the last row's (every row's window has begun by
+// then); of the tiles from 0 on, `gap` are left out after the first `head` ones, which hold the sinks.
+template <bool kWin> struct WindowPart {
+  int lo, lo_all, head, gap;
+};
+template <> struct WindowPart<false> {
+  static constexpr int lo = 0, lo_all = 0, head = 0, gap = 0;
+};
+template <bool kWin> struct Item : WindowPart<kWin> {   // one (sequence, key head, row tile)
   int b, h, rt;
   int len, n;      // tokens before the new ones; new ones
   bool ok;         // lengths fit
   int end;         // first slot that no row sees
-  int tiles;
+  int tiles;       // tiles that some row sees
 };
 
 template <int NT>
@@ -214,31 +224,84 @@ __device__ __forceinline__ int item_end(const AttnArgs &p, int len, int n, bool 
 }
 // The slots below it are seen by every row of the item that has a token: what lies past the first
 // token's place may be hidden from some.
-template <int NT>
-__device__ __forceinline__ int seen_by_all(const AttnArgs &p, const Item &x) {
+template <int NT, bool kWin>
+__device__ __forceinline__ int seen_by_all(const AttnArgs &p, const Item<kWin> &x) {
   const int first = static_cast<int>(static_cast<unsigned>(x.rt) * NT / p.G);
   return min(x.len + (p.a.mask ? 0 : first + 1), x.end);
 }
 __device__ __forceinline__ int tiles_for(int end) { return end > kTile ? (end + kTile - 1) / kTile : 1; }
 
-// tiles of one key head of sequence b
-template <int NT>
-__device__ __forceinline__ int head_tiles(const AttnArgs &p, int b) {
-  int len, n;
-  const bool ok = kv_lengths(p.a, b, len, n);
-  int s = 0;
-#pragma unroll 1
-  for (int rt = 0; rt < p.RT; ++rt) s += tiles_for(item_end<NT>(p, len, n, ok, rt));
-  return s;
-}
-template <int NT>
-__device__ __forceinline__ void item_load(const AttnArgs &p, Item &x) {
-  x.ok = kv_lengths(p.a, x.b, x.len, x.n);
+// What a row tile's item is, from its lengths.
+template <int NT, bool kWin>
+__device__ __forceinline__ void item_span(const AttnArgs &p, Item<kWin> &x) {
   x.end = item_end<NT>(p, x.len, x.n, x.ok, x.rt);
   x.tiles = tiles_for(x.end);
+  if constexpr (kWin) {
+    x.lo = x.lo_all = x.head = x.gap = 0;
+    if (x.end == 0) return;   // (its lengths may be anything)
+    // Positions of the item's rows: a chain's are its tokens', a tree's at least the root's and at most as
+    // deep as it has nodes. (Numbers of at most 2^30, as is the window: no overflow.)
+    const int first = p.a.mask ? 0 : static_cast<int>(static_cast<unsigned>(x.rt) * NT / p.G);
+    const int last = p.a.mask ? p.a.N - 1 : x.end - 1 - x.len;
+    x.lo = max(0, x.len + first - p.window + 1);
+    x.lo_all = max(0, x.len + last - p.window + 1);
+    const int low = min(x.lo / kTile, x.tiles - 1);   // the window's first tile
+    x.head = min((min(p.sinks, x.end) + kTile - 1) / kTile, low);
+    x.gap = low - x.head;
+    x.tiles -= x.gap;
+  }
 }
-template <int NT>
-__device__ __forceinline__ void item_next(const AttnArgs &p, Item &x) {
+// The slot that tile k of the item begins with.
+template <bool kWin>
+__device__ __forceinline__ int tile_slot(const Item<kWin> &x, int k) {
+  return (kWin && k >= x.head ? k + x.gap : k) * kTile;
+}
+// Whether some row's window, or the sinks, reach into slots [slot, slot + n).
+template <bool kWin>
+__device__ __forceinline__ bool span_seen(const AttnArgs &p, const Item<kWin> &x, int slot, int n) {
+  return !kWin || slot + n > x.lo || slot < p.sinks;
+}
+// Whether the windows leave out none of a tile's slots, for any row.
+template <bool kWin>
+__device__ __forceinline__ bool tile_whole(const AttnArgs &p, const Item<kWin> &x, int slot0) {
+  return !kWin || slot0 >= x.lo_all || slot0 + kTile <= p.sinks;
+}
+
+// The first slot in the window of new token i, whose position is its slot's, or in a tree its depth's.
+template <bool kWin>
+__device__ __forceinline__ int window_start(const AttnArgs &p, const Item<kWin> &x, int i) {
+  int at = i;
+  if (p.a.mask) {
+    const uint32_t *m = p.a.mask + (static_cast<long long>(x.b) * p.a.N + i) * p.a.W;
+    int bits = 0;
+#pragma unroll 1
+    for (int w = 0; w < p.a.W; ++w) bits += __popc(__ldg(m + w));
+    at = max(bits - 1, 0);
+  }
+  return x.len + at - p.window + 1;
+}
+
+// tiles of one key head of sequence b
+template <int NT, bool kWin>
+__device__ __forceinline__ int head_tiles(const AttnArgs &p, int b) {
+  Item<kWin> x;
+  x.b = b;
+  x.ok = kv_lengths(p.a, b, x.len, x.n);
+  int s = 0;
+#pragma unroll 1
+  for (x.rt = 0; x.rt < p.RT; ++x.rt) {
+    item_span<NT, kWin>(p, x);
+    s += x.tiles;
+  }
+  return s;
+}
+template <int NT, bool kWin>
+__device__ __forceinline__ void item_load(const AttnArgs &p, Item<kWin> &x) {
+  x.ok = kv_lengths(p.a, x.b, x.len, x.n);
+  item_span<NT, kWin>(p, x);
+}
+template <int NT, bool kWin>
+__device__ __forceinline__ void item_next(const AttnArgs &p, Item<kWin> &x) {
   if (++x.rt == p.RT) {
     x.rt = 0;
     if (++x.h == p.a.Hkv) {
@@ -248,10 +311,9 @@ __device__ __forceinline__ void item_next(const AttnArgs &p, Item &x) {
   }
   if (x.b >= p.a.B) return;
   if (x.h == 0 && x.rt == 0) {   // another sequence
-    item_load<NT>(p, x);
+    item_load<NT, kWin>(p, x);
   } else if (p.RT > 1) {
-    x.end = item_end<NT>(p, x.len, x.n, x.ok, x.rt);
-    x.tiles = tiles_for(x.end);
+    item_span<NT, kWin>(p, x);
   }
 }
 // Range c of G of a line of T tiles begins at floor(T c / G); range_of: the range that holds tile t.
@@ -264,21 +326,21 @@ __device__ __forceinline__ int range_of(int T, int t, int G) {
 
 // The CTA's range [t0, t1) of the line and its first item; called by all threads. Thread t sums
 // the sequences of its own contiguous share; the thread whose share holds t0 finds it there.
-struct LocateScratch {
+template <bool kWin> struct LocateScratch {
   int b0, skip0;
   int warp_sum[32];
-  Item x;
+  Item<kWin> x;
   int t0, t1, total, skip;
 };
-template <int NT, int kThreads>
-__device__ __forceinline__ void locate(const AttnArgs &p, LocateScratch &sm, int &t0, int &t1,
-                                       int &total, Item &x, int &skip) {
+template <int NT, int kThreads, bool kWin>
+__device__ __forceinline__ void locate(const AttnArgs &p, LocateScratch<kWin> &sm, int &t0, int &t1,
+                                       int &total, Item<kWin> &x, int &skip) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int share = (p.a.B + kThreads - 1) / kThreads;
   const int lo = min(p.a.B, tid * share), hi = min(p.a.B, lo + share);
   int mine = 0;
 #pragma unroll 1
-  for (int b = lo; b < hi; ++b) mine += head_tiles<NT>(p, b) * p.a.Hkv;
+  for (int b = lo; b < hi; ++b) mine += head_tiles<NT, kWin>(p, b) * p.a.Hkv;
   int incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -300,7 +362,7 @@ __device__ __forceinline__ void locate(const AttnArgs &p, LocateScratch &sm, int
     int b = lo;
 #pragma unroll 1
     for (;; ++b) {
-      const int n = head_tiles<NT>(p, b) * p.a.Hkv;
+      const int n = head_tiles<NT, kWin>(p, b) * p.a.Hkv;
       if (first < at + n) break;
       at += n;
     }
@@ -314,20 +376,20 @@ __device__ __forceinline__ void locate(const AttnArgs &p, LocateScratch &sm, int
     sm.t0 = first;
     sm.t1 = range_start(all, blockIdx.x + 1, gridDim.x);
     sm.total = all;
-    Item y{};
+    Item<kWin> y{};
     int left = 0;
     if (sm.t0 < sm.t1) {
       y.b = sm.b0;
       left = sm.skip0;
-      const int per_head = head_tiles<NT>(p, y.b);
+      const int per_head = head_tiles<NT, kWin>(p, y.b);
       y.h = left / per_head;
       left -= y.h * per_head;
-      item_load<NT>(p, y);
+      item_load<NT, kWin>(p, y);
 #pragma unroll 1
       while (left >= y.tiles) {
         left -= y.tiles;
         ++y.rt;
-        item_load<NT>(p, y);
+        item_load<NT, kWin>(p, y);
       }
     }
     sm.x = y;
@@ -343,7 +405,8 @@ __device__ __forceinline__ void locate(const AttnArgs &p, LocateScratch &sm, int
 }
 // What the join needs to know of the CTA's range: its first item and the item's tiles before it,
 // the item's tiles, the range, and the length of the line.
-__device__ __forceinline__ void publish_range(const AttnArgs &p, const Item &x, int skip, int t0,
+template <bool kWin>
+__device__ __forceinline__ void publish_range(const AttnArgs &p, const Item<kWin> &x, int skip, int t0,
                                               int t1, int total) {
   if (t0 < t1) p.start[blockIdx.x] = make_int4(x.b, x.h, x.rt, skip);
   p.start[gridDim.x + blockIdx.x] = make_int4(t0 < t1 ? x.tiles : 0, t0, t1, total);
@@ -381,8 +444,8 @@ struct RowMap {
 // at most 2^-10, half the smallest e4m3 value. Blocks of kBlock rows, each
 // term of a block a K-major operand; of the NT rows the first `rows` (a multiple of 16) are written, zero
 // past the item's.
-template <typename T, int D, int NT, int kBlock, int kTerms, int kThreads>
-__device__ __forceinline__ void load_queries(const AttnArgs &p, const Item &x, const RowMap &map,
+template <typename T, int D, int NT, int kBlock, int kTerms, int kThreads, bool kWin>
+__device__ __forceinline__ void load_queries(const AttnArgs &p, const Item<kWin> &x, const RowMap &map,
                                              int rows, int tid, uint8_t *sq, float *qs) {
   constexpr int kLanes = D / 8, kRows = kThreads / kLanes;
   constexpr int kSteps = (NT + kRows - 1) / kRows, kAhead = kSteps < 4 ? kSteps : 4;
@@ -442,15 +505,16 @@ template <int D, int kThreads> struct Widen {
   static constexpr int kRows = kThreads / kLanes;   // tokens a step
   static constexpr int kSteps = kTile / kRows;
 };
-template <int D, int kThreads>
-__device__ __forceinline__ void fetch_values(const uint8_t *sv, int gtid, int valid,
+// Tokens of the tile that no row sees (before `from` and not below `sinks`, or from `valid` on) count as zeros.
+template <int D, int kThreads, bool kWin>
+__device__ __forceinline__ void fetch_values(const uint8_t *sv, int gtid, int valid, int from, int sinks,
                                              uint4 (&w)[Widen<D, kThreads>::kSteps]) {
   using W = Widen<D, kThreads>;
 #pragma unroll
   for (int u = 0; u < W::kSteps; ++u) {
     const int t = u * W::kRows + gtid / W::kLanes;
     w[u] = *reinterpret_cast<const uint4 *>(sv + t * D + gtid % W::kLanes * 16);
-    if (t >= valid) w[u] = make_uint4(0, 0, 0, 0);
+    if (t >= valid || (kWin && t < from && t >= sinks)) w[u] = make_uint4(0, 0, 0, 0);
   }
 }
 __device__ __forceinline__ uint32_t nan_codes(uint32_t w) {   // bit 7 of each NaN byte
@@ -668,8 +732,14 @@ cudaError_t allow_smem(K kernel, int bytes, std::atomic<bool> (&ready)[64]) {
 
 }  // namespace attn
 
-// the kernel for items of more than 32 query rows (spec_kv_attention_rows.cu)
+// the kernels for items of up to 32 query rows and of more (each with and without a window)
+cudaError_t launch_attention_cols(attn::AttnArgs &p, int dtype, const CUtensorMap &mk,
+                                  const CUtensorMap &mv, int ctas, char *ws, cudaStream_t stream);
 cudaError_t launch_attention_rows(attn::AttnArgs &p, int dtype, const CUtensorMap &mk,
                                   const CUtensorMap &mv, int ctas, char *ws, cudaStream_t stream);
+cudaError_t launch_window_cols(attn::AttnArgs &p, int dtype, const CUtensorMap &mk,
+                               const CUtensorMap &mv, int ctas, char *ws, cudaStream_t stream);
+cudaError_t launch_window_rows(attn::AttnArgs &p, int dtype, const CUtensorMap &mk,
+                               const CUtensorMap &mv, int ctas, char *ws, cudaStream_t stream);
 
 }  // namespace specv

@@ -153,3 +153,24 @@ def test_binding_refusals(sv):
 def test_status_texts(sv):
     assert "free page" in sv.spec_status_string(sv.SPEC_ERR_NO_PAGE)
     assert "given back" in sv.spec_status_string(sv.SPEC_ERR_REFS)
+
+
+def _window(sv, cache=None, **kw):
+    c = dict(table=FAKE, pps=4, lens=FAKE, new=None, B=2, N=3, q=FAKE, qs=512, qh=4, dtype=1, scale=0.1, mask=None,
+             window=10, sinks=2, out=FAKE, lse=None, status=FAKE, ws=FAKE, wsb=1 << 30, stream=None)
+    c.update(kw)
+    return sv.load_library().spec_kv_attention_window(cache or _cache(sv), *c.values())
+
+
+@pytest.mark.parametrize("bad,code", [
+    (dict(window=0), -2), (dict(window=-5), -2), (dict(sinks=-1), -2), (dict(mask=FAKE, window=2), -2),
+    (dict(dtype=0), -4), (dict(qh=3), -2), (dict(q=None), -1), (dict(out=None), -1), (dict(ws=None), -1),
+    (dict(wsb=16), -5), (dict(N=1025, mask=FAKE, window=2000), -2), (dict(scale=float("nan")), -2)])
+def test_window_refusals(sv, bad, code):
+    assert _window(sv, **bad) == code
+
+
+def test_window_of_a_tree_and_empty_batch(sv):
+    assert _window(sv, mask=FAKE, window=3, B=0, table=None, lens=None) == sv.SPEC_OK
+    with pytest.raises(ValueError, match="window"):
+        sv.kv_attention(None, None, None, None, sinks=3)
