@@ -224,7 +224,23 @@ __device__ __forceinline__ Pick warp_best(Pick p) {
 }
 __device__ __forceinline__ Pick no_pick() { return Pick{0, -INFINITY, 0x7fffffff, 0}; }
 
+constexpr int kBins = 1024, kMaxUnits = 512, kMaxCands = 512;
+constexpr int kStaged = 2048;   // units whose maxima are kept in shared memory
+
+// Bin of a distance d >= 0 from the best score: 32 bins an octave from 2^-8 to 2^24, what is nearer in the first
+// and what is farther in the last. A distance is known to 2^-22 of itself, a bin is 2^-5 wide, and no bin but
+// the first narrower than 2^-13: a candidate is in its bin or, where that matters, in the next, kSlack included.
+__device__ __forceinline__ int bin_of(float d) {
+  return min(max(static_cast<int>(__float_as_uint(d) >> 18) - ((127 - 8) << 5), 0), kBins - 1);
+}
+
 struct FinishShared {
+  float base[SPEC_MAX_BEAMS];      // how far a beam's best candidate is from the best of all
+  int hist[kBins], warp_count[kFinishWarps], edge, units, cands;
+  float staged[kStaged];
+  int unit_list[kMaxUnits];
+  Pick cand[kMaxCands];            // place: the token
+  int order[kMaxCands];
   double log_sum[SPEC_MAX_BEAMS];   // L_k less the row's largest logit
   float s[SPEC_MAX_BEAMS], top[SPEC_MAX_BEAMS];
   int kind[SPEC_MAX_BEAMS], precise[SPEC_MAX_BEAMS], wanted[SPEC_MAX_BEAMS];
@@ -273,52 +289,58 @@ struct Finish {
     sh.again = 1;
   }
 
-  // L_k from the unit sums, a warp a beam
+  // L_k from the unit sums, a warp a beam: a running sum against a power of two, kept where it is exact
   __device__ __forceinline__ void sums() const {
     for (int k = warp; k < a.K; k += kFinishWarps) {
       float s;
+      float m = -INFINITY;   // of the units so far
+      double t = 0.;         // their sum against the reference of m
       const int kind = beam_kind(a, b * a.K + k, s);
-      if (lane == 0) {
-        sh.kind[k] = kind;
-        sh.s[k] = s;
-        sh.precise[k] = kind != kLive;
-        sh.wanted[k] = 0;
-        sh.top[k] = 0.f;
-        sh.log_sum[k] = 0.;
-        if (kind == kBad) sh.bad = 1;
-      }
-      if (kind != kLive) continue;
-      float m = -INFINITY;
-      for (int c = lane; c < a.C; c += 32) m = fmax_nan(m, __uint_as_float(part(k * a.C + c).x));
-      m = key_float(__reduce_max_sync(0xffffffffu, float_key(m)));
-      if (m != m || m == -INFINITY) {
-        if (lane == 0) sh.bad = 1;
-        continue;
-      }
-      const bool plain = fabsf(m) < kPlainMax;
-      const float R = unit_ref(m);
-      double t = 0.;
-      for (int c = lane; c < a.C; c += 32) {
-        const uint2 w = part(k * a.C + c);
-        const float um = __uint_as_float(w.x);
-        const double us = static_cast<double>(__uint_as_float(w.y));
-        if (um == -INFINITY) continue;
-        if (plain && fabsf(um) < kPlainMax) {
-          const float e = unit_ref(um) - R;   // an integer
-          if (e > -1000.f) t += us * __longlong_as_double(static_cast<long long>(1023 + static_cast<int>(e)) << 52);
-        } else {
-          // from the unit's reference to its maximum, and from there to the row's
-          const double to_max = fabsf(um) < kPlainMax ? unit_ref(um) - um * kLog2ed : 0.;
-          t += us * exp2(to_max + (static_cast<double>(um) - m) * kLog2ed);
+      for (int c0 = 0; c0 < a.C; c0 += 4 * 32) {
+        uint2 w[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int c = c0 + u * 32 + lane;
+          w[u] = c < a.C ? part(k * a.C + c) : make_uint2(0xff800000u, 0u);
+          if (c < a.C && k * a.C + c < kStaged) sh.staged[k * a.C + c] = __uint_as_float(w[u].x);
         }
+        float top = m;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) top = fmax_nan(top, __uint_as_float(w[u].x));
+        top = key_float(__reduce_max_sync(0xffffffffu, float_key(top)));
+        t *= shift(m, top);
+        m = top;
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          t += static_cast<double>(__uint_as_float(w[u].y)) * shift(__uint_as_float(w[u].x), m);
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
       if (lane == 0) {
-        sh.top[k] = m;
-        sh.log_sum[k] = (plain ? R * kLn2d - m : 0.) + log(t);
+        const bool live = kind == kLive;
+        sh.kind[k] = kind;
+        sh.s[k] = s;
+        sh.precise[k] = !live;
+        sh.wanted[k] = 0;
+        sh.top[k] = live ? m : 0.f;
+        sh.log_sum[k] = live ? (fabsf(m) < kPlainMax ? unit_ref(m) * kLn2d - m : 0.) + log(t) : 0.;
+        if (kind == kBad || (live && !(fabsf(m) < INFINITY))) sh.bad = 1;
       }
     }
+  }
+  // What a sum against the reference of maximum m is multiplied by to be one against that of `to` (>= m).
+  static __device__ __forceinline__ double shift(float m, float to) {
+    if (m == -INFINITY) return 0.;
+    if (fabsf(m) < kPlainMax && fabsf(to) < kPlainMax) {
+      const float e = unit_ref(m) - unit_ref(to);   // an integer
+      return e > -1000.f ? __longlong_as_double(static_cast<long long>(1023 + static_cast<int>(e)) << 52) : 0.;
+    }
+    if (m == to) return 1.;
+    // from the reference to its maximum, and from there to the other (which is its own reference: it is
+    // larger in magnitude, or else both are below kPlainMax in it)
+    const double to_max = fabsf(m) < kPlainMax ? unit_ref(m) - m * kLog2ed : 0.;
+    const double from_max = fabsf(to) < kPlainMax ? unit_ref(to) - to * kLog2ed : 0.;
+    return exp2(to_max - from_max + (static_cast<double>(m) - to) * kLog2ed);
   }
 
   // L_k of one beam again, to about 1e-10, by the whole CTA
@@ -350,6 +372,160 @@ struct Finish {
       sh.wanted[k] = 0;
     }
     __syncthreads();
+  }
+
+  // The first bin up to which at least `n` of the counted things lie, to sh.edge (kBins - 1 if there are fewer).
+  __device__ __forceinline__ void find_edge(int n) const {
+    constexpr int kEach = kBins / kFinishThreads;
+    int c[kEach], mine = 0;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) mine += c[i] = sh.hist[tid * kEach + i];
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (lane == 31) sh.warp_count[warp] = incl;
+    if (tid == 0) sh.edge = kBins - 1;
+    __syncthreads();
+    int before = incl - mine;
+    for (int w = 0; w < warp; ++w) before += sh.warp_count[w];
+    if (before < n && before + mine >= n) {
+      int at = 0;
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        if (before < n) at = i;
+        before += c[i];
+      }
+      sh.edge = tid * kEach + at;
+    }
+    __syncthreads();
+  }
+  __device__ __forceinline__ void clear_hist() const {
+#pragma unroll
+    for (int i = 0; i < kBins / kFinishThreads; ++i) sh.hist[i * kFinishThreads + tid] = 0;
+    if (tid == 0) sh.units = sh.cands = 0;
+  }
+  // the distance of unit u's best candidate, negative if it has none
+  __device__ __forceinline__ float unit_distance(int u) const {
+    const int k = u / a.C, chunk = u - k * a.C, kind = sh.kind[k];
+    if (kind == kEnded) return chunk == 0 ? sh.base[k] : -1.f;
+    if (kind != kLive) return -1.f;
+    const float m = u < kStaged ? sh.staged[u] : __uint_as_float(part(u).x);
+    return m > -INFINITY ? sh.base[k] + (sh.top[k] - m) : -1.f;
+  }
+  __device__ __forceinline__ void push(int k, float l, int token) const {
+    const int i = atomicAdd(&sh.cands, 1);
+    if (i < kMaxCands)
+      sh.cand[i] = Pick{order_of(sh.kind[k] == kEnded ? static_cast<double>(sh.s[k]) : score(k, l)), l, k, token};
+  }
+  // calls f(k, l, token, distance) for the listed units' candidates with a distance of at most `most`
+  template <typename F>
+  __device__ __forceinline__ void each_token(float most, F f) const {
+    for (int i = warp; i < sh.units; i += kFinishWarps) {
+      const int u = sh.unit_list[i], k = u / a.C, chunk = u - k * a.C;
+      if (sh.kind[k] == kEnded) {
+        if (lane == 0) f(k, 0.f, a.pad, sh.base[k]);
+        continue;
+      }
+      const float base = sh.base[k], top = sh.top[k];
+      uint4 buf[kVPL];
+#pragma unroll
+      for (int v = 0; v < kVPL; ++v) buf[v] = load_group<E>(row(k), a.V, chunk * kUnitVecs + v * 32 + lane);
+#pragma unroll
+      for (int v = 0; v < kVPL; ++v) {
+        if (!(base + (top - vec_max<E>(buf[v])) <= most)) continue;
+#pragma unroll
+        for (int e = 0; e < Elem<E>::kPerVec; ++e) {
+          const float l = vec_elem<E>(buf[v], e), d = base + (top - l);
+          if (l > -INFINITY && d <= most) f(k, l, (chunk * kUnitVecs + v * 32 + lane) * Elem<E>::kPerVec + e, d);
+        }
+      }
+    }
+  }
+  static __device__ __forceinline__ float bin_end(int bin) {   // distances in it and below are less than this
+    return bin >= kBins - 1 ? INFINITY : __uint_as_float(static_cast<unsigned>(bin + 1 + ((127 - 8) << 5)) << 18);
+  }
+
+  // Where a few hundred candidates are all that can matter: finds them by their distances, and ranks them by
+  // counting. Returns 0 where there are more, 1 when done, -1 if sums have to be improved first.
+  __device__ int select_few() const {
+    if (tid < 32) {   // the best score of all, in 64 bits; distances are then sums of small numbers
+      double top = -INFINITY;
+      for (int k = lane; k < a.K; k += 32)
+        if (sh.kind[k] == kLive || sh.kind[k] == kEnded) top = fmax(top, static_cast<double>(sh.s[k]) - sh.log_sum[k]);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) top = fmax(top, __shfl_xor_sync(0xffffffffu, top, o));
+      for (int k = lane; k < a.K; k += 32)
+        sh.base[k] = static_cast<float>(top - (static_cast<double>(sh.s[k]) - sh.log_sum[k]));
+    }
+    clear_hist();
+    __syncthreads();
+    const int all = a.K * a.C;
+    for (int u = tid; u < all; u += kFinishThreads) {
+      const float d = unit_distance(u);
+      if (d >= 0.f) atomicAdd(&sh.hist[bin_of(d)], 1);
+    }
+    __syncthreads();
+    find_edge(a.n);
+    int edge = sh.edge;
+    for (int u = tid; u < all; u += kFinishThreads) {
+      const float d = unit_distance(u);
+      if (d >= 0.f && bin_of(d) <= edge + 1) {
+        const int i = atomicAdd(&sh.units, 1);
+        if (i < kMaxUnits) sh.unit_list[i] = u;
+      }
+    }
+    __syncthreads();
+    if (sh.units > kMaxUnits) return 0;
+    // With fewer units than candidates wanted, or with too many tokens in that range, the tokens' own distances
+    // give a nearer edge.
+    bool counted = edge == kBins - 1;
+    if (!counted) {
+      each_token(bin_end(edge + 1), [&](int k, float l, int t, float) { push(k, l, t); });
+      __syncthreads();
+      counted = sh.cands > kMaxCands;
+    }
+    if (counted) {
+      const int units = sh.units;
+      __syncthreads();
+      clear_hist();
+      __syncthreads();
+      if (tid == 0) sh.units = units;
+      __syncthreads();
+      each_token(bin_end(edge + 1), [&](int, float, int, float d) { atomicAdd(&sh.hist[bin_of(d)], 1); });
+      __syncthreads();
+      find_edge(a.n);
+      edge = sh.edge;
+      each_token(bin_end(edge + 1), [&](int k, float l, int t, float) { push(k, l, t); });
+      __syncthreads();
+      if (sh.cands > kMaxCands) return 0;
+    }
+    const int count = sh.cands;
+    if (tid < count) {
+      const Pick mine = sh.cand[tid];
+      int rank = 0;
+      for (int i = 0; i < count; ++i) rank += before(sh.cand[i], mine);
+      sh.order[rank] = tid;
+    }
+    __syncthreads();
+    const int found = min(count, a.n);
+    if (tid > 0 && tid < count) {   // with the one before it; those not chosen with the last chosen one
+      const Pick &p = sh.cand[sh.order[tid]], &q = sh.cand[sh.order[min(tid, a.n) - 1]];
+      compare(from_order(q.key), q.k, from_order(p.key), p.k);
+    }
+    __syncthreads();
+    if (sh.again) return -1;
+    for (int j = tid; j < a.n; j += kFinishThreads) {
+      const long long at = static_cast<long long>(b) * a.n + j;
+      const bool some = j < found;
+      const Pick p = some ? sh.cand[sh.order[j]] : no_pick();
+      a.tokens[at] = some ? p.at : -1;
+      a.parents[at] = some ? b * a.K + p.k : -1;
+      a.out_scores[at] = some ? static_cast<float>(from_order(p.key)) : -INFINITY;
+    }
+    return 1;
   }
 
   // the best of this thread's units that ranks after `last`
@@ -399,8 +575,10 @@ struct Finish {
     }
   }
 
-  // Chooses units and tokens, and writes the results; false if sums have to be improved first.
-  __device__ bool select() const {
+  // The same for any numbers of equal candidates: units and then tokens one by one, each the best of what is
+  // left. (16 of 8 beams: about 120 us more.) False if
+  // sums have to be improved first.
+  __device__ bool select_any() const {
     // the n first units by their largest candidates: the n best candidates lie in them
     Pick last{~0ull, 0.f, 0, 0};   // before all others
     Pick mine = next_unit(last);
@@ -497,7 +675,11 @@ __global__ void __launch_bounds__(kFinishThreads, 1) beam_finish_kernel(const __
     }
     return;
   }
-  while (!f.select()) {   // at most once a beam
+  for (;;) {   // at most once a beam, and once more
+    const int done = f.select_few();
+    if (done == 1) return;
+    __syncthreads();
+    if (done == 0 && f.select_any()) return;
     __syncthreads();
     if (tid == 0) sh.again = 0;
     for (int k = 0; k < a.K; ++k)
