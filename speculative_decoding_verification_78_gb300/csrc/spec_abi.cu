@@ -584,7 +584,8 @@ size_t spec_beam_workspace_bytes(int B, int K, int V, int dtype) {
   if (B < 0 || K < 1 || K > SPEC_MAX_BEAMS || V < 1 || V > SPEC_MAX_V ||
       (dtype != SPEC_F32 && dtype != SPEC_BF16))
     return 0;
-  return align256(static_cast<size_t>(B > 0 ? B : 1) * K * beam_chunks(V, dtype) * sizeof(uint2));
+  return align256(static_cast<size_t>(B > 0 ? B : 1) * K * beam_chunks(V, dtype) *
+                  (sizeof(float4) + sizeof(uint2)));
 }
 
 int spec_beam_select(const void *logits, int dtype, const float *scores, const int32_t *done,
@@ -615,7 +616,8 @@ int spec_beam_select(const void *logits, int dtype, const float *scores, const i
   a.parents = parents;
   a.out_scores = out_scores;
   a.status = status;
-  a.part = static_cast<uint2 *>(workspace);
+  a.quarters = static_cast<float4 *>(workspace);
+  a.part = reinterpret_cast<uint2 *>(a.quarters + units);
   a.B = B;
   a.K = K;
   a.V = V;

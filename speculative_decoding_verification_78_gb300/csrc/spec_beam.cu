@@ -106,8 +106,12 @@ __global__ void __launch_bounds__(256, 4) beam_stream_kernel(const __grid_consta
     uint4 buf[kVPL];
 #pragma unroll
     for (int j = 0; j < kVPL; ++j) buf[j] = load_group<E>(row, a.V, chunk * kUnitVecs + j * 32 + lane);
-    float m = unit_lane_max<E>(buf, -INFINITY, -INFINITY);
-    m = key_float(__reduce_max_sync(0xffffffffu, float_key(m)));
+    float quarter[4];   // maxima (NaN ranks highest)
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      quarter[q] = key_float(__reduce_max_sync(
+          0xffffffffu, float_key(fmax_nan(vec_max<E>(buf[2 * q]), vec_max<E>(buf[2 * q + 1])))));
+    float m = fmax_nan(fmax_nan(quarter[0], quarter[1]), fmax_nan(quarter[2], quarter[3]));
     float s = 0.f;
     if (m != -INFINITY) {
       f32x2 acc[4] = {pk2(0.f, 0.f), pk2(0.f, 0.f), pk2(0.f, 0.f), pk2(0.f, 0.f)};
@@ -139,7 +143,10 @@ __global__ void __launch_bounds__(256, 4) beam_stream_kernel(const __grid_consta
       for (int o = 16; o > 0; o >>= 1) s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, o));
       if (m == INFINITY) m = NAN;
     }
-    if (lane == 0) a.part[unit] = make_uint2(__float_as_uint(m), __float_as_uint(s));
+    if (lane == 0) {
+      a.part[unit] = make_uint2(__float_as_uint(m), __float_as_uint(s));
+      a.quarters[unit] = make_float4(quarter[0], quarter[1], quarter[2], quarter[3]);
+    }
   }
 }
 
@@ -187,7 +194,31 @@ __device__ __forceinline__ void exp_pair(float x, float M, float &hi, float &lo)
   lo = low * scale;
 }
 
+// log(n 2^-40) for n > 0, as a sum of two fp32 numbers, to about 1e-10: with n 2^-40 = x 2^e, x in [1, 2),
+// fp32's logarithm y of x, put right by x e^-y - 1, and e ln 2.
+__device__ __forceinline__ void log_pair(unsigned long long n, float &hi, float &lo) {
+  const int top = 63 - __clzll(static_cast<long long>(n));
+  const unsigned long long w = n << (63 - top);          // x 2^63
+  const float xh = __uint_as_float((127u << 23) | static_cast<uint32_t>((w >> 40) & 0x7fffffu));
+  const float xl = static_cast<float>(static_cast<uint32_t>(w >> 8)) * 0x1p-55f;   // its next 32 bits
+  const float y = logf(xh);
+  float eh, el;
+  exp_pair(-y, 0.f, eh, el);
+  const float p = __fmul_rn(xh, eh);   // near 1: p - 1 is exact
+  const float r = __fadd_rn(__fsub_rn(p, 1.f), __fmaf_rn(xh, el, __fmaf_rn(xl, eh, __fmaf_rn(xh, eh, -p))));
+  const float e = static_cast<float>(top - 40);
+  const float th = __fmul_rn(e, kLn2Hi);
+  hi = __fadd_rn(th, y);
+  const float bb = __fsub_rn(hi, th);
+  lo = __fadd_rn(__fadd_rn(__fsub_rn(th, __fsub_rn(hi, bb)), __fsub_rn(y, bb)),
+                 __fadd_rn(r, __fmaf_rn(e, kLn2Lo, __fmaf_rn(e, kLn2Hi, -th))));
+}
+
 // ------------------------------------------------------------------ selection
+//
+// What bounds the selection is the chain of its steps, and 64-bit floating point, of which an SM does two
+// operations a clock (a warp's instruction takes its scheduler 64): scores are taken in 64 bits for the few
+// hundred candidates only, L_k and distances in pairs of fp32 numbers.
 
 // doubles as integers in the same order (no NaN)
 __device__ __forceinline__ unsigned long long order_of(double x) {
@@ -224,7 +255,7 @@ __device__ __forceinline__ Pick warp_best(Pick p) {
 }
 __device__ __forceinline__ Pick no_pick() { return Pick{0, -INFINITY, 0x7fffffff, 0}; }
 
-constexpr int kBins = 1024, kMaxUnits = 512, kMaxCands = 512;
+constexpr int kBins = 1024, kMaxParts = 512, kMaxCands = 512;
 constexpr int kStaged = 2048;   // units whose maxima are kept in shared memory
 
 // Bin of a distance d >= 0 from the best score: 32 bins an octave from 2^-8 to 2^24, what is nearer in the first
@@ -236,12 +267,14 @@ __device__ __forceinline__ int bin_of(float d) {
 
 struct FinishShared {
   float base[SPEC_MAX_BEAMS];      // how far a beam's best candidate is from the best of all
-  int hist[kBins], warp_count[kFinishWarps], edge, units, cands;
+  int hist[kBins], warp_count[kFinishWarps], edge, parts, cands;
   float staged[kStaged];
-  int unit_list[kMaxUnits];
+  int part_list[kMaxParts];        // quarters of units: 4 unit + quarter
+  unsigned long long key[kMaxCands];
   Pick cand[kMaxCands];            // place: the token
   int order[kMaxCands];
   double log_sum[SPEC_MAX_BEAMS];   // L_k less the row's largest logit
+  float2 best_of[SPEC_MAX_BEAMS];   // a beam's best score: s - log_sum, in two words
   float s[SPEC_MAX_BEAMS], top[SPEC_MAX_BEAMS];
   int kind[SPEC_MAX_BEAMS], precise[SPEC_MAX_BEAMS], wanted[SPEC_MAX_BEAMS];
   Pick warp[kFinishWarps], best;
@@ -289,13 +322,14 @@ struct Finish {
     sh.again = 1;
   }
 
-  // L_k from the unit sums, a warp a beam: a running sum against a power of two, kept where it is exact
+  // L_k from the unit sums, a warp a beam. Sums against powers of two are added as whole multiples of 2^-40
+  // (a unit's is at most 2^12, and there are at most 2^10): exactly, but for what lies below that.
   __device__ __forceinline__ void sums() const {
     for (int k = warp; k < a.K; k += kFinishWarps) {
       float s;
-      float m = -INFINITY;   // of the units so far
-      double t = 0.;         // their sum against the reference of m
       const int kind = beam_kind(a, b * a.K + k, s);
+      float m = -INFINITY;          // of the units so far
+      unsigned long long t = 0;     // their sum against the power of two of m
       for (int c0 = 0; c0 < a.C; c0 += 4 * 32) {
         uint2 w[4];
 #pragma unroll
@@ -308,39 +342,77 @@ struct Finish {
 #pragma unroll
         for (int u = 0; u < 4; ++u) top = fmax_nan(top, __uint_as_float(w[u].x));
         top = key_float(__reduce_max_sync(0xffffffffu, float_key(top)));
-        t *= shift(m, top);
+        const float R = unit_ref(top);
+        t = scaled(t, unit_ref(m) - R);
         m = top;
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-          t += static_cast<double>(__uint_as_float(w[u].y)) * shift(__uint_as_float(w[u].x), m);
+        for (int u = 0; u < 4; ++u) {
+          const uint32_t bits = w[u].y;   // a sum in [2^-1, 2^12), or 0
+          const unsigned long long mant = static_cast<unsigned long long>((bits & 0x7fffffu) | 0x800000u);
+          const int e = static_cast<int>(bits >> 23) - 127 - 23 + 40;   // of its last bit, in units of 2^-40
+          if (bits) t += scaled(e >= 0 ? mant << min(e, 40) : mant >> min(-e, 63), unit_ref(__uint_as_float(w[u].x)) - R);
+        }
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+      const bool live = kind == kLive;
+      float h = 0.f, l = 0.f, top = 0.f;
+      if (live && m > 64.f - kPlainMax && m < kPlainMax) {   // (a unit below -kPlainMax adds nothing)
+        top = m;
+        log_pair(t, h, l);
+        // + R ln 2 - m, of which R ln 2 and m may be large and near each other
+        const float R = unit_ref(m), rh = __fmul_rn(R, kLn2Hi);
+        const float rl = __fmaf_rn(R, kLn2Lo, __fmaf_rn(R, kLn2Hi, -rh));
+        float d = rh, dl = rl;
+        pair_add(d, dl, -m, 0.f);
+        pair_add(h, l, d, dl);
+      } else if (live) {
+        top = m;
+        large_sum(k, m, h, l);
+      }
       if (lane == 0) {
-        const bool live = kind == kLive;
         sh.kind[k] = kind;
         sh.s[k] = s;
         sh.precise[k] = !live;
         sh.wanted[k] = 0;
-        sh.top[k] = live ? m : 0.f;
-        sh.log_sum[k] = live ? (fabsf(m) < kPlainMax ? unit_ref(m) * kLn2d - m : 0.) + log(t) : 0.;
+        set_sum(k, top, h, l);
         if (kind == kBad || (live && !(fabsf(m) < INFINITY))) sh.bad = 1;
       }
     }
   }
-  // What a sum against the reference of maximum m is multiplied by to be one against that of `to` (>= m).
-  static __device__ __forceinline__ double shift(float m, float to) {
-    if (m == -INFINITY) return 0.;
-    if (fabsf(m) < kPlainMax && fabsf(to) < kPlainMax) {
-      const float e = unit_ref(m) - unit_ref(to);   // an integer
-      return e > -1000.f ? __longlong_as_double(static_cast<long long>(1023 + static_cast<int>(e)) << 52) : 0.;
+  static __device__ __forceinline__ unsigned long long scaled(unsigned long long t, float e) {   // t 2^e, e <= 0
+    return e > -64.f ? t >> static_cast<int>(-e) : 0ull;
+  }
+  // (h, l) += (x, y), y and l small beside the others
+  static __device__ __forceinline__ void pair_add(float &h, float &l, float x, float y) {
+    const float t = __fadd_rn(h, x), bb = __fsub_rn(t, h);
+    l = __fadd_rn(__fadd_rn(__fsub_rn(h, __fsub_rn(t, bb)), __fsub_rn(x, bb)), __fadd_rn(l, y));
+    h = t;
+  }
+  __device__ __forceinline__ void set_sum(int k, float top, float h, float l) const {
+    sh.top[k] = top;
+    sh.log_sum[k] = static_cast<double>(h) + static_cast<double>(l);
+    float x = sh.s[k], y = 0.f;
+    pair_add(x, y, -h, -l);
+    const float z = __fadd_rn(x, y);   // the first word the sum rounded
+    sh.best_of[k] = make_float2(z, __fsub_rn(y, __fsub_rn(z, x)));
+  }
+  // log sum_v e^(l - m) of a row whose largest logit m is too large for powers of two, in 64 bits
+  __device__ __noinline__ void large_sum(int k, float m, float &h, float &l) const {
+    double t = 0.;
+    for (int c = lane; c < a.C; c += 32) {
+      const uint2 w = part(k * a.C + c);
+      const float um = __uint_as_float(w.x);
+      if (um == -INFINITY) continue;
+      // from the unit's reference to its maximum, and from there to the row's
+      const double to_max = fabsf(um) < kPlainMax ? unit_ref(um) - um * kLog2ed : 0.;
+      t += static_cast<double>(__uint_as_float(w.y)) * exp2(to_max + (static_cast<double>(um) - m) * kLog2ed);
     }
-    if (m == to) return 1.;
-    // from the reference to its maximum, and from there to the other (which is its own reference: it is
-    // larger in magnitude, or else both are below kPlainMax in it)
-    const double to_max = fabsf(m) < kPlainMax ? unit_ref(m) - m * kLog2ed : 0.;
-    const double from_max = fabsf(to) < kPlainMax ? unit_ref(to) - to * kLog2ed : 0.;
-    return exp2(to_max - from_max + (static_cast<double>(m) - to) * kLog2ed);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    const double x = log(t);
+    h = static_cast<float>(x);
+    l = static_cast<float>(x - h);
   }
 
   // L_k of one beam again, to about 1e-10, by the whole CTA
@@ -367,7 +439,9 @@ struct Finish {
     if (tid == 0) {
       double all = 0.;
       for (int w = 0; w < kFinishWarps; ++w) all += sh.sum[w];
-      sh.log_sum[k] = log(all);
+      const double x = log(all);
+      const float h = static_cast<float>(x);
+      set_sum(k, M, h, static_cast<float>(x - h));
       sh.precise[k] = 1;
       sh.wanted[k] = 0;
     }
@@ -405,7 +479,7 @@ struct Finish {
   __device__ __forceinline__ void clear_hist() const {
 #pragma unroll
     for (int i = 0; i < kBins / kFinishThreads; ++i) sh.hist[i * kFinishThreads + tid] = 0;
-    if (tid == 0) sh.units = sh.cands = 0;
+    if (tid == 0) sh.parts = sh.cands = 0;
   }
   // the distance of unit u's best candidate, negative if it has none
   __device__ __forceinline__ float unit_distance(int u) const {
@@ -417,29 +491,44 @@ struct Finish {
   }
   __device__ __forceinline__ void push(int k, float l, int token) const {
     const int i = atomicAdd(&sh.cands, 1);
-    if (i < kMaxCands)
-      sh.cand[i] = Pick{order_of(sh.kind[k] == kEnded ? static_cast<double>(sh.s[k]) : score(k, l)), l, k, token};
+    if (i < kMaxCands) sh.cand[i] = Pick{0, l, k, token};   // its score comes later
   }
-  // calls f(k, l, token, distance) for the listed units' candidates with a distance of at most `most`
+  // calls f(k, l, token, distance) for the listed quarters' candidates with a distance of at most `most`
   template <typename F>
   __device__ __forceinline__ void each_token(float most, F f) const {
-    for (int i = warp; i < sh.units; i += kFinishWarps) {
-      const int u = sh.unit_list[i], k = u / a.C, chunk = u - k * a.C;
-      if (sh.kind[k] == kEnded) {
-        if (lane == 0) f(k, 0.f, a.pad, sh.base[k]);
-        continue;
+    constexpr int kAhead = 4;   // quarters of a warp whose loads are on their way together
+    for (int i0 = warp; i0 < sh.parts; i0 += kAhead * kFinishWarps) {
+      uint4 buf[kAhead][2];
+      int part_of[kAhead];
+#pragma unroll
+      for (int q = 0; q < kAhead; ++q) {
+        const int i = i0 + q * kFinishWarps;
+        part_of[q] = i < sh.parts ? sh.part_list[i] : -1;
+        if (part_of[q] < 0) continue;
+        const int u = part_of[q] >> 2, k = u / a.C, chunk = u - k * a.C;
+        const int g = chunk * kUnitVecs + (part_of[q] & 3) * 64 + lane;
+        if (sh.kind[k] == kEnded) continue;
+#pragma unroll
+        for (int v = 0; v < 2; ++v) buf[q][v] = load_group<E>(row(k), a.V, g + v * 32);
       }
-      const float base = sh.base[k], top = sh.top[k];
-      uint4 buf[kVPL];
 #pragma unroll
-      for (int v = 0; v < kVPL; ++v) buf[v] = load_group<E>(row(k), a.V, chunk * kUnitVecs + v * 32 + lane);
+      for (int q = 0; q < kAhead; ++q) {
+        if (part_of[q] < 0) continue;
+        const int u = part_of[q] >> 2, k = u / a.C, chunk = u - k * a.C;
+        const int g = chunk * kUnitVecs + (part_of[q] & 3) * 64 + lane;
+        const float base = sh.base[k], top = sh.top[k];
+        if (sh.kind[k] == kEnded) {
+          if (lane == 0) f(k, 0.f, a.pad, base);
+          continue;
+        }
 #pragma unroll
-      for (int v = 0; v < kVPL; ++v) {
-        if (!(base + (top - vec_max<E>(buf[v])) <= most)) continue;
+        for (int v = 0; v < 2; ++v) {
+          if (!(base + (top - vec_max<E>(buf[q][v])) <= most)) continue;
 #pragma unroll
-        for (int e = 0; e < Elem<E>::kPerVec; ++e) {
-          const float l = vec_elem<E>(buf[v], e), d = base + (top - l);
-          if (l > -INFINITY && d <= most) f(k, l, (chunk * kUnitVecs + v * 32 + lane) * Elem<E>::kPerVec + e, d);
+          for (int e = 0; e < Elem<E>::kPerVec; ++e) {
+            const float l = vec_elem<E>(buf[q][v], e), d = base + (top - l);
+            if (l > -INFINITY && d <= most) f(k, l, (g + v * 32) * Elem<E>::kPerVec + e, d);
+          }
         }
       }
     }
@@ -448,17 +537,22 @@ struct Finish {
     return bin >= kBins - 1 ? INFINITY : __uint_as_float(static_cast<unsigned>(bin + 1 + ((127 - 8) << 5)) << 18);
   }
 
+  static __device__ __forceinline__ float2 larger(float2 x, float2 y) {
+    return y.x > x.x || (y.x == x.x && y.y > x.y) ? y : x;
+  }
+
   // Where a few hundred candidates are all that can matter: finds them by their distances, and ranks them by
   // counting. Returns 0 where there are more, 1 when done, -1 if sums have to be improved first.
   __device__ int select_few() const {
-    if (tid < 32) {   // the best score of all, in 64 bits; distances are then sums of small numbers
-      double top = -INFINITY;
+    if (tid < 32) {   // the best score of all, in two words; distances are then sums of small numbers
+      float2 top = make_float2(-INFINITY, 0.f);
       for (int k = lane; k < a.K; k += 32)
-        if (sh.kind[k] == kLive || sh.kind[k] == kEnded) top = fmax(top, static_cast<double>(sh.s[k]) - sh.log_sum[k]);
+        if (sh.kind[k] == kLive || sh.kind[k] == kEnded) top = larger(top, sh.best_of[k]);
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = fmax(top, __shfl_xor_sync(0xffffffffu, top, o));
+      for (int o = 16; o > 0; o >>= 1)
+        top = larger(top, make_float2(__shfl_xor_sync(0xffffffffu, top.x, o), __shfl_xor_sync(0xffffffffu, top.y, o)));
       for (int k = lane; k < a.K; k += 32)
-        sh.base[k] = static_cast<float>(top - (static_cast<double>(sh.s[k]) - sh.log_sum[k]));
+        sh.base[k] = __fadd_rn(__fsub_rn(top.x, sh.best_of[k].x), __fsub_rn(top.y, sh.best_of[k].y));
     }
     clear_hist();
     __syncthreads();
@@ -470,31 +564,44 @@ struct Finish {
     __syncthreads();
     find_edge(a.n);
     int edge = sh.edge;
+    const float most = bin_end(edge + 1);
     for (int u = tid; u < all; u += kFinishThreads) {
       const float d = unit_distance(u);
-      if (d >= 0.f && bin_of(d) <= edge + 1) {
-        const int i = atomicAdd(&sh.units, 1);
-        if (i < kMaxUnits) sh.unit_list[i] = u;
+      if (!(d >= 0.f && d <= most)) continue;
+      const int k = u / a.C;
+      if (sh.kind[k] == kEnded) {
+        const int i = atomicAdd(&sh.parts, 1);
+        if (i < kMaxParts) sh.part_list[i] = 4 * u;
+        continue;
+      }
+      const float4 m = __ldcg(a.quarters + static_cast<long long>(b) * all + u);
+      const float base = sh.base[k], top = sh.top[k];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float x = q == 0 ? m.x : q == 1 ? m.y : q == 2 ? m.z : m.w;
+        if (x == -INFINITY || !(base + (top - x) <= most)) continue;
+        const int i = atomicAdd(&sh.parts, 1);
+        if (i < kMaxParts) sh.part_list[i] = 4 * u + q;
       }
     }
     __syncthreads();
-    if (sh.units > kMaxUnits) return 0;
+    if (sh.parts > kMaxParts) return 0;
     // With fewer units than candidates wanted, or with too many tokens in that range, the tokens' own distances
     // give a nearer edge.
     bool counted = edge == kBins - 1;
     if (!counted) {
-      each_token(bin_end(edge + 1), [&](int k, float l, int t, float) { push(k, l, t); });
+      each_token(most, [&](int k, float l, int t, float) { push(k, l, t); });
       __syncthreads();
       counted = sh.cands > kMaxCands;
     }
     if (counted) {
-      const int units = sh.units;
+      const int parts = sh.parts;
       __syncthreads();
       clear_hist();
       __syncthreads();
-      if (tid == 0) sh.units = units;
+      if (tid == 0) sh.parts = parts;
       __syncthreads();
-      each_token(bin_end(edge + 1), [&](int, float, int, float d) { atomicAdd(&sh.hist[bin_of(d)], 1); });
+      each_token(most, [&](int, float, int, float d) { atomicAdd(&sh.hist[bin_of(d)], 1); });
       __syncthreads();
       find_edge(a.n);
       edge = sh.edge;
@@ -503,10 +610,23 @@ struct Finish {
       if (sh.cands > kMaxCands) return 0;
     }
     const int count = sh.cands;
+    Pick mine = no_pick();
     if (tid < count) {
-      const Pick mine = sh.cand[tid];
-      int rank = 0;
-      for (int i = 0; i < count; ++i) rank += before(sh.cand[i], mine);
+      mine = sh.cand[tid];
+      mine.key = order_of(sh.kind[mine.k] == kEnded ? static_cast<double>(sh.s[mine.k]) : score(mine.k, mine.l));
+      sh.cand[tid].key = sh.key[tid] = mine.key;
+    }
+    __syncthreads();
+    if (tid < count) {
+      int rank = 0, equal = 0;
+#pragma unroll 8
+      for (int i = 0; i < count; ++i) {
+        const unsigned long long key = sh.key[i];
+        rank += key > mine.key;
+        equal += key == mine.key;
+      }
+      if (equal > 1)
+        for (int i = 0; i < count; ++i) rank += sh.key[i] == mine.key && before(sh.cand[i], mine);
       sh.order[rank] = tid;
     }
     __syncthreads();

@@ -17,6 +17,7 @@ struct BeamArgs {
   float *out_scores;       // [B, n]
   int32_t *status;
   uint2 *part;             // [B * K * C] (maximum, sum) of each unit
+  float4 *quarters;        // [B * K * C] the maxima of its quarters
   int B, K, V, C, n, pad;
   int units;               // B * K * C
 };

@@ -210,6 +210,17 @@ def test_extreme_logits(sv):
     check(sv, logits, scores, 7)
 
 
+def test_units_of_both_kinds(sv):
+    """Rows whose units' maxima lie on both sides of the magnitude from which fractions are lost (2^20)."""
+    rng = np.random.default_rng(11)
+    logits, scores = some(rng, 8, 2, 5000, torch.float32)
+    step = torch.linspace(-1, 1, 5000, device="cuda")
+    for b, (mid, spread) in enumerate([(-2.0 ** 20, 1), (-2.0 ** 20, 30), (-2.0 ** 20, 70), (-2.0 ** 20, 200),
+                                       (2.0 ** 20, 1), (2.0 ** 20, 30), (2.0 ** 20, 200), (0, 2.0 ** 20)]):
+        logits[b] = mid + spread * step + logits[b] * 0.1
+    check(sv, logits, scores, 5)
+
+
 def test_deterministic_and_workspace_contents(sv):
     rng = np.random.default_rng(9)
     logits, scores = some(rng, 4, 8, 20011, torch.bfloat16)
