@@ -22,14 +22,14 @@ namespace {
 constexpr int kFinishThreads = 512, kFinishWarps = kFinishThreads / 32;
 constexpr float kLog2eHi = 0x1.715476p+0f, kLog2eLo = 0x1.4ae0cp-26f;   // their sum: log2(e) to 2^-50
 constexpr float kLn2Hi = 0x1.62e43p-1f, kLn2Lo = -0x1.05c61p-29f;       // their sum: ln 2 to 2^-53
-constexpr double kLn2d = 0.69314718055994530942, kLog2ed = 1.44269504088896340736;
+constexpr double kLog2ed = 1.44269504088896340736;
 // A unit whose maximum is below this in magnitude is summed against the integer R above its maximum's
 // logarithm: 2^(l log2 e - R), so that units are joined by powers of two. Beyond it (where R would not be an
 // exact fp32 integer with room for a fraction) against its maximum itself.
 constexpr float kPlainMax = 1048576.f;
 // Twice the bound of an fp32 sum's relative error: 2^-22 of ex2; two roundings of the exponent, 2^-24 |t| ln 2
 // each, |t| at most 21 on average (log2 of the largest vocabulary, and one); 25 roundings of sums.
-constexpr double kSlack = 8e-6;
+constexpr float kSlack = 8e-6f;
 
 __device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
   f32x2 r;
@@ -39,20 +39,17 @@ __device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
 
 // ------------------------------------------------------------------ reading a row by token numbers
 
-// Elements g * EPV .. of the row as one vector, -inf past its end. Whole vectors of an unaligned row are put
-// together from the two aligned ones they lie in, where both lie inside the row.
+// Elements e0 .. of the row as one vector, -inf past its end, where that is not a whole aligned vector: one of
+// an unaligned row is put together from the two aligned ones it lies in, if both lie inside the row.
 template <typename E>
-__device__ __forceinline__ uint4 load_group(const E *row, int V, int g) {
+__device__ __noinline__ uint4 load_uneven(const E *row, int V, int e0) {
   constexpr int kEPV = Elem<E>::kPerVec;
-  const int e0 = g * kEPV;
   const uint32_t ni = Elem<E>::kNegInfWord;
-  uint4 r = make_uint4(ni, ni, ni, ni);
-  if (e0 >= V) return r;
+  uint32_t r[4] = {ni, ni, ni, ni};
+  if (e0 >= V) return make_uint4(ni, ni, ni, ni);
   const E *at = row + e0;
   const unsigned mis = static_cast<unsigned>(reinterpret_cast<uintptr_t>(row) & 15u);
-  if (mis == 0) {
-    if (e0 + kEPV <= V) return ld_stream(reinterpret_cast<const uint4 *>(at));
-  } else if (e0 > 0 && e0 + 2 * kEPV <= V) {
+  if (mis != 0 && e0 > 0 && e0 + 2 * kEPV <= V) {
     const uint4 *p = reinterpret_cast<const uint4 *>(reinterpret_cast<uintptr_t>(at) - mis);
     const uint4 a = __ldg(p), b = __ldg(p + 1);
     uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
@@ -66,17 +63,29 @@ __device__ __forceinline__ uint4 load_group(const E *row, int V, int g) {
     return make_uint4(__funnelshift_r(w[0], w[1], sh), __funnelshift_r(w[1], w[2], sh),
                       __funnelshift_r(w[2], w[3], sh), __funnelshift_r(w[3], w[4], sh));
   }
-  uint32_t w[4] = {ni, ni, ni, ni};
 #pragma unroll
   for (int e = 0; e < kEPV; ++e)
     if (e0 + e < V) {
       const uint32_t bits = __float_as_uint(ld_elem<E>(at + e));
       if (sizeof(E) == 4)
-        w[e] = bits;
+        r[e] = bits;
       else
-        w[e / 2] = (e & 1) ? (w[e / 2] & 0xffffu) | (bits & 0xffff0000u) : (w[e / 2] & 0xffff0000u) | (bits >> 16);
+        r[e / 2] = (e & 1) ? (r[e / 2] & 0xffffu) | (bits & 0xffff0000u) : (r[e / 2] & 0xffff0000u) | (bits >> 16);
     }
-  return make_uint4(w[0], w[1], w[2], w[3]);
+  return make_uint4(r[0], r[1], r[2], r[3]);
+}
+// Vectors g, g + 32, ... of the row: the whole ones first, whose loads are on their way together.
+template <typename E, int kN>
+__device__ __forceinline__ void load_groups(const E *row, int V, int g, uint4 (&buf)[kN]) {
+  constexpr int kEPV = Elem<E>::kPerVec;
+  const bool even = (reinterpret_cast<uintptr_t>(row) & 15u) == 0;
+#pragma unroll
+  for (int j = 0; j < kN; ++j)
+    if (even && (g + 32 * j + 1) * kEPV <= V) buf[j] = ld_stream(reinterpret_cast<const uint4 *>(row) + g + 32 * j);
+  if (even && (g + 32 * (kN - 1) + 1) * kEPV <= V) return;
+#pragma unroll
+  for (int j = 0; j < kN; ++j)
+    if (!even || (g + 32 * j + 1) * kEPV > V) buf[j] = load_uneven<E>(row, V, (g + 32 * j) * kEPV);
 }
 
 // What a beam contributes: nothing (score -inf), one candidate (at its end), or its row.
@@ -104,8 +113,7 @@ __global__ void __launch_bounds__(256, 4) beam_stream_kernel(const __grid_consta
     if (!SPEC_CHECK(a, row_i < a.B * a.K && chunk < a.C)) continue;
     const E *row = static_cast<const E *>(a.logits) + static_cast<long long>(row_i) * a.V;
     uint4 buf[kVPL];
-#pragma unroll
-    for (int j = 0; j < kVPL; ++j) buf[j] = load_group<E>(row, a.V, chunk * kUnitVecs + j * 32 + lane);
+    load_groups<E>(row, a.V, chunk * kUnitVecs + lane, buf);
     float quarter[4];   // maxima (NaN ranks highest)
 #pragma unroll
     for (int q = 0; q < 4; ++q)
@@ -220,13 +228,23 @@ __device__ __forceinline__ void log_pair(unsigned long long n, float &hi, float 
 // operations a clock (a warp's instruction takes its scheduler 64): scores are taken in 64 bits for the few
 // hundred candidates only, L_k and distances in pairs of fp32 numbers.
 
-// doubles as integers in the same order (no NaN)
-__device__ __forceinline__ unsigned long long order_of(double x) {
-  const unsigned long long b = static_cast<unsigned long long>(__double_as_longlong(x + 0.0));
-  return b >> 63 ? ~b : b | (1ull << 63);
+// A score: two fp32 numbers, the first the sum rounded, the second what that left; as an integer in the same order
+// (no NaN; never 0).
+__device__ __forceinline__ unsigned long long order_of(float2 x) {
+  return static_cast<unsigned long long>(float_key(__fadd_rn(x.x, 0.f))) << 32 | float_key(__fadd_rn(x.y, 0.f));
 }
-__device__ __forceinline__ double from_order(unsigned long long k) {
-  return __longlong_as_double(static_cast<long long>(k >> 63 ? k & ~(1ull << 63) : ~k));
+__device__ __forceinline__ float2 from_order(unsigned long long k) {
+  return make_float2(key_float(static_cast<unsigned>(k >> 32)), key_float(static_cast<unsigned>(k)));
+}
+// (h, l) += (x, y), y and l small beside the others
+__device__ __forceinline__ void pair_add(float &h, float &l, float x, float y) {
+  const float t = __fadd_rn(h, x), bb = __fsub_rn(t, h);
+  l = __fadd_rn(__fadd_rn(__fsub_rn(h, __fsub_rn(t, bb)), __fsub_rn(x, bb)), __fadd_rn(l, y));
+  h = t;
+}
+__device__ __forceinline__ float2 pair_of(float h, float l) {   // the first word the sum rounded
+  const float z = __fadd_rn(h, l);
+  return make_float2(z, __fsub_rn(l, __fsub_rn(z, h)));
 }
 
 // A candidate: its score (as order_of; 0: none), beam, logit and place in the beam. Equal scores go by beam;
@@ -267,13 +285,13 @@ __device__ __forceinline__ int bin_of(float d) {
 
 struct FinishShared {
   float base[SPEC_MAX_BEAMS];      // how far a beam's best candidate is from the best of all
-  int hist[kBins], warp_count[kFinishWarps], edge, parts, cands;
+  __align__(16) int hist[kBins];
+  int edge, parts, cands;
   float staged[kStaged];
   int part_list[kMaxParts];        // quarters of units: 4 unit + quarter
-  unsigned long long key[kMaxCands];
+  ulonglong2 key[kMaxCands];
   Pick cand[kMaxCands];            // place: the token
   int order[kMaxCands];
-  double log_sum[SPEC_MAX_BEAMS];   // L_k less the row's largest logit
   float2 best_of[SPEC_MAX_BEAMS];   // a beam's best score: s - log_sum, in two words
   float s[SPEC_MAX_BEAMS], top[SPEC_MAX_BEAMS];
   int kind[SPEC_MAX_BEAMS], precise[SPEC_MAX_BEAMS], wanted[SPEC_MAX_BEAMS];
@@ -301,7 +319,7 @@ struct Finish {
     const int k = u / a.C, chunk = u - k * a.C;
     Pick p{0, 0.f, k, chunk};
     if (sh.kind[k] == kEnded) {
-      if (chunk == 0) p.key = order_of(sh.s[k]);
+      if (chunk == 0) p.key = order_of(sh.best_of[k]);
     } else if (sh.kind[k] == kLive) {
       const float m = __uint_as_float(part(u).x);
       p.l = m;
@@ -309,14 +327,21 @@ struct Finish {
     }
     return p;
   }
-  __device__ __forceinline__ double score(int k, float l) const {
-    return static_cast<double>(sh.s[k]) + ((static_cast<double>(l) - sh.top[k]) - sh.log_sum[k]);
+  // the score of a live beam's candidate with logit l
+  __device__ __forceinline__ float2 score(int k, float l) const {
+    float d = l, dl = 0.f;
+    pair_add(d, dl, -sh.top[k], 0.f);
+    if (!(d > -INFINITY)) return make_float2(-INFINITY, 0.f);   // beyond fp32
+    const float2 best = sh.best_of[k];
+    pair_add(d, dl, best.x, best.y);
+    return pair_of(d, dl);
   }
   // two candidates whose order the sums as they are do not tell: asks for better ones
-  __device__ __forceinline__ void compare(double x, int k, double y, int j) const {
+  __device__ __forceinline__ void compare(unsigned long long x, int k, unsigned long long y, int j) const {
     if (k == j || (sh.precise[k] && sh.precise[j])) return;
-    const double gap = fabs(x - y);
-    if (gap == 0. || gap > kSlack) return;   // (0: beams with the same logits and scores)
+    const float2 u = from_order(x), v = from_order(y);
+    const float gap = fabsf(__fadd_rn(__fsub_rn(u.x, v.x), __fsub_rn(u.y, v.y)));
+    if (!(gap > 0.f && gap <= kSlack)) return;   // (0: beams with the same logits and scores)
     if (!sh.precise[k]) sh.wanted[k] = 1;
     if (!sh.precise[j]) sh.wanted[j] = 1;
     sh.again = 1;
@@ -383,19 +408,11 @@ struct Finish {
   static __device__ __forceinline__ unsigned long long scaled(unsigned long long t, float e) {   // t 2^e, e <= 0
     return e > -64.f ? t >> static_cast<int>(-e) : 0ull;
   }
-  // (h, l) += (x, y), y and l small beside the others
-  static __device__ __forceinline__ void pair_add(float &h, float &l, float x, float y) {
-    const float t = __fadd_rn(h, x), bb = __fsub_rn(t, h);
-    l = __fadd_rn(__fadd_rn(__fsub_rn(h, __fsub_rn(t, bb)), __fsub_rn(x, bb)), __fadd_rn(l, y));
-    h = t;
-  }
   __device__ __forceinline__ void set_sum(int k, float top, float h, float l) const {
     sh.top[k] = top;
-    sh.log_sum[k] = static_cast<double>(h) + static_cast<double>(l);
     float x = sh.s[k], y = 0.f;
     pair_add(x, y, -h, -l);
-    const float z = __fadd_rn(x, y);   // the first word the sum rounded
-    sh.best_of[k] = make_float2(z, __fsub_rn(y, __fsub_rn(z, x)));
+    sh.best_of[k] = pair_of(x, y);
   }
   // log sum_v e^(l - m) of a row whose largest logit m is too large for powers of two, in 64 bits
   __device__ __noinline__ void large_sum(int k, float m, float &h, float &l) const {
@@ -420,11 +437,12 @@ struct Finish {
     const float M = sh.top[k];
     float h = 0.f, l = 0.f;
     for (int g = tid; g * Elem<E>::kPerVec < a.V; g += kFinishThreads) {
-      const uint4 v = load_group<E>(row(k), a.V, g);
+      uint4 v[1];
+      load_groups<E>(row(k), a.V, g, v);
 #pragma unroll
       for (int e = 0; e < Elem<E>::kPerVec; ++e) {
         float xh, xl;
-        exp_pair(vec_elem<E>(v, e), M, xh, xl);
+        exp_pair(vec_elem<E>(v[0], e), M, xh, xl);
         const float s = __fadd_rn(h, xh), bb = __fsub_rn(s, h);
         l = __fadd_rn(l, __fadd_rn(__fadd_rn(__fsub_rn(h, __fsub_rn(s, bb)), __fsub_rn(xh, bb)), xl));
         h = s;
@@ -450,29 +468,45 @@ struct Finish {
 
   // The first bin up to which at least `n` of the counted things lie, to sh.edge (kBins - 1 if there are fewer).
   __device__ __forceinline__ void find_edge(int n) const {
-    constexpr int kEach = kBins / kFinishThreads;
-    int c[kEach], mine = 0;
+    if (warp == 0) {
+      constexpr int kChunks = kBins / 128;   // a lane has four bins of each
+      int4 c[kChunks];
+      int sum[kChunks];
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) mine += c[i] = sh.hist[tid * kEach + i];
-    int incl = mine;
+      for (int i = 0; i < kChunks; ++i) c[i] = reinterpret_cast<const int4 *>(sh.hist)[i * 32 + lane];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
-    }
-    if (lane == 31) sh.warp_count[warp] = incl;
-    if (tid == 0) sh.edge = kBins - 1;
-    __syncthreads();
-    int before = incl - mine;
-    for (int w = 0; w < warp; ++w) before += sh.warp_count[w];
-    if (before < n && before + mine >= n) {
-      int at = 0;
+      for (int i = 0; i < kChunks; ++i) sum[i] = __reduce_add_sync(0xffffffffu, c[i].x + c[i].y + c[i].z + c[i].w);
+      int before = 0, at = -1;
+      int4 mine = make_int4(0, 0, 0, 0);
 #pragma unroll
-      for (int i = 0; i < kEach; ++i) {
-        if (before < n) at = i;
-        before += c[i];
+      for (int i = 0; i < kChunks; ++i)
+        if (at < 0) {
+          if (before + sum[i] >= n) {
+            at = i;
+            mine = c[i];
+          } else {
+            before += sum[i];
+          }
+        }
+      if (at < 0) {
+        if (lane == 0) sh.edge = kBins - 1;
+      } else {
+        const int all = mine.x + mine.y + mine.z + mine.w;
+        int incl = all;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += y;
+        }
+        int x = before + incl - all;
+        if (x < n && x + all >= n) {
+          int e = at * 128 + lane * 4;
+          if ((x += mine.x) < n) ++e;
+          if (x < n && (x += mine.y) < n) ++e;
+          if (x < n && (x += mine.z) < n) ++e;
+          sh.edge = e;
+        }
       }
-      sh.edge = tid * kEach + at;
     }
     __syncthreads();
   }
@@ -493,45 +527,63 @@ struct Finish {
     const int i = atomicAdd(&sh.cands, 1);
     if (i < kMaxCands) sh.cand[i] = Pick{0, l, k, token};   // its score comes later
   }
-  // calls f(k, l, token, distance) for the listed quarters' candidates with a distance of at most `most`
-  template <typename F>
-  __device__ __forceinline__ void each_token(float most, F f) const {
-    constexpr int kAhead = 4;   // quarters of a warp whose loads are on their way together
+  // Lists (or, with `count`, counts by their distances) the listed quarters' candidates with a distance of at
+  // most `most`.
+  __device__ __noinline__ void each_token(float most, bool count) const {
+    constexpr int kAhead = 2;   // quarters of a warp whose loads are on their way together
     for (int i0 = warp; i0 < sh.parts; i0 += kAhead * kFinishWarps) {
       uint4 buf[kAhead][2];
-      int part_of[kAhead];
+      int beam[kAhead], token[kAhead];
 #pragma unroll
       for (int q = 0; q < kAhead; ++q) {
         const int i = i0 + q * kFinishWarps;
-        part_of[q] = i < sh.parts ? sh.part_list[i] : -1;
-        if (part_of[q] < 0) continue;
-        const int u = part_of[q] >> 2, k = u / a.C, chunk = u - k * a.C;
-        const int g = chunk * kUnitVecs + (part_of[q] & 3) * 64 + lane;
+        beam[q] = -1;
+        if (i >= sh.parts) continue;
+        const int part = sh.part_list[i], k = (part >> 2) / a.C;
+        const int g = ((part >> 2) - k * a.C) * kUnitVecs + (part & 3) * 64 + lane;
+        beam[q] = k;
+        token[q] = g * Elem<E>::kPerVec;
         if (sh.kind[k] == kEnded) continue;
-#pragma unroll
-        for (int v = 0; v < 2; ++v) buf[q][v] = load_group<E>(row(k), a.V, g + v * 32);
+        load_groups<E>(row(k), a.V, g, buf[q]);
       }
 #pragma unroll
       for (int q = 0; q < kAhead; ++q) {
-        if (part_of[q] < 0) continue;
-        const int u = part_of[q] >> 2, k = u / a.C, chunk = u - k * a.C;
-        const int g = chunk * kUnitVecs + (part_of[q] & 3) * 64 + lane;
+        const int k = beam[q];
+        if (k < 0) continue;
         const float base = sh.base[k], top = sh.top[k];
-        if (sh.kind[k] == kEnded) {
-          if (lane == 0) f(k, 0.f, a.pad, base);
-          continue;
+        const bool ended = sh.kind[k] == kEnded;
+        if (ended && lane == 0) {
+          if (count)
+            atomicAdd(&sh.hist[bin_of(base)], 1);
+          else
+            push(k, 0.f, a.pad);
         }
 #pragma unroll
         for (int v = 0; v < 2; ++v) {
-          if (!(base + (top - vec_max<E>(buf[q][v])) <= most)) continue;
+          if (ended || !(base + (top - vec_max<E>(buf[q][v])) <= most)) continue;
+          unsigned near = 0;
 #pragma unroll
           for (int e = 0; e < Elem<E>::kPerVec; ++e) {
-            const float l = vec_elem<E>(buf[q][v], e), d = base + (top - l);
-            if (l > -INFINITY && d <= most) f(k, l, (g + v * 32) * Elem<E>::kPerVec + e, d);
+            const float l = vec_elem<E>(buf[q][v], e);
+            if (l > -INFINITY && base + (top - l) <= most) near |= 1u << e;
+          }
+#pragma unroll 1
+          for (; near; near &= near - 1) {
+            const int e = __ffs(near) - 1;
+            const float l = element(buf[q][v], e);
+            if (count)
+              atomicAdd(&sh.hist[bin_of(base + (top - l))], 1);
+            else
+              push(k, l, token[q] + v * 32 * Elem<E>::kPerVec + e);
           }
         }
       }
     }
+  }
+  static __device__ __forceinline__ float element(const uint4 &v, int e) {   // e not known when compiled
+    const int i = sizeof(E) == 4 ? e : e >> 1;
+    const uint32_t w = i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+    return sizeof(E) == 4 ? __uint_as_float(w) : (e & 1) ? bf_hi(w) : bf_lo(w);
   }
   static __device__ __forceinline__ float bin_end(int bin) {   // distances in it and below are less than this
     return bin >= kBins - 1 ? INFINITY : __uint_as_float(static_cast<unsigned>(bin + 1 + ((127 - 8) << 5)) << 18);
@@ -590,7 +642,7 @@ struct Finish {
     // give a nearer edge.
     bool counted = edge == kBins - 1;
     if (!counted) {
-      each_token(most, [&](int k, float l, int t, float) { push(k, l, t); });
+      each_token(most, false);
       __syncthreads();
       counted = sh.cands > kMaxCands;
     }
@@ -601,39 +653,39 @@ struct Finish {
       __syncthreads();
       if (tid == 0) sh.parts = parts;
       __syncthreads();
-      each_token(most, [&](int, float, int, float d) { atomicAdd(&sh.hist[bin_of(d)], 1); });
+      each_token(most, true);
       __syncthreads();
       find_edge(a.n);
       edge = sh.edge;
-      each_token(bin_end(edge + 1), [&](int k, float l, int t, float) { push(k, l, t); });
+      each_token(bin_end(edge + 1), false);
       __syncthreads();
       if (sh.cands > kMaxCands) return 0;
     }
     const int count = sh.cands;
-    Pick mine = no_pick();
+    ulonglong2 mine = make_ulonglong2(0, 0);
     if (tid < count) {
-      mine = sh.cand[tid];
-      mine.key = order_of(sh.kind[mine.k] == kEnded ? static_cast<double>(sh.s[mine.k]) : score(mine.k, mine.l));
-      sh.cand[tid].key = sh.key[tid] = mine.key;
+      Pick &p = sh.cand[tid];
+      p.key = order_of(sh.kind[p.k] == kEnded ? sh.best_of[p.k] : score(p.k, p.l));
+      // among equal scores: beam, logit (the largest first), token
+      mine = make_ulonglong2(p.key, static_cast<unsigned long long>(p.k) << 52 |
+                                        static_cast<unsigned long long>(~float_key(__fadd_rn(p.l, 0.f))) << 20 | p.at);
+      sh.key[tid] = mine;
     }
     __syncthreads();
     if (tid < count) {
-      int rank = 0, equal = 0;
-#pragma unroll 8
+      int rank = 0;
+#pragma unroll 4
       for (int i = 0; i < count; ++i) {
-        const unsigned long long key = sh.key[i];
-        rank += key > mine.key;
-        equal += key == mine.key;
+        const ulonglong2 x = sh.key[i];
+        rank += x.x > mine.x || (x.x == mine.x && x.y < mine.y);
       }
-      if (equal > 1)
-        for (int i = 0; i < count; ++i) rank += sh.key[i] == mine.key && before(sh.cand[i], mine);
       sh.order[rank] = tid;
     }
     __syncthreads();
     const int found = min(count, a.n);
     if (tid > 0 && tid < count) {   // with the one before it; those not chosen with the last chosen one
       const Pick &p = sh.cand[sh.order[tid]], &q = sh.cand[sh.order[min(tid, a.n) - 1]];
-      compare(from_order(q.key), q.k, from_order(p.key), p.k);
+      compare(q.key, q.k, p.key, p.k);
     }
     __syncthreads();
     if (sh.again) return -1;
@@ -643,7 +695,7 @@ struct Finish {
       const Pick p = some ? sh.cand[sh.order[j]] : no_pick();
       a.tokens[at] = some ? p.at : -1;
       a.parents[at] = some ? b * a.K + p.k : -1;
-      a.out_scores[at] = some ? static_cast<float>(from_order(p.key)) : -INFINITY;
+      a.out_scores[at] = some ? from_order(p.key).x : -INFINITY;
     }
     return 1;
   }
@@ -669,13 +721,14 @@ struct Finish {
         t = a.pad;
       }
     } else {
+      uint4 w[kVPL];
+      load_groups<E>(row(k), a.V, chunk * kUnitVecs + lane, w);
 #pragma unroll
       for (int v = 0; v < kVPL; ++v) {
         const int g = chunk * kUnitVecs + v * 32 + lane;
-        const uint4 w = load_group<E>(row(k), a.V, g);
 #pragma unroll
         for (int e = 0; e < Elem<E>::kPerVec; ++e) {
-          const float x = vec_elem<E>(w, e);
+          const float x = vec_elem<E>(w[v], e);
           const int at = g * Elem<E>::kPerVec + e;
           const bool after = x < last_l || (x == last_l && at > last_t);
           if (x > -INFINITY && after && (x > l || (x == l && at < t))) {
@@ -691,7 +744,7 @@ struct Finish {
     }
     if (lane == 0) {
       const bool some = t != 0x7fffffff;
-      sh.head[j] = Pick{!some ? 0 : sh.kind[k] == kEnded ? order_of(sh.s[k]) : order_of(score(k, l)), l, k, t};
+      sh.head[j] = Pick{!some ? 0 : sh.kind[k] == kEnded ? order_of(sh.best_of[k]) : order_of(score(k, l)), l, k, t};
     }
   }
 
@@ -712,7 +765,7 @@ struct Finish {
         if (lane == 0) {
           sh.best = all;
           if (units > 0 && all.key)
-            compare(from_order(last.key), last.k, from_order(all.key), all.k);
+            compare(last.key, last.k, all.key, all.k);
         }
       }
       __syncthreads();
@@ -723,10 +776,9 @@ struct Finish {
       last = p;
     }
     if (units == a.n) {
-      const double least = from_order(last.key);
       for (int u = tid; u < a.K * a.C; u += kFinishThreads) {
         const Pick p = unit_pick(u);
-        if (p.key && before(last, p)) compare(least, last.k, from_order(p.key), p.k);
+        if (p.key && before(last, p)) compare(last.key, last.k, p.key, p.k);
       }
     }
     __syncthreads();
@@ -736,7 +788,7 @@ struct Finish {
     int32_t *tokens = a.tokens + static_cast<long long>(b) * a.n;
     int32_t *parents = a.parents + static_cast<long long>(b) * a.n;
     float *scores = a.out_scores + static_cast<long long>(b) * a.n;
-    double before_key = 0.;
+    unsigned long long before_key = 0;
     int before_k = -1, found = 0;
     for (; found < a.n; ++found) {
       Pick p = no_pick();   // every warp finds the best head by itself
@@ -748,14 +800,13 @@ struct Finish {
       while (sh.unit[j] != p.k * a.C + (sh.kind[p.k] == kEnded ? 0 : p.at / (kUnitVecs * Elem<E>::kPerVec))) ++j;
       const int k = p.k, token = p.at;
       const float l = p.l;
-      const double x = from_order(p.key);
       if (tid == 0) {
-        if (found > 0) compare(before_key, before_k, x, k);
+        if (found > 0) compare(before_key, before_k, p.key, k);
         tokens[found] = token;
         parents[found] = b * a.K + k;
-        scores[found] = static_cast<float>(x);
+        scores[found] = from_order(p.key).x;
       }
-      before_key = x;
+      before_key = p.key;
       before_k = k;
       __syncthreads();
       if (warp == j % kFinishWarps) next_token(j, sh.kind[k] == kEnded ? -INFINITY : l, token);
@@ -763,7 +814,7 @@ struct Finish {
     }
     if (found == a.n)
       for (int j = tid; j < units; j += kFinishThreads)
-        if (sh.head[j].key) compare(before_key, before_k, from_order(sh.head[j].key), sh.head[j].k);
+        if (sh.head[j].key) compare(before_key, before_k, sh.head[j].key, sh.head[j].k);
     __syncthreads();
     if (sh.again) return false;
     for (int j = found + tid; j < a.n; j += kFinishThreads) {
