@@ -684,6 +684,11 @@ def spec_beam_select(logits, scores, done, pad_token, n, tokens, parents, out_sc
         *_workspace(workspace), _stream(stream))
 
 
+@functools.lru_cache(maxsize=None)
+def _state_array(n):
+    return SpecState * n
+
+
 def spec_beam_reorder(states, parents, outs, status, stream=None) -> int:
     """states: tensors [R, ...] of any types, contiguous; outs: the same with parents.numel() rows;
     parents int32."""
@@ -692,17 +697,17 @@ def spec_beam_reorder(states, parents, outs, status, stream=None) -> int:
     if not isinstance(parents, torch.Tensor) or parents.dtype != _I32:
         raise TypeError("parents must be an int32 tensor")
     R, C = states[0].shape[0], parents.numel()
-    arr = (SpecState * len(states))()
+    arr = _state_array(len(states))()
     for i, (t, o) in enumerate(zip(states, outs)):
-        if t.dim() < 1 or t.shape[0] != R or o.shape != (C, *t.shape[1:]) or o.dtype != t.dtype:
-            raise ValueError(f"state {i}: {tuple(t.shape)} {t.dtype} to {tuple(o.shape)} {o.dtype}, "
+        shape = t.shape
+        if shape[0] != R or o.shape != (C, *shape[1:]) or o.dtype != t.dtype:
+            raise ValueError(f"state {i}: {tuple(shape)} {t.dtype} to {tuple(o.shape)} {o.dtype}, "
                              f"with {R} rows to {C}")
         for x in (t, o):
-            if x.numel() and not (x.is_cuda and x.is_contiguous()):
-                _ptr(x)   # raises
-        arr[i].in_, arr[i].out = t.data_ptr() or None, o.data_ptr() or None
-        arr[i].row_bytes = t[0].numel() * t.element_size() if R else \
-            o[0].numel() * o.element_size() if C else 1
+            if not x.is_contiguous() or not x.is_cuda:
+                _ptr(x)   # raises, or an empty tensor
+        n, rows = (t.numel(), R) if R else (o.numel(), C)
+        arr[i] = (t.data_ptr() or None, o.data_ptr() or None, n // rows * t.element_size() if rows else 1)
     return load_library().spec_beam_reorder(arr, len(states), _operand(parents, "parents", C, _I32), R, C,
                                             _operand(status, "status", 1, _I32), _stream(stream))
 
