@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   int t0 = 0, t1 = 0, total = 0, skip = 0;
   Item<F::kWin> x{};
   tc::fence_before_sync();
-  locate<F::NT, kAttnThreads, F::kWin>(p, sm.loc, t0, t1, total, x, skip);
+  locate<F::NT, kAttnThreads, F::kWin, true>(p, sm.loc, t0, t1, total, x, skip);
   tc::fence_after_sync();
   const uint32_t tmem = sm.tmem;
   if (tid == 0) publish_range(p, x, skip, t0, t1, total);

@@ -250,7 +250,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
   int t0 = 0, t1 = 0, total = 0, skip = 0;
   Item<kWin> x{};
   tc::fence_before_sync();
-  locate<NT, kRowsThreads, kWin>(p, *reinterpret_cast<LocateScratch<kWin> *>(smem + F::kOffQ), t0, t1, total, x, skip);
+  locate<NT, kRowsThreads, kWin, false>(p, *reinterpret_cast<LocateScratch<kWin> *>(smem + F::kOffQ), t0, t1, total, x, skip);
   tc::fence_after_sync();
   const uint32_t tmem = sm.tmem;
   if (tid == 0) publish_range(p, x, skip, t0, t1, total);

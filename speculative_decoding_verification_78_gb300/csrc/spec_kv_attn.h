@@ -281,20 +281,6 @@ __device__ __forceinline__ int window_start(const AttnArgs &p, const Item<kWin> 
   return x.len + at - p.window + 1;
 }
 
-// tiles of one key head of sequence b
-template <int NT, bool kWin>
-__device__ __forceinline__ int head_tiles(const AttnArgs &p, int b) {
-  Item<kWin> x;
-  x.b = b;
-  x.ok = kv_lengths(p.a, b, x.len, x.n);
-  int s = 0;
-#pragma unroll 1
-  for (x.rt = 0; x.rt < p.RT; ++x.rt) {
-    item_span<NT, kWin>(p, x);
-    s += x.tiles;
-  }
-  return s;
-}
 template <int NT, bool kWin>
 __device__ __forceinline__ void item_load(const AttnArgs &p, Item<kWin> &x) {
   x.ok = kv_lengths(p.a, x.b, x.len, x.n);
@@ -316,85 +302,137 @@ __device__ __forceinline__ void item_next(const AttnArgs &p, Item<kWin> &x) {
     item_span<NT, kWin>(p, x);
   }
 }
-// Range c of G of a line of T tiles begins at floor(T c / G); range_of: the range that holds tile t.
+// Range c of G of a line of T tiles begins at floor(T c / G), in 32 bits (c <= G <= kMaxCtas); range_of: the range
+// that holds tile t.
 __device__ __forceinline__ int range_start(int T, int c, int G) {
-  return static_cast<int>(static_cast<unsigned long long>(T) * c / G);
+  const int q = T / G;
+  return q * c + (T - q * G) * c / G;
 }
 __device__ __forceinline__ int range_of(int T, int t, int G) {
   return static_cast<int>((static_cast<unsigned long long>(t + 1) * G + T - 1) / T) - 1;
 }
 
-// The CTA's range [t0, t1) of the line and its first item; called by all threads. Thread t sums
-// the sequences of its own contiguous share; the thread whose share holds t0 finds it there.
+// The CTA's range [t0, t1) of the line and its first item; called by all threads. With one row tile an item each
+// thread sums the sequences of its own contiguous share; with more, each warp does, its lanes a row tile each.
+// Whoever's share holds t0 finds the item there. (One thread that went through the row tiles one after
+// another took 94000 clocks for 47 of them.)
 template <bool kWin> struct LocateScratch {
-  int b0, skip0;
   int warp_sum[32];
   Item<kWin> x;
   int t0, t1, total, skip;
 };
+// The sum over the lanes of the tiles of one key head of x.b, 32 row tiles at a time; all lanes.
+template <int NT, bool kWin>
+__device__ __forceinline__ int warp_head_tiles(const AttnArgs &p, Item<kWin> &x, int lane) {
+  x.ok = kv_lengths(p.a, x.b, x.len, x.n);
+  int s = 0;
+#pragma unroll 1
+  for (x.rt = lane; x.rt < p.RT; x.rt += 32) {
+    item_span<NT, kWin>(p, x);
+    s += x.tiles;
+  }
+  return __reduce_add_sync(0xffffffffu, s);
+}
 template <int NT, int kThreads, bool kWin>
-__device__ __forceinline__ void locate(const AttnArgs &p, LocateScratch<kWin> &sm, int &t0, int &t1,
-                                       int &total, Item<kWin> &x, int &skip) {
+__device__ __forceinline__ void search_line(const AttnArgs &p, LocateScratch<kWin> &sm) {
+  constexpr int kWarps = kThreads / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int share = (p.a.B + kThreads - 1) / kThreads;
-  const int lo = min(p.a.B, tid * share), hi = min(p.a.B, lo + share);
+  const bool one = p.RT == 1;
+  const int sharers = one ? kThreads : kWarps, me = one ? tid : warp;
+  const int share = (p.a.B + sharers - 1) / sharers;
+  const int lo = min(p.a.B, me * share), hi = min(p.a.B, lo + share);
+  Item<kWin> y{};
   int mine = 0;
 #pragma unroll 1
-  for (int b = lo; b < hi; ++b) mine += head_tiles<NT, kWin>(p, b) * p.a.Hkv;
-  int incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += v;
+  for (y.b = lo; y.b < hi; ++y.b) {
+    if (one) {
+      item_load<NT, kWin>(p, y);
+      mine += y.tiles * p.a.Hkv;
+    } else {
+      mine += warp_head_tiles<NT, kWin>(p, y, lane) * p.a.Hkv;
+    }
   }
+  int incl = mine;   // of the thread's share within the warp
+  if (one)
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
   if (lane == 31) sm.warp_sum[warp] = incl;
   __syncthreads();
-  int before = 0, all = 0;
-#pragma unroll 1
-  for (int w = 0; w < kThreads / 32; ++w) {
-    const int v = sm.warp_sum[w];
-    if (w < warp) before += v;
-    all += v;
+  const int w = lane < kWarps ? sm.warp_sum[lane] : 0;
+  int upto = w;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += v;
   }
+  const int all = __shfl_sync(0xffffffffu, upto, 31);
+  int at = __shfl_sync(0xffffffffu, upto - w, warp) + incl - mine;
   const int first = range_start(all, blockIdx.x, gridDim.x);
-  int at = before + incl - mine;
-  if (first >= at && first < at + mine) {
-    int b = lo;
-#pragma unroll 1
-    for (;; ++b) {
-      const int n = head_tiles<NT, kWin>(p, b) * p.a.Hkv;
-      if (first < at + n) break;
-      at += n;
-    }
-    sm.b0 = b;
-    sm.skip0 = first - at;
-  }
-  __syncthreads();
-  // one thread works out the item; all take it from shared memory, so that nothing of the search stays
-  // in (or is spilled from) the registers of the roles that follow
   if (tid == 0) {
     sm.t0 = first;
     sm.t1 = range_start(all, blockIdx.x + 1, gridDim.x);
     sm.total = all;
-    Item<kWin> y{};
-    int left = 0;
-    if (sm.t0 < sm.t1) {
-      y.b = sm.b0;
-      left = sm.skip0;
-      const int per_head = head_tiles<NT, kWin>(p, y.b);
-      y.h = left / per_head;
-      left -= y.h * per_head;
-      item_load<NT, kWin>(p, y);
+  }
+  if (first >= at && first < at + mine) {
+    y.rt = 0;
+    int left, per_head;
 #pragma unroll 1
-      while (left >= y.tiles) {
-        left -= y.tiles;
-        ++y.rt;
+    for (y.b = lo;; ++y.b) {
+      if (one) {
         item_load<NT, kWin>(p, y);
+        per_head = y.tiles;
+      } else {
+        per_head = warp_head_tiles<NT, kWin>(p, y, lane);
+      }
+      left = first - at;
+      if (left < per_head * p.a.Hkv) break;
+      at += per_head * p.a.Hkv;
+    }
+    y.h = left / per_head;
+    left -= y.h * per_head;
+    if (one) {
+      sm.x = y;
+      sm.skip = left;
+    } else {
+#pragma unroll 1
+      for (y.rt = lane;; y.rt += 32) {   // 32 row tiles at a time
+        int n = 0;
+        if (y.rt < p.RT) {
+          item_span<NT, kWin>(p, y);
+          n = y.tiles;
+        }
+        int sum = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int v = __shfl_up_sync(0xffffffffu, sum, o);
+          if (lane >= o) sum += v;
+        }
+        if (left >= sum - n && left < sum) {
+          sm.x = y;
+          sm.skip = left - (sum - n);
+        }
+        const int chunk = __shfl_sync(0xffffffffu, sum, 31);
+        if (left < chunk) break;
+        left -= chunk;
       }
     }
-    sm.x = y;
-    sm.skip = left;
   }
+}
+template <int NT, int kThreads, bool kWin>
+__device__ __noinline__ void search_line_apart(const AttnArgs &p, LocateScratch<kWin> &sm) {
+  search_line<NT, kThreads, kWin>(p, sm);
+}
+// kApart: by a call, with registers of its own (the kernel for few rows spills less with it, the other more).
+template <int NT, int kThreads, bool kWin, bool kApart>
+__device__ __forceinline__ void locate(const AttnArgs &p, LocateScratch<kWin> &sm, int &t0, int &t1,
+                                       int &total, Item<kWin> &x, int &skip) {
+  if constexpr (kApart)
+    search_line_apart<NT, kThreads, kWin>(p, sm);
+  else
+    search_line<NT, kThreads, kWin>(p, sm);
   __syncthreads();
   x = sm.x;
   t0 = sm.t0;
