@@ -138,19 +138,30 @@ __device__ __forceinline__ float reduce_columns(float (&v)[C], int lane) {
 struct Token {
   float ks2;       // scale * log2(e) * key scale
   float lvs, ivs;  // log2 of the value scale, and one over it
-  int from;        // columns from this one on see it (a mask: all that its bits allow)
-  int j;           // number among the new tokens (mask), or -1
-  int slot;        // (with a window) columns whose `lo` is at most this see it
 };
 
+// Which of the thread's columns see the token in `slot` (bit c: column col0 + c).
 template <class F>
-__device__ __forceinline__ bool sees(const AttnArgs &p, const Item<F::kWin> &x, const Token &t, int n,
-                                     const int *tok) {
-  bool see = n >= t.from;
-  if (t.j >= 0 && see)
-    see = (__ldg(p.a.mask + (static_cast<long long>(x.b) * p.a.N + tok[n]) * p.a.W + (t.j >> 5)) >>
-           (t.j & 31)) & 1u;
-  if (F::kWin) see = see && tok[F::NT + n] <= t.slot;   // `lo` lies behind tok
+__device__ __forceinline__ uint32_t columns_seeing(const AttnArgs &p, const Item<F::kWin> &x, int slot,
+                                                   int col0, const int *tok) {
+  const int j = slot - x.len;   // number among the new tokens
+  uint32_t see = ~0u;
+  if (j >= 0 && p.a.mask) {
+    const uint32_t *m = p.a.mask + static_cast<long long>(x.b) * p.a.N * p.a.W + (j >> 5);
+    see = 0;
+#pragma unroll
+    for (int c = 0; c < F::C; ++c)
+      see |= (__ldg(m + static_cast<long long>(tok[col0 + c]) * p.a.W) >> (j & 31) & 1u) << c;
+  } else if (j >= 0) {   // rows of token j and later ones
+    const long long from = static_cast<long long>(j) * p.G - col0;
+    see = from <= 0 ? ~0u : from < F::C ? ~0u << from : 0u;
+  }
+  if constexpr (F::kWin) {
+    if (slot >= p.sinks)
+#pragma unroll
+      for (int c = 0; c < F::C; ++c)
+        if (tok[F::NT + col0 + c] > slot) see &= ~(1u << c);   // its window's start, behind tok
+  }
   return see;
 }
 
@@ -158,9 +169,8 @@ __device__ __forceinline__ bool sees(const AttnArgs &p, const Item<F::kWin> &x, 
 // scale) added to l; true if one exceeds what fp16 holds comfortably. The scores of the next
 // columns are on their way from tensor memory while these are worked on.
 template <class F, bool kMasked>
-__device__ __forceinline__ bool weigh(const AttnArgs &p, const Item<F::kWin> &x, const Token &t, bool poison,
-                                      uint32_t ts, int col0, uint8_t *sp, const float *qs,
-                                      const float *nm, const int *tok, int row,
+__device__ __forceinline__ bool weigh(const Token &t, uint32_t see, bool poison, uint32_t ts, int col0,
+                                      uint8_t *sp, const float *qs, const float *nm, int row,
                                       f32x2 (&l)[F::C / 2]) {
   const f32x2 ks2 = pk2(t.ks2, t.ks2), lvs2 = pk2(t.lvs, t.lvs), ivs2 = pk2(t.ivs, t.ivs);
   float big = -INFINITY;
@@ -185,10 +195,9 @@ __device__ __forceinline__ bool weigh(const AttnArgs &p, const Item<F::kWin> &x,
         float y0, y1;
         up2(fma2(mul2(sv, ks2), q2, add2(m2, lvs2)), y0, y1);
         if (kMasked) {
-          const int n = col0 + c0 + k;
           if (poison) y0 = y1 = NAN;
-          if (!sees<F>(p, x, t, n, tok)) y0 = -INFINITY;
-          if (!sees<F>(p, x, t, n + 1, tok)) y1 = -INFINITY;
+          if (!(see >> (c0 + k) & 1u)) y0 = -INFINITY;
+          if (!(see >> (c0 + k) & 2u)) y1 = -INFINITY;
         }
         big = fmaxf(big, fmaxf(y0, y1));
         const float p0 = ex2(y0), p1 = ex2(y1);
@@ -204,16 +213,14 @@ __device__ __forceinline__ bool weigh(const AttnArgs &p, const Item<F::kWin> &x,
   return big > kTrigger;
 }
 
-// Before a tile is taken again: the largest y of each of this thread's columns over the warp's 32
-// tokens, to wmax[column], and what the first attempt added to l, by the same expression, taken off
-// again. (That leaves at most half a unit of the sum, which the new sum is not smaller than. Where the sum
+// The largest y of each of this thread's columns over the warp's 32 tokens, to wmax[column]; and, before a tile
+// is taken again (kRetract), what the first attempt added to l, by the same expression, taken off again. (That leaves at most half a unit of the sum, which the new sum is not smaller than. Where the sum
 // was infinite the old one is dropped: with value scales within 2^80 of each other each weight in it is
 // below 2^-32 of the new one's, for y passed m by 128, or by 48 and more where 1 / vs is what passed the
 // range. A NaN stays.)
-template <class F>
-__device__ __forceinline__ void retract(const AttnArgs &p, const Item<F::kWin> &x, const Token &t, uint32_t ts,
-                                        int col0, const float *qs, const float *nm, const int *tok,
-                                        int lane, float *wmax, f32x2 (&l)[F::C / 2]) {
+template <class F, bool kRetract>
+__device__ __forceinline__ void maxima(const Token &t, uint32_t see, uint32_t ts, int col0, const float *qs,
+                                       const float *nm, int lane, float *wmax, f32x2 (&l)[F::C / 2]) {
 #pragma unroll
   for (int c0 = 0; c0 < F::C; c0 += F::CH) {
     uint32_t s[F::CH];
@@ -226,25 +233,54 @@ __device__ __forceinline__ void retract(const AttnArgs &p, const Item<F::kWin> &
       const int n = col0 + c0 + c;
       const float z = __uint_as_float(s[c]) * t.ks2;
       y[c] = __fmaf_rn(z, qs[n], t.lvs);
-      w[c] = ex2(__fmaf_rn(z, qs[n], __fadd_rn(nm[n], t.lvs)));
-      if (!sees<F>(p, x, t, n, tok)) {
+      if (kRetract) w[c] = ex2(__fmaf_rn(z, qs[n], __fadd_rn(nm[n], t.lvs)));
+      if (!(see >> (c0 + c) & 1u)) {
         y[c] = -INFINITY;
         w[c] = 0.f;
       }
     }
 #pragma unroll
     for (int c = 0; c < F::CH; c += 2) {
-      float l0, l1;
-      up2(l[(c0 + c) / 2], l0, l1);
-      l0 = l0 == INFINITY ? 0.f : __fmaf_rn(-w[c], t.ivs, l0);
-      l1 = l1 == INFINITY ? 0.f : __fmaf_rn(-w[c + 1], t.ivs, l1);
-      l[(c0 + c) / 2] = pk2(l0, l1);
+      if (kRetract) {
+        float l0, l1;
+        up2(l[(c0 + c) / 2], l0, l1);
+        l0 = l0 == INFINITY ? 0.f : __fmaf_rn(-w[c], t.ivs, l0);
+        l1 = l1 == INFINITY ? 0.f : __fmaf_rn(-w[c + 1], t.ivs, l1);
+        l[(c0 + c) / 2] = pk2(l0, l1);
+      }
       if (y[c] != y[c]) y[c] = -INFINITY;
       if (y[c + 1] != y[c + 1]) y[c + 1] = -INFINITY;
     }
     const float m = reduce_columns<F::CH, true>(y, lane);
     if (lane < F::CH) wmax[col0 + c0 + lane] = m;
   }
+}
+
+// The queries of an item by the softmax threads: an eighth of a row each at most (D / 8 lanes a row, at least as
+// many rows at once as there are columns), on their way while the item before is brought to its end.
+template <class F>
+__device__ __forceinline__ const typename F::T *query_of(const AttnArgs &p, int b, int h, int tid, int &i) {
+  constexpr int kLanes = F::D / 8;
+  static_assert(kSoftThreads / kLanes >= F::NT, "one vector a thread");
+  const int n = tid / kLanes;
+  int g;
+  RowMap::of<F::NT>(p, 0).row(n < F::NT ? n : 0, i, g);
+  if (n >= F::NT || i >= p.a.N) return nullptr;
+  return static_cast<const typename F::T *>(p.q) +
+         (static_cast<long long>(b) * p.a.N + i) * p.q_stride +
+         (static_cast<long long>(h) * p.G + g) * F::D + tid % kLanes * 8;
+}
+template <class F>
+__device__ __forceinline__ uint4 fetch_query(const AttnArgs &p, const Item<F::kWin> &x, int tid) {
+  int i;
+  const typename F::T *at = query_of<F>(p, x.b, x.h, tid, i);
+  return at && i < x.n && x.ok ? __ldg(reinterpret_cast<const uint4 *>(at)) : make_uint4(0, 0, 0, 0);
+}
+template <class F>
+__device__ __forceinline__ void place_query(uint4 raw, int tid, uint8_t *sq, float *qs) {
+  constexpr int kLanes = F::D / 8;
+  if (tid / kLanes < F::NT)   // (whole warps)
+    store_query<typename F::T, F::D, F::NT, F::kTerms, kLanes>(raw, tid / kLanes, tid % kLanes, sq, qs);
 }
 
 template <class F>
@@ -423,19 +459,25 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       ok = ok && wait_for(bar, parity);
       __syncwarp();
     };
+    if (t0 < t1) place_query<F>(fetch_query<F>(p, x, tid), tid, smem + F::kOffQ, qs);
     for (int t = t0; t < t1;) {
       const int cnt = min(x.tiles - skip, t1 - t);
-      load_queries<typename F::T, F::D, F::NT, F::NT, F::kTerms, kSoftThreads, F::kWin>(
-          p, x, RowMap::of<F::NT>(p, x.rt), F::NT, tid, smem + F::kOffQ, qs);
       if (tid < F::NT) {
         nm[tid] = nm[F::NT + tid] = kNoRef;
-        const long long i = (static_cast<long long>(x.rt) * F::NT + tid) / p.G;
-        tok[tid] = static_cast<int>(min(i, static_cast<long long>(p.a.N - 1)));
+        const int i = tid / p.G;   // (one row tile)
+        tok[tid] = min(i, p.a.N - 1);
         if (F::kWin) tok[F::NT + tid] = window_start(p, x, tok[tid]);
       }
       fence_async();
       soft_sync();
-      if (tid == 0) mbar_arrive(&sm.qfull);
+      const bool more = t + cnt < t1;
+      if (t == t0 && tid == 0) mbar_arrive(&sm.qfull);   // (later ones were placed at the end of the item before)
+      if (more) {   // asks L2 for the next item's queries
+        int i;
+        const int next = x.h + 1 == p.a.Hkv;
+        const auto *at = query_of<F>(p, x.b + next, next ? 0 : x.h + 1, tid, i);
+        if (at) asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
+      }
       f32x2 l[F::C / 2];
 #pragma unroll
       for (int c = 0; c < F::C / 2; ++c) l[c] = pk2(0.f, 0.f);
@@ -461,38 +503,36 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         tk.ks2 = ks * p.scale2;
         tk.lvs = __log2f(vse);
         tk.ivs = vs == vs ? __frcp_rn(vse) : 1.f;
-        const int j = slot0 + row - x.len;
-        tk.j = -1;
-        tk.from = 0;
-        if (F::kWin) tk.slot = slot0 + row < p.sinks ? 0x7fffffff : slot0 + row;   // a sink: for all
-        // no scale was copied for a page that no row sees
+        uint32_t see = ~0u;
         if (slot0 + row >= x.end || !span_seen<F::kWin>(p, x, slot0 + row, 1)) {
-          tk.from = F::NT;
+          see = 0;   // (no scale was copied for a page that no row sees)
           tk.ks2 = tk.lvs = tk.ivs = 0.f;
-        } else if (j >= 0 && p.a.mask)
-          tk.j = j;
-        else if (j >= 0)
-          tk.from = static_cast<int>(
-              min(static_cast<long long>(F::NT),
-                  static_cast<long long>(j) * p.G - static_cast<long long>(x.rt) * F::NT));
+        } else if (masked) {
+          see = columns_seeing<F>(p, x, slot0 + row, col0, tok);
+        }
         wait(&sm.sfull[grp], use & 1);
         tc::fence_after_sync();
         bool again = false;
+        bool first = k < 2;   // the group's first tile of the item: no references yet
 #pragma unroll 1
         for (;;) {
-          bool over;
-          if (masked || again)
-            over = weigh<F, true>(p, x, tk, again && vnan[row], ts, col0, sp, qs, gnm, tok, row, l);
-          else
-            over = weigh<F, false>(p, x, tk, false, ts, col0, sp, qs, gnm, tok, row, l);
-          fence_async();
-          tc::fence_before_sync();
-          if (!group_any(grp, !again && (over || nan))) break;
-          tc::fence_after_sync();
-          // new references: maxima over the tile's tokens (P's buffer holds them meanwhile)
+          // maxima over the tile's tokens lie in P's buffer meanwhile
           float *wmax = reinterpret_cast<float *>(sp), *fac = wmax + 4 * F::NT;
-          retract<F>(p, x, tk, ts, col0, qs, gnm, tok, lane, wmax + quad * F::NT, l);
-          group_sync(grp);
+          if (first) {
+            maxima<F, false>(tk, see, ts, col0, qs, gnm, lane, wmax + quad * F::NT, l);
+          } else {
+            bool over;
+            if (masked || again)
+              over = weigh<F, true>(tk, see, again && vnan[row], ts, col0, sp, qs, gnm, row, l);
+            else
+              over = weigh<F, false>(tk, see, false, ts, col0, sp, qs, gnm, row, l);
+            fence_async();
+            tc::fence_before_sync();
+            if (!group_any(grp, !again && (over || nan))) break;
+            tc::fence_after_sync();
+            maxima<F, true>(tk, see, ts, col0, qs, gnm, lane, wmax + quad * F::NT, l);
+          }
+          group_sync(grp);   // new references
           if (gtid < F::NT) {
             const float m = fmaxf(fmaxf(wmax[gtid], wmax[F::NT + gtid]),
                                   fmaxf(wmax[2 * F::NT + gtid], wmax[3 * F::NT + gtid]));
@@ -503,6 +543,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             gnm[gtid] = now;
           }
           group_sync(grp);
+          if (first) {   // nothing has been added yet
+            first = false;
+            continue;
+          }
           // (the group's last value MMAs completed before its buffers were written)
 #pragma unroll
           for (int c0 = 0; c0 < F::C; c0 += F::CH) {
@@ -534,6 +578,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         if (gtid == 0) mbar_arrive(&sm.pfull[grp]);
       }
       it += cnt;
+      Item<F::kWin> y = x;   // the next item; its queries go where these were, once both groups' scores are done
+      uint4 raw = make_uint4(0, 0, 0, 0);
+      if (more) {
+        item_next<F::NT, F::kWin>(p, y);
+        raw = fetch_query<F>(p, y, tid);
+      }
       // The item's (or its part's) result. All value MMAs have completed: each group's denominators
       // over the tile's 128 lanes, then the groups joined, each lane's dim of every column.
       for (int last = it - 1; last >= 0 && last >= it - 2; --last)
@@ -541,6 +591,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       tc::fence_after_sync();
       float *lsum = reinterpret_cast<float *>(smem + F::kOffP), *fac = lsum + 8 * F::NT;
       soft_sync();
+      if (more) {
+        place_query<F>(raw, tid, smem + F::kOffQ, qs);
+        fence_async();
+      }
 #pragma unroll
       for (int c0 = 0; c0 < F::C; c0 += F::CH) {
         float v[F::CH];
@@ -550,6 +604,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         if (lane < F::CH) lsum[(grp * 4 + quad) * F::NT + col0 + c0 + lane] = sum;
       }
       soft_sync();
+      if (more && tid == 0) mbar_arrive(&sm.qfull);
       const bool whole = skip == 0 && cnt == x.tiles;
       const long long part = 2LL * blockIdx.x + (skip == 0 ? 1 : 0);
       if (tid < F::NT) {
@@ -618,7 +673,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       soft_sync();   // lsum, fac and tok are read before the next item's writes
       t += cnt;
       skip = 0;
-      if (t < t1) item_next<F::NT, F::kWin>(p, x);
+      x = y;
     }
   }
   if (!ok) set_status(p.a.status, SPEC_ERR_TIMEOUT);

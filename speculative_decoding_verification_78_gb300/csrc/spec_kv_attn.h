@@ -476,12 +476,39 @@ struct RowMap {
   }
 };
 
-// Rows 0 .. NT - 1 of the item as e4m3 terms in shared memory (D / 8 lanes a row), each in units of a
-// power of two that puts its largest element in [2^7, 2^8); qs[n] undoes it. Two terms hold bf16's 8
+// Eight dims (number `sub`) of row n as e4m3 terms in shared memory, by the kLanes lanes that have the row, in
+// units of a power of two that puts its largest element in [2^7, 2^8); qs[n] undoes it. Two terms hold bf16's 8
 // significant bits exactly for elements from 2^-2 on, three fp16's 11 from 2 on; below that they are off by
-// at most 2^-10, half the smallest e4m3 value. Blocks of kBlock rows, each
-// term of a block a K-major operand; of the NT rows the first `rows` (a multiple of 16) are written, zero
-// past the item's.
+// at most 2^-10, half the smallest e4m3 value. Blocks of kBlock rows, each term of a block a K-major operand.
+template <typename T, int D, int kBlock, int kTerms, int kLanes>
+__device__ __forceinline__ void store_query(uint4 raw, int n, int sub, uint8_t *sq, float *qs) {
+  float f[8];
+  vec_to_floats<T>(raw, f);
+  float m = 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) m = fmax_nan(m, fabsf(f[e]));
+#pragma unroll
+  for (int o = kLanes / 2; o > 0; o >>= 1) m = fmax_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const int e = max(static_cast<int>(__float_as_uint(m) >> 23), 27);   // exponent, at least -100
+  const float mul = __uint_as_float(static_cast<uint32_t>(127 + 127 + 7 - e) << 23);
+  if (sub == 0)
+    qs[n] = m < INFINITY ? __uint_as_float(static_cast<uint32_t>(e - 7) << 23) : NAN;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) f[k] *= mul;
+  uint8_t *blk = sq + n / kBlock * (kTerms * kBlock * D);
+#pragma unroll
+  for (int t = 0; t < kTerms; ++t) {
+    const uint2 w = floats_to_e4m3(f, 1.f);
+    *reinterpret_cast<uint2 *>(blk + t * (kBlock * D) + swz<D>(n % kBlock * D + sub * 8)) = w;
+    if (t + 1 < kTerms) {
+      float g8[8];
+      e4m3_to_floats(w, g8);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) f[k] -= g8[k];   // exact
+    }
+  }
+}
+// The rows 0 .. NT - 1 of an item: of them the first `rows` (a multiple of 16) are written, zero past the item's.
 template <typename T, int D, int NT, int kBlock, int kTerms, int kThreads, bool kWin>
 __device__ __forceinline__ void load_queries(const AttnArgs &p, const Item<kWin> &x, const RowMap &map,
                                              int rows, int tid, uint8_t *sq, float *qs) {
@@ -508,31 +535,7 @@ __device__ __forceinline__ void load_queries(const AttnArgs &p, const Item<kWin>
     for (int u = 0; u < kAhead; ++u) {
       const int n = n0 + u * kRows;
       if (n >= rows) break;
-      float f[8];
-      vec_to_floats<T>(raw[u], f);
-      float m = 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) m = fmax_nan(m, fabsf(f[e]));
-#pragma unroll
-      for (int o = kLanes / 2; o > 0; o >>= 1) m = fmax_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-      const int e = max(static_cast<int>(__float_as_uint(m) >> 23), 27);   // exponent, at least -100
-      const float mul = __uint_as_float(static_cast<uint32_t>(127 + 127 + 7 - e) << 23);
-      if (sub == 0)
-        qs[n] = m < INFINITY ? __uint_as_float(static_cast<uint32_t>(e - 7) << 23) : NAN;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) f[k] *= mul;
-      uint8_t *blk = sq + n / kBlock * (kTerms * kBlock * D);
-#pragma unroll
-      for (int t = 0; t < kTerms; ++t) {
-        const uint2 w = floats_to_e4m3(f, 1.f);
-        *reinterpret_cast<uint2 *>(blk + t * (kBlock * D) + swz<D>(n % kBlock * D + sub * 8)) = w;
-        if (t + 1 < kTerms) {
-          float g8[8];
-          e4m3_to_floats(w, g8);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) f[k] -= g8[k];   // exact
-        }
-      }
+      store_query<T, D, kBlock, kTerms, kLanes>(raw[u], n, sub, sq, qs);
     }
   }
 }
