@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   locate<F::NT, kAttnThreads, F::kWin, true>(p, sm.loc, t0, t1, total, x, skip);
   tc::fence_after_sync();
   const uint32_t tmem = sm.tmem;
-  if (tid == 0) publish_range(p, x, skip, t0, t1, total);
+  if (tid == 32 * kProducer) publish_range(p, x, skip, t0, t1, total);   // (not of a softmax warp)
   bool ok = true;   // false after a wait gave up: no further waits, and no further work is issued
   if (warp == kProducer) {
     int it = 0;

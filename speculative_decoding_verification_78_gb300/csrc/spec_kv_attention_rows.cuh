@@ -62,6 +62,7 @@ constexpr int kCopyK = kWidenWarp + kWidenWarps, kMma = kCopyK + 1, kCopyV = kCo
 // prompts): 49 / 165 / 240 / 246; eight widening warps, 72 registers a thread: 52 / 167 / 249 / 255; those
 // with an instruction in each role's branch, which is undefined: 48 / 152 / 233 / 237.
 constexpr int kRowsThreads = 32 * (kConsts + 1);
+constexpr int kEdge = 1 << 31;      // (with a window) beside a tile's first slot: it needs masks
 constexpr float kBias = 8.f;        // a new reference puts the row's largest weight at 2^8 ...
 constexpr float kTrigger = 15.f;    // ... and is taken when one exceeds 2^15 (fp16 ends at 2^16)
 
@@ -253,7 +254,9 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
   locate<NT, kRowsThreads, kWin, false>(p, *reinterpret_cast<LocateScratch<kWin> *>(smem + F::kOffQ), t0, t1, total, x, skip);
   tc::fence_after_sync();
   const uint32_t tmem = sm.tmem;
-  if (tid == 0) publish_range(p, x, skip, t0, t1, total);
+  // (by a lane of another warp than softmax's first: what one lane of that does here sets it apart from its warp
+  // until the first item's end, 18000 clocks for the queries instead of 7000)
+  if (tid == 32 * kConsts) publish_range(p, x, skip, t0, t1, total);
   bool ok = true;   // false after a wait gave up: no further waits, and no further work is issued
   // A lane's wait; after one that gave up its lane waits no more but keeps step with its warp, whose
   // loops end by their counts (an `ok` agreed on by vote cost each hand-over about 60 clocks).
@@ -338,6 +341,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
                    ? make_float2(__ldg(p.a.k_scale + head), __ldg(p.a.v_scale + head))
                    : make_float2(NAN, NAN);   // what reads a bad page is NaN
       };
+      const int full = seen_by_all<NT, kWin>(p, x);
       const int second = page_of(1);
       int next = page_of(2);
       float2 sc = scales_of(page_of(0)), sc1 = scales_of(second);
@@ -350,9 +354,14 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         // a NaN scale makes its tokens' scores NaN through log2 vs; 1 / vs multiplies the zero weights of
         // the rows that do not see them too, so it stays finite, as everything past the end
         const float vse = now.y < kMinValueScale ? kMinValueScale : now.y;
-        const float4 c = want ? make_float4(now.x * p.scale2, __log2f(vse),
-                                            now.y == now.y ? __frcp_rn(vse) : 1.f, 0.f)
-                              : make_float4(0.f, 0.f, 0.f, 0.f);
+        float4 c = want ? make_float4(now.x * p.scale2, __log2f(vse),
+                                      now.y == now.y ? __frcp_rn(vse) : 1.f, 0.f)
+                        : make_float4(0.f, 0.f, 0.f, 0.f);
+        if (kWin) {   // the tile's first slot, and whether it needs masks, for the softmax threads
+          const int slot0 = tile_slot<kWin>(x, skip + k);
+          const bool edge = slot0 + kTile > full || !tile_whole<kWin>(p, x, slot0);
+          c.w = __int_as_float(slot0 | (edge ? kEdge : 0));
+        }
         wait(&sm.room[it & 7], (it >> 3) & 1);
         if (lane < per_tile)
           for (int e = 0; e < chunks; ++e) pages[it % F::kPages * 8 + lane * chunks + e] = c;
@@ -502,14 +511,24 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       const float q = qs[n];
       rows_sync();   // `top` takes its place
       float nm = kNoRef, l = 0.f;
-      const int plain = seen_by_all<NT, kWin>(p, x) - kTile;   // tiles from slots past this on need masks
+      const int plain = kWin ? 0 : seen_by_all<NT, kWin>(p, x) - kTile;   // tiles from slots past this on need masks
       const int lo = kWin && live ? window_start(p, x, i) : 0;
       const int step = F::RTC == 2 ? 1 : 2;
       const int k0 = F::RTC == 2 ? 0 : grp;
       for (int k = quad < quads ? k0 : cnt; k < cnt; k += step, ++use) {
         const int tile = it + k, buf = tile & 1;
-        const int slot0 = tile_slot<kWin>(x, skip + k);
-        const bool edge = slot0 > plain || !tile_whole<kWin>(p, x, slot0);
+        const float4 *page = pages + (tile % F::kPages * 8 + 4 * half);
+        int slot0;
+        bool edge;
+        if constexpr (kWin) {
+          wait(&sm.cfull[tile % F::kPages], (tile / F::kPages) & 1);
+          const int at = __float_as_int(page->w);
+          slot0 = at & ~kEdge;
+          edge = __any_sync(0xffffffffu, at & kEdge);   // (the same in all lanes, and known to be)
+        } else {
+          slot0 = (skip + k) * kTile;
+          edge = slot0 > plain;
+        }
         uint32_t see[2] = {~0u, ~0u};
         if (edge)
 #pragma unroll
@@ -518,8 +537,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
             see[w] = live ? seen_bits(p, x.b, i, from - x.len, x.n) : 0u;
             if (kWin) see[w] &= window_bits(from, lo, p.sinks);
           }
-        const float4 *page = pages + (tile % F::kPages * 8 + 4 * half);
-        wait(&sm.cfull[tile % F::kPages], (tile / F::kPages) & 1);
+        if (!kWin) wait(&sm.cfull[tile % F::kPages], (tile / F::kPages) & 1);
         wait(&sm.sfull[grp], use & 1);
         __syncwarp();
         tc::fence_after_sync();
