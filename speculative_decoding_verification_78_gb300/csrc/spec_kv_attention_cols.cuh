@@ -53,6 +53,9 @@ constexpr int kGroupThreads = 32 * kGroupWarps;
 constexpr int kSoftThreads = 2 * kGroupThreads;
 constexpr int kProducer = 2 * kGroupWarps, kMma = kProducer + 1;   // warps
 constexpr int kAttnThreads = 32 * (kMma + 1);
+// Shares of whole items may be this much longer (see search_line): 64 x 1 token with a window of 512 48 us (6 tiles an
+// item) for 52, of 1024 63 for 65 (if taken, 24); of 4096 142 for 128 (24), so they are not.
+constexpr int kWholeTiles = 12;
 constexpr float kBias = 8.f;        // a new reference puts the largest weight at 2^8 ...
 constexpr float kTrigger = 15.f;    // ... and is taken when one exceeds 2^15 (fp16 ends at 2^16)
 
@@ -315,7 +318,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   int t0 = 0, t1 = 0, total = 0, skip = 0;
   Item<F::kWin> x{};
   tc::fence_before_sync();
-  locate<F::NT, kAttnThreads, F::kWin, true>(p, sm.loc, t0, t1, total, x, skip);
+  locate<F::NT, kAttnThreads, F::kWin, true, kWholeTiles>(p, sm.loc, t0, t1, total, x, skip);
   tc::fence_after_sync();
   const uint32_t tmem = sm.tmem;
   if (tid == 32 * kProducer) publish_range(p, x, skip, t0, t1, total);   // (not of a softmax warp)

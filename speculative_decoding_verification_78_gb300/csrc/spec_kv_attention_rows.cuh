@@ -63,6 +63,9 @@ constexpr int kCopyK = kWidenWarp + kWidenWarps, kMma = kCopyK + 1, kCopyV = kCo
 // with an instruction in each role's branch, which is undefined: 48 / 152 / 233 / 237.
 constexpr int kRowsThreads = 32 * (kConsts + 1);
 constexpr int kEdge = 1 << 31;      // (with a window) beside a tile's first slot: it needs masks
+// Shares of whole items may be this much longer (see search_line): 32 trees of 64 nodes with a window of 2048 110 us
+// for 128, 2 x 1500 tokens of 8 rows with 1000 60 for 69; with 4000 they would be 131 for 110 (40), so they are not.
+constexpr int kWholeTiles = 20;
 constexpr float kBias = 8.f;        // a new reference puts the row's largest weight at 2^8 ...
 constexpr float kTrigger = 15.f;    // ... and is taken when one exceeds 2^15 (fp16 ends at 2^16)
 
@@ -251,7 +254,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
   int t0 = 0, t1 = 0, total = 0, skip = 0;
   Item<kWin> x{};
   tc::fence_before_sync();
-  locate<NT, kRowsThreads, kWin, false>(p, *reinterpret_cast<LocateScratch<kWin> *>(smem + F::kOffQ), t0, t1, total, x, skip);
+  locate<NT, kRowsThreads, kWin, false, kWholeTiles>(p, *reinterpret_cast<LocateScratch<kWin> *>(smem + F::kOffQ), t0, t1, total, x, skip);
   tc::fence_after_sync();
   const uint32_t tmem = sm.tmem;
   // (by a lane of another warp than softmax's first: what one lane of that does here sets it apart from its warp

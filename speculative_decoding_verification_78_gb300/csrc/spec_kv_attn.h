@@ -314,26 +314,31 @@ __device__ __forceinline__ int range_of(int T, int t, int G) {
 
 // The CTA's range [t0, t1) of the line and its first item; called by all threads. With one row tile an item each
 // thread sums the sequences of its own contiguous share; with more, each warp does, its lanes a row tile each.
-// Whoever's share holds t0 finds the item there. (One thread that went through the row tiles one after
-// another took 94000 clocks for 47 of them.)
+// Whoever's share holds an end of the range finds the item there. (One thread that went through the row tiles
+// one after another took 94000 clocks for 47 of them.)
+//
+// Ranges are equal, but for this: with a window (items are short there), where shares of whole items would be at
+// most kWhole tiles longer, the CTAs take those. Then no item has parts that are written, read back and joined,
+// which costs more than the tiles.
 template <bool kWin> struct LocateScratch {
-  int warp_sum[32];
+  int warp_sum[32], warp_most[32];
   Item<kWin> x;
   int t0, t1, total, skip;
 };
 // The sum over the lanes of the tiles of one key head of x.b, 32 row tiles at a time; all lanes.
 template <int NT, bool kWin>
-__device__ __forceinline__ int warp_head_tiles(const AttnArgs &p, Item<kWin> &x, int lane) {
+__device__ __forceinline__ int warp_head_tiles(const AttnArgs &p, Item<kWin> &x, int lane, int &most) {
   x.ok = kv_lengths(p.a, x.b, x.len, x.n);
   int s = 0;
 #pragma unroll 1
   for (x.rt = lane; x.rt < p.RT; x.rt += 32) {
     item_span<NT, kWin>(p, x);
     s += x.tiles;
+    most = max(most, x.tiles);
   }
   return __reduce_add_sync(0xffffffffu, s);
 }
-template <int NT, int kThreads, bool kWin>
+template <int NT, int kThreads, bool kWin, int kWhole>
 __device__ __forceinline__ void search_line(const AttnArgs &p, LocateScratch<kWin> &sm) {
   constexpr int kWarps = kThreads / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -342,16 +347,18 @@ __device__ __forceinline__ void search_line(const AttnArgs &p, LocateScratch<kWi
   const int share = (p.a.B + sharers - 1) / sharers;
   const int lo = min(p.a.B, me * share), hi = min(p.a.B, lo + share);
   Item<kWin> y{};
-  int mine = 0;
+  int mine = 0, most = 0;
 #pragma unroll 1
   for (y.b = lo; y.b < hi; ++y.b) {
     if (one) {
       item_load<NT, kWin>(p, y);
       mine += y.tiles * p.a.Hkv;
+      most = max(most, y.tiles);
     } else {
-      mine += warp_head_tiles<NT, kWin>(p, y, lane) * p.a.Hkv;
+      mine += warp_head_tiles<NT, kWin>(p, y, lane, most) * p.a.Hkv;
     }
   }
+  if (kWin) most = __reduce_max_sync(0xffffffffu, most);
   int incl = mine;   // of the thread's share within the warp
   if (one)
 #pragma unroll
@@ -359,7 +366,10 @@ __device__ __forceinline__ void search_line(const AttnArgs &p, LocateScratch<kWi
       const int v = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += v;
     }
-  if (lane == 31) sm.warp_sum[warp] = incl;
+  if (lane == 31) {
+    sm.warp_sum[warp] = incl;
+    if (kWin) sm.warp_most[warp] = most;
+  }
   __syncthreads();
   const int w = lane < kWarps ? sm.warp_sum[lane] : 0;
   int upto = w;
@@ -369,11 +379,38 @@ __device__ __forceinline__ void search_line(const AttnArgs &p, LocateScratch<kWi
     if (lane >= o) upto += v;
   }
   const int all = __shfl_sync(0xffffffffu, upto, 31);
+  const int G = gridDim.x;
+  if constexpr (kWin) {
+    most = __reduce_max_sync(0xffffffffu, lane < kWarps ? sm.warp_most[lane] : 0);
+    const int items = p.a.B * p.a.Hkv * p.RT;
+    const int each = (items + G - 1) / G;
+    if (static_cast<long long>(each) * most <= all / G + kWhole) {   // (so the numbers below are small)
+      const int i0 = range_start(items, blockIdx.x, G), n = range_start(items, blockIdx.x + 1, G) - i0;
+      if (warp == 0) {
+        int sum = 0;
+        for (int i = lane; i < n; i += 32) {
+          y.rt = (i0 + i) % p.RT;
+          y.h = (i0 + i) / p.RT % p.a.Hkv;
+          y.b = (i0 + i) / p.RT / p.a.Hkv;
+          item_load<NT, kWin>(p, y);
+          sum += y.tiles;
+          if (i == 0) sm.x = y;
+        }
+        sum = __reduce_add_sync(0xffffffffu, sum);
+        if (lane == 0) {
+          sm.t0 = sm.skip = 0;
+          sm.t1 = sum;
+          sm.total = all;
+        }
+      }
+      return;
+    }
+  }
   int at = __shfl_sync(0xffffffffu, upto - w, warp) + incl - mine;
-  const int first = range_start(all, blockIdx.x, gridDim.x);
+  const int first = range_start(all, blockIdx.x, G);
   if (tid == 0) {
     sm.t0 = first;
-    sm.t1 = range_start(all, blockIdx.x + 1, gridDim.x);
+    sm.t1 = range_start(all, blockIdx.x + 1, G);
     sm.total = all;
   }
   if (first >= at && first < at + mine) {
@@ -385,7 +422,7 @@ __device__ __forceinline__ void search_line(const AttnArgs &p, LocateScratch<kWi
         item_load<NT, kWin>(p, y);
         per_head = y.tiles;
       } else {
-        per_head = warp_head_tiles<NT, kWin>(p, y, lane);
+        per_head = warp_head_tiles<NT, kWin>(p, y, lane, most);
       }
       left = first - at;
       if (left < per_head * p.a.Hkv) break;
@@ -421,18 +458,18 @@ __device__ __forceinline__ void search_line(const AttnArgs &p, LocateScratch<kWi
     }
   }
 }
-template <int NT, int kThreads, bool kWin>
+template <int NT, int kThreads, bool kWin, int kWhole>
 __device__ __noinline__ void search_line_apart(const AttnArgs &p, LocateScratch<kWin> &sm) {
-  search_line<NT, kThreads, kWin>(p, sm);
+  search_line<NT, kThreads, kWin, kWhole>(p, sm);
 }
 // kApart: by a call, with registers of its own (the kernel for few rows spills less with it, the other more).
-template <int NT, int kThreads, bool kWin, bool kApart>
+template <int NT, int kThreads, bool kWin, bool kApart, int kWhole>
 __device__ __forceinline__ void locate(const AttnArgs &p, LocateScratch<kWin> &sm, int &t0, int &t1,
                                        int &total, Item<kWin> &x, int &skip) {
   if constexpr (kApart)
-    search_line_apart<NT, kThreads, kWin>(p, sm);
+    search_line_apart<NT, kThreads, kWin, kWhole>(p, sm);
   else
-    search_line<NT, kThreads, kWin>(p, sm);
+    search_line<NT, kThreads, kWin, kWhole>(p, sm);
   __syncthreads();
   x = sm.x;
   t0 = sm.t0;
