@@ -699,15 +699,15 @@ def spec_beam_reorder(states, parents, outs, status, stream=None) -> int:
     R, C = states[0].shape[0], parents.numel()
     arr = _state_array(len(states))()
     for i, (t, o) in enumerate(zip(states, outs)):
-        shape = t.shape
-        if shape[0] != R or o.shape != (C, *shape[1:]) or o.dtype != t.dtype:
-            raise ValueError(f"state {i}: {tuple(shape)} {t.dtype} to {tuple(o.shape)} {o.dtype}, "
+        a, b = t.shape, o.shape
+        if a[0] != R or b[0] != C or a[1:] != b[1:] or t.dtype != o.dtype:
+            raise ValueError(f"state {i}: {tuple(a)} {t.dtype} to {tuple(b)} {o.dtype}, "
                              f"with {R} rows to {C}")
-        for x in (t, o):
-            if not x.is_contiguous() or not x.is_cuda:
-                _ptr(x)   # raises, or an empty tensor
-        n, rows = (t.numel(), R) if R else (o.numel(), C)
-        arr[i] = (t.data_ptr() or None, o.data_ptr() or None, n // rows * t.element_size() if rows else 1)
+        n, m = t.numel(), o.numel()
+        if not (t.is_cuda and t.is_contiguous() and o.is_cuda and o.is_contiguous()):
+            _ptr(t), _ptr(o)   # raises, or empty tensors
+        row = n // R if R else m // C if C else 1
+        arr[i] = (t.data_ptr() or None, o.data_ptr() or None, row * t.element_size())
     return load_library().spec_beam_reorder(arr, len(states), _operand(parents, "parents", C, _I32), R, C,
                                             _operand(status, "status", 1, _I32), _stream(stream))
 

@@ -197,47 +197,36 @@ __device__ __forceinline__ Parent parent_of(const PageArgs &a, int p) {
   return x;
 }
 
-// CTAs 0 .. C - 1: a child's row of full pages. The others: a parent's pages, whose counts grow by the
-// children that share them and shrink by one where the parent ends.
-__global__ void __launch_bounds__(128) kv_fork_rows_kernel(const __grid_constant__ PageArgs a,
-                                                           const __grid_constant__ ForkArgs f) {
-  pdl_wait();
-  __shared__ int children;
-  if (blockIdx.x < static_cast<unsigned>(f.C)) {
-    const int c = blockIdx.x, p = __ldg(f.parents + c);
-    Parent x{};
-    x.ok = p >= 0 && p < a.B;
-    if (x.ok) x = parent_of(a, p);
-    if (threadIdx.x == 0) {
-      if (p < -1 || p >= a.B) set_status(a.status, SPEC_ERR_PARENT);
-      if (p >= 0 && p < a.B && !x.ok) set_status(a.status, SPEC_ERR_LENGTH);
-      f.lens_out[c] = x.ok ? x.len : p == -1 ? 0 : -1;
-    }
-    const int32_t *row = a.table + static_cast<long long>(x.ok ? p : 0) * a.pps;
-    int32_t *out = f.table_out + static_cast<long long>(c) * a.pps;
-    for (int j = threadIdx.x; j < a.pps; j += blockDim.x) {
-      if (x.rest && j == x.full) continue;   // the next kernel's
-      int page = j < x.full ? row[j] : -1;
-      if (page >= a.num_pages) {
-        set_status(a.status, SPEC_ERR_PAGE);
-        page = -1;
-      }
-      out[j] = max(page, -1);
-    }
-    return;
+// A child's row of full pages, by threads `me`, `me` + `step`, ... (the place after them is left to fork_pages).
+__device__ __forceinline__ void fork_child(const PageArgs &a, const ForkArgs &f, int c, int me, int step) {
+  const int p = __ldg(f.parents + c);
+  Parent x{};
+  x.ok = p >= 0 && p < a.B;
+  if (x.ok) x = parent_of(a, p);
+  if (me == 0) {
+    if (p < -1 || p >= a.B) set_status(a.status, SPEC_ERR_PARENT);
+    if (p >= 0 && p < a.B && !x.ok) set_status(a.status, SPEC_ERR_LENGTH);
+    f.lens_out[c] = x.ok ? x.len : p == -1 ? 0 : -1;
   }
-  const int p = blockIdx.x - f.C;
-  if (threadIdx.x == 0) children = 0;
-  __syncthreads();
-  int n = 0;
-  for (int c = threadIdx.x; c < f.C; c += blockDim.x) n += __ldg(f.parents + c) == p;
-  if (n) atomicAdd(&children, n);
-  __syncthreads();
-  n = children;
+  const int32_t *row = a.table + static_cast<long long>(x.ok ? p : 0) * a.pps;
+  int32_t *out = f.table_out + static_cast<long long>(c) * a.pps;
+  for (int j = me; j < a.pps; j += step) {
+    if (x.rest && j == x.full) continue;
+    int page = j < x.full ? row[j] : -1;
+    if (page >= a.num_pages) {
+      set_status(a.status, SPEC_ERR_PAGE);
+      page = -1;
+    }
+    out[j] = max(page, -1);
+  }
+}
+// A parent's pages, whose counts grow by the n children that share them and shrink by one where the parent ends.
+__device__ __forceinline__ void fork_parent(const PageArgs &a, const ForkArgs &f, int p, int n, int me,
+                                            int step) {
   const Parent x = parent_of(a, p);
-  if (!x.ok && threadIdx.x == 0) set_status(a.status, SPEC_ERR_LENGTH);
+  if (!x.ok && me == 0) set_status(a.status, SPEC_ERR_LENGTH);
   const int32_t *row = a.table + static_cast<long long>(p) * a.pps;
-  for (int j = threadIdx.x; j < a.pps; j += blockDim.x) {
+  for (int j = me; j < a.pps; j += step) {
     const int page = row[j];
     if (page < 0) continue;
     if (page >= a.num_pages) {
@@ -255,21 +244,59 @@ __global__ void __launch_bounds__(128) kv_fork_rows_kernel(const __grid_constant
   }
 }
 
+// CTAs 0 .. C - 1: a child each; the others a parent.
+__global__ void __launch_bounds__(128) kv_fork_rows_kernel(const __grid_constant__ PageArgs a,
+                                                           const __grid_constant__ ForkArgs f) {
+  pdl_wait();
+  __shared__ int children;
+  if (blockIdx.x < static_cast<unsigned>(f.C)) {
+    fork_child(a, f, blockIdx.x, threadIdx.x, blockDim.x);
+    return;
+  }
+  const int p = blockIdx.x - f.C;
+  if (threadIdx.x == 0) children = 0;
+  __syncthreads();
+  int n = 0;
+  for (int c = threadIdx.x; c < f.C; c += blockDim.x) n += __ldg(f.parents + c) == p;
+  if (n) atomicAdd(&children, n);
+  __syncthreads();
+  fork_parent(a, f, p, children, threadIdx.x, blockDim.x);
+}
+
 // One CTA: pages for the children that need a copy of the last page, in the order of the children, and the
-// list of copies. A child that finds no page has none (its length is -1).
+// list of copies. A child that finds no page has none (its length is -1). kAll: it does the rows too, a warp a
+// sequence: a launch less, which is worth it for up to kForkOne sequences, two a warp (4 beams: 10 us less of the
+// host's time; 256 sequences of 9 pages take 7 us longer that way).
+constexpr int kForkOne = 64, kForkPlaces = 1024;
+template <bool kAll>
 __global__ void __launch_bounds__(kScanThreads) kv_fork_pages_kernel(const __grid_constant__ PageArgs a,
                                                                      const __grid_constant__ ForkArgs f) {
-  extern __shared__ int first[];   // [B] the first child of each parent
+  extern __shared__ int first[];   // [B] the first child of each parent; then, with kAll, their numbers
   __shared__ int sums[kScanWarps];
   pdl_wait();
   const int tid = threadIdx.x;
-  for (int p = tid; p < a.B; p += kScanThreads) first[p] = f.C;
+  int *children = first + a.B;
+  for (int p = tid; p < a.B; p += kScanThreads) {
+    first[p] = f.C;
+    if (kAll) children[p] = 0;
+  }
   __syncthreads();
-  if (f.release)
+  if (f.release || kAll)
     for (int c = tid; c < f.C; c += kScanThreads) {
       const int p = __ldg(f.parents + c);
-      if (p >= 0 && p < a.B) atomicMin(&first[p], c);
+      if (p < 0 || p >= a.B) continue;
+      if (f.release) atomicMin(&first[p], c);
+      if (kAll) atomicAdd(&children[p], 1);
     }
+  if (kAll) {
+    __syncthreads();
+    const int lane = tid & 31, warp = tid >> 5;
+    for (int i = warp; i < f.C + a.B; i += kScanWarps)
+      if (i < f.C)
+        fork_child(a, f, i, lane, 32);
+      else
+        fork_parent(a, f, i - f.C, children[i - f.C], lane, 32);
+  }
   __syncthreads();
   struct Child {
     int p, src;   // src: the parent's last page if it is not full, else -1
@@ -402,7 +429,7 @@ __global__ void __launch_bounds__(kScanThreads) kv_compact_map_kernel(const __gr
   }
 }
 
-constexpr int kMoveBytes = 16384;   // of a CTA's step
+constexpr int kMoveBytes = 32768, kMoveVecs = kMoveBytes / (16 * 256);   // of a CTA's step; of a thread in it
 
 // Moves the listed pages, whole, in every layer, with their counts; and puts the new numbers into the table.
 __global__ void __launch_bounds__(256) kv_compact_move_kernel(const __grid_constant__ PageArgs a,
@@ -429,13 +456,13 @@ __global__ void __launch_bounds__(256) kv_compact_move_kernel(const __grid_const
     const uint4 *s = reinterpret_cast<const uint4 *>(pool + src * bytes + static_cast<long long>(step) * kMoveBytes);
     uint4 *d = reinterpret_cast<uint4 *>(pool + dst * bytes + static_cast<long long>(step) * kMoveBytes);
     const int vecs = static_cast<int>(min(static_cast<long long>(kMoveBytes), bytes - static_cast<long long>(step) * kMoveBytes) / 16);
-    uint4 w[4];
+    uint4 w[kMoveVecs];
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
-      if (u * 256 + tid < vecs) w[u] = s[u * 256 + tid];
+    for (int u = 0; u < kMoveVecs; ++u)
+      if (u * 256 + tid < vecs) w[u] = __ldcs(s + u * 256 + tid);
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
-      if (u * 256 + tid < vecs) d[u * 256 + tid] = w[u];
+    for (int u = 0; u < kMoveVecs; ++u)
+      if (u * 256 + tid < vecs) __stcs(d + u * 256 + tid, w[u]);
     if (step == 0) {
       float *scale = side ? m.v_scale : m.k_scale;
       for (int h = tid; h < m.Hkv; h += 256) scale[dst * m.Hkv + h] = scale[src * m.Hkv + h];
@@ -482,9 +509,14 @@ cudaError_t launch_kv_fork(const PageArgs &a, const PoolArgs &m, ForkArgs f, voi
   f.count = static_cast<int32_t *>(ws);
   f.copies = reinterpret_cast<int4 *>(f.count + 4);
   f.list = reinterpret_cast<int32_t *>(f.copies + f.C);
-  cudaError_t e = launch_kv(kv_fork_rows_kernel, static_cast<long long>(f.C) + a.B, 128, 0, stream, a, f);
-  if (e != cudaSuccess) return e;
-  e = launch_kv(kv_fork_pages_kernel, 1, kScanThreads, a.B * sizeof(int), stream, a, f);
+  cudaError_t e;
+  if (f.C + a.B <= kForkOne && a.pps <= kForkPlaces) {
+    e = launch_kv(kv_fork_pages_kernel<true>, 1, kScanThreads, 2 * a.B * sizeof(int), stream, a, f);
+  } else {
+    e = launch_kv(kv_fork_rows_kernel, static_cast<long long>(f.C) + a.B, 128, 0, stream, a, f);
+    if (e != cudaSuccess) return e;
+    e = launch_kv(kv_fork_pages_kernel<false>, 1, kScanThreads, a.B * sizeof(int), stream, a, f);
+  }
   if (e != cudaSuccess) return e;
   const long long warps = static_cast<long long>(f.C) * m.layers * m.Hkv * 2;
   return launch_kv(kv_copy_rows_kernel, grid_for((warps + 7) / 8, 152 * 8), 256, 0, stream, m,
