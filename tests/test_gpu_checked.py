@@ -119,3 +119,59 @@ def test_checked_lmhead(both, orc):
     assert int(got[2][0]) == 0 and int(want[2][0]) == 0
     for g, w in zip(got, want):
         np.testing.assert_array_equal(g, w)
+
+
+def test_checked_beams(both):
+    """Beam selection (few candidates and many equal ones, aligned rows and not, beams at their end) and
+    reordering."""
+    bnd, lib, clib = both
+    g = torch.Generator(device="cuda").manual_seed(3)
+    for V, off, n in ((9000, 0, 16), (4099, 1, 40), (700, 0, 64)):
+        flat = torch.randn(3 * 4 * V + off, generator=g, device="cuda")
+        for logits in (flat[off:].view(3, 4, V), flat[off:].view(3, 4, V).round(), flat.bfloat16()[off:].view(3, 4, V)):
+            scores = -torch.rand(3, 4, generator=g, device="cuda")
+            done = (torch.rand(3, 4, generator=g, device="cuda") < 0.2).int()
+            args = (logits, scores, n, done, 5)
+            want, got = (_np(_run(bnd, l, bnd.beam_select, *args)) for l in (lib, clib))
+            assert int(got[-1][0]) == 0
+            for x, y in zip(got, want):
+                np.testing.assert_array_equal(x, y)
+    states = [torch.randn(6, 33, generator=g, device="cuda"), torch.randn(6, 512, generator=g, device="cuda")]
+    parents = torch.tensor([5, 0, -1, 2], dtype=torch.int32, device="cuda")
+    want, got = (_np(_run(bnd, l, bnd.beam_reorder, states, parents)) for l in (lib, clib))
+    for x, y in zip(got, want):
+        np.testing.assert_array_equal(x, y)
+
+
+def test_checked_pages_and_window(both):
+    """A step's page calls on few and many sequences, and windowed attention with both kernels."""
+    bnd, lib, clib = both
+
+    def steps(B):
+        cache = bnd.new_kv_cache(40 * B, 2, 64, 16, 2)
+        for x in (cache.k, cache.v):
+            x.view(torch.uint8).random_(0, 100, generator=torch.Generator(device="cuda").manual_seed(4))
+        refs = bnd.new_page_refs(cache)
+        table = torch.full((B, 12), -1, dtype=torch.int32, device="cuda")
+        lens = torch.zeros(B, dtype=torch.int32, device="cuda")
+        new = (torch.arange(B, device="cuda") * 7 % 60 + 90).int()
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        granted, _ = bnd.kv_reserve(cache, refs, table, lens, 150, new_lens=new, status=st)
+        lens += granted
+        parents = (torch.arange(B, device="cuda") // 2).int()
+        table, lens, _ = bnd.kv_fork(cache, refs, table, lens, parents, release=True, status=st)
+        bnd.kv_trim(cache, refs, table, lens, window=40, sinks=3, status=st)
+        outs = [table, lens]
+        for N, Hq in ((1, 4), (6, 16)):
+            q = torch.randn(B, N, Hq, 64, generator=torch.Generator(device="cuda").manual_seed(5), device="cuda").bfloat16()
+            out, lse, _ = bnd.kv_attention(cache, table, lens - N, q, window=40 - N, sinks=3, status=st, return_lse=True)
+            outs += [out.view(torch.int16), lse]
+        page_map, live, _ = bnd.kv_compact(cache, refs, table, status=st)
+        bnd.kv_free(cache, refs, table, lens, (parents % 2).contiguous(), status=st)
+        return [*outs, page_map, live, refs, table, lens, cache.k.view(torch.uint8), st]
+
+    for B in (5, 70):
+        want, got = (_np(_run(bnd, l, steps, B)) for l in (lib, clib))
+        assert int(got[-1][0]) == 0
+        for x, y in zip(got, want):
+            np.testing.assert_array_equal(x, y)
