@@ -7,8 +7,9 @@
 // row then picks units by their maxima and tokens from those units.
 //
 // Exactness. The order of two candidates of one beam is that of their logits, whatever L_k. Candidates of
-// different beams are compared by L_k from fp32 sums, whose error is bounded (kSlack); where two that matter
-// lie nearer than that, the L_k concerned are computed again to about 1e-10 and the selection is repeated. So
+// different beams are compared by L_k from fp32 sums, whose error is bounded (kCoarse); where two that matter
+// lie nearer than that, the units that make up most of the L_k concerned are summed again to about 1e-10, as many
+// as it takes to tell the two apart, and the selection is repeated. So
 // tokens and parents are those of exact arithmetic (but for scores closer than 1e-9). The sums are taken in
 // the order of the token numbers wherever a row lies in memory, so that beams with equal logits have equal L_k.
 #include "spec_beam.h"
@@ -27,9 +28,10 @@ constexpr double kLog2ed = 1.44269504088896340736;
 // logarithm: 2^(l log2 e - R), so that units are joined by powers of two. Beyond it (where R would not be an
 // exact fp32 integer with room for a fraction) against its maximum itself.
 constexpr float kPlainMax = 1048576.f;
-// Twice the bound of an fp32 sum's relative error: 2^-22 of ex2; two roundings of the exponent, 2^-24 |t| ln 2
-// each, |t| at most 21 on average (log2 of the largest vocabulary, and one); 25 roundings of sums.
-constexpr float kSlack = 8e-6f;
+// The bound of a unit sum's relative error: 2^-22 of ex2; two roundings of the exponent, 2^-24 |t| ln 2 each, where
+// |t| of 2048 terms below one of at least 2^-1 is at most 8 on average; 16 roundings of sums. And that of a sum
+// taken again (exp_pair), with what its logarithm adds.
+constexpr float kCoarse = 2e-6f, kFine = 2e-10f;
 
 __device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
   f32x2 r;
@@ -278,7 +280,7 @@ constexpr int kStaged = 2048;   // units whose maxima are kept in shared memory
 
 // Bin of a distance d >= 0 from the best score: 32 bins an octave from 2^-8 to 2^24, what is nearer in the first
 // and what is farther in the last. A distance is known to 2^-22 of itself, a bin is 2^-5 wide, and no bin but
-// the first narrower than 2^-13: a candidate is in its bin or, where that matters, in the next, kSlack included.
+// the first narrower than 2^-13: a candidate is in its bin or, where that matters, in the next, kCoarse included.
 __device__ __forceinline__ int bin_of(float d) {
   return min(max(static_cast<int>(__float_as_uint(d) >> 18) - ((127 - 8) << 5), 0), kBins - 1);
 }
@@ -294,13 +296,26 @@ struct FinishShared {
   int order[kMaxCands];
   float2 best_of[SPEC_MAX_BEAMS];   // a beam's best score: s - log_sum, in two words
   float s[SPEC_MAX_BEAMS], top[SPEC_MAX_BEAMS];
-  int kind[SPEC_MAX_BEAMS], precise[SPEC_MAX_BEAMS], wanted[SPEC_MAX_BEAMS];
+  int kind[SPEC_MAX_BEAMS];
+  float slack[SPEC_MAX_BEAMS];     // how far L_k may be off
+  int target[SPEC_MAX_BEAMS];      // what that has to come down to (as the bits of a positive float)
   Pick warp[kFinishWarps], best;
   int unit[SPEC_MAX_BEST];     // chosen units, in order
   Pick head[SPEC_MAX_BEST];    // the best of each that is left; place: the token
   double sum[kFinishWarps];
   int bad, again;
+  float least;
+  unsigned long long rest;
 };
+
+// The longer parts of it that are seldom taken are functions of their own, made of the same members (one that were a
+// member itself would keep the others' fields in memory).
+template <typename E>
+__device__ __noinline__ float2 large_sum_apart(const BeamArgs &a, FinishShared &sh, int b, int k, float m);
+template <typename E>
+__device__ __noinline__ void refine_apart(const BeamArgs &a, FinishShared &sh, int b, int k);
+template <typename E>
+__device__ __noinline__ bool select_any_apart(const BeamArgs &a, FinishShared &sh, int b);
 
 template <typename E>
 struct Finish {
@@ -338,12 +353,16 @@ struct Finish {
   }
   // two candidates whose order the sums as they are do not tell: asks for better ones
   __device__ __forceinline__ void compare(unsigned long long x, int k, unsigned long long y, int j) const {
-    if (k == j || (sh.precise[k] && sh.precise[j])) return;
+    if (k == j) return;
     const float2 u = from_order(x), v = from_order(y);
     const float gap = fabsf(__fadd_rn(__fsub_rn(u.x, v.x), __fsub_rn(u.y, v.y)));
-    if (!(gap > 0.f && gap <= kSlack)) return;   // (0: beams with the same logits and scores)
-    if (!sh.precise[k]) sh.wanted[k] = 1;
-    if (!sh.precise[j]) sh.wanted[j] = 1;
+    if (!(gap > 0.f && gap <= sh.slack[k] + sh.slack[j])) return;   // (0: beams with the same logits and scores)
+    want(k, 0.4f * gap);
+    want(j, 0.4f * gap);
+  }
+  __device__ __forceinline__ void want(int k, float slack) const {
+    if (sh.slack[k] <= kFine || sh.slack[k] <= slack) return;
+    atomicMin(&sh.target[k], __float_as_int(slack));
     sh.again = 1;
   }
 
@@ -371,18 +390,13 @@ struct Finish {
         t = scaled(t, unit_ref(m) - R);
         m = top;
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const uint32_t bits = w[u].y;   // a sum in [2^-1, 2^12), or 0
-          const unsigned long long mant = static_cast<unsigned long long>((bits & 0x7fffffu) | 0x800000u);
-          const int e = static_cast<int>(bits >> 23) - 127 - 23 + 40;   // of its last bit, in units of 2^-40
-          if (bits) t += scaled(e >= 0 ? mant << min(e, 40) : mant >> min(-e, 63), unit_ref(__uint_as_float(w[u].x)) - R);
-        }
+        for (int u = 0; u < 4; ++u) t += fixed(w[u], R);
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
       const bool live = kind == kLive;
       float h = 0.f, l = 0.f, top = 0.f;
-      if (live && m > 64.f - kPlainMax && m < kPlainMax) {   // (a unit below -kPlainMax adds nothing)
+      if (live && plain_row(m)) {
         top = m;
         log_pair(t, h, l);
         // + R ln 2 - m, of which R ln 2 and m may be large and near each other
@@ -393,17 +407,29 @@ struct Finish {
         pair_add(h, l, d, dl);
       } else if (live) {
         top = m;
-        large_sum(k, m, h, l);
+        const float2 x = large_sum_apart<E>(a, sh, b, k, m);
+        h = x.x;
+        l = x.y;
       }
       if (lane == 0) {
         sh.kind[k] = kind;
         sh.s[k] = s;
-        sh.precise[k] = !live;
-        sh.wanted[k] = 0;
+        sh.slack[k] = live ? kCoarse : 0.f;
+        sh.target[k] = 0x7f800000;
         set_sum(k, top, h, l);
         if (kind == kBad || (live && !(fabsf(m) < INFINITY))) sh.bad = 1;
       }
     }
+  }
+  // a row that is summed against powers of two (a unit below -kPlainMax adds nothing to it)
+  static __device__ __forceinline__ bool plain_row(float m) { return m > 64.f - kPlainMax && m < kPlainMax; }
+  // a unit's sum against 2^R, in units of 2^-40
+  static __device__ __forceinline__ unsigned long long fixed(uint2 w, float R) {
+    const uint32_t bits = w.y;   // a sum in [2^-1, 2^12), or 0
+    if (!bits) return 0;
+    const unsigned long long mant = (bits & 0x7fffffu) | 0x800000u;
+    const int e = static_cast<int>(bits >> 23) - 127 - 23 + 40;   // of its last bit
+    return scaled(e >= 0 ? mant << min(e, 40) : mant >> min(-e, 63), unit_ref(__uint_as_float(w.x)) - R);
   }
   static __device__ __forceinline__ unsigned long long scaled(unsigned long long t, float e) {   // t 2^e, e <= 0
     return e > -64.f ? t >> static_cast<int>(-e) : 0ull;
@@ -415,7 +441,7 @@ struct Finish {
     sh.best_of[k] = pair_of(x, y);
   }
   // log sum_v e^(l - m) of a row whose largest logit m is too large for powers of two, in 64 bits
-  __device__ __noinline__ void large_sum(int k, float m, float &h, float &l) const {
+  __device__ __forceinline__ float2 large_sum(int k, float m) const {
     double t = 0.;
     for (int c = lane; c < a.C; c += 32) {
       const uint2 w = part(k * a.C + c);
@@ -428,40 +454,72 @@ struct Finish {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
     const double x = log(t);
-    h = static_cast<float>(x);
-    l = static_cast<float>(x - h);
+    const float h = static_cast<float>(x);
+    return make_float2(h, static_cast<float>(x - h));
   }
 
-  // L_k of one beam again, to about 1e-10, by the whole CTA
-  __device__ void precise_sum(int k) const {
-    const float M = sh.top[k];
+  // L_k again, to within sh.target[k], by the whole CTA: the units that hold most of the sum are summed again, the
+  // others (all that may stay out by their shares) count as they are.
+  __device__ __forceinline__ void refine(int k) const {
+    const float M = sh.top[k], target = __int_as_float(sh.target[k]);
+    const bool plain = plain_row(M);
+    const float R = unit_ref(M);
+    float *weight = reinterpret_cast<float *>(sh.key);   // of each unit, against 2^R (at most 2^10 units)
+    static_assert(sizeof(sh.key) >= 4 * (SPEC_MAX_V / (4 * kUnitVecs)), "room for a row's units");
+    for (int c = tid; c < a.C; c += kFinishThreads) {
+      const uint2 w = part(k * a.C + c);
+      weight[c] = plain ? static_cast<float>(fixed(w, R)) * 0x1p-40f : 1.f;
+    }
+    if (tid == 0) sh.least = 0.f;
+    __syncthreads();
+    if (warp == 0 && plain) {   // a threshold a lane: 2^(10 - lane); the largest that leaves out little enough
+      const float at = ldexpf(1.f, 10 - lane);
+      float all = 0.f, out = 0.f;
+      for (int c = 0; c < a.C; ++c) {
+        all += weight[c];
+        if (weight[c] < at) out += weight[c];
+      }
+      const unsigned fits = __ballot_sync(0xffffffffu, out * (1.01f * kCoarse) + kFine * all <= target * all);
+      if (lane == 0 && fits) sh.least = ldexpf(1.f, 10 - (__ffs(fits) - 1));
+    }
+    __syncthreads();
+    const float least = sh.least;
+    if (warp == kFinishWarps - 1) {
+      unsigned long long rest = 0;
+      for (int c = lane; c < a.C; c += 32)
+        if (weight[c] < least) rest += fixed(part(k * a.C + c), R);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) rest += __shfl_xor_sync(0xffffffffu, rest, o);
+      if (lane == 0) sh.rest = rest;
+    }
     float h = 0.f, l = 0.f;
-    for (int g = tid; g * Elem<E>::kPerVec < a.V; g += kFinishThreads) {
+    int n = 0;
+    for (int c = 0; c < a.C; ++c) {   // half of the CTA a unit
+      if (weight[c] < least) continue;
+      if ((n++ & 1) != tid / kUnitVecs) continue;
       uint4 v[1];
-      load_groups<E>(row(k), a.V, g, v);
+      load_groups<E>(row(k), a.V, c * kUnitVecs + tid % kUnitVecs, v);
 #pragma unroll
       for (int e = 0; e < Elem<E>::kPerVec; ++e) {
         float xh, xl;
         exp_pair(vec_elem<E>(v[0], e), M, xh, xl);
-        const float s = __fadd_rn(h, xh), bb = __fsub_rn(s, h);
-        l = __fadd_rn(l, __fadd_rn(__fadd_rn(__fsub_rn(h, __fsub_rn(s, bb)), __fsub_rn(xh, bb)), xl));
-        h = s;
+        pair_add(h, l, xh, xl);
       }
     }
     double t = static_cast<double>(h) + static_cast<double>(l);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-    __syncthreads();
     if (lane == 0) sh.sum[warp] = t;
     __syncthreads();
     if (tid == 0) {
       double all = 0.;
       for (int w = 0; w < kFinishWarps; ++w) all += sh.sum[w];
-      const double x = log(all);
-      const float h = static_cast<float>(x);
-      set_sum(k, M, h, static_cast<float>(x - h));
-      sh.precise[k] = 1;
-      sh.wanted[k] = 0;
+      const double out = sh.rest ? static_cast<double>(sh.rest) * 0x1p-40 * exp(R / kLog2ed - M) : 0.;
+      const double x = log(all + out);
+      const float hi = static_cast<float>(x);
+      set_sum(k, M, hi, static_cast<float>(x - hi));
+      sh.slack[k] = kFine + static_cast<float>(out / (all + out)) * kCoarse;
+      sh.target[k] = 0x7f800000;
     }
     __syncthreads();
   }
@@ -510,9 +568,12 @@ struct Finish {
     }
     __syncthreads();
   }
-  __device__ __forceinline__ void clear_hist() const {
+  __device__ __forceinline__ void clear_hist_only() const {
 #pragma unroll
     for (int i = 0; i < kBins / kFinishThreads; ++i) sh.hist[i * kFinishThreads + tid] = 0;
+  }
+  __device__ __forceinline__ void clear_hist() const {
+    clear_hist_only();
     if (tid == 0) sh.parts = sh.cands = 0;
   }
   // the distance of unit u's best candidate, negative if it has none
@@ -529,7 +590,7 @@ struct Finish {
   }
   // Lists (or, with `count`, counts by their distances) the listed quarters' candidates with a distance of at
   // most `most`.
-  __device__ __noinline__ void each_token(float most, bool count) const {
+  __device__ __forceinline__ void each_token(float most, bool count) const {
     constexpr int kAhead = 2;   // quarters of a warp whose loads are on their way together
     for (int i0 = warp; i0 < sh.parts; i0 += kAhead * kFinishWarps) {
       uint4 buf[kAhead][2];
@@ -638,28 +699,32 @@ struct Finish {
     }
     __syncthreads();
     if (sh.parts > kMaxParts) return 0;
-    // With fewer units than candidates wanted, or with too many tokens in that range, the tokens' own distances
-    // give a nearer edge.
-    bool counted = edge == kBins - 1;
-    if (!counted) {
-      each_token(most, false);
+    // Lists the tokens. With fewer units than candidates wanted, or with too many tokens in that range, their own
+    // distances are counted first and give a nearer edge.
+    float limit = most;
+    bool counting = edge == kBins - 1, counted = false;
+    if (counting) {   // (the units' counts give way to the tokens')
       __syncthreads();
-      counted = sh.cands > kMaxCands;
+      clear_hist_only();
+      __syncthreads();
     }
-    if (counted) {
-      const int parts = sh.parts;
+    for (;;) {
+      each_token(limit, counting);
       __syncthreads();
-      clear_hist();
-      __syncthreads();
-      if (tid == 0) sh.parts = parts;
-      __syncthreads();
-      each_token(most, true);
-      __syncthreads();
-      find_edge(a.n);
-      edge = sh.edge;
-      each_token(bin_end(edge + 1), false);
-      __syncthreads();
-      if (sh.cands > kMaxCands) return 0;
+      if (!counting && sh.cands <= kMaxCands) break;
+      if (!counting && counted) return 0;
+      if (counting) {
+        find_edge(a.n);
+        limit = bin_end(sh.edge + 1);
+        counting = false;
+        counted = true;
+      } else {
+        counting = true;
+        __syncthreads();   // all have seen how many there were
+        clear_hist_only();
+        if (tid == 0) sh.cands = 0;
+        __syncthreads();
+      }
     }
     const int count = sh.cands;
     ulonglong2 mine = make_ulonglong2(0, 0);
@@ -825,6 +890,24 @@ struct Finish {
   }
 };
 
+template <typename E>
+__device__ __forceinline__ Finish<E> finish_of(const BeamArgs &a, FinishShared &sh, int b) {
+  const int tid = threadIdx.x;
+  return Finish<E>{a, sh, b, tid, tid & 31, tid >> 5};
+}
+template <typename E>
+__device__ __noinline__ float2 large_sum_apart(const BeamArgs &a, FinishShared &sh, int b, int k, float m) {
+  return finish_of<E>(a, sh, b).large_sum(k, m);
+}
+template <typename E>
+__device__ __noinline__ void refine_apart(const BeamArgs &a, FinishShared &sh, int b, int k) {
+  finish_of<E>(a, sh, b).refine(k);
+}
+template <typename E>
+__device__ __noinline__ bool select_any_apart(const BeamArgs &a, FinishShared &sh, int b) {
+  return finish_of<E>(a, sh, b).select_any();
+}
+
 // One CTA a batch row.
 template <typename E>
 __global__ void __launch_bounds__(kFinishThreads, 1) beam_finish_kernel(const __grid_constant__ BeamArgs a) {
@@ -832,7 +915,7 @@ __global__ void __launch_bounds__(kFinishThreads, 1) beam_finish_kernel(const __
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int tid = threadIdx.x, b = blockIdx.x;
-  const Finish<E> f{a, sh, b, tid, tid & 31, tid >> 5};
+  const Finish<E> f = finish_of<E>(a, sh, b);
   if (tid == 0) sh.bad = sh.again = 0;
   __syncthreads();
   f.sums();
@@ -846,15 +929,15 @@ __global__ void __launch_bounds__(kFinishThreads, 1) beam_finish_kernel(const __
     }
     return;
   }
-  for (;;) {   // at most once a beam, and once more
+  for (;;) {   // each time around the sums of two beams are better than before; they end at kFine
     const int done = f.select_few();
     if (done == 1) return;
     __syncthreads();
-    if (done == 0 && f.select_any()) return;
+    if (done == 0 && select_any_apart<E>(a, sh, b)) return;
     __syncthreads();
     if (tid == 0) sh.again = 0;
     for (int k = 0; k < a.K; ++k)
-      if (sh.wanted[k]) f.precise_sum(k);
+      if (sh.target[k] != 0x7f800000) refine_apart<E>(a, sh, b, k);
     __syncthreads();
   }
 }
