@@ -331,13 +331,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       // the page number of this lane's page in tile k of the segment (0 past the end)
       const int32_t *table = p.a.page_table + static_cast<long long>(x.b) * p.a.pps;
       auto page_of = [&](int k) {
-        const int slot = tile_slot<F::kWin>(x, skip + k) + (lane << p.a.page_shift);
+        const int slot = slot_of<F::kWin>(x, (skip + k) * kTile + (lane << p.a.page_shift));
         return lane < per_tile && slot < x.end && span_seen<F::kWin>(p, x, slot, p.a.page) ? __ldg(table + (slot >> p.a.page_shift)) : 0;
       };
       int next = page_of(0);
       for (int k = 0; k < cnt && ok; ++k, ++it) {
         const int s = it % F::S;
-        const int slot = tile_slot<F::kWin>(x, skip + k) + (lane << p.a.page_shift);
+        const int slot = slot_of<F::kWin>(x, (skip + k) * kTile + (lane << p.a.page_shift));
         const bool want = lane < per_tile && slot < x.end && span_seen<F::kWin>(p, x, slot, p.a.page);
         const int page = next;
         if (k + 1 < cnt) next = page_of(k + 1);   // on its way while this tile waits for room
@@ -486,14 +486,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       for (int c = 0; c < F::C / 2; ++c) l[c] = pk2(0.f, 0.f);
       for (int k = (it ^ grp) & 1; k < cnt; k += 2) {
         const int n = it + k, s = n % F::S, use = n >> 1;
-        const int slot0 = tile_slot<F::kWin>(x, skip + k);
+        const int slot = slot_of<F::kWin>(x, (skip + k) * kTile + row);
         wait(&sm.full[s], (n / F::S) & 1);
         uint4 w[Widen<F::D, kGroupThreads>::kSteps];
-        fetch_values<F::D, kGroupThreads, F::kWin>(smem + s * 2 * F::kSideBytes + F::kSideBytes, gtid, x.end - slot0,
-                                                   x.lo - slot0, p.sinks - slot0, w);
+        fetch_values<F::D, kGroupThreads, F::kWin>(p, x, smem + s * 2 * F::kSideBytes + F::kSideBytes, gtid,
+                                                   skip + k, w);
         const float ks = sm.ks[s][row >> p.a.page_shift], vs = sm.vs[s][row >> p.a.page_shift];
         wait(&sm.pfree[grp], (use & 1) ^ 1);
-        const bool masked = slot0 + kTile > min(x.len, x.end) || !tile_whole<F::kWin>(p, x, slot0);
+        const bool masked = tile_edge<F::kWin>(p, x, skip + k, min(x.len, x.end));
         const bool nan = masked && scrub_values<F::D, kGroupThreads>(
                                        w, gtid, [&](int at) { vnan[at] = 1; });
         widen<F::D, kGroupThreads>(w, sv16, gtid);
@@ -507,11 +507,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         tk.lvs = __log2f(vse);
         tk.ivs = vs == vs ? __frcp_rn(vse) : 1.f;
         uint32_t see = ~0u;
-        if (slot0 + row >= x.end || !span_seen<F::kWin>(p, x, slot0 + row, 1)) {
+        if (slot >= x.end || !span_seen<F::kWin>(p, x, slot, 1)) {
           see = 0;   // (no scale was copied for a page that no row sees)
           tk.ks2 = tk.lvs = tk.ivs = 0.f;
         } else if (masked) {
-          see = columns_seeing<F>(p, x, slot0 + row, col0, tok);
+          see = columns_seeing<F>(p, x, slot, col0, tok);
         }
         wait(&sm.sfull[grp], use & 1);
         tc::fence_after_sync();

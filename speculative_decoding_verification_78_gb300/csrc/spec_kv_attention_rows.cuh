@@ -62,7 +62,7 @@ constexpr int kCopyK = kWidenWarp + kWidenWarps, kMma = kCopyK + 1, kCopyV = kCo
 // prompts): 49 / 165 / 240 / 246; eight widening warps, 72 registers a thread: 52 / 167 / 249 / 255; those
 // with an instruction in each role's branch, which is undefined: 48 / 152 / 233 / 237.
 constexpr int kRowsThreads = 32 * (kConsts + 1);
-constexpr int kEdge = 1 << 31;      // (with a window) beside a tile's first slot: it needs masks
+constexpr int kEdge = 1 << 31;      // (with a window) beside a page's first slot: the tile needs masks
 // Shares of whole items may be this much longer (see search_line): 32 trees of 64 nodes with a window of 2048 110 us
 // for 128, 2 x 1500 tokens of 8 rows with 1000 60 for 69; with 4000 they would be 131 for 110 (40), so they are not.
 constexpr int kWholeTiles = 20;
@@ -282,7 +282,10 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       // this lane's page of the next tile: its number, on its way while the tile before waits for room
       const int32_t *table = p.a.page_table + static_cast<long long>(x.b) * p.a.pps;
       const int pages_end = (x.end + p.a.page - 1) >> p.a.page_shift;
-      int at = (tile_slot<kWin>(x, skip) >> p.a.page_shift) + lane;   // place in the table
+      auto place = [&](int k) {   // in the table, of this lane's page in tile k of the segment
+        return slot_of<kWin>(x, (skip + k) * kTile + (lane << p.a.page_shift)) >> p.a.page_shift;
+      };
+      int at = place(0);
       auto wanted = [&]() {
         return lane < per_tile && at < pages_end &&
                span_seen<kWin>(p, x, at << p.a.page_shift, p.a.page);
@@ -292,8 +295,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       for (int k = 0; k < cnt; ++k, ++it) {
         const int s = it % F::S, page = next;
         const bool want = wanted();
-        at += per_tile;
-        if (kWin && skip + k + 1 == x.head) at += x.gap * per_tile;
+        at = kWin ? place(k + 1) : at + per_tile;
         next = page_of();
         const bool good = page >= 0 && page < p.a.num_pages;
         if (want && !good) set_status(p.a.status, SPEC_ERR_PAGE);
@@ -330,7 +332,9 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       const int32_t *table = p.a.page_table + static_cast<long long>(x.b) * p.a.pps;
       const int pages_end = (x.end + p.a.page - 1) >> p.a.page_shift;
       // this lane's place in tile k of the segment
-      auto place = [&](int k) { return (tile_slot<kWin>(x, skip + k) >> p.a.page_shift) + lane; };
+      auto place = [&](int k) {
+        return slot_of<kWin>(x, (skip + k) * kTile + (lane << p.a.page_shift)) >> p.a.page_shift;
+      };
       auto wanted = [&](int at) {
         return lane < per_tile && at < pages_end && span_seen<kWin>(p, x, at << p.a.page_shift, p.a.page);
       };
@@ -360,14 +364,14 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         float4 c = want ? make_float4(now.x * p.scale2, __log2f(vse),
                                       now.y == now.y ? __frcp_rn(vse) : 1.f, 0.f)
                         : make_float4(0.f, 0.f, 0.f, 0.f);
-        if (kWin) {   // the tile's first slot, and whether it needs masks, for the softmax threads
-          const int slot0 = tile_slot<kWin>(x, skip + k);
-          const bool edge = slot0 + kTile > full || !tile_whole<kWin>(p, x, slot0);
-          c.w = __int_as_float(slot0 | (edge ? kEdge : 0));
-        }
+        if (kWin)   // the page's first slot, and whether the tile needs masks, for the softmax threads
+          c.w = __int_as_float(place(k) << p.a.page_shift | (tile_edge<kWin>(p, x, skip + k, full) ? kEdge : 0));
         wait(&sm.room[it & 7], (it >> 3) & 1);
         if (lane < per_tile)
-          for (int e = 0; e < chunks; ++e) pages[it % F::kPages * 8 + lane * chunks + e] = c;
+          for (int e = 0; e < chunks; ++e) {
+            pages[it % F::kPages * 8 + lane * chunks + e] = c;
+            if (kWin) c.w = __int_as_float(__float_as_int(c.w) + 16);   // by 16 tokens
+          }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.cfull[it % F::kPages]);
       }
@@ -459,14 +463,12 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       const int cnt = min(x.tiles - skip, t1 - t), full = seen_by_all<NT, kWin>(p, x);
       for (int k = 0; k < cnt; ++k, ++it) {
         const int s = it % F::S, buf = it & 1;
-        const int slot0 = tile_slot<kWin>(x, skip + k);
         wait(&sm.full[s], (it / F::S) & 1);
         uint4 w[Widen<D, kWidenThreads>::kSteps];
-        fetch_values<D, kWidenThreads, kWin>(smem + s * 2 * F::kSideBytes + F::kSideBytes, wtid,
-                                             x.end - slot0, x.lo - slot0, p.sinks - slot0, w);
+        fetch_values<D, kWidenThreads, kWin>(p, x, smem + s * 2 * F::kSideBytes + F::kSideBytes, wtid, skip + k, w);
         wait(&sm.vfree[buf], ((it >> 1) & 1) ^ 1);
         __syncwarp();
-        if (slot0 + kTile > full || !tile_whole<kWin>(p, x, slot0)) {
+        if (tile_edge<kWin>(p, x, skip + k, full)) {
           if (wtid < 4) sm.vnan[buf][wtid] = 0;
           widen_sync();
           scrub_values<D, kWidenThreads>(
@@ -521,22 +523,18 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       for (int k = quad < quads ? k0 : cnt; k < cnt; k += step, ++use) {
         const int tile = it + k, buf = tile & 1;
         const float4 *page = pages + (tile % F::kPages * 8 + 4 * half);
-        int slot0;
         bool edge;
         if constexpr (kWin) {
           wait(&sm.cfull[tile % F::kPages], (tile / F::kPages) & 1);
-          const int at = __float_as_int(page->w);
-          slot0 = at & ~kEdge;
-          edge = __any_sync(0xffffffffu, at & kEdge);   // (the same in all lanes, and known to be)
+          edge = __any_sync(0xffffffffu, __float_as_int(page->w) & kEdge);   // (the same in all lanes, and known to be)
         } else {
-          slot0 = (skip + k) * kTile;
-          edge = slot0 > plain;
+          edge = (skip + k) * kTile > plain;
         }
         uint32_t see[2] = {~0u, ~0u};
         if (edge)
 #pragma unroll
           for (int w = 0; w < 2; ++w) {
-            const int from = slot0 + 64 * half + 32 * w;
+            const int from = kWin ? __float_as_int(page[2 * w].w) & ~kEdge : (skip + k) * kTile + 64 * half + 32 * w;
             see[w] = live ? seen_bits(p, x.b, i, from - x.len, x.n) : 0u;
             if (kWin) see[w] &= window_bits(from, lo, p.sinks);
           }

@@ -198,7 +198,8 @@ __host__ __device__ constexpr uint32_t attn_idesc(int M, int N, bool mn_major) {
 // ------------------------------------------------------------------ the line of tiles
 
 // With a window: the first slot of any row's window, and of the last row's (every row's window has begun by
-// then); of the tiles from 0 on, `gap` are left out after the first `head` ones, which hold the sinks.
+// then); of the slots from 0 on, `gap` are left out after the first `head` ones, which hold the sinks (both whole
+// pages and multiples of 32).
 template <bool kWin> struct WindowPart {
   int lo, lo_all, head, gap;
 };
@@ -245,26 +246,32 @@ __device__ __forceinline__ void item_span(const AttnArgs &p, Item<kWin> &x) {
     const int last = p.a.mask ? p.a.N - 1 : x.end - 1 - x.len;
     x.lo = max(0, x.len + first - p.window + 1);
     x.lo_all = max(0, x.len + last - p.window + 1);
-    const int low = min(x.lo / kTile, x.tiles - 1);   // the window's first tile
-    x.head = min((min(p.sinks, x.end) + kTile - 1) / kTile, low);
-    x.gap = low - x.head;
-    x.tiles -= x.gap;
+    const int grain = max(p.a.page, 32);
+    const int low = min(x.lo, x.end - 1) & -grain, early = (min(p.sinks, x.end) + grain - 1) & -grain;
+    if (low > early) {
+      x.head = early;
+      x.gap = low - early;
+    }
+    x.tiles = tiles_for(x.end - x.gap);
   }
 }
-// The slot that tile k of the item begins with.
+// The tokens of an item's tiles are its slots in order, but for the gap: the slot that token v is in.
 template <bool kWin>
-__device__ __forceinline__ int tile_slot(const Item<kWin> &x, int k) {
-  return (kWin && k >= x.head ? k + x.gap : k) * kTile;
+__device__ __forceinline__ int slot_of(const Item<kWin> &x, int v) {
+  return kWin && v >= x.head ? v + x.gap : v;
 }
 // Whether some row's window, or the sinks, reach into slots [slot, slot + n).
 template <bool kWin>
 __device__ __forceinline__ bool span_seen(const AttnArgs &p, const Item<kWin> &x, int slot, int n) {
   return !kWin || slot + n > x.lo || slot < p.sinks;
 }
-// Whether the windows leave out none of a tile's slots, for any row.
+// Whether some row does not see all of tile k; slots below `full` are hidden from none but by its window.
 template <bool kWin>
-__device__ __forceinline__ bool tile_whole(const AttnArgs &p, const Item<kWin> &x, int slot0) {
-  return !kWin || slot0 >= x.lo_all || slot0 + kTile <= p.sinks;
+__device__ __forceinline__ bool tile_edge(const AttnArgs &p, const Item<kWin> &x, int k, int full) {
+  const int v = k * kTile, s = slot_of<kWin>(x, v);
+  if (!kWin) return v + kTile > full;
+  if (v < x.head && v + kTile > x.head) return true;   // sinks and window
+  return s + kTile > full || (s < x.lo_all && s + kTile > p.sinks);
 }
 
 // The first slot in the window of new token i, whose position is its slot's, or in a tree its depth's.
@@ -317,8 +324,8 @@ __device__ __forceinline__ int range_of(int T, int t, int G) {
 // Whoever's share holds an end of the range finds the item there. (One thread that went through the row tiles
 // one after another took 94000 clocks for 47 of them.)
 //
-// Ranges are equal, but for this: with a window (items are short there), where shares of whole items would be at
-// most kWhole tiles longer, the CTAs take those. Then no item has parts that are written, read back and joined,
+// Ranges are equal, but for this: where windows make items short, and shares of whole items would be at most
+// kWhole tiles longer, the CTAs take those. Then no item has parts that are written, read back and joined,
 // which costs more than the tiles.
 template <bool kWin> struct LocateScratch {
   int warp_sum[32], warp_most[32];
@@ -327,7 +334,8 @@ template <bool kWin> struct LocateScratch {
 };
 // The sum over the lanes of the tiles of one key head of x.b, 32 row tiles at a time; all lanes.
 template <int NT, bool kWin>
-__device__ __forceinline__ int warp_head_tiles(const AttnArgs &p, Item<kWin> &x, int lane, int &most) {
+__device__ __forceinline__ int warp_head_tiles(const AttnArgs &p, Item<kWin> &x, int lane, int &most,
+                                               int &gaps) {
   x.ok = kv_lengths(p.a, x.b, x.len, x.n);
   int s = 0;
 #pragma unroll 1
@@ -335,6 +343,7 @@ __device__ __forceinline__ int warp_head_tiles(const AttnArgs &p, Item<kWin> &x,
     item_span<NT, kWin>(p, x);
     s += x.tiles;
     most = max(most, x.tiles);
+    gaps |= x.gap;
   }
   return __reduce_add_sync(0xffffffffu, s);
 }
@@ -347,18 +356,22 @@ __device__ __forceinline__ void search_line(const AttnArgs &p, LocateScratch<kWi
   const int share = (p.a.B + sharers - 1) / sharers;
   const int lo = min(p.a.B, me * share), hi = min(p.a.B, lo + share);
   Item<kWin> y{};
-  int mine = 0, most = 0;
+  int mine = 0, most = 0, gaps = 0;
 #pragma unroll 1
   for (y.b = lo; y.b < hi; ++y.b) {
     if (one) {
       item_load<NT, kWin>(p, y);
       mine += y.tiles * p.a.Hkv;
       most = max(most, y.tiles);
+      gaps |= y.gap;
     } else {
-      mine += warp_head_tiles<NT, kWin>(p, y, lane, most) * p.a.Hkv;
+      mine += warp_head_tiles<NT, kWin>(p, y, lane, most, gaps) * p.a.Hkv;
     }
   }
-  if (kWin) most = __reduce_max_sync(0xffffffffu, most);
+  if (kWin) {   // (a gap: some item is shorter for its window)
+    most = __reduce_max_sync(0xffffffffu, most);
+    gaps = __any_sync(0xffffffffu, gaps != 0);
+  }
   int incl = mine;   // of the thread's share within the warp
   if (one)
 #pragma unroll
@@ -368,7 +381,7 @@ __device__ __forceinline__ void search_line(const AttnArgs &p, LocateScratch<kWi
     }
   if (lane == 31) {
     sm.warp_sum[warp] = incl;
-    if (kWin) sm.warp_most[warp] = most;
+    if (kWin) sm.warp_most[warp] = 2 * most + gaps;
   }
   __syncthreads();
   const int w = lane < kWarps ? sm.warp_sum[lane] : 0;
@@ -381,10 +394,12 @@ __device__ __forceinline__ void search_line(const AttnArgs &p, LocateScratch<kWi
   const int all = __shfl_sync(0xffffffffu, upto, 31);
   const int G = gridDim.x;
   if constexpr (kWin) {
-    most = __reduce_max_sync(0xffffffffu, lane < kWarps ? sm.warp_most[lane] : 0);
+    const int known = lane < kWarps ? sm.warp_most[lane] : 0;
+    most = __reduce_max_sync(0xffffffffu, known) >> 1;
+    gaps = __any_sync(0xffffffffu, known & 1);
     const int items = p.a.B * p.a.Hkv * p.RT;
     const int each = (items + G - 1) / G;
-    if (static_cast<long long>(each) * most <= all / G + kWhole) {   // (so the numbers below are small)
+    if (gaps && static_cast<long long>(each) * most <= all / G + kWhole) {   // (so the numbers below are small)
       const int i0 = range_start(items, blockIdx.x, G), n = range_start(items, blockIdx.x + 1, G) - i0;
       if (warp == 0) {
         int sum = 0;
@@ -422,7 +437,7 @@ __device__ __forceinline__ void search_line(const AttnArgs &p, LocateScratch<kWi
         item_load<NT, kWin>(p, y);
         per_head = y.tiles;
       } else {
-        per_head = warp_head_tiles<NT, kWin>(p, y, lane, most);
+        per_head = warp_head_tiles<NT, kWin>(p, y, lane, most, gaps);
       }
       left = first - at;
       if (left < per_head * p.a.Hkv) break;
@@ -583,16 +598,17 @@ template <int D, int kThreads> struct Widen {
   static constexpr int kRows = kThreads / kLanes;   // tokens a step
   static constexpr int kSteps = kTile / kRows;
 };
-// Tokens of the tile that no row sees (before `from` and not below `sinks`, or from `valid` on) count as zeros.
+// Tokens of tile k that no row sees count as zeros.
 template <int D, int kThreads, bool kWin>
-__device__ __forceinline__ void fetch_values(const uint8_t *sv, int gtid, int valid, int from, int sinks,
-                                             uint4 (&w)[Widen<D, kThreads>::kSteps]) {
+__device__ __forceinline__ void fetch_values(const AttnArgs &p, const Item<kWin> &x, const uint8_t *sv, int gtid,
+                                             int k, uint4 (&w)[Widen<D, kThreads>::kSteps]) {
   using W = Widen<D, kThreads>;
 #pragma unroll
   for (int u = 0; u < W::kSteps; ++u) {
     const int t = u * W::kRows + gtid / W::kLanes;
     w[u] = *reinterpret_cast<const uint4 *>(sv + t * D + gtid % W::kLanes * 16);
-    if (t >= valid || (kWin && t < from && t >= sinks)) w[u] = make_uint4(0, 0, 0, 0);
+    const int slot = slot_of<kWin>(x, k * kTile + t);
+    if (slot >= x.end || !span_seen<kWin>(p, x, slot, 1)) w[u] = make_uint4(0, 0, 0, 0);
   }
 }
 __device__ __forceinline__ uint32_t nan_codes(uint32_t w) {   // bit 7 of each NaN byte
