@@ -28,9 +28,10 @@ constexpr double kLog2ed = 1.44269504088896340736;
 // logarithm: 2^(l log2 e - R), so that units are joined by powers of two. Beyond it (where R would not be an
 // exact fp32 integer with room for a fraction) against its maximum itself.
 constexpr float kPlainMax = 1048576.f;
-// The bound of a unit sum's relative error: 2^-22 of ex2; two roundings of the exponent, 2^-24 |t| ln 2 each, where
-// |t| of 2048 terms below one of at least 2^-1 is at most 8 on average; 16 roundings of sums. And that of a sum
-// taken again (exp_pair), with what its logarithm adds.
+// The bound of a unit sum's relative error, 1.8e-6: 2^-22 of ex2; the rounding of the exponent, 2^-24 |t| ln 2, and
+// what log2(e)'s second word leaves of it, 10^-8 |t|, where |t| of 2048 terms below one of at least 2^-1 is at most 8
+// on average; 18 roundings of sums and of the second word's factor. And that of a sum taken again (exp_pair), with
+// what its logarithm adds.
 constexpr float kCoarse = 2e-6f, kFine = 2e-10f;
 
 __device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
@@ -127,14 +128,14 @@ __global__ void __launch_bounds__(256, 4) beam_stream_kernel(const __grid_consta
       f32x2 acc[4] = {pk2(0.f, 0.f), pk2(0.f, 0.f), pk2(0.f, 0.f), pk2(0.f, 0.f)};
       if (fabsf(m) < kPlainMax) {
         const float R = unit_ref(m);
-        const f32x2 hi = pk2(kLog2eHi, kLog2eHi), lo = pk2(kLog2eLo, kLog2eLo), nr = pk2(-R, -R);
+        const f32x2 hi = pk2(kLog2eHi, kLog2eHi), nr = pk2(-R, -R);
 #pragma unroll
         for (int j = 0; j < kVPL; ++j)
 #pragma unroll
           for (int e = 0; e < kEPV; e += 2) {
             const f32x2 x = pk2(vec_elem<E>(buf[j], e), vec_elem<E>(buf[j], e + 1));
             float t0, t1;
-            up2(fma2(x, lo, fma2(x, hi, nr)), t0, t1);
+            up2(fma2(x, hi, nr), t0, t1);
             f32x2 &c = acc[(j * (kEPV / 2) + e / 2) & 3];
             c = add2(c, pk2(ex2(t0), ex2(t1)));
           }
@@ -151,6 +152,11 @@ __global__ void __launch_bounds__(256, 4) beam_stream_kernel(const __grid_consta
       s = __fadd_rn(v0, v1);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, o));
+      // 2^(m lo) for log2(e)'s second word, with the largest logit for each: those that count are near it
+      if (fabsf(m) < kPlainMax) {
+        const float y = m * (kLog2eLo * kLn2Hi);
+        s = __fmaf_rn(s, __fmaf_rn(y * y, __fmaf_rn(y, 1.f / 6.f, 0.5f), y), s);
+      }
       if (m == INFINITY) m = NAN;
     }
     if (lane == 0) {
