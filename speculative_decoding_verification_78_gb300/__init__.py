@@ -3,9 +3,10 @@
 The C library libspec_verify.so (csrc/, declared in include/spec_verify.h) holds the kernels:
 batched chain verification by rejection sampling, greedy and stochastic tree verification, the
 temperature softmax, the drafter-side sampler and top-k, the tree-attention mask, chain
-verification fused with its LM-head GEMMs on the tensor cores, and the paged 8-bit KV cache that a
-verification step appends to, attends over and keeps the accepted path of. This package is its thin Python
-binding (argument marshalling only); see _binding.py.
+verification fused with its LM-head GEMMs on the tensor cores, the paged 8-bit KV cache that a
+verification step appends to, attends over (whole, or by a window and sinks) and keeps the accepted path
+of, the pages of that cache, and beam selection. This package is its thin Python binding (argument
+marshalling only); see _binding.py.
 """
 
 from ._binding import (  # noqa: F401

@@ -29,7 +29,9 @@
 // most two per CTA), and a second kernel joins them in order, so results do not depend on timing.
 //
 // What bounds it: HBM, which it does not quite fill. 64 sequences of about 15000 tokens, one new token,
-// 32 query and 8 key heads of 128: 322 us for 1.95 GB, 6.05 TB/s (90 % of the measured copy rate). A
+// 32 query and 8 key heads of 128: 307 us for 1.95 GB, 6.35 TB/s (94 % of the measured copy rate); with a window
+// of 4096 tokens and 4 sinks 120 us for 0.54 GB, 4.5 TB/s, for an item then ends every 33 tiles (about 9000
+// clocks: its accumulators out, the next one's first tile). A
 // tile's chain (wait, widen, scores, weights, barrier) takes a group about 3600 clocks, which two groups
 // in turn hide but for a tenth; issuing the 16 MMAs takes their own warp 950 of a tile's 1650. With one
 // group 607 us; with the MMAs issued from a branch of one lane, where their descriptors are not known to
@@ -37,7 +39,8 @@
 // added by the softmax: 362 against 333 us), the page constants worked out by the copying warp (407), scores
 // two tiles ahead of the values with the weights before the widening (390: a stage is held longer than
 // four of them last), waits without a vote, as the kernel for many rows has them (354: more spills). At 96
-// registers, what 18 warps leave, all forms but that of 16 columns and 64 dims spill 40 to 44 bytes.
+// registers, what 18 warps leave, all forms but that of 16 columns and 64 dims spill 12 to 70 bytes (with the search
+// for the first item in line 40 to 90).
 #pragma once
 
 #include "spec_kv_attn.h"
