@@ -21,9 +21,10 @@
 // One thread of the softmax warps has one token of the tile and half of the columns. Weights are
 // taken against m as it stands; only when some y exceeds m by 2^7 in a tile (one barrier with an
 // OR, which the tile needs anyway) are the maxima reduced over the tokens, the accumulators
-// rescaled and the tile taken again. m starts at -1e30, so a row's first visible token does that.
+// rescaled and the tile taken again. m starts at -1e30, so a row's first visible token does that (a group's
+// first tile of an item has its maxima taken before its weights).
 //
-// Work is cut evenly whatever the lengths: the 128-token tiles of all (sequence, key head, row
+// Work is cut evenly whatever the lengths (but see search_line): the 128-token tiles of all (sequence, key head, row
 // tile) items form one line, CTA c of G takes tiles [T c / G, T (c+1) / G). An item inside one
 // CTA's range is written directly; the parts of one that crosses ranges go to the workspace (at
 // most two per CTA), and a second kernel joins them in order, so results do not depend on timing.
