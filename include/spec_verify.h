@@ -298,7 +298,7 @@ int spec_topk(const void *logits, int dtype, int rows, int V, int k, int32_t *ou
  *   - A NaN or +inf score, or an invalid logits row of a beam in use, makes the whole batch row -1 with NaN
  *     scores and sets *status (SPEC_ERR_NONFINITE).
  *   logits [B, K, V] dtype     scores [B, K] fp32     done [B, K] int32 or NULL
- *   tokens, parents [B, n] int32 out     out_scores [B, n] fp32 out (apart from scores)
+ *   tokens, parents [B, n] int32 out     out_scores [B, n] fp32 out (none over scores or done)
  *   workspace  at least spec_beam_workspace_bytes(B, K, V, dtype) bytes (scratch)
  * Limits: 1 <= K <= SPEC_MAX_BEAMS, 1 <= n <= SPEC_MAX_BEST, 1 <= V <= SPEC_MAX_V, 0 <= pad_token < V, B >= 0
  * (B == 0 does nothing); units of 4 KB of a row's logits are counted in 31 bits over all rows.

@@ -6,6 +6,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <initializer_list>
+
 #include "spec_beam.h"
 #include "spec_launch.h"
 #include "spec_verify.h"
@@ -53,6 +55,11 @@ Layout layout(long long B, long long R, long long C) {
 }
 
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+bool apart(const void *p, const void *q, size_t n, size_t m) {   // n bytes from p, m from q
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return a + n <= b || b + m <= a;
+}
 
 bool temp_ok(float T) { return T == 0.f || (T >= FLT_MIN && T <= FLT_MAX); }
 
@@ -606,7 +613,12 @@ int spec_beam_select(const void *logits, int dtype, const float *scores, const i
       !aligned(tokens, 4) || !aligned(parents, 4) || !aligned(out_scores, 4) || !aligned(status, 4) ||
       !aligned(workspace, 16))
     return SPEC_ERR_ALIGN;
-  if (scores == out_scores) return SPEC_ERR_SHAPE;
+  // (a batch row's results may be written before another's scores are read)
+  const size_t in_bytes = 4 * static_cast<size_t>(B) * K, out_bytes = 4 * static_cast<size_t>(B) * n;
+  for (const void *out : {static_cast<const void *>(tokens), static_cast<const void *>(parents),
+                          static_cast<const void *>(out_scores)})
+    if (!apart(out, scores, out_bytes, in_bytes) || (done && !apart(out, done, out_bytes, in_bytes)))
+      return SPEC_ERR_SHAPE;
   if (workspace_bytes < spec_beam_workspace_bytes(B, K, V, dtype)) return SPEC_ERR_WORKSPACE;
   BeamArgs a{};
   a.logits = logits;

@@ -539,7 +539,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             tc::fence_after_sync();
             maxima<F, true>(tk, see, ts, col0, qs, gnm, lane, wmax + quad * F::NT, l);
           }
-          group_sync(grp);   // new references
+          if (first)
+            again = group_any(grp, nan);   // NaN values among the tile's: marked at the weights at once
+          else
+            group_sync(grp);
+          // new references
           if (gtid < F::NT) {
             const float m = fmaxf(fmaxf(wmax[gtid], wmax[F::NT + gtid]),
                                   fmaxf(wmax[2 * F::NT + gtid], wmax[3 * F::NT + gtid]));

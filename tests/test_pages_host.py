@@ -92,8 +92,8 @@ def test_workspaces(sv):
 
 
 def _select(sv, **kw):
-    c = dict(logits=FAKE, dtype=1, scores=FAKE, done=None, pad=0, B=2, K=4, V=1000, n=8, tokens=FAKE, parents=FAKE,
-             out=FAKE + 64, status=FAKE, ws=FAKE, wsb=1 << 20, stream=None)
+    c = dict(logits=FAKE, dtype=1, scores=FAKE, done=None, pad=0, B=2, K=4, V=1000, n=8, tokens=FAKE + 64,
+             parents=FAKE + 64, out=FAKE + 64, status=FAKE, ws=FAKE, wsb=1 << 20, stream=None)
     c.update(kw)
     return sv.load_library().spec_beam_select(*c.values())
 
@@ -107,6 +107,16 @@ def _select(sv, **kw):
     (dict(done=FAKE + 2), -6), (dict(ws=FAKE + 8), -6), (dict(out=FAKE), -2), (dict(wsb=8), -5)])
 def test_select_refusals(sv, bad, code):
     assert _select(sv, **bad) == code
+
+
+def test_select_outputs_over_inputs(sv):
+    far = dict(logits=FAKE, scores=FAKE + 4096, done=FAKE + 8192, tokens=FAKE + 12288, parents=FAKE + 16384,
+               out=FAKE + 20480, wsb=1)   # (refused for its workspace, after the outputs were found fine)
+    assert _select(sv, **far) == sv.SPEC_ERR_WORKSPACE
+    for name in ("tokens", "parents", "out"):
+        for at in (4096 - 60, 4096, 4096 + 28, 8192 + 4):
+            assert _select(sv, **{**far, name: FAKE + at}) == sv.SPEC_ERR_SHAPE
+    assert _select(sv, **{**far, "out": FAKE + 4096 + 32}) == sv.SPEC_ERR_WORKSPACE
 
 
 def test_reorder_refusals(sv):
