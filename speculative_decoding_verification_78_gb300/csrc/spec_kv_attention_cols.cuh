@@ -319,6 +319,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   }
   if (tid < 2 * kTile) sm.vnan[tid / kTile][tid % kTile] = 0;
   if (warp == kMma) tmem_alloc(&sm.tmem, F::kTmem);
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // what is above may run under the kernel before
   int t0 = 0, t1 = 0, total = 0, skip = 0;
   Item<F::kWin> x{};
   tc::fence_before_sync();
@@ -493,11 +494,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const int slot = slot_of<F::kWin>(x, (skip + k) * kTile + row);
         wait(&sm.full[s], (n / F::S) & 1);
         uint4 w[Widen<F::D, kGroupThreads>::kSteps];
+        const bool masked = tile_edge<F::kWin>(p, x, skip + k, min(x.len, x.end));
         fetch_values<F::D, kGroupThreads, F::kWin>(p, x, smem + s * 2 * F::kSideBytes + F::kSideBytes, gtid,
-                                                   skip + k, w);
+                                                   skip + k, masked, w);
         const float ks = sm.ks[s][row >> p.a.page_shift], vs = sm.vs[s][row >> p.a.page_shift];
         wait(&sm.pfree[grp], (use & 1) ^ 1);
-        const bool masked = tile_edge<F::kWin>(p, x, skip + k, min(x.len, x.end));
         const bool nan = masked && scrub_values<F::D, kGroupThreads>(
                                        w, gtid, [&](int at) { vnan[at] = 1; });
         widen<F::D, kGroupThreads>(w, sv16, gtid);
@@ -511,7 +512,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         tk.lvs = __log2f(vse);
         tk.ivs = vs == vs ? __frcp_rn(vse) : 1.f;
         uint32_t see = ~0u;
-        if (slot >= x.end || !span_seen<F::kWin>(p, x, slot, 1)) {
+        if ((!F::kWin || masked) && (slot >= x.end || !span_seen<F::kWin>(p, x, slot, 1))) {
           see = 0;   // (no scale was copied for a page that no row sees)
           tk.ks2 = tk.lvs = tk.ivs = 0.f;
         } else if (masked) {
@@ -707,10 +708,7 @@ cudaError_t launch_cfg(AttnArgs &p, const CUtensorMap &mk, const CUtensorMap &mv
   cudaError_t e = allow_smem(kv_attention_kernel<F>, smem, ready);
   if (e != cudaSuccess) return e;
   plan_parts(p, ws, F::NT);
-  // In plain stream order, so the kernel waits for nothing itself; it lets its join be scheduled early.
-  // (Not measured: a launch as a programmatic dependent, whose set-up would run under the kernel before.)
-  kv_attention_kernel<F><<<ctas, kAttnThreads, smem, stream>>>(mk, mv, p);
-  e = cudaGetLastError();
+  e = launch_kv(kv_attention_kernel<F>, ctas, kAttnThreads, smem, stream, mk, mv, static_cast<const AttnArgs &>(p));
   return e != cudaSuccess ? e : launch_join<typename F::T, F::D, F::NT>(p, ctas, stream);
 }
 

@@ -252,6 +252,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     tc::mbar_fence_init();
   }
   if (warp == kMma) tmem_alloc(&sm.tmem, 512);
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // what is above may run under the kernel before
   int t0 = 0, t1 = 0, total = 0, skip = 0;
   Item<kWin> x{};
   tc::fence_before_sync();
@@ -466,10 +467,12 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         const int s = it % F::S, buf = it & 1;
         wait(&sm.full[s], (it / F::S) & 1);
         uint4 w[Widen<D, kWidenThreads>::kSteps];
-        fetch_values<D, kWidenThreads, kWin>(p, x, smem + s * 2 * F::kSideBytes + F::kSideBytes, wtid, skip + k, w);
+        const bool edge = tile_edge<kWin>(p, x, skip + k, full);
+        fetch_values<D, kWidenThreads, kWin>(p, x, smem + s * 2 * F::kSideBytes + F::kSideBytes, wtid, skip + k,
+                                             edge, w);
         wait(&sm.vfree[buf], ((it >> 1) & 1) ^ 1);
         __syncwarp();
-        if (tile_edge<kWin>(p, x, skip + k, full)) {
+        if (edge) {
           if (wtid < 4) sm.vnan[buf][wtid] = 0;
           widen_sync();
           scrub_values<D, kWidenThreads>(
@@ -691,10 +694,7 @@ cudaError_t launch_cfg(AttnArgs &p, const CUtensorMap &mk, const CUtensorMap &mv
   cudaError_t e = allow_smem(kv_attention_rows_kernel<F>, smem, ready);
   if (e != cudaSuccess) return e;
   plan_parts(p, ws, F::NT);
-  // In plain stream order, so the kernel waits for nothing itself; it lets its join be scheduled early.
-  // (Not measured: a launch as a programmatic dependent, whose set-up would run under the kernel before.)
-  kv_attention_rows_kernel<F><<<ctas, kRowsThreads, smem, stream>>>(mk, mv, p);
-  e = cudaGetLastError();
+  e = launch_kv(kv_attention_rows_kernel<F>, ctas, kRowsThreads, smem, stream, mk, mv, static_cast<const AttnArgs &>(p));
   return e != cudaSuccess ? e : launch_join<typename F::T, F::D, F::NT>(p, ctas, stream);
 }
 

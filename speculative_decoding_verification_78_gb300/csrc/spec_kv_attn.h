@@ -598,18 +598,23 @@ template <int D, int kThreads> struct Widen {
   static constexpr int kRows = kThreads / kLanes;   // tokens a step
   static constexpr int kSteps = kTile / kRows;
 };
-// Tokens of tile k that no row sees count as zeros.
+// Tokens of tile k that no row sees count as zeros. (edge: see tile_edge; with a window only such tiles have any.)
 template <int D, int kThreads, bool kWin>
 __device__ __forceinline__ void fetch_values(const AttnArgs &p, const Item<kWin> &x, const uint8_t *sv, int gtid,
-                                             int k, uint4 (&w)[Widen<D, kThreads>::kSteps]) {
+                                             int k, bool edge, uint4 (&w)[Widen<D, kThreads>::kSteps]) {
   using W = Widen<D, kThreads>;
 #pragma unroll
   for (int u = 0; u < W::kSteps; ++u) {
     const int t = u * W::kRows + gtid / W::kLanes;
     w[u] = *reinterpret_cast<const uint4 *>(sv + t * D + gtid % W::kLanes * 16);
-    const int slot = slot_of<kWin>(x, k * kTile + t);
-    if (slot >= x.end || !span_seen<kWin>(p, x, slot, 1)) w[u] = make_uint4(0, 0, 0, 0);
+    if (!kWin && k * kTile + t >= x.end) w[u] = make_uint4(0, 0, 0, 0);
   }
+  if (kWin && edge)
+#pragma unroll
+    for (int u = 0; u < W::kSteps; ++u) {
+      const int slot = slot_of<kWin>(x, k * kTile + u * W::kRows + gtid / W::kLanes);
+      if (slot >= x.end || !span_seen<kWin>(p, x, slot, 1)) w[u] = make_uint4(0, 0, 0, 0);
+    }
 }
 __device__ __forceinline__ uint32_t nan_codes(uint32_t w) {   // bit 7 of each NaN byte
   return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
