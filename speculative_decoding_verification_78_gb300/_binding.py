@@ -81,6 +81,8 @@ def load_library(checked: bool = False):
     """Loads libspec_verify.so (built in-tree by __graft_entry__.build()), or with
     checked=True its checked build libspec_verify_checked.so."""
     global _lib, _checked_lib
+    if _lib is not None and not checked:   # (set once, when it is ready)
+        return _lib
     with _lock:
         if (_checked_lib if checked else _lib) is not None:
             return _checked_lib if checked else _lib
@@ -488,7 +490,7 @@ def _operand(t, name, numel, dtype):
     _expect and _ptr in one pass."""
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.numel() != numel:
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.numel() != numel:
         _expect(t, name, numel, (dtype,))
     if not t.is_contiguous() or not t.is_cuda:
         return _ptr(t)   # raises, or an empty tensor
@@ -700,7 +702,7 @@ def spec_beam_reorder(states, parents, outs, status, stream=None) -> int:
     arr = _state_array(len(states))()
     for i, (t, o) in enumerate(zip(states, outs)):
         a, b = t.shape, o.shape
-        if a[0] != R or b[0] != C or a[1:] != b[1:] or t.dtype != o.dtype:
+        if a[0] != R or b[0] != C or (a != b if R == C else a[1:] != b[1:]) or t.dtype is not o.dtype:
             raise ValueError(f"state {i}: {tuple(a)} {t.dtype} to {tuple(b)} {o.dtype}, "
                              f"with {R} rows to {C}")
         n, m = t.numel(), o.numel()
@@ -1082,7 +1084,8 @@ def beam_reorder(states, parents, outs=None, status=None, stream=None):
     (the reordered tensors ..., status)."""
     C = parents.numel()
     if outs is None:
-        outs = [torch.empty((C, *t.shape[1:]), dtype=t.dtype, device=t.device) for t in states]
+        outs = [torch.empty_like(t) if t.shape[0] == C else
+                torch.empty((C, *t.shape[1:]), dtype=t.dtype, device=t.device) for t in states]
     status = _status(status, parents.device)
     check(spec_beam_reorder(states, parents, outs, status, stream), "spec_beam_reorder")
     return (*outs, status)

@@ -629,8 +629,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           wt[g] = ex2(m - nm[g * F::NT + tid]);   // 0 for a group that saw nothing, beside one that did
         }
         const float total = sum[0] * wt[0] + sum[1] * wt[1];
-        const long long r = static_cast<long long>(x.rt) * F::NT + tid;
-        const int i = static_cast<int>(r / p.G), g = static_cast<int>(r - static_cast<long long>(i) * p.G);
+        const int i = tok[tid], g = tid - i * p.G;   // (a row past the last has g >= G)
         float lse2 = total == 0.f ? -INFINITY : log2f(total) - m;
         float f = total == 0.f ? 0.f : 1.f / total;
         if (!x.ok) {
@@ -643,13 +642,17 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         fac[F::NT + tid] = sum[1] == 0.f ? 0.f * f : wt[1] * f;
         if (!whole)
           p.part_lse[part * F::NT + tid] = lse2;
-        else if (p.lse && i < p.a.N)
+        else if (p.lse && g < p.G)
           p.lse[(static_cast<long long>(x.b) * p.a.N + i) * p.a.Hq + static_cast<long long>(x.h) * p.G + g] =
               lse2 * kLn2;
       }
       soft_sync();
       using T = typename F::T;
       const int e0 = (warp >> 2) * F::EC;
+      // (at most 32 rows: offsets within an item's results are small)
+      T *out = static_cast<T *>(p.out) + (static_cast<long long>(x.b) * p.a.N * p.a.Hq +
+                                          static_cast<long long>(x.h) * p.G) * F::D + row;
+      float *po = p.part_o + part * F::NT * F::D + row;
 #pragma unroll 1
       for (int c0 = e0; c0 < e0 + F::EC; c0 += F::ECH) {
         uint32_t o[F::ECH], o1[F::ECH];
@@ -667,15 +670,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                             (f1 == 0.f ? 0.f : __uint_as_float(o1[c]) * f1);
             if (!SPEC_CHECK(p.a, n < F::NT && part < 2LL * gridDim.x && x.b < p.a.B)) continue;
             if (!whole) {
-              p.part_o[(part * F::NT + n) * F::D + row] = v;
+              po[n * F::D] = v;
             } else {
-              const long long r = static_cast<long long>(x.rt) * F::NT + n;
-              const int i = tok[n];
-              const long long g = r - static_cast<long long>(i) * p.G;
-              if (g < p.G)
-                static_cast<T *>(p.out)[((static_cast<long long>(x.b) * p.a.N + i) * p.a.Hq +
-                                         static_cast<long long>(x.h) * p.G + g) * F::D + row] =
-                    static_cast<T>(v);
+              const int i = tok[n], g = n - i * p.G;
+              if (g < p.G) out[(i * p.a.Hq + g) * F::D] = static_cast<T>(v);
             }
           }
         }

@@ -229,7 +229,7 @@ __device__ __forceinline__ void fork_child(const PageArgs &a, const ForkArgs &f,
 __device__ __forceinline__ void fork_parent(const PageArgs &a, const ForkArgs &f, int p, int n, int me,
                                             int step) {
   const Parent x = parent_of(a, p);
-  if (!x.ok && me == 0) set_status(a.status, SPEC_ERR_LENGTH);
+  if (!x.ok && f.release && me == 0) set_status(a.status, SPEC_ERR_LENGTH);   // (else its children say so)
   const int32_t *row = a.table + static_cast<long long>(p) * a.pps;
   for (int j = me; j < a.pps; j += step) {
     const int page = row[j];

@@ -250,6 +250,23 @@ def test_fork_bad_tables(sv, release):
     w.check(d_refs, (got_t, want[0]), (got_n, want[1]))
 
 
+def test_fork_leaves_others_alone(sv):
+    """A parent with a bad length that no child continues from is nobody's error, unless it ends."""
+    w = World(sv, 20, 50)
+    table, lens = w.sequences([37, 40], 6)
+    lens[1] = -1
+    parents = np.array([0, 0], np.int32)
+    d_refs, d_table, d_lens, d_par = w.up(w.refs, table, lens, parents)
+    got_t, got_n, _ = sv.kv_fork(w.cache, d_refs, d_table, d_lens, d_par, status=w.status)
+    want = ref.fork(w.refs, table, lens, parents, False, 16, w.pools, w.scales, w.codes)
+    assert not w.codes
+    w.check(d_refs, (got_t, want[0]), (got_n, want[1]))
+    sv.kv_fork(w.cache, d_refs, d_table, d_lens, d_par, release=True, status=w.status)
+    ref.fork(w.refs, table, lens, parents, True, 16, w.pools, w.scales, w.codes)
+    assert set(w.codes) == {ref.LENGTH}
+    w.check(d_refs)
+
+
 @pytest.mark.parametrize("P,B,page,Hkv,D,layers", [(1, 1, 16, 1, 64, 1), (40, 3, 16, 2, 64, 2), (3000, 60, 16, 1, 64, 1),
                                                    (70, 4, 128, 8, 128, 3), (33, 2, 64, 3, 128, 1)])
 @pytest.mark.parametrize("share", [0.0, 0.3, 1.0])
