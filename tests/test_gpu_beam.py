@@ -197,6 +197,22 @@ def test_scores_nearer_than_fp32_tells(sv, V):
         check(sv, logits, scores, n)
 
 
+@pytest.mark.parametrize("V", [500, 29270])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
+def test_rows_that_one_token_fills(sv, V, dtype):
+    """Beams with equal scores and largest logits, whose sums differ by less than fp32 holds beside that token: by 3e-9
+    and more, which is told apart, or not at all."""
+    x = np.full((3, 4, V), -60.0)              # all of these together: below 1e-21 of the sum
+    x[:, :, V // 3] = 0.0
+    x[0, :, V - 2] = -18.0, -18.5, -19.0, -20.0      # exp: 15.2e-9, 9.2e-9, 5.6e-9, 2.1e-9; 1 in fp32 with the 1
+    x[1, :, V - 2] = -18.5, -20.0, -18.5, -20.0
+    x[2, :, V - 2] = -18.0
+    logits = torch.from_numpy(x).to(dtype).cuda()
+    scores = torch.full((3, 4), -1.5, device="cuda")
+    for n in (1, 3, 4, 8, 10):
+        check(sv, logits, scores, n)
+
+
 def test_extreme_logits(sv):
     """Magnitudes at which fp32 has no fractions left, up to its largest."""
     rng = np.random.default_rng(8)
