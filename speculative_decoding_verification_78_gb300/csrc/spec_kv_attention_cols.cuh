@@ -30,8 +30,8 @@
 // most two per CTA), and a second kernel joins them in order, so results do not depend on timing.
 //
 // What bounds it: HBM, which it does not quite fill. 64 sequences of about 15000 tokens, one new token,
-// 32 query and 8 key heads of 128: 307 us for 1.95 GB, 6.35 TB/s (94 % of the measured copy rate); with a window
-// of 4096 tokens and 4 sinks 120 us for 0.54 GB, 4.5 TB/s, for an item then ends every 33 tiles (about 9000
+// 32 query and 8 key heads of 128: 299 us for 1.95 GB, 6.5 TB/s (96 % of the measured copy rate); with a window
+// of 4096 tokens and 4 sinks 112 us for 0.54 GB, 4.8 TB/s, for an item then ends every 33 tiles (about 9000
 // clocks: its accumulators out, the next one's first tile). A
 // tile's chain (wait, widen, scores, weights, barrier) takes a group about 3600 clocks, which two groups
 // in turn hide but for a tenth; issuing the 16 MMAs takes their own warp 950 of a tile's 1650. With one
