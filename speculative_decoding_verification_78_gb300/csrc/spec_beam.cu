@@ -38,6 +38,7 @@ constexpr float kPlainMax = 1048576.f;
 // on average; 18 roundings of sums and of the second word's factor. And that of a sum taken again (exp_pair), with
 // what its logarithm adds.
 constexpr float kCoarse = 2e-6f, kFine = 2e-10f;
+constexpr int kRounds = 16;   // in which sums are improved as far as a gap asks for; then whole rows are summed
 
 __device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
   f32x2 r;
@@ -314,7 +315,7 @@ struct FinishShared {
   int unit[SPEC_MAX_BEST];     // chosen units, in order
   Pick head[SPEC_MAX_BEST];    // the best of each that is left; place: the token
   double sum[kFinishWarps];
-  int bad, again;
+  int bad, again, round;
   float least;
   unsigned long long rest;
 };
@@ -368,7 +369,8 @@ struct Finish {
     const float2 u = from_order(x), v = from_order(y);
     const float gap = fabsf(__fadd_rn(__fsub_rn(u.x, v.x), __fsub_rn(u.y, v.y)));
     if (!(gap <= sh.slack[k] + sh.slack[j])) return;
-    const float to = fmaxf(0.4f * gap, kFine);   // (0 as well: sums that fp32 rounds alike are not the same yet)
+    // 0 as well: sums that fp32 rounds alike are not the same yet
+    const float to = sh.round < kRounds ? 0.4f * gap : 0.f;
     want(k, to);
     want(j, to);
   }
@@ -493,7 +495,7 @@ struct Finish {
   __device__ __forceinline__ void refine(int k) const {
     const float M = sh.top[k], target = __int_as_float(sh.target[k]);
     for (int j = 0; j < k; ++j)
-      if (sh.kind[j] == kLive && sh.s[j] == sh.s[k] && sh.top[j] == M && sh.slack[j] <= target) {
+      if (sh.kind[j] == kLive && sh.s[j] == sh.s[k] && sh.top[j] == M && sh.slack[j] <= fmaxf(target, kFine)) {
         if (!same_row(k, j)) break;   // (what else there is that looks the same is not searched for)
         if (tid == 0) {
           sh.best_of[k] = sh.best_of[j];
@@ -513,7 +515,7 @@ struct Finish {
     }
     if (tid == 0) sh.least = 0.f;
     __syncthreads();
-    if (warp == 0 && plain) {   // a threshold a lane: 2^(10 - lane); the largest that leaves out little enough
+    if (warp == 0 && plain && target > kFine) {   // a threshold a lane: 2^(10 - lane); the largest that leaves out little enough
       const float at = ldexpf(1.f, 10 - lane);
       float all = 0.f, out = 0.f;
       for (int c = 0; c < a.C; ++c) {
@@ -559,7 +561,8 @@ struct Finish {
       const double x = log(all + out);
       const float hi = static_cast<float>(x);
       set_sum(k, M, hi, static_cast<float>(x - hi));
-      sh.slack[k] = kFine + static_cast<float>(out / (all + out)) * kCoarse;
+      // not above what was asked for, whatever was rounded: else the same would be asked for again
+      sh.slack[k] = least > 0.f ? fminf(kFine + static_cast<float>(out / (all + out)) * kCoarse, target) : kFine;
       sh.target[k] = 0x7f800000;
     }
     __syncthreads();
@@ -970,7 +973,11 @@ __global__ void __launch_bounds__(kFinishThreads, 1) beam_finish_kernel(const __
     }
     return;
   }
-  for (;;) {   // each time around the sums of two beams are better than before; they end at kFine
+  // Each time around, a beam's slack comes down: to its target or, where that is kFine or less, to kFine, below which
+  // nothing is asked for. From round kRounds on all targets are 0, so it ends after kRounds + K at the latest.
+  for (int round = 0; round <= kRounds + SPEC_MAX_BEAMS; ++round) {
+    if (tid == 0) sh.round = round;
+    __syncthreads();
     const int done = f.select_few();
     if (done == 1) return;
     __syncthreads();

@@ -213,6 +213,26 @@ def test_rows_that_one_token_fills(sv, V, dtype):
         check(sv, logits, scores, n)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
+def test_equal_beams_with_a_little_elsewhere(sv, dtype):
+    """Equal beams, part of whose sums (1e-13 to 1e-11 of them) is too little for the finest sums asked for, but not 0."""
+    V = 9000
+    x = np.full((40, 3, V), -60.0)
+    x[:, :, 10] = 0.0
+    x[:, :, 11] = np.linspace(-1.5, 0.0, 8).repeat(5)[:, None]
+    x[:, :, V - 3] = np.tile(np.linspace(-29.0, -25.0, 20), 2)[:, None]
+    x[20:, 2, V - 3] += 0.25
+    logits = torch.from_numpy(x).to(dtype).cuda()
+    scores = torch.full((40, 3), -1.5, device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    tok, par, best, _ = sv.beam_select(logits, scores, 6, status=st)
+    wt, wp, wb = select(as64(logits), as64(scores), 6)
+    # the third beam differs from the others by less than 1e-9: the first 20 batch rows have one order, the others' scores
+    np.testing.assert_array_equal(par.cpu().numpy()[:20], wp[:20])
+    np.testing.assert_array_equal(tok.cpu().numpy()[:20], wt[:20])
+    assert (np.abs(as64(best) - wb) <= 2.0 ** -24 * np.abs(wb) + 4e-6).all() and int(st.item()) == 0
+
+
 def test_extreme_logits(sv):
     """Magnitudes at which fp32 has no fractions left, up to its largest."""
     rng = np.random.default_rng(8)
