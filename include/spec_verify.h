@@ -485,9 +485,10 @@ size_t spec_kv_pages_workspace_bytes(int num_pages, int B);
 
 /*
  * Free pages for the slots seq_lens[b] .. seq_lens[b] + new_lens[b] - 1 (new_lens NULL: N each) that have
- * none: page_table [B, pages_per_seq] and refs are brought up to date. A sequence gets all that it needs or
- * nothing: served are those whose needs and those of all sequences before them fit into the free pages
- * (a sequence that needs none always is); the others set *status (SPEC_ERR_NO_PAGE).
+ * none (or an entry of num_pages or more, which the new page replaces): page_table [B, pages_per_seq] and
+ * refs are brought up to date. A sequence gets all that it needs or nothing: served are those whose needs and
+ * those of all sequences before them fit into the free pages (a sequence that needs none always is); the
+ * others set *status (SPEC_ERR_NO_PAGE).
  *   granted [B] int32 out: new_lens[b], or 0 for a sequence that was not served or whose lengths are bad
  *           (so it may be the new_lens of spec_kv_append and spec_kv_attention)
  * A new page's contents are left as they were. Limits: 1 <= N <= 2^20.

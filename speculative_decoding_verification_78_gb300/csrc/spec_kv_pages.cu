@@ -128,8 +128,8 @@ __device__ int lowest_free(const PageArgs &a, int want, int32_t *list, int *sums
 }
 
 // One CTA. Item i of the call is place i % touched of those that sequence i / touched's new tokens can touch;
-// items without a page are numbered in order, and number r gets the r-th free page. A sequence whose last
-// number is past the free pages gets none.
+// items without a page (or with an entry past the pool, which is reported) are numbered in order, and number r gets the
+// r-th free page. A sequence whose last number is past the free pages gets none.
 __global__ void __launch_bounds__(kScanThreads) kv_reserve_kernel(const __grid_constant__ PageArgs a,
                                                                   const int32_t *new_lens, int N,
                                                                   int touched, int32_t *granted,
@@ -147,7 +147,9 @@ __global__ void __launch_bounds__(kScanThreads) kv_reserve_kernel(const __grid_c
     const int place = (len >> a.page_shift) + j;
     if (place > (len + n - 1) >> a.page_shift) return -1;
     const long long at = static_cast<long long>(b) * a.pps + place;
-    return a.table[at] < 0 ? at : -1;
+    const int page = a.table[at];
+    if (page >= a.num_pages) set_status(a.status, SPEC_ERR_PAGE);
+    return page < 0 || page >= a.num_pages ? at : -1;
   };
   int total = 0;
   for (int i0 = 0; i0 < items; i0 += kScanThreads) {
