@@ -9,9 +9,10 @@
 // Exactness. The order of two candidates of one beam is that of their logits, whatever L_k. Candidates of
 // different beams are compared by L_k from fp32 sums, whose error is bounded (kCoarse); where two that matter
 // lie nearer than that, the units that make up most of the L_k concerned are summed again to about 1e-10, as many
-// as it takes to tell the two apart, and the selection is repeated. So tokens and parents are those of exact
-// arithmetic (but for scores closer than 1e-9). The sums are taken in the order of the token numbers wherever a
-// row lies in memory, so that beams with equal logits have equal L_k.
+// as it takes to tell the two apart, and the selection is repeated. Scores are compared as integers of 192 bits, whole
+// multiples of 2^-48, which hold any sum of fp32 numbers: beside a score of -1e9 fp32 pairs lose what tells beams
+// apart. So tokens and parents are those of exact arithmetic (but for scores closer than 1e-9). The sums are taken in
+// the order of the token numbers wherever a row lies in memory, so that beams with equal logits have equal L_k.
 //
 // What bounds it: for many beams HBM while the logits stream (64 x 8 beams x 152064 in bf16: 156 MB in 26 us, 5.9
 // TB/s; 58 % of the issue slots, the rest waits for ex2 and for loads), then the finishing CTAs' chain of about ten
@@ -239,16 +240,54 @@ __device__ __forceinline__ void log_pair(unsigned long long n, float &hi, float 
 // ------------------------------------------------------------------ selection
 //
 // What bounds the selection is the chain of its steps, and 64-bit floating point, of which an SM does two
-// operations a clock (a warp's instruction takes its scheduler 64): scores are taken in 64 bits for the few
-// hundred candidates only, L_k and distances in pairs of fp32 numbers.
+// operations a clock (a warp's instruction takes its scheduler 64): L_k is a pair of fp32 numbers, and scores,
+// taken for the few hundred candidates only, are integers.
 
-// A score: two fp32 numbers, the first the sum rounded, the second what that left; as an integer in the same order
-// (no NaN; never 0).
-__device__ __forceinline__ unsigned long long order_of(float2 x) {
-  return static_cast<unsigned long long>(float_key(__fadd_rn(x.x, 0.f))) << 32 | float_key(__fadd_rn(x.y, 0.f));
+// A number as a whole multiple of 2^-48: 192 bits, two's complement (fp32's range is 2^128: sums of a few of its
+// numbers fit). Rounding to it keeps the order of numbers, and nothing is rounded after.
+struct Fixed {
+  unsigned long long lo, mid;
+  long long hi;
+};
+__device__ __forceinline__ Fixed operator+(const Fixed &x, const Fixed &y) {
+  Fixed r;
+  asm("add.cc.u64 %0, %3, %6;\n\taddc.cc.u64 %1, %4, %7;\n\taddc.u64 %2, %5, %8;"
+      : "=l"(r.lo), "=l"(r.mid), "=l"(r.hi)
+      : "l"(x.lo), "l"(x.mid), "l"(x.hi), "l"(y.lo), "l"(y.mid), "l"(y.hi));
+  return r;
 }
-__device__ __forceinline__ float2 from_order(unsigned long long k) {
-  return make_float2(key_float(static_cast<unsigned>(k >> 32)), key_float(static_cast<unsigned>(k)));
+__device__ __forceinline__ Fixed operator-(const Fixed &x, const Fixed &y) {
+  Fixed r;
+  asm("sub.cc.u64 %0, %3, %6;\n\tsubc.cc.u64 %1, %4, %7;\n\tsubc.u64 %2, %5, %8;"
+      : "=l"(r.lo), "=l"(r.mid), "=l"(r.hi)
+      : "l"(x.lo), "l"(x.mid), "l"(x.hi), "l"(y.lo), "l"(y.mid), "l"(y.hi));
+  return r;
+}
+__device__ __forceinline__ bool operator==(const Fixed &x, const Fixed &y) {
+  return x.lo == y.lo && x.mid == y.mid && x.hi == y.hi;
+}
+__device__ __forceinline__ bool operator>(const Fixed &x, const Fixed &y) {
+  return x.hi != y.hi ? x.hi > y.hi : x.mid != y.mid ? x.mid > y.mid : x.lo > y.lo;
+}
+__device__ __forceinline__ Fixed fixed_of(long long v) {   // v 2^-48
+  return Fixed{static_cast<unsigned long long>(v), static_cast<unsigned long long>(v >> 63), v >> 63};
+}
+__device__ __forceinline__ long long near_fixed(float f) { return __float2ll_rn(f * 0x1p48f); }   // |f| < 2^14
+__device__ __forceinline__ Fixed fixed_of(float f) {   // (no infinity, no NaN)
+  if (fabsf(f) < 16384.f) return fixed_of(near_fixed(f));
+  const uint32_t bits = __float_as_uint(f);
+  const unsigned long long mant = (bits & 0x7fffffu) | 0x800000u;
+  const int up = static_cast<int>(bits >> 23 & 255u) - 127 - 23 + 48, word = up >> 6, at = up & 63;   // 39 .. 152
+  const unsigned long long low = mant << at, high = at > 40 ? mant >> (64 - at) : 0ull;
+  const Fixed r{word == 0 ? low : 0ull, word == 0 ? high : word == 1 ? low : 0ull,
+                static_cast<long long>(word == 0 ? 0ull : word == 1 ? high : low)};
+  return bits >> 31 ? Fixed{0, 0, 0} - r : r;
+}
+__device__ __forceinline__ float float_of(const Fixed &x) {   // x >= 0
+  float f = static_cast<float>(x.lo) * 0x1p-48f;
+  if (x.mid | static_cast<unsigned long long>(x.hi))
+    f += static_cast<float>(x.mid) * 0x1p16f + static_cast<float>(x.hi) * 0x1p80f;
+  return f;
 }
 // (h, l) += (x, y), y and l small beside the others
 __device__ __forceinline__ void pair_add(float &h, float &l, float x, float y) {
@@ -256,36 +295,45 @@ __device__ __forceinline__ void pair_add(float &h, float &l, float x, float y) {
   l = __fadd_rn(__fadd_rn(__fsub_rn(h, __fsub_rn(t, bb)), __fsub_rn(x, bb)), __fadd_rn(l, y));
   h = t;
 }
-__device__ __forceinline__ float2 pair_of(float h, float l) {   // the first word the sum rounded
-  const float z = __fadd_rn(h, l);
-  return make_float2(z, __fsub_rn(l, __fsub_rn(z, h)));
-}
 
-// A candidate: its score (as order_of; 0: none), beam, logit and place in the beam. Equal scores go by beam;
-// within one by logit (which may differ where 64 bits of score do not), then by place.
-struct Pick {
-  unsigned long long key;
+// A candidate: its beam, logit and place in the beam.
+struct Cand {
   float l;
   int k, at;
 };
-__device__ __forceinline__ bool before(const Pick &x, const Pick &y) {
-  if (x.key != y.key) return x.key > y.key;
+// Equal scores go by beam; within one by logit (which may differ by less than scores tell), then by place.
+__device__ __forceinline__ bool before(const Cand &x, const Cand &y) {
   if (x.k != y.k) return x.k < y.k;
   return x.l > y.l || (x.l == y.l && x.at < y.at);
+}
+// One with its score; none (k: kNoBeam) comes last.
+constexpr int kNoBeam = 0x7fffffff;
+struct Pick {
+  Fixed score;
+  Cand c;
+  __device__ __forceinline__ bool some() const { return c.k != kNoBeam; }
+};
+__device__ __forceinline__ bool before(const Pick &x, const Pick &y) {
+  if (!x.some() || !y.some()) return x.some();
+  return x.score == y.score ? before(x.c, y.c) : x.score > y.score;
+}
+__device__ __forceinline__ Fixed shuffle_xor(const Fixed &x, int o) {
+  return Fixed{__shfl_xor_sync(0xffffffffu, x.lo, o), __shfl_xor_sync(0xffffffffu, x.mid, o),
+               __shfl_xor_sync(0xffffffffu, x.hi, o)};
 }
 __device__ __forceinline__ Pick warp_best(Pick p) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     Pick q;
-    q.key = __shfl_xor_sync(0xffffffffu, p.key, o);
-    q.l = __shfl_xor_sync(0xffffffffu, p.l, o);
-    q.k = __shfl_xor_sync(0xffffffffu, p.k, o);
-    q.at = __shfl_xor_sync(0xffffffffu, p.at, o);
+    q.score = shuffle_xor(p.score, o);
+    q.c.l = __shfl_xor_sync(0xffffffffu, p.c.l, o);
+    q.c.k = __shfl_xor_sync(0xffffffffu, p.c.k, o);
+    q.c.at = __shfl_xor_sync(0xffffffffu, p.c.at, o);
     if (before(q, p)) p = q;
   }
   return p;
 }
-__device__ __forceinline__ Pick no_pick() { return Pick{0, -INFINITY, 0x7fffffff, 0}; }
+__device__ __forceinline__ Pick no_pick() { return Pick{{0, 0, 0}, {-INFINITY, kNoBeam, 0}}; }
 
 constexpr int kBins = 1024, kMaxParts = 512, kMaxCands = 512;
 constexpr int kStaged = 2048;   // units whose maxima are kept in shared memory
@@ -297,16 +345,21 @@ __device__ __forceinline__ int bin_of(float d) {
   return min(max(static_cast<int>(__float_as_uint(d) >> 18) - ((127 - 8) << 5), 0), kBins - 1);
 }
 
+static_assert(SPEC_MAX_BEST <= kFinishThreads, "a thread for each result");
+
 struct FinishShared {
   float base[SPEC_MAX_BEAMS];      // how far a beam's best candidate is from the best of all
   __align__(16) int hist[kBins];
   int edge, parts, cands;
   float staged[kStaged];
   int part_list[kMaxParts];        // quarters of units: 4 unit + quarter
-  ulonglong2 key[kMaxCands];
-  Pick cand[kMaxCands];            // place: the token
+  ulonglong2 key[kMaxCands];       // a candidate's distance from the best, and what equal ones go by
+  Cand cand[kMaxCands];            // place: the token
   int order[kMaxCands];
-  float2 best_of[SPEC_MAX_BEAMS];   // a beam's best score: s - log_sum, in two words
+  Fixed offset[SPEC_MAX_BEAMS];    // what a beam's logits lack to be scores: s - top - log_sum
+  Fixed best_of[SPEC_MAX_BEAMS];   // a beam's best score
+  Fixed best_score;                // of all
+  float2 log_sum[SPEC_MAX_BEAMS];  // L_k - top: the sum of two words
   float s[SPEC_MAX_BEAMS], top[SPEC_MAX_BEAMS];
   int kind[SPEC_MAX_BEAMS];
   float slack[SPEC_MAX_BEAMS];     // how far L_k may be off
@@ -327,6 +380,8 @@ __device__ __noinline__ float2 large_sum_apart(const BeamArgs &a, FinishShared &
 template <typename E>
 __device__ __noinline__ void refine_apart(const BeamArgs &a, FinishShared &sh, int b, int k);
 template <typename E>
+__device__ __noinline__ int rank_far_apart(const BeamArgs &a, FinishShared &sh, int b, int count);
+template <typename E>
 __device__ __noinline__ bool select_any_apart(const BeamArgs &a, FinishShared &sh, int b);
 
 template <typename E>
@@ -344,31 +399,26 @@ struct Finish {
   // unit u = k C + chunk of the batch row, by its largest candidate
   __device__ __forceinline__ Pick unit_pick(int u) const {
     const int k = u / a.C, chunk = u - k * a.C;
-    Pick p{0, 0.f, k, chunk};
-    if (sh.kind[k] == kEnded) {
-      if (chunk == 0) p.key = order_of(sh.best_of[k]);
-    } else if (sh.kind[k] == kLive) {
-      const float m = __uint_as_float(part(u).x);
-      p.l = m;
-      if (m > -INFINITY) p.key = order_of(score(k, m));
-    }
-    return p;
+    if (sh.kind[k] == kEnded && chunk == 0) return Pick{sh.best_of[k], {0.f, k, chunk}};
+    if (sh.kind[k] != kLive) return no_pick();
+    const float m = __uint_as_float(part(u).x);
+    return m > -INFINITY ? Pick{score(k, m), {m, k, chunk}} : no_pick();
   }
-  // the score of a live beam's candidate with logit l
-  __device__ __forceinline__ float2 score(int k, float l) const {
-    float d = l, dl = 0.f;
-    pair_add(d, dl, -sh.top[k], 0.f);
-    if (!(d > -INFINITY)) return make_float2(-INFINITY, 0.f);   // beyond fp32
-    const float2 best = sh.best_of[k];
-    pair_add(d, dl, best.x, best.y);
-    return pair_of(d, dl);
+  // the score of a beam's candidate with logit l (an ended beam's: 0)
+  __device__ __forceinline__ Fixed score(int k, float l) const { return sh.offset[k] + fixed_of(l); }
+  // and as it is returned, of the words that it is made of
+  __device__ __forceinline__ float score_out(const Cand &c) const {
+    float x = sh.s[c.k], y = 0.f, d = c.l, dl = 0.f;
+    pair_add(x, y, -sh.log_sum[c.k].x, -sh.log_sum[c.k].y);
+    pair_add(d, dl, -sh.top[c.k], 0.f);
+    const float far = __fadd_rn(x, d);
+    if (!(far > -INFINITY)) return -INFINITY;   // beyond fp32
+    pair_add(x, y, d, dl);
+    return __fadd_rn(x, y);
   }
-  // two candidates whose order the sums as they are do not tell: asks for better ones
-  __device__ __forceinline__ void compare(unsigned long long x, int k, unsigned long long y, int j) const {
-    if (k == j) return;
-    const float2 u = from_order(x), v = from_order(y);
-    const float gap = fabsf(__fadd_rn(__fsub_rn(u.x, v.x), __fsub_rn(u.y, v.y)));
-    if (!(gap <= sh.slack[k] + sh.slack[j])) return;
+  // two candidates of beams k and j, `gap` apart, whose order the sums as they are do not tell: asks for better ones
+  __device__ __forceinline__ void compare(float gap, int k, int j) const {
+    if (k == j || !(gap <= sh.slack[k] + sh.slack[j])) return;
     // 0 as well: sums that fp32 rounds alike are not the same yet
     const float to = sh.round < kRounds ? 0.4f * gap : 0.f;
     want(k, to);
@@ -430,8 +480,10 @@ struct Finish {
         sh.s[k] = s;
         sh.slack[k] = live ? kCoarse : 0.f;
         sh.target[k] = 0x7f800000;
-        set_sum(k, top, h, l);
-        if (kind == kBad || (live && !(fabsf(m) < INFINITY))) sh.bad = 1;
+        if (kind == kBad || (live && !(fabsf(m) < INFINITY)))
+          sh.bad = 1;
+        else
+          set_sum(k, top, h, l);
       }
     }
   }
@@ -450,9 +502,10 @@ struct Finish {
   }
   __device__ __forceinline__ void set_sum(int k, float top, float h, float l) const {
     sh.top[k] = top;
-    float x = sh.s[k], y = 0.f;
-    pair_add(x, y, -h, -l);
-    sh.best_of[k] = pair_of(x, y);
+    sh.log_sum[k] = make_float2(h, l);
+    if (sh.kind[k] != kLive && sh.kind[k] != kEnded) return;
+    sh.best_of[k] = fixed_of(sh.s[k]) - fixed_of(near_fixed(h) + near_fixed(l));
+    sh.offset[k] = sh.best_of[k] - fixed_of(top);
   }
   // log sum_v e^(l - m) of a row whose largest logit m is too large for powers of two, in 64 bits
   __device__ __forceinline__ float2 large_sum(int k, float m) const {
@@ -498,6 +551,8 @@ struct Finish {
       if (sh.kind[j] == kLive && sh.s[j] == sh.s[k] && sh.top[j] == M && sh.slack[j] <= fmaxf(target, kFine)) {
         if (!same_row(k, j)) break;   // (what else there is that looks the same is not searched for)
         if (tid == 0) {
+          sh.log_sum[k] = sh.log_sum[j];
+          sh.offset[k] = sh.offset[j];
           sh.best_of[k] = sh.best_of[j];
           sh.slack[k] = sh.slack[j];
           sh.target[k] = 0x7f800000;
@@ -630,7 +685,7 @@ struct Finish {
   }
   __device__ __forceinline__ void push(int k, float l, int token) const {
     const int i = atomicAdd(&sh.cands, 1);
-    if (i < kMaxCands) sh.cand[i] = Pick{0, l, k, token};   // its score comes later
+    if (i < kMaxCands) sh.cand[i] = Cand{l, k, token};
   }
   // Lists (or, with `count`, counts by their distances) the listed quarters' candidates with a distance of at
   // most `most`.
@@ -694,22 +749,39 @@ struct Finish {
     return bin >= kBins - 1 ? INFINITY : __uint_as_float(static_cast<unsigned>(bin + 1 + ((127 - 8) << 5)) << 18);
   }
 
-  static __device__ __forceinline__ float2 larger(float2 x, float2 y) {
-    return y.x > x.x || (y.x == x.x && y.y > x.y) ? y : x;
+  // The places of `count` listed candidates by their whole scores.
+  __device__ __forceinline__ int rank_far(int count) const {
+    if (tid >= count) return 0;
+    const Cand me = sh.cand[tid];
+    const Fixed mine = score(me.k, me.l);
+    int rank = 0;
+#pragma unroll 1
+    for (int i = 0; i < count; ++i) {
+      const Cand c = sh.cand[i];
+      const Fixed x = score(c.k, c.l);
+      rank += x == mine ? before(c, me) : x > mine;
+    }
+    return rank;
   }
 
   // Where a few hundred candidates are all that can matter: finds them by their distances, and ranks them by
   // counting. Returns 0 where there are more, 1 when done, -1 if sums have to be improved first.
   __device__ int select_few() const {
-    if (tid < 32) {   // the best score of all, in two words; distances are then sums of small numbers
-      float2 top = make_float2(-INFINITY, 0.f);
+    if (tid < 32) {   // the best score of all; distances are then sums of small numbers
+      Fixed top{0, 0, static_cast<long long>(1ull << 63)};   // (less than any)
       for (int k = lane; k < a.K; k += 32)
-        if (sh.kind[k] == kLive || sh.kind[k] == kEnded) top = larger(top, sh.best_of[k]);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1)
-        top = larger(top, make_float2(__shfl_xor_sync(0xffffffffu, top.x, o), __shfl_xor_sync(0xffffffffu, top.y, o)));
+        if ((sh.kind[k] == kLive || sh.kind[k] == kEnded) && sh.best_of[k] > top) top = sh.best_of[k];
+#pragma unroll 1
+      for (int o = 16; o > 0; o >>= 1) {
+        if (o >= a.K) continue;   // (lanes without a beam have none to give)
+        const Fixed x = shuffle_xor(top, o);
+        if (x > top) top = x;
+      }
+      top = Fixed{__shfl_sync(0xffffffffu, top.lo, 0), __shfl_sync(0xffffffffu, top.mid, 0),
+                  __shfl_sync(0xffffffffu, top.hi, 0)};
+      if (lane == 0) sh.best_score = top;
       for (int k = lane; k < a.K; k += 32)
-        sh.base[k] = __fadd_rn(__fsub_rn(top.x, sh.best_of[k].x), __fsub_rn(top.y, sh.best_of[k].y));
+        if (sh.kind[k] == kLive || sh.kind[k] == kEnded) sh.base[k] = float_of(top - sh.best_of[k]);
     }
     clear_hist();
     __syncthreads();
@@ -771,50 +843,61 @@ struct Finish {
       }
     }
     const int count = sh.cands;
+    // Distances from the best score, which as a rule fit 64 bits; among equal ones: beam, logit (the largest first), token
     ulonglong2 mine = make_ulonglong2(0, 0);
+    Cand c{0.f, 0, 0};
+    float out = 0.f;
+    bool far = false;
     if (tid < count) {
-      Pick &p = sh.cand[tid];
-      p.key = order_of(sh.kind[p.k] == kEnded ? sh.best_of[p.k] : score(p.k, p.l));
-      // among equal scores: beam, logit (the largest first), token
-      mine = make_ulonglong2(p.key, static_cast<unsigned long long>(p.k) << 52 |
-                                        static_cast<unsigned long long>(~float_key(__fadd_rn(p.l, 0.f))) << 20 | p.at);
+      c = sh.cand[tid];
+      out = score_out(c);
+      const Fixed d = sh.best_score - score(c.k, c.l);
+      far = (d.mid | static_cast<unsigned long long>(d.hi)) != 0;
+      mine = make_ulonglong2(d.lo, static_cast<unsigned long long>(c.k) << 52 |
+                                       static_cast<unsigned long long>(~float_key(__fadd_rn(c.l, 0.f))) << 20 | c.at);
       sh.key[tid] = mine;
     }
-    __syncthreads();
-    if (tid < count) {
-      int rank = 0;
+    far = __syncthreads_or(far);
+    int rank = 0;
+    if (far) {
+      rank = rank_far_apart<E>(a, sh, b, count);
+    } else if (tid < count) {
 #pragma unroll 4
       for (int i = 0; i < count; ++i) {
         const ulonglong2 x = sh.key[i];
-        rank += x.x > mine.x || (x.x == mine.x && x.y < mine.y);
+        rank += x.x < mine.x || (x.x == mine.x && x.y < mine.y);
       }
-      sh.order[rank] = tid;
     }
+    if (tid < count) sh.order[rank] = tid;
     __syncthreads();
-    const int found = min(count, a.n);
     if (tid > 0 && tid < count) {   // with the one before it; those not chosen with the last chosen one
-      const Pick &p = sh.cand[sh.order[tid]], &q = sh.cand[sh.order[min(tid, a.n) - 1]];
-      compare(q.key, q.k, p.key, p.k);
+      const int i = sh.order[min(tid, a.n) - 1], j = sh.order[tid];
+      const Cand &p = sh.cand[i], &q = sh.cand[j];
+      if (p.k != q.k)
+        compare(far ? float_of(score(p.k, p.l) - score(q.k, q.l)) : static_cast<float>(sh.key[j].x - sh.key[i].x) * 0x1p-48f,
+                p.k, q.k);
     }
     __syncthreads();
     if (sh.again) return -1;
-    for (int j = tid; j < a.n; j += kFinishThreads) {
-      const long long at = static_cast<long long>(b) * a.n + j;
-      const bool some = j < found;
-      const Pick p = some ? sh.cand[sh.order[j]] : no_pick();
-      a.tokens[at] = some ? p.at : -1;
-      a.parents[at] = some ? b * a.K + p.k : -1;
-      a.out_scores[at] = some ? from_order(p.key).x : -INFINITY;
+    const long long row = static_cast<long long>(b) * a.n;
+    if (tid < count && rank < a.n) {
+      a.tokens[row + rank] = c.at;
+      a.parents[row + rank] = b * a.K + c.k;
+      a.out_scores[row + rank] = out;
+    }
+    if (tid >= count && tid < a.n) {
+      a.tokens[row + tid] = a.parents[row + tid] = -1;
+      a.out_scores[row + tid] = -INFINITY;
     }
     return 1;
   }
 
-  // the best of this thread's units that ranks after `last`
+  // the best of this thread's units that ranks after `last` (none: of all)
   __device__ __forceinline__ Pick next_unit(const Pick &last) const {
     Pick best = no_pick();
     for (int u = tid; u < a.K * a.C; u += kFinishThreads) {
       const Pick p = unit_pick(u);
-      if (p.key && before(last, p) && before(p, best)) best = p;
+      if (p.some() && (!last.some() || before(last, p)) && before(p, best)) best = p;
     }
     return best;
   }
@@ -852,8 +935,7 @@ struct Finish {
       l = key_float(top);
     }
     if (lane == 0) {
-      const bool some = t != 0x7fffffff;
-      sh.head[j] = Pick{!some ? 0 : sh.kind[k] == kEnded ? order_of(sh.best_of[k]) : order_of(score(k, l)), l, k, t};
+      sh.head[j] = t != 0x7fffffff ? Pick{score(k, l), {l, k, t}} : no_pick();
     }
   }
 
@@ -862,7 +944,7 @@ struct Finish {
   // sums have to be improved first.
   __device__ bool select_any() const {
     // the n first units by their largest candidates: the n best candidates lie in them
-    Pick last{~0ull, 0.f, 0, 0};   // before all others
+    Pick last = no_pick();
     Pick mine = next_unit(last);
     int units = 0;
     for (; units < a.n; ++units) {
@@ -873,21 +955,20 @@ struct Finish {
         const Pick all = warp_best(lane < kFinishWarps ? sh.warp[lane] : no_pick());
         if (lane == 0) {
           sh.best = all;
-          if (units > 0 && all.key)
-            compare(last.key, last.k, all.key, all.k);
+          if (units > 0 && all.some()) compare(float_of(last.score - all.score), last.c.k, all.c.k);
         }
       }
       __syncthreads();
       const Pick p = sh.best;
-      if (!p.key) break;
-      if (tid == 0) sh.unit[units] = p.k * a.C + p.at;
-      if (mine.k == p.k && mine.at == p.at) mine = next_unit(p);
+      if (!p.some()) break;
+      if (tid == 0) sh.unit[units] = p.c.k * a.C + p.c.at;
+      if (mine.c.k == p.c.k && mine.c.at == p.c.at) mine = next_unit(p);
       last = p;
     }
     if (units == a.n) {
       for (int u = tid; u < a.K * a.C; u += kFinishThreads) {
         const Pick p = unit_pick(u);
-        if (p.key && before(last, p)) compare(last.key, last.k, p.key, p.k);
+        if (p.some() && before(last, p)) compare(float_of(last.score - p.score), last.c.k, p.c.k);
       }
     }
     __syncthreads();
@@ -897,33 +978,33 @@ struct Finish {
     int32_t *tokens = a.tokens + static_cast<long long>(b) * a.n;
     int32_t *parents = a.parents + static_cast<long long>(b) * a.n;
     float *scores = a.out_scores + static_cast<long long>(b) * a.n;
-    unsigned long long before_key = 0;
-    int before_k = -1, found = 0;
+    Pick one_before = no_pick();
+    int found = 0;
     for (; found < a.n; ++found) {
       Pick p = no_pick();   // every warp finds the best head by itself
       int j = 0;
       for (int i = lane; i < units; i += 32)
-        if (sh.head[i].key && before(sh.head[i], p)) p = sh.head[i];
+        if (before(sh.head[i], p)) p = sh.head[i];
       p = warp_best(p);
-      if (!p.key) break;
-      while (sh.unit[j] != p.k * a.C + (sh.kind[p.k] == kEnded ? 0 : p.at / (kUnitVecs * Elem<E>::kPerVec))) ++j;
-      const int k = p.k, token = p.at;
-      const float l = p.l;
+      if (!p.some()) break;
+      const int k = p.c.k, token = p.c.at;
+      const float l = p.c.l;
+      while (sh.unit[j] != k * a.C + (sh.kind[k] == kEnded ? 0 : token / (kUnitVecs * Elem<E>::kPerVec))) ++j;
       if (tid == 0) {
-        if (found > 0) compare(before_key, before_k, p.key, k);
+        if (found > 0) compare(float_of(one_before.score - p.score), one_before.c.k, k);
         tokens[found] = token;
         parents[found] = b * a.K + k;
-        scores[found] = from_order(p.key).x;
+        scores[found] = score_out(p.c);
       }
-      before_key = p.key;
-      before_k = k;
+      one_before = p;
       __syncthreads();
       if (warp == j % kFinishWarps) next_token(j, sh.kind[k] == kEnded ? -INFINITY : l, token);
       __syncthreads();
     }
     if (found == a.n)
       for (int j = tid; j < units; j += kFinishThreads)
-        if (sh.head[j].key) compare(before_key, before_k, sh.head[j].key, sh.head[j].k);
+        if (sh.head[j].some())
+          compare(float_of(one_before.score - sh.head[j].score), one_before.c.k, sh.head[j].c.k);
     __syncthreads();
     if (sh.again) return false;
     for (int j = found + tid; j < a.n; j += kFinishThreads) {
@@ -946,6 +1027,10 @@ __device__ __noinline__ float2 large_sum_apart(const BeamArgs &a, FinishShared &
 template <typename E>
 __device__ __noinline__ void refine_apart(const BeamArgs &a, FinishShared &sh, int b, int k) {
   finish_of<E>(a, sh, b).refine(k);
+}
+template <typename E>
+__device__ __noinline__ int rank_far_apart(const BeamArgs &a, FinishShared &sh, int b, int count) {
+  return finish_of<E>(a, sh, b).rank_far(count);
 }
 template <typename E>
 __device__ __noinline__ bool select_any_apart(const BeamArgs &a, FinishShared &sh, int b) {
