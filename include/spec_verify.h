@@ -290,7 +290,8 @@ int spec_topk(const void *logits, int dtype, int rows, int V, int k, int32_t *ou
  * tokens, parents and out_scores [b, 0..n) are the best of them, the largest score first, equal scores by
  * beam, then by token: v, the row b * K + k (what spec_beam_reorder and spec_kv_fork take as parents) and the
  * score. The order is that of the scores in exact arithmetic, whatever their magnitude (two whose difference is
- * not 0 but below 1e-9 may be taken for each other); out_scores are within 4e-6 of them, rounded to fp32.
+ * not 0 but below 1e-9 may be taken for each other; equal scores are those of beams whose rows hold the same
+ * logits, in any order); out_scores are within 4e-6 of them, rounded to fp32.
  *   - A beam whose score is -inf is not in use: it has no candidates, and its logits are not read.
  *   - A beam with done[b, k] != 0 has ended: its one candidate is pad_token at its own score, and its logits
  *     are not read. (done NULL: none has.)

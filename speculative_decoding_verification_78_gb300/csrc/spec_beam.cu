@@ -12,7 +12,8 @@
 // as it takes to tell the two apart, and the selection is repeated. Scores are compared as integers of 192 bits, whole
 // multiples of 2^-48, which hold any sum of fp32 numbers: beside a score of -1e9 fp32 pairs lose what tells beams
 // apart. So tokens and parents are those of exact arithmetic (but for scores closer than 1e-9). The sums are taken in
-// the order of the token numbers wherever a row lies in memory, so that beams with equal logits have equal L_k.
+// the order of the token numbers wherever a row lies in memory, so that beams with equal logits have equal L_k; those
+// that are taken again are sums of integers, which are equal for rows that hold the same logits in another order too.
 //
 // What bounds it: for many beams HBM while the logits stream (64 x 8 beams x 152064 in bf16: 156 MB in 26 us, 5.9
 // TB/s; 58 % of the issue slots, the rest waits for ex2 and for loads), then the finishing CTAs' chain of about ten
@@ -217,6 +218,37 @@ __device__ __forceinline__ void exp_pair(float x, float M, float &hi, float &lo)
   lo = low * scale;
 }
 
+// A sum of such pairs (each at most 1, at most 2^20 of them) that does not depend on their order: each is cut into
+// multiples of 2^-20, 2^-41 and 2^-62, which leaves less than 2^-62 of it; up to eight are added in fp32, which holds
+// those sums exactly, and then as integers. (4 equal beams x 32000, one of which is summed again: 2 us of 41 for it;
+// with two conversions of each term to 64 bits 14 of 53.)
+struct ExactSum {
+  long long n[3] = {0, 0, 0};
+  // x rounded to a multiple of 2^-23 kOne, |x| < kOne / 4
+  static __device__ __forceinline__ float cut(float x, float kOne) {
+    return __fsub_rn(__fadd_rn(x, 1.5f * kOne), 1.5f * kOne);
+  }
+  static __device__ __forceinline__ void split(float hi, float lo, float (&t)[3]) {
+    const float x = __fadd_rn(hi, lo);   // (lo may be 2^-10 of it)
+    lo = __fsub_rn(lo, __fsub_rn(x, hi));
+    const float a = cut(x, 0x1p3f), r = __fsub_rn(x, a);
+    const float b = cut(r, 0x1p-18f), c = cut(lo, 0x1p-18f);
+    const float d = cut(__fadd_rn(__fsub_rn(r, b), __fsub_rn(lo, c)), 0x1p-39f);
+    t[0] = __fadd_rn(t[0], a);
+    t[1] = __fadd_rn(t[1], __fadd_rn(b, c));
+    t[2] = __fadd_rn(t[2], d);
+  }
+  __device__ __forceinline__ void add(const float (&t)[3]) {
+    n[0] += __float2int_rn(t[0] * 0x1p20f);
+    n[1] += __float2int_rn(t[1] * 0x1p41f);
+    n[2] += __float2int_rn(t[2] * 0x1p62f);
+  }
+  __device__ __forceinline__ double value() const {
+    return static_cast<double>(n[0]) * 0x1p-20 +
+           (static_cast<double>(n[1]) * 0x1p-41 + static_cast<double>(n[2]) * 0x1p-62);
+  }
+};
+
 // log(n 2^-40) for n > 0, as a sum of two fp32 numbers, to about 1e-10: with n 2^-40 = x 2^e, x in [1, 2),
 // fp32's logarithm y of x, put right by x e^-y - 1, and e ln 2.
 __device__ __forceinline__ void log_pair(unsigned long long n, float &hi, float &lo) {
@@ -367,7 +399,7 @@ struct FinishShared {
   Pick warp[kFinishWarps], best;
   int unit[SPEC_MAX_BEST];     // chosen units, in order
   Pick head[SPEC_MAX_BEST];    // the best of each that is left; place: the token
-  double sum[kFinishWarps];
+  ExactSum sum[kFinishWarps];
   int bad, again, round;
   float least;
   unsigned long long rest;
@@ -590,28 +622,32 @@ struct Finish {
       for (int o = 16; o > 0; o >>= 1) rest += __shfl_xor_sync(0xffffffffu, rest, o);
       if (lane == 0) sh.rest = rest;
     }
-    float h = 0.f, l = 0.f;
+    ExactSum sum;
     int n = 0;
     for (int c = 0; c < a.C; ++c) {   // half of the CTA a unit
       if (weight[c] < least) continue;
       if ((n++ & 1) != tid / kUnitVecs) continue;
       uint4 v[1];
       load_groups<E>(row(k), a.V, c * kUnitVecs + tid % kUnitVecs, v);
+      float t[3] = {0.f, 0.f, 0.f};
 #pragma unroll
       for (int e = 0; e < Elem<E>::kPerVec; ++e) {
         float xh, xl;
         exp_pair(vec_elem<E>(v[0], e), M, xh, xl);
-        pair_add(h, l, xh, xl);
+        ExactSum::split(xh, xl, t);
       }
+      sum.add(t);
     }
-    double t = static_cast<double>(h) + static_cast<double>(l);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-    if (lane == 0) sh.sum[warp] = t;
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+      for (int i = 0; i < 3; ++i) sum.n[i] += __shfl_xor_sync(0xffffffffu, sum.n[i], o);
+    if (lane == 0) sh.sum[warp] = sum;
     __syncthreads();
     if (tid == 0) {
-      double all = 0.;
-      for (int w = 0; w < kFinishWarps; ++w) all += sh.sum[w];
+      for (int w = 1; w < kFinishWarps; ++w)
+        for (int i = 0; i < 3; ++i) sum.n[i] += sh.sum[w].n[i];
+      const double all = sum.value();
       const double out = sh.rest ? static_cast<double>(sh.rest) * 0x1p-40 * exp(R / kLog2ed - M) : 0.;
       const double x = log(all + out);
       const float hi = static_cast<float>(x);

@@ -1,4 +1,5 @@
-"""GPU tests of beam selection where candidates of different beams lie near each other, at scores of any magnitude.
+"""GPU tests of beam selection where candidates of different beams lie near each other: scores of any magnitude, rows
+that hold the same logits in another order.
 
 The order has to be that of exact scores: the scores, logits and their differences as fractions, and the logarithm of a
 row's sum in fp64 over its sorted logits (off by at most 2^-52 of itself and 2^-53 a term of its sorted sum, below 1e-13
@@ -102,4 +103,18 @@ def test_equal_scores_of_unlike_beams(sv):
     scores = torch.tensor([[-2.0, -2.5, -1.75, -3.0]]).repeat(8, 1).cuda()
     scores[4:] -= 1e6
     for n in (4, 17, 60):
+        check(sv, logits, scores, n)
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
+@pytest.mark.parametrize("V", [50, 2100, 33000])
+def test_rows_in_another_order(sv, V, dtype):
+    """Beams with equal scores whose rows hold the same logits in another order: their scores are equal."""
+    rng = np.random.default_rng(V + 1)
+    x = rng.standard_normal((12, 1, V)).repeat(4, 1) * np.linspace(0.5, 6, 12)[:, None, None]
+    for b in range(12):
+        for k in range(4):
+            x[b, k] = x[b, k, rng.permutation(V)]
+    logits = torch.from_numpy(x.astype(np.float32)).to(dtype).cuda()
+    scores = torch.from_numpy(rng.random((12, 1)).astype(np.float32)).cuda().repeat(1, 4).contiguous()
+    for n in (1, 4, 15):
         check(sv, logits, scores, n)
