@@ -40,7 +40,7 @@ constexpr float kPlainMax = 1048576.f;
 // on average; 18 roundings of sums and of the second word's factor. And that of a sum taken again (exp_pair), with
 // what its logarithm adds.
 constexpr float kCoarse = 2e-6f, kFine = 2e-10f;
-constexpr int kRounds = 16;   // in which sums are improved as far as a gap asks for; then whole rows are summed
+constexpr float kUnitCut = 0x1p-40f;   // what a unit that is not summed again may lack, beside 2^R (see fixed)
 
 __device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
   f32x2 r;
@@ -400,9 +400,10 @@ struct FinishShared {
   int unit[SPEC_MAX_BEST];     // chosen units, in order
   Pick head[SPEC_MAX_BEST];    // the best of each that is left; place: the token
   ExactSum sum[kFinishWarps];
-  int bad, again, round;
+  int bad, again;
   float least;
   unsigned long long rest;
+  int left;   // units
 };
 
 // The longer parts of it that are seldom taken are functions of their own, made of the same members (one that were a
@@ -452,13 +453,13 @@ struct Finish {
   __device__ __forceinline__ void compare(float gap, int k, int j) const {
     if (k == j || !(gap <= sh.slack[k] + sh.slack[j])) return;
     // 0 as well: sums that fp32 rounds alike are not the same yet
-    const float to = sh.round < kRounds ? 0.4f * gap : 0.f;
-    want(k, to);
-    want(j, to);
+    want(k, 0.4f * gap);
+    want(j, 0.4f * gap);
   }
+  // A beam whose sum has been improved and does not tell either is summed whole: the gap was the sums' errors.
   __device__ __forceinline__ void want(int k, float slack) const {
     if (sh.slack[k] <= kFine || sh.slack[k] <= slack) return;
-    atomicMin(&sh.target[k], __float_as_int(slack));
+    atomicMin(&sh.target[k], sh.slack[k] < kCoarse ? 0 : __float_as_int(slack));
     sh.again = 1;
   }
 
@@ -604,23 +605,35 @@ struct Finish {
     __syncthreads();
     if (warp == 0 && plain && target > kFine) {   // a threshold a lane: 2^(10 - lane); the largest that leaves out little enough
       const float at = ldexpf(1.f, 10 - lane);
-      float all = 0.f, out = 0.f;
+      float all = 0.f, out = 0.f, cut_off = 0.f;
       for (int c = 0; c < a.C; ++c) {
         all += weight[c];
-        if (weight[c] < at) out += weight[c];
+        if (weight[c] < at) {
+          out += weight[c];
+          cut_off += kUnitCut;
+        }
       }
-      const unsigned fits = __ballot_sync(0xffffffffu, out * (1.01f * kCoarse) + kFine * all <= target * all);
+      const unsigned fits =
+          __ballot_sync(0xffffffffu, out * (1.01f * kCoarse) + kFine * all + cut_off <= target * all);
       if (lane == 0 && fits) sh.least = ldexpf(1.f, 10 - (__ffs(fits) - 1));
     }
     __syncthreads();
     const float least = sh.least;
     if (warp == kFinishWarps - 1) {
       unsigned long long rest = 0;
+      int left = 0;
       for (int c = lane; c < a.C; c += 32)
-        if (weight[c] < least) rest += fixed(part(k * a.C + c), R);
+        if (weight[c] < least) {
+          rest += fixed(part(k * a.C + c), R);
+          ++left;
+        }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) rest += __shfl_xor_sync(0xffffffffu, rest, o);
-      if (lane == 0) sh.rest = rest;
+      left = __reduce_add_sync(0xffffffffu, left);
+      if (lane == 0) {
+        sh.rest = rest;
+        sh.left = left;
+      }
     }
     ExactSum sum;
     int n = 0;
@@ -653,7 +666,10 @@ struct Finish {
       const float hi = static_cast<float>(x);
       set_sum(k, M, hi, static_cast<float>(x - hi));
       // not above what was asked for, whatever was rounded: else the same would be asked for again
-      sh.slack[k] = least > 0.f ? fminf(kFine + static_cast<float>(out / (all + out)) * kCoarse, target) : kFine;
+      // (a sum is at least half of 2^R)
+      const float cut_off = static_cast<float>(sh.left) * (2.f * kUnitCut);
+      sh.slack[k] =
+          sh.left ? fminf(kFine + static_cast<float>(out / (all + out)) * kCoarse + cut_off, target) : kFine;
       sh.target[k] = 0x7f800000;
     }
     __syncthreads();
@@ -1094,11 +1110,9 @@ __global__ void __launch_bounds__(kFinishThreads, 1) beam_finish_kernel(const __
     }
     return;
   }
-  // Each time around, a beam's slack comes down: to its target or, where that is kFine or less, to kFine, below which
-  // nothing is asked for. From round kRounds on all targets are 0, so it ends after kRounds + K at the latest.
-  for (int round = 0; round <= kRounds + SPEC_MAX_BEAMS; ++round) {
-    if (tid == 0) sh.round = round;
-    __syncthreads();
+  // Each time around, a beam that asks is improved, at most twice: to its target, below what it had, and then to kFine,
+  // below which nothing is asked for. So it ends after 2 K at the latest.
+  for (int round = 0; round <= 2 * SPEC_MAX_BEAMS; ++round) {
     const int done = f.select_few();
     if (done == 1) return;
     __syncthreads();

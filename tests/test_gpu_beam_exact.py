@@ -1,5 +1,5 @@
 """GPU tests of beam selection where candidates of different beams lie near each other: scores of any magnitude, rows
-that hold the same logits in another order.
+that hold the same logits in another order, sums of many small units.
 
 The order has to be that of exact scores: the scores, logits and their differences as fractions, and the logarithm of a
 row's sum in fp64 over its sorted logits (off by at most 2^-52 of itself and 2^-53 a term of its sorted sum, below 1e-13
@@ -117,4 +117,16 @@ def test_rows_in_another_order(sv, V, dtype):
     logits = torch.from_numpy(x.astype(np.float32)).to(dtype).cuda()
     scores = torch.from_numpy(rng.random((12, 1)).astype(np.float32)).cuda().repeat(1, 4).contiguous()
     for n in (1, 4, 15):
+        check(sv, logits, scores, n)
+
+def test_many_units_with_little_each(sv):
+    """1023 units, each just below 2^-40 of the sum's power of two: 1.86e-9 of the sum together. The scores bring its
+    beam 0.81e-9 nearer, so that it is 1.05e-9 behind."""
+    V = 1 << 20
+    x = np.full((2, 2, V), -np.inf)
+    x[:, :, 0] = 1e-3
+    x[0, 0, 1024::1024] = x[1, 1, 1024::1024] = -39 * math.log(2) - 1e-3
+    logits = torch.from_numpy(x.astype(np.float32)).cuda()
+    scores = torch.tensor([[0.81e-9, 0.0], [0.0, 0.81e-9]]).cuda()
+    for n in (1, 2):
         check(sv, logits, scores, n)
