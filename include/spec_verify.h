@@ -302,7 +302,7 @@ int spec_topk(const void *logits, int dtype, int rows, int V, int k, int32_t *ou
  *   tokens, parents [B, n] int32 out     out_scores [B, n] fp32 out (none over scores or done)
  *   workspace  at least spec_beam_workspace_bytes(B, K, V, dtype) bytes (scratch)
  * Limits: 1 <= K <= SPEC_MAX_BEAMS, 1 <= n <= SPEC_MAX_BEST, 1 <= V <= SPEC_MAX_V, 0 <= pad_token < V, B >= 0
- * (B == 0 does nothing); units of 4 KB of a row's logits are counted in 31 bits over all rows.
+ * (B == 0 does nothing); fewer than 2^31 - 2^16 units of 4 KB of a row's logits over all rows.
  */
 size_t spec_beam_workspace_bytes(int B, int K, int V, int dtype);
 int spec_beam_select(const void *logits, int dtype, const float *scores, const int32_t *done,

@@ -63,12 +63,15 @@ bool apart(const void *p, const void *q, size_t n, size_t m) {   // n bytes from
 
 bool temp_ok(float T) { return T == 0.f || (T >= FLT_MIN && T <= FLT_MAX); }
 
-// Fills the unit counts of p; returns SPEC_OK, or SPEC_ERR_SHAPE when the call has 2^31 - 64
-// units or more (unit ids are 32-bit on the device).
+// Unit ids are 32-bit on the device, and the step of its loops over units (warps of a grid: below 2^16) is added to the
+// last ones too.
+constexpr long long kMaxUnits = (1LL << 31) - (1 << 16);
+
+// Fills the unit counts of p; returns SPEC_OK, or SPEC_ERR_SHAPE when the call has kMaxUnits or more.
 int plan_units(Params &p, int dtype) {
   p.C = chunks_per_row(p.V, dtype);
   const long long units = static_cast<long long>(p.B) * p.R * p.C;
-  if (units >= (1LL << 31) - 64) return SPEC_ERR_SHAPE;
+  if (units >= kMaxUnits) return SPEC_ERR_SHAPE;
   p.units = static_cast<int>(units);
   p.upb = p.R * p.C;
   return SPEC_OK;
@@ -605,7 +608,7 @@ int spec_beam_select(const void *logits, int dtype, const float *scores, const i
     return SPEC_ERR_SHAPE;
   const int C = beam_chunks(V, dtype);
   const long long units = static_cast<long long>(B) * K * C;
-  if (units >= (1LL << 31) - 64) return SPEC_ERR_SHAPE;
+  if (units >= kMaxUnits) return SPEC_ERR_SHAPE;
   if (B == 0) return SPEC_OK;
   if (!logits || !scores || !tokens || !parents || !out_scores || !status || !workspace)
     return SPEC_ERR_NULL;
