@@ -299,7 +299,7 @@ int spec_topk(const void *logits, int dtype, int rows, int V, int k, int32_t *ou
  *   - A NaN or +inf score, or an invalid logits row of a beam in use, makes the whole batch row -1 with NaN
  *     scores and sets *status (SPEC_ERR_NONFINITE).
  *   logits [B, K, V] dtype     scores [B, K] fp32     done [B, K] int32 or NULL
- *   tokens, parents [B, n] int32 out     out_scores [B, n] fp32 out (none over scores or done)
+ *   tokens, parents [B, n] int32 out     out_scores [B, n] fp32 out (none over an input or another)
  *   workspace  at least spec_beam_workspace_bytes(B, K, V, dtype) bytes (scratch)
  * Limits: 1 <= K <= SPEC_MAX_BEAMS, 1 <= n <= SPEC_MAX_BEST, 1 <= V <= SPEC_MAX_V, 0 <= pad_token < V, B >= 0
  * (B == 0 does nothing); fewer than 2^31 - 2^16 units of 4 KB of a row's logits over all rows.
@@ -314,7 +314,8 @@ int spec_beam_select(const void *logits, int dtype, const float *scores, const i
  * Reorders what belongs to the beams (token histories, hidden or recurrent states) by their parents:
  *   out[c, :] = in[parents[c], :]   for c = 0 .. rows_out - 1, and zeros where parents[c] is -1
  * for `count` tensors of rows_in and rows_out rows of row_bytes bytes, one after another. Any other parent
- * outside [0, rows_in) counts as -1 and sets *status (SPEC_ERR_PARENT). No out may overlap an in.
+ * outside [0, rows_in) counts as -1 and sets *status (SPEC_ERR_PARENT). No out may overlap an in, another out or
+ * parents.
  * Limits: 1 <= count <= SPEC_MAX_STATES, row_bytes >= 1, rows_in, rows_out >= 0, rows_out * count < 2^31,
  * rows * row_bytes < 2^62. (The KV cache is reordered by spec_kv_fork.)
  */
@@ -491,7 +492,7 @@ size_t spec_kv_pages_workspace_bytes(int num_pages, int B);
  * those of all sequences before them fit into the free pages (a sequence that needs none always is); the
  * others set *status (SPEC_ERR_NO_PAGE).
  *   granted [B] int32 out: new_lens[b], or 0 for a sequence that was not served or whose lengths are bad
- *           (so it may be the new_lens of spec_kv_append and spec_kv_attention)
+ *           (so it may be the new_lens of spec_kv_append and spec_kv_attention; and new_lens itself)
  * A new page's contents are left as they were. Limits: 1 <= N <= 2^20.
  */
 int spec_kv_reserve(const spec_kv_cache_t *cache, int32_t *refs, int32_t *page_table, int pages_per_seq,
@@ -509,7 +510,7 @@ int spec_kv_trim(const spec_kv_cache_t *cache, int32_t *refs, int32_t *page_tabl
 
 /*
  * Ends sequences: those with ended[b] != 0 (NULL: all) give back their pages; their table entries become -1
- * and their lengths 0. (Lengths are not read: any table is fine.)
+ * and their lengths 0. (Lengths are not read: any table is fine.) `ended` and seq_lens lie apart.
  */
 int spec_kv_free(const spec_kv_cache_t *cache, int32_t *refs, int32_t *page_table, int pages_per_seq,
                  int32_t *seq_lens, const int32_t *ended, int B, int32_t *status, void *stream);
@@ -523,7 +524,7 @@ int spec_kv_free(const spec_kv_cache_t *cache, int32_t *refs, int32_t *page_tabl
  * others. page_table is not changed: with release it is void after the call.
  *   parents [C] int32: -1 for none (an empty child: length 0); any other value outside [0, B) sets *status
  *           (SPEC_ERR_PARENT) and the child's length to -1, as a parent with a bad length does
- *   page_table_out [C, pages_per_seq], lens_out [C] int32 out, apart from page_table and seq_lens
+ *   page_table_out [C, pages_per_seq], lens_out [C] int32 out, apart from each other and from the inputs
  * Places past the last token have no page in a child. A child for whose copy no page is left has no pages and
  * the length -1 (SPEC_ERR_NO_PAGE); copies are served in the order of the children.
  */
@@ -538,7 +539,7 @@ int spec_kv_fork(const spec_kv_cache_t *cache, int layers, int32_t *refs, const 
  * below. The entries of page_table follow.
  *   page_map [num_pages] int32 out: where each page's contents are now, -1 for a page that was free (for other
  *            tables of the same pool)
- *   live     [1] int32 out: pages in use
+ *   live     [1] int32 out: pages in use (both apart from each other and from the inputs)
  */
 int spec_kv_compact(const spec_kv_cache_t *cache, int layers, int32_t *refs, int32_t *page_table,
                     int pages_per_seq, int B, int32_t *page_map, int32_t *live, int32_t *status,

@@ -623,6 +623,11 @@ int spec_beam_select(const void *logits, int dtype, const float *scores, const i
     if (!apart(out, scores, out_bytes, in_bytes) || (done && !apart(out, done, out_bytes, in_bytes)))
       return SPEC_ERR_SHAPE;
   if (workspace_bytes < spec_beam_workspace_bytes(B, K, V, dtype)) return SPEC_ERR_WORKSPACE;
+  const size_t logits_bytes = static_cast<size_t>(B) * K * V * elem_size(dtype);
+  const void *outs[3] = {tokens, parents, out_scores};
+  for (int i = 0; i < 3; ++i)
+    if (!apart(outs[i], logits, out_bytes, logits_bytes) || !apart(outs[i], outs[(i + 1) % 3], out_bytes, out_bytes))
+      return SPEC_ERR_SHAPE;
   BeamArgs a{};
   a.logits = logits;
   a.scores = scores;
@@ -667,6 +672,7 @@ int spec_beam_reorder(const spec_state_t *states, int count, const int32_t *pare
       if (rows_in > 0 && out < from + rows_in * len && from < out + rows_out * bytes) return SPEC_ERR_SHAPE;
       if (i != j && out < to + rows_out * len && to < out + rows_out * bytes) return SPEC_ERR_SHAPE;
     }
+    if (!apart(states[i].out, parents, rows_out * bytes, 4 * static_cast<size_t>(rows_out))) return SPEC_ERR_SHAPE;
     const uintptr_t all = in | out | bytes;
     a.in[i] = static_cast<const char *>(states[i].in);
     a.out[i] = static_cast<char *>(states[i].out);

@@ -247,6 +247,9 @@ int spec_kv_reserve(const spec_kv_cache_t *cache, int32_t *refs, int32_t *page_t
   if (!aligned(granted, 4) || !aligned(new_lens, 4)) return SPEC_ERR_ALIGN;
   if ((rc = pages_workspace_ok(workspace, workspace_bytes, a.num_pages, B)) != SPEC_OK) return rc;
   if (B == 0) return SPEC_OK;
+  const size_t pages = 4 * static_cast<size_t>(a.num_pages), seqs = 4 * static_cast<size_t>(B);
+  if (!apart(granted, refs, seqs, pages) || !apart(granted, page_table, seqs, seqs * pages_per_seq))
+    return SPEC_ERR_SHAPE;
   return launch_result(launch_kv_reserve(g, new_lens, N, granted, workspace,
                                          static_cast<cudaStream_t>(stream)));
 }
@@ -272,6 +275,8 @@ int spec_kv_free(const spec_kv_cache_t *cache, int32_t *refs, int32_t *page_tabl
   if (rc != SPEC_OK) return rc;
   if (!aligned(ended, 4)) return SPEC_ERR_ALIGN;
   if (B == 0) return SPEC_OK;
+  const size_t seqs = 4 * static_cast<size_t>(B);
+  if (ended && !apart(ended, seq_lens, seqs, seqs)) return SPEC_ERR_SHAPE;
   return launch_result(launch_kv_release(g, ended, seq_lens, 0, 0, static_cast<cudaStream_t>(stream)));
 }
 
@@ -295,6 +300,15 @@ int spec_kv_fork(const spec_kv_cache_t *cache, int layers, int32_t *refs, const 
     return SPEC_ERR_SHAPE;
   if ((rc = pages_workspace_ok(workspace, workspace_bytes, a.num_pages, C)) != SPEC_OK) return rc;
   if (C == 0 && (B == 0 || !release)) return SPEC_OK;
+  if (C > 0) {
+    const size_t pages = 4 * static_cast<size_t>(a.num_pages), seqs = 4 * static_cast<size_t>(B);
+    const size_t children = 4 * static_cast<size_t>(C);
+    if (!apart(page_table_out, lens_out, row * C, children) || !apart(page_table_out, parents, row * C, children) ||
+        !apart(lens_out, parents, children, children) || !apart(page_table_out, refs, row * C, pages) ||
+        !apart(lens_out, refs, children, pages) ||
+        (B > 0 && (!apart(page_table_out, seq_lens, row * C, seqs) || !apart(lens_out, page_table, children, row * B))))
+      return SPEC_ERR_SHAPE;
+  }
   ForkArgs f{};
   f.parents = parents;
   f.table_out = page_table_out;
@@ -317,6 +331,10 @@ int spec_kv_compact(const spec_kv_cache_t *cache, int layers, int32_t *refs, int
   if (!page_map || !live) return SPEC_ERR_NULL;
   if (!aligned(page_map, 4) || !aligned(live, 4)) return SPEC_ERR_ALIGN;
   if ((rc = pages_workspace_ok(workspace, workspace_bytes, a.num_pages, B)) != SPEC_OK) return rc;
+  const size_t pages = 4 * static_cast<size_t>(a.num_pages), places = 4 * static_cast<size_t>(B) * pages_per_seq;
+  if (!apart(page_map, refs, pages, pages) || !apart(live, refs, 4, pages) || !apart(page_map, live, pages, 4) ||
+      (B > 0 && (!apart(page_map, page_table, pages, places) || !apart(live, page_table, 4, places))))
+    return SPEC_ERR_SHAPE;
   return launch_result(launch_kv_compact(g, pool_of(a, layers), page_map, live, workspace,
                                          static_cast<cudaStream_t>(stream)));
 }
