@@ -186,12 +186,14 @@ def _ptr(t):
     return ctypes.c_void_p(t.data_ptr()) if t.numel() else None
 
 
-def dtype_flag(t: torch.Tensor) -> int:
-    if t.dtype == torch.float32:
+def dtype_flag(t) -> int:
+    """Of a logits tensor or its dtype."""
+    dtype = t.dtype if isinstance(t, torch.Tensor) else t
+    if dtype == torch.float32:
         return SPEC_F32
-    if t.dtype in (torch.bfloat16, torch.int16) or str(t.dtype) == "torch.uint16":
+    if dtype in (torch.bfloat16, torch.int16) or str(dtype) == "torch.uint16":
         return SPEC_BF16
-    raise TypeError(f"logits must be float32 or bfloat16 (got {t.dtype})")
+    raise TypeError(f"logits must be float32 or bfloat16 (got {dtype})")
 
 
 def _stream(stream):
@@ -1055,7 +1057,7 @@ def kv_compact(cache, refs, page_table, page_map=None, live=None, workspace=None
 
 def new_beam_workspace(B, K, V, dtype=torch.bfloat16, device=None) -> torch.Tensor:
     """A workspace for beam_select calls of this shape (scratch; never needs zeroing)."""
-    n = spec_beam_workspace_bytes(B, K, V, SPEC_F32 if dtype == torch.float32 else SPEC_BF16)
+    n = spec_beam_workspace_bytes(B, K, V, dtype_flag(dtype))
     if n == 0:
         raise SpecError(SPEC_ERR_SHAPE, "spec_beam_workspace_bytes")
     return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
