@@ -695,13 +695,13 @@ def _state_array(n):
 
 def spec_beam_reorder(states, parents, outs, status, stream=None) -> int:
     """states: tensors [R, ...] of any types, contiguous; outs: the same with parents.numel() rows;
-    parents int32."""
+    parents int32. (States whose rows have no elements need nothing.)"""
     if len(states) != len(outs) or not states:
         raise ValueError("as many outputs as states, at least one")
     if not isinstance(parents, torch.Tensor) or parents.dtype != _I32:
         raise TypeError("parents must be an int32 tensor")
     R, C = states[0].shape[0], parents.numel()
-    arr = _state_array(len(states))()
+    arr, count = _state_array(len(states))(), 0
     for i, (t, o) in enumerate(zip(states, outs)):
         a, b = t.shape, o.shape
         if a[0] != R or b[0] != C or (a != b if R == C else a[1:] != b[1:]) or t.dtype is not o.dtype:
@@ -711,8 +711,12 @@ def spec_beam_reorder(states, parents, outs, status, stream=None) -> int:
         if not (t.is_cuda and t.is_contiguous() and o.is_cuda and o.is_contiguous()):
             _ptr(t), _ptr(o)   # raises, or empty tensors
         row = n // R if R else m // C if C else 1
-        arr[i] = (t.data_ptr() or None, o.data_ptr() or None, row * t.element_size())
-    return load_library().spec_beam_reorder(arr, len(states), _operand(parents, "parents", C, _I32), R, C,
+        if row:
+            arr[count] = (t.data_ptr() or None, o.data_ptr() or None, row * t.element_size())
+            count += 1
+    if not count:
+        return SPEC_OK
+    return load_library().spec_beam_reorder(arr, count, _operand(parents, "parents", C, _I32), R, C,
                                             _operand(status, "status", 1, _I32), _stream(stream))
 
 
