@@ -102,10 +102,10 @@ __device__ __forceinline__ void load_groups(const E *row, int V, int g, uint4 (&
 // What a beam contributes: nothing (score -inf), one candidate (at its end), or its row.
 enum BeamKind : int { kUnused = 0, kEnded = 1, kLive = 2, kBad = 3 };
 __device__ __forceinline__ int beam_kind(const BeamArgs &a, int row, float &s) {
-  s = __ldg(a.scores + row);
+  s = ld_given(a.scores + row);
   if (s == -INFINITY) return kUnused;
   if (s != s || s == INFINITY) return kBad;
-  return a.done && __ldg(a.done + row) ? kEnded : kLive;
+  return a.done && ld_given(a.done + row) ? kEnded : kLive;
 }
 
 __device__ __forceinline__ float unit_ref(float m) { return ceilf(__fmul_rn(m, kLog2eHi)); }
@@ -1147,7 +1147,7 @@ __global__ void __launch_bounds__(256) beam_reorder_kernel(const __grid_constant
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int c = blockIdx.x / a.states, s = blockIdx.x - c * a.states;
-  const int p = __ldg(a.parents + c);
+  const int p = ld_given(a.parents + c);
   const bool ok = p >= 0 && p < a.rows_in;
   if (!ok && p != -1 && threadIdx.x == 0) set_status(a.status, SPEC_ERR_PARENT);
   const long long bytes = a.bytes[s];

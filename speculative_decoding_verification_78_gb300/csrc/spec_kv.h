@@ -14,6 +14,11 @@ namespace specv {
 constexpr float kE4m3Max = 448.f;
 constexpr float kMinPageScale = 5.421010862427522e-20f;   // 2^-64
 
+// A load of what a kernel before on the stream may have written (lengths, tables, queries, page scales). Not __ldg: the
+// memory that reads has to stay as it is for the whole kernel, and one that is launched as a programmatic dependent
+// begins while the kernel before still writes.
+template <typename T> __device__ __forceinline__ T ld_given(const T *p) { return *p; }
+
 struct KvArgs {
   uint8_t *k, *v;            // [num_pages, Hkv, page, D] e4m3
   float *k_scale, *v_scale;  // [num_pages, Hkv]
@@ -29,14 +34,14 @@ struct KvArgs {
 // Tokens of sequence b before the new ones and how many new ones it has; false (and a status)
 // when they do not fit its page table.
 __device__ __forceinline__ bool kv_lengths(const KvArgs &a, int b, int &len, int &n) {
-  len = __ldg(a.seq_lens + b);
-  n = a.new_lens ? __ldg(a.new_lens + b) : a.N;
+  len = ld_given(a.seq_lens + b);
+  n = a.new_lens ? ld_given(a.new_lens + b) : a.N;
   const long long cap = static_cast<long long>(a.pps) << a.page_shift;
   return len >= 0 && n >= 0 && n <= a.N && static_cast<long long>(len) + n <= cap;
 }
 
 __device__ __forceinline__ bool kv_page(const KvArgs &a, int b, int local, int &page) {
-  page = __ldg(a.page_table + static_cast<long long>(b) * a.pps + local);
+  page = ld_given(a.page_table + static_cast<long long>(b) * a.pps + local);
   return page >= 0 && page < a.num_pages;
 }
 

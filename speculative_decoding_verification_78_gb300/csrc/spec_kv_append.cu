@@ -22,11 +22,11 @@ __device__ __forceinline__ int kv_position(const KvArgs &a, const RopeArgs &r, i
                                            int len) {
   long long pos;
   if (r.positions) {
-    pos = __ldg(r.positions + static_cast<long long>(b) * a.N + i);
+    pos = ld_given(r.positions + static_cast<long long>(b) * a.N + i);
   } else if (a.mask) {   // ancestors and itself: depth + 1 bits
     int bits = 0;
     const uint32_t *row = a.mask + (static_cast<long long>(b) * a.N + i) * a.W;
-    for (int w = 0; w < a.W; ++w) bits += __popc(__ldg(row + w));
+    for (int w = 0; w < a.W; ++w) bits += __popc(ld_given(row + w));
     pos = static_cast<long long>(len) + (bits > 0 ? bits - 1 : 0);
   } else {
     pos = static_cast<long long>(len) + i;
@@ -244,8 +244,8 @@ __global__ void __launch_bounds__(kThreads, 512 / kThreads)
     for (int k = 0; k < kU; ++k) {
       const int slot = p0 + row[k];
       if (row[k] >= 0 && slot >= from && slot < to) {
-        raw[k][0] = __ldg(reinterpret_cast<const uint4 *>(at[k] + h * a.D + un[k].a));
-        raw[k][1] = __ldg(reinterpret_cast<const uint4 *>(at[k] + h * a.D + un[k].b));
+        raw[k][0] = ld_given(reinterpret_cast<const uint4 *>(at[k] + h * a.D + un[k].a));
+        raw[k][1] = ld_given(reinterpret_cast<const uint4 *>(at[k] + h * a.D + un[k].b));
       }
     }
   };
@@ -367,15 +367,15 @@ __global__ void __launch_bounds__(32 * kCommitWarps)
   x /= a.Hkv;
   const int b = static_cast<int>(x % a.B);
   const long long layer = x / a.B;
-  const int len = __ldg(a.seq_lens + b), acc = __ldg(accept_len + b);
+  const int len = ld_given(a.seq_lens + b), acc = ld_given(accept_len + b);
   const int32_t *path = path_nodes + static_cast<long long>(b) * a.N;
   bool bad = acc < -1 || acc >= a.N;
   bool moves = false;
   int top = 0;   // the path's last node
   if (!bad) {
     for (int k = lane; k <= acc; k += 32) {
-      const int p = __ldg(path + k);
-      bad = bad || (k == 0 ? p != 0 : p <= __ldg(path + k - 1)) || p >= a.N;
+      const int p = ld_given(path + k);
+      bad = bad || (k == 0 ? p != 0 : p <= ld_given(path + k - 1)) || p >= a.N;
       moves = moves || p != k;
       top = max(top, p);
     }
@@ -412,7 +412,7 @@ __global__ void __launch_bounds__(32 * kCommitWarps)
     // node k's row, dequantised; false if it stays where it is or its page is bad
     auto source = [&](int k, float (&f)[8]) {
       if (k >= k1) return false;
-      const int node = __ldg(path + k);
+      const int node = ld_given(path + k);
       if (node == k) return false;
       const int slot = len + node;
       int spage;

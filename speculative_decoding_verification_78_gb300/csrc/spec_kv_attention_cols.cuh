@@ -158,7 +158,7 @@ __device__ __forceinline__ uint32_t columns_seeing(const AttnArgs &p, const Item
     see = 0;
 #pragma unroll
     for (int c = 0; c < F::C; ++c)
-      see |= (__ldg(m + static_cast<long long>(tok[col0 + c]) * p.a.W) >> (j & 31) & 1u) << c;
+      see |= (ld_given(m + static_cast<long long>(tok[col0 + c]) * p.a.W) >> (j & 31) & 1u) << c;
   } else if (j >= 0) {   // rows of token j and later ones
     const long long from = static_cast<long long>(j) * p.G - col0;
     see = from <= 0 ? ~0u : from < F::C ? ~0u << from : 0u;
@@ -281,7 +281,7 @@ template <class F>
 __device__ __forceinline__ uint4 fetch_query(const AttnArgs &p, const Item<F::kWin> &x, int tid) {
   int i;
   const typename F::T *at = query_of<F>(p, x.b, x.h, tid, i);
-  return at && i < x.n && x.ok ? __ldg(reinterpret_cast<const uint4 *>(at)) : make_uint4(0, 0, 0, 0);
+  return at && i < x.n && x.ok ? ld_given(reinterpret_cast<const uint4 *>(at)) : make_uint4(0, 0, 0, 0);
 }
 template <class F>
 __device__ __forceinline__ void place_query(uint4 raw, int tid, uint8_t *sq, float *qs) {
@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       const int32_t *table = p.a.page_table + static_cast<long long>(x.b) * p.a.pps;
       auto page_of = [&](int k) {
         const int slot = slot_of<F::kWin>(x, (skip + k) * kTile + (lane << p.a.page_shift));
-        return lane < per_tile && slot < x.end && span_seen<F::kWin>(p, x, slot, p.a.page) ? __ldg(table + (slot >> p.a.page_shift)) : 0;
+        return lane < per_tile && slot < x.end && span_seen<F::kWin>(p, x, slot, p.a.page) ? ld_given(table + (slot >> p.a.page_shift)) : 0;
       };
       int next = page_of(0);
       for (int k = 0; k < cnt && ok; ++k, ++it) {

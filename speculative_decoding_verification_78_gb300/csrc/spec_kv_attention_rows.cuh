@@ -139,10 +139,10 @@ __device__ __forceinline__ uint32_t seen_bits(const AttnArgs &p, int b, int i, i
   if (p.a.mask && j0 > -32) {
     const uint32_t *m = p.a.mask + (static_cast<long long>(b) * p.a.N + i) * p.a.W;
     if (j0 < 0) {
-      r = (__ldg(m) << -j0) | ((1u << -j0) - 1u);
+      r = (ld_given(m) << -j0) | ((1u << -j0) - 1u);
     } else {
       const int w = j0 >> 5;
-      const uint32_t lo = __ldg(m + w), hi = w + 1 < p.a.W ? __ldg(m + w + 1) : 0u;
+      const uint32_t lo = ld_given(m + w), hi = w + 1 < p.a.W ? ld_given(m + w + 1) : 0u;
       r = __funnelshift_r(lo, hi, j0 & 31);
     }
   }
@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         return lane < per_tile && at < pages_end &&
                span_seen<kWin>(p, x, at << p.a.page_shift, p.a.page);
       };
-      auto page_of = [&]() { return wanted() ? __ldg(table + at) : -1; };
+      auto page_of = [&]() { return wanted() ? ld_given(table + at) : -1; };
       int next = page_of();
       for (int k = 0; k < cnt; ++k, ++it) {
         const int s = it % F::S, page = next;
@@ -342,12 +342,12 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       };
       auto page_of = [&](int k) {
         const int at = place(k);
-        return k < cnt && wanted(at) ? __ldg(table + at) : -1;
+        return k < cnt && wanted(at) ? ld_given(table + at) : -1;
       };
       auto scales_of = [&](int page) {
         const int head = page * p.a.Hkv + x.h;
         return page >= 0 && page < p.a.num_pages
-                   ? make_float2(__ldg(p.a.k_scale + head), __ldg(p.a.v_scale + head))
+                   ? make_float2(ld_given(p.a.k_scale + head), ld_given(p.a.v_scale + head))
                    : make_float2(NAN, NAN);   // what reads a bad page is NaN
       };
       const int full = seen_by_all<NT, kWin>(p, x);

@@ -282,7 +282,7 @@ __device__ __forceinline__ int window_start(const AttnArgs &p, const Item<kWin> 
     const uint32_t *m = p.a.mask + (static_cast<long long>(x.b) * p.a.N + i) * p.a.W;
     int bits = 0;
 #pragma unroll 1
-    for (int w = 0; w < p.a.W; ++w) bits += __popc(__ldg(m + w));
+    for (int w = 0; w < p.a.W; ++w) bits += __popc(ld_given(m + w));
     at = max(bits - 1, 0);
   }
   return x.len + at - p.window + 1;
@@ -580,7 +580,7 @@ __device__ __forceinline__ void load_queries(const AttnArgs &p, const Item<kWin>
       map.row(n, i, g);
       raw[u] = make_uint4(0, 0, 0, 0);
       if (n < rows && i < x.n && x.ok)
-        raw[u] = __ldg(reinterpret_cast<const uint4 *>(
+        raw[u] = ld_given(reinterpret_cast<const uint4 *>(
             base + static_cast<long long>(i) * p.q_stride + static_cast<long long>(g) * D));
     }
 #pragma unroll

@@ -77,10 +77,10 @@ __global__ void __launch_bounds__(128) kv_release_kernel(const __grid_constant__
   int32_t *row = a.table + static_cast<long long>(b) * a.pps;
   int lo = 0, hi = a.pps, tail = a.pps;   // places [lo, hi) and [tail, pps) go
   if (window == 0) {
-    if (ended && !__ldg(ended + b)) return;
+    if (ended && !ld_given(ended + b)) return;
     if (threadIdx.x == 0) lens_io[b] = 0;
   } else {
-    const int len = __ldg(a.seq_lens + b);
+    const int len = ld_given(a.seq_lens + b);
     if (!length_ok(a, len)) {
       if (threadIdx.x == 0) set_status(a.status, SPEC_ERR_LENGTH);
       return;
@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kScanThreads) kv_reserve_kernel(const __grid_c
   // the item's place in the table if it lacks a page, else -1
   auto lacks = [&](int i) -> long long {
     const int b = i / touched, j = i - b * touched;
-    const int len = __ldg(a.seq_lens + b), n = new_lens ? __ldg(new_lens + b) : N;
+    const int len = ld_given(a.seq_lens + b), n = new_lens ? ld_given(new_lens + b) : N;
     if (n <= 0 || n > N || len < 0 || !length_ok(a, len) || !length_ok(a, len + n)) return -1;
     const int place = (len >> a.page_shift) + j;
     if (place > (len + n - 1) >> a.page_shift) return -1;
@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(kScanThreads) kv_reserve_kernel(const __grid_c
     base += sum;
   }
   for (int b = tid; b < a.B; b += kScanThreads) {
-    const int len = __ldg(a.seq_lens + b), n = new_lens ? __ldg(new_lens + b) : N;
+    const int len = ld_given(a.seq_lens + b), n = new_lens ? ld_given(new_lens + b) : N;
     int g = n;
     if (n < 0 || n > N || len < 0 || !length_ok(a, len) || !length_ok(a, len + n)) {
       set_status(a.status, SPEC_ERR_LENGTH);
@@ -197,7 +197,7 @@ struct Parent {
 };
 __device__ __forceinline__ Parent parent_of(const PageArgs &a, int p) {
   Parent x;
-  x.len = __ldg(a.seq_lens + p);
+  x.len = ld_given(a.seq_lens + p);
   x.ok = length_ok(a, x.len);
   x.full = x.ok ? x.len >> a.page_shift : 0;
   x.rest = x.ok ? x.len & (a.page - 1) : 0;
@@ -206,7 +206,7 @@ __device__ __forceinline__ Parent parent_of(const PageArgs &a, int p) {
 
 // A child's row of full pages, by threads `me`, `me` + `step`, ... (the place after them is left to fork_pages).
 __device__ __forceinline__ void fork_child(const PageArgs &a, const ForkArgs &f, int c, int me, int step) {
-  const int p = __ldg(f.parents + c);
+  const int p = ld_given(f.parents + c);
   Parent x{};
   x.ok = p >= 0 && p < a.B;
   if (x.ok) x = parent_of(a, p);
@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(128) kv_fork_rows_kernel(const __grid_constant
   if (threadIdx.x == 0) children = 0;
   __syncthreads();
   int n = 0;
-  for (int c = threadIdx.x; c < f.C; c += blockDim.x) n += __ldg(f.parents + c) == p;
+  for (int c = threadIdx.x; c < f.C; c += blockDim.x) n += ld_given(f.parents + c) == p;
   if (n) atomicAdd(&children, n);
   __syncthreads();
   fork_parent(a, f, p, children, threadIdx.x, blockDim.x);
@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(kScanThreads) kv_fork_pages_kernel(const __gri
   __syncthreads();
   if (f.release || kAll)
     for (int c = tid; c < f.C; c += kScanThreads) {
-      const int p = __ldg(f.parents + c);
+      const int p = ld_given(f.parents + c);
       if (p < 0 || p >= a.B) continue;
       if (f.release) atomicMin(&first[p], c);
       if (kAll) atomicAdd(&children[p], 1);
@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(kScanThreads) kv_fork_pages_kernel(const __gri
   auto child = [&](int c) {
     Child k{-1, -1, {}, false};
     if (c >= f.C) return k;
-    k.p = __ldg(f.parents + c);
+    k.p = ld_given(f.parents + c);
     if (k.p < 0 || k.p >= a.B) {
       k.p = -1;
       return k;
