@@ -51,7 +51,7 @@ __device__ __forceinline__ int unit_token(const Params &p, const UnitId &u) {
     if (u.r != p.gamma) {
       const int i = (u.r < p.Rt) ? u.r : u.r - p.Rt;
       if (!SPEC_CHECK(p, u.b >= 0 && u.b < p.B && i >= 0 && i < p.gamma)) return -1;
-      return __ldg(p.tokens + static_cast<long long>(u.b) * p.gamma + i);
+      return p.tokens[static_cast<long long>(u.b) * p.gamma + i];
     }
   }
   return -1;

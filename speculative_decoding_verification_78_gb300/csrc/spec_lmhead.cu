@@ -194,12 +194,12 @@ __device__ __forceinline__ void lm_epilogue_row(const Params &p, const LmArgs &a
       b = j / p.gamma;
       const int i = j - b * p.gamma;
       r = g1 + i;
-      tok = __ldg(p.tokens + static_cast<long long>(b) * p.gamma + i);
+      tok = p.tokens[static_cast<long long>(b) * p.gamma + i];
     } else {
       b = j / g1;
       const int i = j - b * g1;
       r = i;
-      tok = i < p.gamma ? __ldg(p.tokens + static_cast<long long>(b) * p.gamma + i) : -1;
+      tok = i < p.gamma ? p.tokens[static_cast<long long>(b) * p.gamma + i] : -1;
     }
   }
   const int n0 = hc * kLmHalf;
