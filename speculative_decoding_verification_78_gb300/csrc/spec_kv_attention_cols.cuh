@@ -58,7 +58,8 @@ constexpr int kSoftThreads = 2 * kGroupThreads;
 constexpr int kProducer = 2 * kGroupWarps, kMma = kProducer + 1;   // warps
 constexpr int kAttnThreads = 32 * (kMma + 1);
 // Shares of whole items may be this much longer (see search_line): 64 x 1 token with a window of 512 48 us (6 tiles an
-// item) for 52, of 1024 63 for 65 (if taken, 24); of 4096 142 for 128 (24), so they are not.
+// item) for 52, of 1024 63 for 65 (if taken, 24); of 4096 142 for 128 (24), so they are not. 16 x 6 tokens (32 columns)
+// with 512 17 for 25, with 1024 20 for 28.
 constexpr int kWholeTiles = 12;
 constexpr float kBias = 8.f;        // a new reference puts the largest weight at 2^8 ...
 constexpr float kTrigger = 15.f;    // ... and is taken when one exceeds 2^15 (fp16 ends at 2^16)
@@ -94,6 +95,10 @@ struct Cfg {
   static constexpr int CH = 8;                           // columns read at a time
   static constexpr int EC = NT / 4;                      // columns of a thread in the epilogue
   static constexpr int ECH = EC < 16 ? EC : 16;
+  // Whole items of up to this many tiles where there are less than two a CTA: 1 x 1 token with a window of 768 14.2 us
+  // (8 tiles) for 13.9, with 1536 18.1 for 16.1, 2 x 1 18.1 for 15.7; 1 x 6 tokens with 1024 18.9 (10) for 19.0, with
+  // 1536 22.2 for 20.7. (The groups take tiles in turn, so two are hardly longer than one.)
+  static constexpr int kFewTiles = NT == 16 ? 8 : 10, kFewLoad = 15;
   static constexpr int kSideBytes = kTile * D;           // K or V of a stage
   static constexpr int kPSpan = 2 * NT;                  // bytes of a row of P
   static constexpr int kPBytes = kTile * kPSpan;
@@ -323,7 +328,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   int t0 = 0, t1 = 0, total = 0, skip = 0;
   Item<F::kWin> x{};
   tc::fence_before_sync();
-  locate<F::NT, kAttnThreads, F::kWin, true, kWholeTiles>(p, sm.loc, t0, t1, total, x, skip);
+  locate<F::NT, kAttnThreads, F::kWin, true, kWholeTiles, F::kFewTiles, F::kFewLoad>(p, sm.loc, t0, t1, total, x, skip);
   tc::fence_after_sync();
   const uint32_t tmem = sm.tmem;
   if (tid == 32 * kProducer) publish_range(p, x, skip, t0, t1, total);   // (not of a softmax warp)

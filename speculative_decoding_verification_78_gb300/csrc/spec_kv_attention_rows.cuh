@@ -64,9 +64,6 @@ constexpr int kCopyK = kWidenWarp + kWidenWarps, kMma = kCopyK + 1, kCopyV = kCo
 // with an instruction in each role's branch, which is undefined: 48 / 152 / 233 / 237.
 constexpr int kRowsThreads = 32 * (kConsts + 1);
 constexpr int kEdge = 1 << 31;      // (with a window) beside a page's first slot: the tile needs masks
-// Shares of whole items may be this much longer (see search_line): 32 trees of 64 nodes with a window of 2048 110 us
-// for 128, 2 x 1500 tokens of 8 rows with 1000 60 for 69; with 4000 they would be 131 for 110 (40), so they are not.
-constexpr int kWholeTiles = 20;
 constexpr float kBias = 8.f;        // a new reference puts the row's largest weight at 2^8 ...
 constexpr float kTrigger = 15.f;    // ... and is taken when one exceeds 2^15 (fp16 ends at 2^16)
 
@@ -111,6 +108,15 @@ struct RowsCfg {
   // A tile's page constants give way to those of kPages tiles later, which are written when the
   // scores of the tile S before those are done, so after the values of at least two tiles more.
   static constexpr int kPages = RTC == 2 ? 4 : 8;
+  // Shares of whole items may be this much longer (see search_line). 256 rows: 32 trees of 64 nodes with a window of
+  // 2048 99 us (6) for 123, 24 97 (14) for 106, 5 50 (14) for 48, 3 48 (16) for 45; 2 x 1500 tokens of 8 rows with 1000
+  // 47 (7) for 58. 128 rows: trees of 24 nodes, 3 with 2048 29 (16) for 31, 8 with 4096 46 (20) for 45.
+  static constexpr int kWholeTiles = RTC == 2 ? 15 : 18;
+  // And whole items of up to this many tiles where there is at most one a CTA (128 rows: less than two, for the groups
+  // take tiles in turn): one tree of 64 nodes with a window of 512 25.1 us (6 tiles) for 25.8, of 768 28.4 for 27.0, of
+  // 2048 45 for 33; two with 1152 (170 tiles) 37 for 43. Of 24 nodes, two with 1536 24.5 (14) for 24.1, with 2048 28.2
+  // for 24.1.
+  static constexpr int kFewTiles = RTC == 2 ? 6 : 16, kFewLoad = RTC == 2 ? 8 : 15;
   static_assert(S + (RTC == 2 ? 2 : 3) <= kPages, "page constants are read by then");
   static constexpr uint32_t kColS = 0, kColO = 256;      // tensor memory: S of each group, O of each
 };
@@ -256,7 +262,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
   int t0 = 0, t1 = 0, total = 0, skip = 0;
   Item<kWin> x{};
   tc::fence_before_sync();
-  locate<NT, kRowsThreads, kWin, false, kWholeTiles>(p, *reinterpret_cast<LocateScratch<kWin> *>(smem + F::kOffQ), t0, t1, total, x, skip);
+  locate<NT, kRowsThreads, kWin, false, F::kWholeTiles, F::kFewTiles, F::kFewLoad>(p, *reinterpret_cast<LocateScratch<kWin> *>(smem + F::kOffQ), t0, t1, total, x, skip);
   tc::fence_after_sync();
   const uint32_t tmem = sm.tmem;
   // (by a lane of another warp than softmax's first: what one lane of that does here sets it apart from its warp

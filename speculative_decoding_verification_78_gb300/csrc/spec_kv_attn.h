@@ -326,7 +326,8 @@ __device__ __forceinline__ int range_of(int T, int t, int G) {
 //
 // Ranges are equal, but for this: where windows make items short, and shares of whole items would be at most
 // kWhole tiles longer, the CTAs take those. Then no item has parts that are written, read back and joined,
-// which costs more than the tiles.
+// which costs more than the tiles. Where there are so few tiles a CTA (up to kFewLoad eighths) that with an even cut
+// hardly any begins a second item, that costs less: there whole items are taken up to kFew tiles.
 template <bool kWin> struct LocateScratch {
   int warp_sum[32], warp_most[32];
   Item<kWin> x;
@@ -347,7 +348,7 @@ __device__ __forceinline__ int warp_head_tiles(const AttnArgs &p, Item<kWin> &x,
   }
   return __reduce_add_sync(0xffffffffu, s);
 }
-template <int NT, int kThreads, bool kWin, int kWhole>
+template <int NT, int kThreads, bool kWin, int kWhole, int kFew, int kFewLoad>
 __device__ __forceinline__ void search_line(const AttnArgs &p, LocateScratch<kWin> &sm) {
   constexpr int kWarps = kThreads / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -399,7 +400,8 @@ __device__ __forceinline__ void search_line(const AttnArgs &p, LocateScratch<kWi
     gaps = __any_sync(0xffffffffu, known & 1);
     const int items = p.a.B * p.a.Hkv * p.RT;
     const int each = (items + G - 1) / G;
-    if (gaps && static_cast<long long>(each) * most <= all / G + kWhole) {   // (so the numbers below are small)
+    const bool whole = 8LL * all <= kFewLoad * G ? most <= kFew : static_cast<long long>(each) * most <= all / G + kWhole;
+    if (gaps && whole) {   // (so the numbers below are small)
       const int i0 = range_start(items, blockIdx.x, G), n = range_start(items, blockIdx.x + 1, G) - i0;
       if (warp == 0) {
         int sum = 0;
@@ -473,18 +475,18 @@ __device__ __forceinline__ void search_line(const AttnArgs &p, LocateScratch<kWi
     }
   }
 }
-template <int NT, int kThreads, bool kWin, int kWhole>
+template <int NT, int kThreads, bool kWin, int kWhole, int kFew, int kFewLoad>
 __device__ __noinline__ void search_line_apart(const AttnArgs &p, LocateScratch<kWin> &sm) {
-  search_line<NT, kThreads, kWin, kWhole>(p, sm);
+  search_line<NT, kThreads, kWin, kWhole, kFew, kFewLoad>(p, sm);
 }
 // kApart: by a call, with registers of its own (the kernel for few rows spills less with it, the other more).
-template <int NT, int kThreads, bool kWin, bool kApart, int kWhole>
+template <int NT, int kThreads, bool kWin, bool kApart, int kWhole, int kFew, int kFewLoad>
 __device__ __forceinline__ void locate(const AttnArgs &p, LocateScratch<kWin> &sm, int &t0, int &t1,
                                        int &total, Item<kWin> &x, int &skip) {
   if constexpr (kApart)
-    search_line_apart<NT, kThreads, kWin, kWhole>(p, sm);
+    search_line_apart<NT, kThreads, kWin, kWhole, kFew, kFewLoad>(p, sm);
   else
-    search_line<NT, kThreads, kWin, kWhole>(p, sm);
+    search_line<NT, kThreads, kWin, kWhole, kFew, kFewLoad>(p, sm);
   __syncthreads();
   x = sm.x;
   t0 = sm.t0;
