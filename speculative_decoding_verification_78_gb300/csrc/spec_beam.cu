@@ -305,8 +305,8 @@ __device__ __forceinline__ Fixed fixed_of(long long v) {   // v 2^-48
   return Fixed{static_cast<unsigned long long>(v), static_cast<unsigned long long>(v >> 63), v >> 63};
 }
 __device__ __forceinline__ long long near_fixed(float f) { return __float2ll_rn(f * 0x1p48f); }   // |f| < 2^14
-__device__ __forceinline__ Fixed fixed_of(float f) {   // (no infinity, no NaN)
-  if (fabsf(f) < 16384.f) return fixed_of(near_fixed(f));
+// (What numbers of ordinary size do not need is called: a CTA runs this code once, so that fetching it costs as much.)
+__device__ __noinline__ Fixed far_fixed(float f) {
   const uint32_t bits = __float_as_uint(f);
   const unsigned long long mant = (bits & 0x7fffffu) | 0x800000u;
   const int up = static_cast<int>(bits >> 23 & 255u) - 127 - 23 + 48, word = up >> 6, at = up & 63;   // 39 .. 152
@@ -315,11 +315,14 @@ __device__ __forceinline__ Fixed fixed_of(float f) {   // (no infinity, no NaN)
                 static_cast<long long>(word == 0 ? 0ull : word == 1 ? high : low)};
   return bits >> 31 ? Fixed{0, 0, 0} - r : r;
 }
+__device__ __forceinline__ Fixed fixed_of(float f) {   // (no infinity, no NaN)
+  return fabsf(f) < 16384.f ? fixed_of(near_fixed(f)) : far_fixed(f);
+}
+__device__ __noinline__ float far_float(const Fixed &x) {
+  return static_cast<float>(x.lo) * 0x1p-48f + (static_cast<float>(x.mid) * 0x1p16f + static_cast<float>(x.hi) * 0x1p80f);
+}
 __device__ __forceinline__ float float_of(const Fixed &x) {   // x >= 0
-  float f = static_cast<float>(x.lo) * 0x1p-48f;
-  if (x.mid | static_cast<unsigned long long>(x.hi))
-    f += static_cast<float>(x.mid) * 0x1p16f + static_cast<float>(x.hi) * 0x1p80f;
-  return f;
+  return x.mid | static_cast<unsigned long long>(x.hi) ? far_float(x) : static_cast<float>(x.lo) * 0x1p-48f;
 }
 // (h, l) += (x, y), y and l small beside the others
 __device__ __forceinline__ void pair_add(float &h, float &l, float x, float y) {
