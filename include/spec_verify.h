@@ -480,7 +480,8 @@ int spec_kv_commit(const spec_kv_cache_t *cache, int layers, const int32_t *page
  * memory; layers lie one after another as for spec_kv_commit). Tables may share pages; the rows of one call's
  * table do not overlap. B and C are at most SPEC_MAX_SEQS.
  *   workspace  at least spec_kv_pages_workspace_bytes(num_pages, B) bytes (scratch; of spec_kv_fork: C for B)
- * In the data: a bad length (SPEC_ERR_LENGTH) leaves the sequence as it is; an entry of num_pages or more
+ * In the data: a bad length (SPEC_ERR_LENGTH) leaves the sequence as it is (a parent that ends gives back its
+ * pages all the same); an entry of num_pages or more
  * (SPEC_ERR_PAGE) counts as none; a page that is given back though nothing holds it stays free (SPEC_ERR_REFS).
  */
 size_t spec_kv_pages_workspace_bytes(int num_pages, int B);

@@ -17,8 +17,9 @@
 //
 // What bounds it: for many beams HBM while the logits stream (64 x 8 beams x 152064 in bf16: 156 MB in 26 us, 5.9
 // TB/s; 58 % of the issue slots, the rest waits for ex2 and for loads), then the finishing CTAs' chain of about ten
-// short steps (10 000 clocks, of which a row's sums 2600, reading quarters of units again 4400); together 33 us a call
-// among others. For few beams that chain and the host (4 beams x 32000: 11 us in a graph, 21 among others).
+// short steps (17 000 clocks, of which a row's sums 3400, counting distances 2700, listing quarters of units 3200,
+// reading those again 4200; each part runs once, and fetching its code is a good deal of it); together 34 us a call among
+// others. For few beams that chain and the host (4 beams x 32000: 9 us a call in a graph of ten, 22 among others).
 #include "spec_beam.h"
 #include "spec_common.cuh"
 #include "spec_kv.h"
@@ -579,8 +580,8 @@ struct Finish {
 
   // L_k again, to within sh.target[k], by the whole CTA: the units that hold most of the sum are summed again, the
   // others (all that may stay out by their shares) count as they are. Beams that start from one row with one score
-  // are all nearer than their sums tell: the first is summed, the others only compared with it (bf16, 4 x 32000 alike:
-  // 42 us a call, 87 with each summed; 2 x 64 x 152064: 600, 4900).
+  // are all nearer than their sums tell: the first is summed, the others only compared with it (bf16, in a
+  // graph of ten: 4 x 32000 alike 38 us a call, the same in other orders, each summed, 90; 2 x 64 x 152064 alike 480).
   __device__ __forceinline__ void refine(int k) const {
     const float M = sh.top[k], target = __int_as_float(sh.target[k]);
     for (int j = 0; j < k; ++j)
@@ -995,7 +996,7 @@ struct Finish {
   }
 
   // The same for any numbers of equal candidates: units and then tokens one by one, each the best of what is
-  // left. (16 of 8 beams: about 120 us more.) False if
+  // left. (4 x 8 beams x 32000 of one value each, 16 best: 179 us for 14.) False if
   // sums have to be improved first.
   __device__ bool select_any() const {
     // the n first units by their largest candidates: the n best candidates lie in them

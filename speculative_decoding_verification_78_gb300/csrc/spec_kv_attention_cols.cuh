@@ -40,8 +40,8 @@
 // added by the softmax: 362 against 333 us), the page constants worked out by the copying warp (407), scores
 // two tiles ahead of the values with the weights before the widening (390: a stage is held longer than
 // four of them last), waits without a vote, as the kernel for many rows has them (354: more spills). At 96
-// registers, what 18 warps leave, all forms but that of 16 columns and 64 dims spill 12 to 70 bytes (with the search
-// for the first item in line 40 to 90).
+// registers, what 18 warps leave, forms of 16 columns spill up to 4 bytes, of 32 84; with a window up to 16, and 108
+// to 120.
 #pragma once
 
 #include "spec_kv_attn.h"

@@ -27,7 +27,7 @@
 // MMA warp, its MMAs (1050) behind the other group's, a hand-over back; an item's start and end cost
 // another 20000. 32 trees of 64 nodes, four query heads a key head, 8192 tokens: 234 us with the join,
 // 1100 TFLOP/s (233 in the form these clocks were taken of, see the registers below); with a window of 2048 and 64
-// sinks 106 us, 670 TFLOP/s, two items of 17 tiles a CTA; at the steps before
+// sinks 100 us, 710 TFLOP/s, two items of 17 tiles a CTA; at the steps before
 // it with full rows per thread 367 us, with one MMA warp waiting for each hand-over in turn
 // 294 us, with spills in the epilogue 251, with the MMA warp asking for the keys after the weights and
 // issuing values and scores apart 244. No one part bounds it: dropping the second e4m3 term, half of the
